@@ -55,7 +55,8 @@ typedef enum {
   ATTN_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed (launch, allocation, ...) */
   ATTN_ERR_TIMEOUT = 4,     /* a device-side pipeline wait gave up (sticky, see attn_sync_status) */
   ATTN_ERR_ARCH = 5,        /* current device is not compute capability 10.3 (sm_103) */
-  ATTN_ERR_DEVICE_CHECK = 6 /* a kernel's own device-side check failed (sticky) */
+  ATTN_ERR_DEVICE_CHECK = 6 /* a kernel's own device-side check failed (sticky): a page table, length or row
+                               offset out of range (paged cache) */
 } attn_status_t;
 
 /*
@@ -233,6 +234,133 @@ int attn_fwd_fp8(const void* q, const void* k, const void* v, float descale_q, f
  */
 int attn_decode(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
                 int L, int d, float scale, void* stream);
+
+/*
+ * Paged key/value cache: storage of ragged sequences for serving, filled by
+ * attn_paged_append, read by attn_paged_decode and, in part, through
+ * attn_paged_select.  The pages name decode as the case where no N x N matrix
+ * exists and the cost is reading the cache (FlashAttention (PKM page), "注意");
+ * the layout of the cache in pages is this library's.
+ *
+ * Sequence b's token at position p lies in page block_table[b][p / page_size],
+ * slot p % page_size.  All arrays are caller-owned device memory; the struct
+ * itself is host memory, read during the call only.
+ *   k_pages, v_pages : [num_pages, kv_heads, page_size, head_dim] with strides
+ *                (in elements) between pages, heads and tokens as given, the
+ *                channels contiguous.  Strides are multiples of 16 bytes and
+ *                such that no two rows overlap; an order of dimensions is not
+ *                implied (pages of [page_size, kv_heads, head_dim], or K and V
+ *                in turns in one array, are strides of their own).
+ *   k_min, k_max : [num_pages, kv_heads, head_dim] contiguous, the cache's
+ *                type: channelwise minimum and maximum of a page's keys as
+ *                stored.  Both or neither; attn_paged_select needs them.
+ *   block_table : [B, max_pages] int32, rows table_stride ints apart.  Entries
+ *                behind a sequence's last page are never read.
+ *   seq_lens   : [B] int32, tokens in the cache (0: the slot holds no sequence).
+ *   type       : element type of the cache; bf16 and fp16 caches take rows of
+ *                their own type, e4m3 either.  The value of an e4m3 element is
+ *                k_scale (v_scale) times what is stored, finite and > 0; the
+ *                scales of the other types are 1.
+ *   Supported: head_dim in {32, 64, 128}; page_size a multiple of 8, at most
+ *   1024; max_pages * page_size <= 2^30; B * kv_heads and B * query heads
+ *   <= 65535.
+ * Table entries and lengths are read on the device only, so a captured graph
+ * may be replayed after they changed.  A page number outside [0, num_pages) or
+ * a length outside [0, max_pages * page_size] is never followed: what it would
+ * reach is left out, and attn_sync_status returns ATTN_ERR_DEVICE_CHECK.
+ */
+typedef enum { ATTN_TYPE_BF16 = 0, ATTN_TYPE_F16 = 1, ATTN_TYPE_E4M3 = 2 } attn_type_t;
+
+typedef struct {
+  void *k_pages, *v_pages;
+  long long k_strides[3], v_strides[3]; /* page, head, token; elements */
+  void *k_min, *k_max;                  /* or NULL */
+  const int* block_table;
+  const int* seq_lens;
+  long long table_stride;
+  int num_pages, page_size, kv_heads, head_dim, max_pages, B;
+  int type; /* attn_type_t */
+  float k_scale, v_scale;
+} attn_paged_kv_t;
+
+/* Token-major rows [rows, heads, head_dim], bf16 or fp16, channels contiguous:
+ * strides in elements (multiples of 8; of no effect along an extent of 1), so
+ * a slice of a projection's output needs no copy. */
+typedef struct {
+  void* data;
+  long long row_stride, head_stride;
+} attn_rows_t;
+
+/*
+ * Appends new tokens' keys and values to the cache, with the position rotation
+ * applied on the way.
+ *   k, v    : in, [rows, kv_heads, head_dim] of x_type.
+ *   q       : in, [rows, q_heads, head_dim], or NULL with q_heads = 0;
+ *   q_out   : out, the rotated q; may be q itself (same strides) and must not
+ *             overlap it otherwise.
+ *   token_start : [B + 1] int32, ascending: rows token_start[b] .. token_start[b + 1] - 1
+ *             are the last tokens of sequence b, at positions up to
+ *             seq_lens[b] - 1 (seq_lens counts them already).  Rows outside
+ *             [token_start[0], token_start[B]) are padding.  NULL: rows = B,
+ *             row b is the last token of sequence b.
+ *   cos, sin : [table_rows, rot_dim / 2] fp32, row p for position p; rot_dim a
+ *             multiple of 16 up to head_dim (0: no rotation).  Channels (i,
+ *             i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved, turn by angle i
+ *             in fp32: x1 cos - x2 sin, x2 cos + x1 sin; one rounding.
+ * An e4m3 cache holds x / scale rounded to nearest even, saturated at +-448
+ * (NaN stays NaN).  Summaries, where the cache has them: a page's is started
+ * by the token in its first slot and widened by later ones (a NaN is passed
+ * over); after a sequence was cut back it still covers the dropped tokens.
+ * Slots with seq_lens[b] = 0 and rows of padding write nothing, nor do
+ * positions at or past table_rows (ATTN_ERR_DEVICE_CHECK through
+ * attn_sync_status, as for a token_start that is not ascending within rows
+ * or gives a sequence more rows than tokens).  Two sequences must not append
+ * to one page.  Launches 1 kernel (0 where rows = 0).
+ */
+int attn_paged_append(const attn_paged_kv_t* kv, const attn_rows_t* k, const attn_rows_t* v, const attn_rows_t* q,
+                      const attn_rows_t* q_out, int q_heads, int rows, const int* token_start, const float* cos,
+                      const float* sin, int table_rows, int rot_dim, int interleaved, int x_type, void* stream);
+
+/*
+ * Exact attention of one new token per sequence over the cache.
+ *   q    : in,  [B, q_heads, head_dim] of x_type; query heads h * q_heads / kv_heads
+ *          and following share key/value head h.
+ *   o    : out, [B, q_heads, head_dim] contiguous, x_type
+ *   lse  : out, [B, q_heads] fp32
+ *   pages: NULL (all seq_lens[b] tokens), or [B, kv_heads, n_pages] int32 page
+ *          indices within the sequence (attn_paged_select's output): attention
+ *          over the tokens of those pages only.  Negative entries are skipped,
+ *          as are indices at or past the sequence's last page; a page that is
+ *          listed twice counts twice.
+ * A sequence without visible tokens gets o = 0, lse = -inf.  Slots behind a
+ * sequence's end may hold anything (NaN too).
+ *   workspace : attn_paged_decode_workspace() bytes of device memory, 16-byte
+ *          aligned, or NULL where that is 0; the call's own until it is done.
+ * Launches at most 2 kernels.
+ */
+int attn_paged_decode(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, void* o, float* lse,
+                      const int* pages, int n_pages, float scale, int x_type, void* workspace, void* stream);
+
+/*
+ * For each sequence and key/value head the n_select pages on which the new
+ * token's queries can have their largest logits (scale > 0):
+ *   score(p) = max over the head's query heads g of
+ *              sum_c max(q_gc k_min[p]_c, q_gc k_max[p]_c),
+ * an upper bound of q_g . k over the page's keys.  The first keep_first and the
+ * last keep_last pages (their sum at most n_select) are taken whatever their
+ * score; of equal scores the lower index.  The order is that of the scores in
+ * 64 bits, not of a rounded sum.  A NaN score ranks first.
+ *   pages : out, [B, kv_heads, n_select] int32, ascending; a sequence of fewer
+ *           pages gets all of them, then -1.
+ *   workspace : attn_paged_select_workspace() bytes, as for attn_paged_decode.
+ */
+int attn_paged_select(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, int* pages, int n_select,
+                      int keep_first, int keep_last, int x_type, void* workspace, void* stream);
+
+/* Bytes of workspace (0 for arguments the calls reject).  n_pages as for
+ * attn_paged_decode, 0 for all pages.  They depend on the sizes only. */
+long long attn_paged_decode_workspace(const attn_paged_kv_t* kv, int q_heads, int n_pages);
+long long attn_paged_select_workspace(const attn_paged_kv_t* kv);
 
 /*
  * attn_bwd without any memory allocation (bf16).  The pages have no

@@ -9,7 +9,8 @@ There is no fallback: if the library is missing or fails to load, every call
 raises.
 
 Layout: q, k, v, o, do and the gradients are contiguous [B, H, N, d] tensors
-(bf16 or fp16) on one CUDA device; lse is fp32 [B, H, N].
+(bf16 or fp16) on one CUDA device; lse is fp32 [B, H, N].  The paged-cache
+calls take token-major rows [rows, heads, d] and a ``PagedKV``.
 """
 from __future__ import annotations
 
@@ -20,7 +21,8 @@ import os
 import torch
 
 __all__ = ["attention", "attn_fwd", "attn_bwd", "attn_fwd_dropout", "attn_bwd_dropout", "attn_decode", "attn_fwd_fp8", "attn_fwd_blocksparse", "attn_bwd_blocksparse",
-           "attn_fwd_blocksparse_dropout", "attn_bwd_blocksparse_dropout", "sync_status", "status_string", "last_launch_count", "lib",
+           "attn_fwd_blocksparse_dropout", "attn_bwd_blocksparse_dropout", "PagedKV", "attn_paged_append",
+           "attn_paged_decode", "attn_paged_select", "rotation_tables", "sync_status", "status_string", "last_launch_count", "lib",
            "AttnError", "LIB_PATH", "STATUS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn.so")
@@ -33,6 +35,20 @@ class AttnError(RuntimeError):
     def __init__(self, fn: str, code: int):
         super().__init__("%s failed: %s (%d)" % (fn, STATUS.get(code, "?"), code))
         self.code = code
+
+
+class _PagedKvStruct(ctypes.Structure):  # attn_paged_kv_t
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_strides", ctypes.c_longlong * 3), ("v_strides", ctypes.c_longlong * 3),
+                ("k_min", ctypes.c_void_p), ("k_max", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("max_pages", ctypes.c_int), ("B", ctypes.c_int),
+                ("type", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class _RowsStruct(ctypes.Structure):  # attn_rows_t
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
 
 
 _lib = None
@@ -76,6 +92,15 @@ def lib() -> ctypes.CDLL:
         L.attn_fwd_fp8.restype = I
         L.attn_decode.argtypes = [P, P, P, P, P, I, I, I, I, F, P]
         L.attn_decode.restype = I
+        L.attn_paged_append.argtypes = [P, P, P, P, P, I, I, P, P, P, I, I, I, I, P]
+        L.attn_paged_decode.argtypes = [P, P, I, P, P, P, I, F, I, P, P]
+        L.attn_paged_select.argtypes = [P, P, I, P, I, I, I, I, P, P]
+        for f in (L.attn_paged_append, L.attn_paged_decode, L.attn_paged_select):
+            f.restype = I
+        L.attn_paged_decode_workspace.argtypes = [P, I, I]
+        L.attn_paged_select_workspace.argtypes = [P]
+        for f in (L.attn_paged_decode_workspace, L.attn_paged_select_workspace):
+            f.restype = ctypes.c_longlong
         L.attn_sync_status.argtypes = [P]
         L.attn_sync_status.restype = I
         L.attn_status_string.argtypes = [I]
@@ -289,6 +314,241 @@ def attn_decode(q, k, v, scale=None, o=None, lse=None, stream=None):
     if rc:
         raise AttnError("attn_decode", rc)
     return o, lse
+
+
+_TYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+
+
+class PagedKV:
+    """A paged key/value cache (attn_paged_kv_t): the caller's tensors, checked
+    once, and what the paged calls need to know of them.
+
+    k_pages, v_pages : [num_pages, kv_heads, page_size, d] bf16, fp16 or
+        float8_e4m3fn; any strides whose channels are contiguous and whose rows
+        do not overlap (pages stored as [page_size, kv_heads, d] come in as
+        ``t.permute(0, 2, 1, 3)``).
+    block_table : [B, max_pages] int32; seq_lens : [B] int32.  Both are read by
+        the kernels, so a program updates them in place, also between replays of
+        a captured graph.
+    k_scale, v_scale : value of one unit of an e4m3 cache (1 otherwise).
+    k_min, k_max : [num_pages, kv_heads, d] of the cache's type, contiguous: key
+        summaries for attn_paged_select, kept by attn_paged_append.
+
+    The object holds references to the tensors and no data of its own."""
+
+    __slots__ = ("k_pages", "v_pages", "block_table", "seq_lens", "k_min", "k_max", "k_scale", "v_scale", "device",
+                 "B", "kv_heads", "page_size", "head_dim", "max_pages", "dtype", "_struct", "_ref", "_ws")
+
+    def __init__(self, k_pages, v_pages, block_table, seq_lens, k_scale=1.0, v_scale=1.0, k_min=None, k_max=None):
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError("%s must be a CUDA tensor" % name)
+            if t.dtype not in _TYPE_CODES:
+                raise TypeError("%s must be bf16, fp16 or float8_e4m3fn" % name)
+            if t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError("%s must be [num_pages, kv_heads, page_size, d] with contiguous channels" % name)
+        dev = k_pages.device
+        if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.device != dev:
+            raise ValueError("v_pages must match k_pages' shape, type and device")
+        for name, t, dim in (("block_table", block_table, 2), ("seq_lens", seq_lens, 1)):
+            if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != torch.int32:
+                raise TypeError("%s must be an int32 tensor on the cache's device" % name)
+            if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+                raise ValueError("%s must have %d dimension(s), the last contiguous" % (name, dim))
+        if seq_lens.shape[0] != block_table.shape[0]:
+            raise ValueError("block_table and seq_lens must have one row per sequence")
+        if (k_min is None) != (k_max is None):
+            raise ValueError("k_min and k_max come together")
+        P, H, page, d = (int(x) for x in k_pages.shape)
+        for name, t in (("k_min", k_min), ("k_max", k_max)):
+            if t is None:
+                continue
+            if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != k_pages.dtype:
+                raise TypeError("%s must be of the cache's type on its device" % name)
+            if tuple(t.shape) != (P, H, d) or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous [num_pages, kv_heads, d]" % name)
+        self.k_pages, self.v_pages, self.block_table, self.seq_lens = k_pages, v_pages, block_table, seq_lens
+        self.k_min, self.k_max, self.k_scale, self.v_scale = k_min, k_max, float(k_scale), float(v_scale)
+        self.device, self.dtype = dev, k_pages.dtype
+        self.B, self.max_pages = int(block_table.shape[0]), int(block_table.shape[1])
+        self.kv_heads, self.page_size, self.head_dim = H, page, d
+        three = ctypes.c_longlong * 3
+        self._struct = _PagedKvStruct(
+            k_pages.data_ptr(), v_pages.data_ptr(), three(*k_pages.stride()[:3]), three(*v_pages.stride()[:3]),
+            k_min.data_ptr() if k_min is not None else None, k_max.data_ptr() if k_max is not None else None,
+            block_table.data_ptr(), seq_lens.data_ptr(), int(block_table.stride(0)), P, page, H, d, self.max_pages,
+            self.B, _TYPE_CODES[k_pages.dtype], self.k_scale, self.v_scale)
+        self._ref = ctypes.byref(self._struct)
+        self._ws = {}  # (kind, heads, pages) -> workspace bytes, a function of the sizes
+
+
+def _paged_rows(name, t, kv, heads=None, rows=None, dtype=None):
+    """(attn_rows_t reference, heads) of a [rows, heads, d] tensor."""
+    if not isinstance(t, torch.Tensor) or t.device != kv.device:
+        raise TypeError("%s must be a tensor on the cache's device" % name)
+    if t.dtype != dtype if dtype is not None else t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("%s must be %s" % (name, dtype if dtype is not None else "bf16 or fp16"))
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != kv.head_dim or stride[2] != 1 or (rows is not None and shape[0] != rows) or (
+            heads is not None and shape[1] != heads):
+        raise ValueError("%s must be [%s, %s, %d] with contiguous channels" % (
+            name, "rows" if rows is None else rows, "heads" if heads is None else heads, kv.head_dim))
+    return ctypes.byref(_RowsStruct(t.data_ptr(), stride[0], stride[1]))
+
+
+def _paged_x(kv, x):
+    """Element type code of new rows; the cache's own type, or either for e4m3."""
+    if kv.dtype != torch.float8_e4m3fn and x.dtype != kv.dtype:
+        raise TypeError("a %s cache takes rows of its own type" % kv.dtype)
+    return _TYPE_CODES[x.dtype]
+
+
+def _on_stream(stream):
+    """What a call allocates belongs to the stream that it runs on."""
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
+
+
+def rotation_tables(positions, rot_dim, base=10000.0, device=None):
+    """cos and sin [positions, rot_dim / 2] (fp32) of the angles
+    p * base^(-2 i / rot_dim), computed in 64 bits, for attn_paged_append."""
+    inv = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv
+    return angle.cos().float(), angle.sin().float()
+
+
+def attn_paged_append(kv, k, v, q=None, q_out=None, token_start=None, cos=None, sin=None, interleaved=False,
+                      stream=None):
+    """Append new tokens' k, v [rows, kv_heads, d] to the cache, rotated by the
+    tables cos, sin [positions, rot_dim / 2] (none: not rotated), and rotate q
+    [rows, q_heads, d] with them.  kv.seq_lens counts the new tokens already;
+    token_start [B + 1] int32 gives each sequence's rows (None: one row per
+    sequence).  Returns q_out (allocated where None; may be q itself), or None
+    without q.  Rows of padding and empty slots are left as they are."""
+    if not isinstance(kv, PagedKV):
+        raise TypeError("kv must be a PagedKV")
+    rk = _paged_rows("k", k, kv, kv.kv_heads)
+    rows = int(k.shape[0])
+    rv = _paged_rows("v", v, kv, kv.kv_heads, rows, k.dtype)
+    x = _paged_x(kv, k)
+    if token_start is not None:
+        if (not isinstance(token_start, torch.Tensor) or token_start.device != kv.device
+                or token_start.dtype != torch.int32 or tuple(token_start.shape) != (kv.B + 1,)
+                or token_start.stride(0) != 1):
+            raise ValueError("token_start must be a contiguous int32 [%d] on the cache's device" % (kv.B + 1))
+        start = token_start.data_ptr()
+    elif rows != kv.B:
+        raise ValueError("without token_start k and v must have one row per sequence (%d)" % kv.B)
+    else:
+        start = None
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    table_rows = rot = 0
+    pc = ps = None
+    if cos is not None:
+        for name, t in (("cos", cos), ("sin", sin)):
+            if not isinstance(t, torch.Tensor) or t.device != kv.device or t.dtype != torch.float32:
+                raise TypeError("%s must be a float32 tensor on the cache's device" % name)
+            if t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
+                raise ValueError("cos and sin must be contiguous [positions, rot_dim / 2] of one shape")
+        table_rows, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
+        pc, ps = cos.data_ptr(), sin.data_ptr()
+    with _on_device(k):
+        rq = ro = None
+        heads = 0
+        if q is not None:
+            rq = _paged_rows("q", q, kv, None, rows, k.dtype)
+            heads = int(q.shape[1])
+            if q_out is None:
+                with _on_stream(stream):
+                    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            ro = _paged_rows("q_out", q_out, kv, heads, rows, k.dtype)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        rc = lib().attn_paged_append(kv._ref, rk, rv, rq, ro, heads, rows, start, pc, ps, table_rows, rot,
+                                     int(bool(interleaved)), x, _stream_handle(stream))
+    if rc:
+        raise AttnError("attn_paged_append", rc)
+    return q_out
+
+
+def _paged_pages(kv, pages):
+    if (not isinstance(pages, torch.Tensor) or pages.device != kv.device or pages.dtype != torch.int32
+            or pages.dim() != 3 or tuple(pages.shape[:2]) != (kv.B, kv.kv_heads) or pages.shape[2] < 1
+            or not pages.is_contiguous()):
+        raise ValueError("pages must be a contiguous int32 [%d, %d, n >= 1] on the cache's device"
+                         % (kv.B, kv.kv_heads))
+    return int(pages.shape[2])
+
+
+def attn_paged_decode(kv, q, pages=None, scale=None, o=None, lse=None, stream=None):
+    """One decode step over the paged cache: q [B, q_heads, d] (query heads in
+    groups of q_heads / kv_heads share a key/value head) against each
+    sequence's seq_lens tokens, or the tokens of the listed ``pages``
+    [B, kv_heads, n] (attn_paged_select).  Returns (o [B, q_heads, d],
+    lse [B, q_heads]); an empty sequence gets o = 0, lse = -inf."""
+    if not isinstance(kv, PagedKV):
+        raise TypeError("kv must be a PagedKV")
+    rq = _paged_rows("q", q, kv, None, kv.B)
+    x = _paged_x(kv, q)
+    heads = int(q.shape[1])
+    n = 0 if pages is None else _paged_pages(kv, pages)
+    if scale is None:
+        scale = 1.0 / math.sqrt(kv.head_dim)
+    need = kv._ws.get((0, heads, n))
+    if need is None:
+        need = kv._ws[(0, heads, n)] = lib().attn_paged_decode_workspace(kv._ref, heads, n)
+    with _on_device(q), _on_stream(stream):
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif tuple(o.shape) != tuple(q.shape):
+            raise ValueError("o must have q's shape")
+        if lse is None:
+            lse = torch.empty((kv.B, heads), dtype=torch.float32, device=q.device)
+        elif tuple(lse.shape) != (kv.B, heads):
+            raise ValueError("lse must be [B, q_heads]")
+        for name, t, dtype in (("o", o, q.dtype), ("lse", lse, torch.float32)):
+            _check(name, t, None, dtype)
+            if t.device != kv.device:
+                raise ValueError("%s must be on the cache's device" % name)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        rc = lib().attn_paged_decode(kv._ref, rq, heads, o.data_ptr(), lse.data_ptr(),
+                                     pages.data_ptr() if pages is not None else None, n, float(scale), x,
+                                     ws.data_ptr() if need else None, _stream_handle(stream))
+    if rc:
+        raise AttnError("attn_paged_decode", rc)
+    return o, lse
+
+
+def attn_paged_select(kv, q, n_select, keep_first=1, keep_last=1, pages=None, stream=None):
+    """The ``n_select`` pages of each sequence and key/value head on which q
+    [B, q_heads, d] can have its largest logits (scale > 0), by the bound that
+    the cache's key summaries give; the first keep_first and last keep_last
+    pages always, equal scores by the lower index.  Returns int32
+    [B, kv_heads, n_select] page indices, ascending, -1 behind the pages of a
+    shorter sequence, for attn_paged_decode."""
+    if not isinstance(kv, PagedKV):
+        raise TypeError("kv must be a PagedKV")
+    if kv.k_min is None:
+        raise ValueError("the cache has no key summaries (k_min, k_max)")
+    rq = _paged_rows("q", q, kv, None, kv.B)
+    x = _paged_x(kv, q)
+    n = int(n_select)
+    if n < 1 or keep_first < 0 or keep_last < 0 or keep_first + keep_last > n:
+        raise ValueError("n_select must be at least 1 and keep_first + keep_last, both at least 0")
+    need = kv._ws.get(1)
+    if need is None:
+        need = kv._ws[1] = lib().attn_paged_select_workspace(kv._ref)
+    with _on_device(q), _on_stream(stream):
+        if pages is None:
+            pages = torch.empty((kv.B, kv.kv_heads, n), dtype=torch.int32, device=q.device)
+        elif _paged_pages(kv, pages) != n:
+            raise ValueError("pages must be [B, kv_heads, n_select]")
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        rc = lib().attn_paged_select(kv._ref, rq, int(q.shape[1]), pages.data_ptr(), n, int(keep_first),
+                                     int(keep_last), x, ws.data_ptr() if need else None, _stream_handle(stream))
+    if rc:
+        raise AttnError("attn_paged_select", rc)
+    return pages
 
 
 def _check_block_mask(block_mask, H, N):

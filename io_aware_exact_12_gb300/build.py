@@ -19,8 +19,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libattn.so")
-SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_noalloc.cu", "attn_diag.cu", "attn_decode.cu", "attn_fwd_fp8.cu"]
-HEADERS = ["attn_internal.h", "block_order.h", "tc_sm103.cuh", "dropout.cuh"]
+SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_noalloc.cu", "attn_diag.cu", "attn_decode.cu", "attn_fwd_fp8.cu",
+           "attn_paged_append.cu", "attn_paged_decode.cu", "attn_paged_select.cu"]
+HEADERS = ["attn_internal.h", "block_order.h", "tc_sm103.cuh", "dropout.cuh", "attn_paged.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

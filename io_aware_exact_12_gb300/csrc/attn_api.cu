@@ -5,14 +5,20 @@
 #include <cmath>
 #include <cstdint>
 #include <atomic>
+#include <initializer_list>
 #include <cstring>
 #include <mutex>
 
 #include "attn.h"
 #include "attn_internal.h"
+#include "attn_paged.h"
 
 // Sticky device-side status (one copy per device that loads the library).
 __device__ int g_attn_status;
+// Sticky word of the paged kernels' checks of tables and lengths.  Apart from
+// g_attn_status, which a pipeline wait reads to stop early: a bad table entry
+// must not stop an unrelated call.
+__device__ int g_attn_check;
 
 namespace attn {
 namespace {
@@ -22,6 +28,7 @@ thread_local int t_last_launches = 0;
 
 std::mutex g_mu;
 int* g_status_ptr[kMaxDevices] = {};
+int* g_check_ptr[kMaxDevices] = {};
 int g_arch_ok[kMaxDevices] = {};  // 0 unknown, 1 ok, -1 wrong arch
 cuuint64_t g_smem_attr_done[kMaxDevices][8] = {};
 const void* g_smem_attr_func[kMaxDevices][8] = {};
@@ -68,6 +75,16 @@ int* status_ptr(int dev) {
     g_status_ptr[dev] = static_cast<int*>(p);
   }
   return g_status_ptr[dev];
+}
+
+int* check_ptr(int dev) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_check_ptr[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_attn_check) != cudaSuccess) return nullptr;
+    g_check_ptr[dev] = static_cast<int*>(p);
+  }
+  return g_check_ptr[dev];
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -427,6 +444,303 @@ int fp8_entry(const void* q, const void* k, const void* v, float dq_s, float dk_
 }  // namespace
 }  // namespace attn
 
+namespace attn {
+namespace {
+
+// ---------------------------------------------------------------- paged cache
+
+struct Dim {
+  int64_t n, stride;  // extent, stride in bytes
+};
+
+// Strides of a tensor whose rows hold `row` contiguous bytes: multiples of 16;
+// for outputs also such that no two rows share a byte (each stride, in
+// ascending order, steps over all that the smaller ones span).
+bool strides_ok(Dim* dims, int count, int64_t row, bool output) {
+  for (int i = 0; i < count; ++i) {
+    if (dims[i].n == 1) dims[i].stride = row;  // never stepped along
+    if (dims[i].stride < 0 || dims[i].stride % 16 || dims[i].stride >= (int64_t{1} << 40)) return false;
+  }
+  if (!output) return true;
+  Dim s[3];
+  std::copy(dims, dims + count, s);
+  std::sort(s, s + count, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  int64_t span = row;
+  for (int i = 0; i < count; ++i) {
+    if (s[i].n == 1) continue;
+    if (s[i].stride < span) return false;
+    span = s[i].stride * (s[i].n - 1) + span;
+  }
+  return true;
+}
+
+size_t span_of(const Dim* dims, int count, int64_t row) {
+  int64_t n = row;
+  for (int i = 0; i < count; ++i) n += (dims[i].n - 1) * dims[i].stride;
+  return static_cast<size_t>(n);
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+bool any_overlap(const Span& out, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (o.p && out.p && overlaps(out.p, out.n, o.p, o.n)) return true;
+  return false;
+}
+
+// What the library needs of a cache, in bytes; host logic only.
+int paged_kv(const attn_paged_kv_t* c, int x_type, PagedKv* kv, Span* ks, Span* vs) {
+  if (!c || !c->k_pages || !c->v_pages || !c->block_table || !c->seq_lens) return kStatusInvalid;
+  if (c->B < 1 || c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->max_pages < 1) return kStatusInvalid;
+  if (c->type != kTypeBf16 && c->type != kTypeF16 && c->type != kTypeE4m3) return kStatusInvalid;
+  if (x_type != kTypeBf16 && x_type != kTypeF16) return kStatusInvalid;
+  if (c->type != kTypeE4m3 && c->type != x_type) return kStatusInvalid;
+  if (!std::isfinite(c->k_scale) || !std::isfinite(c->v_scale) || c->k_scale <= 0.f || c->v_scale <= 0.f)
+    return kStatusInvalid;
+  if (c->type != kTypeE4m3 && (c->k_scale != 1.f || c->v_scale != 1.f)) return kStatusInvalid;
+  if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return kStatusUnsupported;
+  if (c->page_size % 8 || c->page_size > 1024) return kStatusUnsupported;
+  if (c->B > 65535 || c->kv_heads > 65535 || static_cast<int64_t>(c->B) * c->kv_heads > 65535)
+    return kStatusUnsupported;
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > (int64_t{1} << 30)) return kStatusUnsupported;
+  if (c->table_stride < 0 || (c->B > 1 && c->table_stride < c->max_pages)) return kStatusInvalid;
+  if ((c->k_min == nullptr) != (c->k_max == nullptr)) return kStatusInvalid;
+  for (const void* p : {static_cast<const void*>(c->k_pages), static_cast<const void*>(c->v_pages),
+                        static_cast<const void*>(c->k_min), static_cast<const void*>(c->k_max)})
+    if (!aligned16(p)) return kStatusInvalid;
+  if ((reinterpret_cast<uintptr_t>(c->block_table) & 3u) || (reinterpret_cast<uintptr_t>(c->seq_lens) & 3u))
+    return kStatusInvalid;
+  const int e = type_bytes(c->type);
+  const int64_t row = static_cast<int64_t>(c->head_dim) * e;
+  for (int which = 0; which < 2; ++which) {
+    const long long* st = which ? c->v_strides : c->k_strides;
+    for (int i = 0; i < 3; ++i)
+      if (st[i] < 0 || st[i] >= (1ll << 40)) return kStatusInvalid;
+    Dim dims[3] = {{c->num_pages, st[0] * e}, {c->kv_heads, st[1] * e}, {c->page_size, st[2] * e}};
+    if (!strides_ok(dims, 3, row, true)) return kStatusInvalid;
+    *(which ? vs : ks) = {which ? c->v_pages : c->k_pages, span_of(dims, 3, row)};
+    (which ? kv->v_page : kv->k_page) = dims[0].stride;
+    (which ? kv->v_head : kv->k_head) = dims[1].stride;
+    (which ? kv->v_tok : kv->k_tok) = dims[2].stride;
+  }
+  if (c->k_pages == c->v_pages) return kStatusInvalid;
+  const size_t sum = static_cast<size_t>(c->num_pages) * c->kv_heads * row;
+  if (c->k_min && (overlaps(c->k_min, sum, c->k_max, sum) || any_overlap({c->k_min, sum}, {*ks, *vs}) ||
+                   any_overlap({c->k_max, sum}, {*ks, *vs})))
+    return kStatusInvalid;
+  kv->k = static_cast<uint8_t*>(c->k_pages);
+  kv->v = static_cast<uint8_t*>(c->v_pages);
+  kv->kmin = static_cast<uint8_t*>(c->k_min);
+  kv->kmax = static_cast<uint8_t*>(c->k_max);
+  kv->table = c->block_table;
+  kv->table_stride = c->table_stride;
+  kv->lens = c->seq_lens;
+  kv->num_pages = c->num_pages;
+  kv->page = c->page_size;
+  kv->H = c->kv_heads;
+  kv->d = c->head_dim;
+  kv->max_pages = c->max_pages;
+  kv->B = c->B;
+  kv->type = c->type;
+  kv->k_scale = c->k_scale;
+  kv->v_scale = c->v_scale;
+  return kStatusOk;
+}
+
+// Rows [rows][heads][d] of two-byte elements.
+int paged_rows(const attn_rows_t* r, int64_t rows, int heads, int d, bool output, PagedRows* out, Span* span) {
+  if (!r || !r->data || !aligned16(r->data)) return kStatusInvalid;
+  for (long long s : {r->row_stride, r->head_stride})
+    if (s < 0 || s >= (1ll << 38)) return kStatusInvalid;
+  Dim dims[2] = {{rows, r->row_stride * 2}, {heads, r->head_stride * 2}};
+  if (!strides_ok(dims, 2, static_cast<int64_t>(d) * 2, output)) return kStatusInvalid;
+  *out = {static_cast<uint8_t*>(r->data), dims[0].stride, dims[1].stride};
+  *span = {r->data, span_of(dims, 2, static_cast<int64_t>(d) * 2)};
+  return kStatusOk;
+}
+
+int query_heads_ok(int q_heads, const PagedKv& kv) {
+  if (q_heads < 1 || q_heads % kv.H) return kStatusInvalid;
+  return static_cast<int64_t>(kv.B) * q_heads > 65535 ? kStatusUnsupported : kStatusOk;
+}
+
+int paged_device(PagedKv* kv, int** status) {
+  int dev = 0;
+  const int rc = current_device(&dev);
+  if (rc) return rc;
+  *status = status_ptr(dev);
+  kv->check = check_ptr(dev);
+  return *status && kv->check ? kStatusOk : kStatusCuda;
+}
+
+int paged_append_entry(const attn_paged_kv_t* c, const attn_rows_t* k, const attn_rows_t* v, const attn_rows_t* q,
+                       const attn_rows_t* q_out, int q_heads, int rows, const int* token_start, const float* cos,
+                       const float* sin, int table_rows, int rot_dim, int interleaved, int x_type, void* stream) {
+  PagedAppendArgs a = {};
+  Span ks, vs, kn, vn, qn = {}, qo = {};
+  int rc = paged_kv(c, x_type, &a.kv, &ks, &vs);
+  if (rc) return rc;
+  if (rows < 0 || q_heads < 0 || rot_dim < 0) return kStatusInvalid;
+  if (!token_start && rows != c->B) return kStatusInvalid;
+  if ((q == nullptr) != (q_heads == 0) || (q == nullptr) != (q_out == nullptr)) return kStatusInvalid;
+  if (rows > (1 << 30) || q_heads > 65535) return kStatusUnsupported;
+  if (rot_dim % 16 || rot_dim > c->head_dim) return kStatusUnsupported;
+  if (rot_dim && (!cos || !sin || table_rows < 1 || !aligned16(cos) || !aligned16(sin))) return kStatusInvalid;
+  if (reinterpret_cast<uintptr_t>(token_start) & 3u) return kStatusInvalid;
+  if (rows == 0) {
+    t_last_launches = 0;
+    return kStatusOk;
+  }
+  if ((rc = paged_rows(k, rows, c->kv_heads, c->head_dim, false, &a.k, &kn))) return rc;
+  if ((rc = paged_rows(v, rows, c->kv_heads, c->head_dim, false, &a.v, &vn))) return rc;
+  if (q) {
+    if ((rc = paged_rows(q, rows, q_heads, c->head_dim, false, &a.q, &qn))) return rc;
+    if ((rc = paged_rows(q_out, rows, q_heads, c->head_dim, true, &a.q_out, &qo))) return rc;
+    // q may be rotated in place (k and v may then lie between its rows)
+    const bool in_place = a.q.p == a.q_out.p && a.q.row == a.q_out.row && a.q.head == a.q_out.head;
+    if (!in_place && any_overlap(qo, {qn, kn, vn})) return kStatusInvalid;
+  }
+  const Span ts = {token_start, (static_cast<size_t>(c->B) + 1) * 4};
+  const size_t tb = static_cast<size_t>(rot_dim ? table_rows : 0) * (rot_dim / 2) * 4;
+  const Span lens = {c->seq_lens, static_cast<size_t>(c->B) * 4}, cs = {tb ? cos : nullptr, tb}, sn = {tb ? sin : nullptr, tb};
+  const Span table = {c->block_table, (static_cast<size_t>(c->B - 1) * c->table_stride + c->max_pages) * 4};
+  const size_t sum = static_cast<size_t>(c->num_pages) * c->kv_heads * c->head_dim * type_bytes(c->type);
+  for (const Span& out : {ks, vs, Span{c->k_min, sum}, Span{c->k_max, sum}})
+    if (any_overlap(out, {kn, vn, qn, qo, ts, lens, cs, sn, table})) return kStatusInvalid;
+  if (any_overlap(qo, {ts, lens, cs, sn, table})) return kStatusInvalid;
+  a.Hq = q_heads;
+  a.rows = rows;
+  a.token_start = token_start;
+  a.cos = cos;
+  a.sin = sin;
+  a.table_rows = table_rows;
+  a.rot = rot_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.x_type = x_type;
+  a.stream = static_cast<cudaStream_t>(stream);
+  int* status = nullptr;
+  if ((rc = paged_device(&a.kv, &status))) return rc;
+  int launches = 0;
+  if ((rc = launch_paged_append(a, &launches)) == kStatusOk) t_last_launches = launches;
+  return rc;
+}
+
+int paged_decode_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_heads, void* o, float* lse,
+                       const int* pages, int n_pages, float scale, int x_type, void* workspace, void* stream) {
+  PagedDecodeArgs a = {};
+  Span ks, vs, qn;
+  int rc = paged_kv(c, x_type, &a.kv, &ks, &vs);
+  if (rc) return rc;
+  if (!o || !lse || !std::isfinite(scale) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return kStatusInvalid;
+  if (pages && (n_pages < 1 || (reinterpret_cast<uintptr_t>(pages) & 3u))) return kStatusInvalid;
+  if ((rc = query_heads_ok(q_heads, a.kv))) return rc;
+  if (pages && static_cast<int64_t>(n_pages) * c->page_size > (int64_t{1} << 30)) return kStatusUnsupported;
+  if ((rc = paged_rows(q, c->B, q_heads, c->head_dim, false, &a.q, &qn))) return rc;
+  const int64_t need = paged_decode_workspace(c->B, q_heads, c->kv_heads, c->head_dim, c->page_size,
+                                              pages ? n_pages : c->max_pages);
+  if (need && (!workspace || !aligned16(workspace))) return kStatusInvalid;
+  const size_t obytes = static_cast<size_t>(c->B) * q_heads * c->head_dim * 2, lbytes = static_cast<size_t>(c->B) * q_heads * 4;
+  const Span list = {pages, pages ? static_cast<size_t>(c->B) * c->kv_heads * n_pages * 4 : 0};
+  const Span table = {c->block_table, (static_cast<size_t>(c->B - 1) * c->table_stride + c->max_pages) * 4};
+  const Span lens = {c->seq_lens, static_cast<size_t>(c->B) * 4};
+  const Span outs[3] = {{o, obytes}, {lse, lbytes}, {need ? workspace : nullptr, static_cast<size_t>(need)}};
+  for (int i = 0; i < 3; ++i) {
+    if (any_overlap(outs[i], {ks, vs, qn, list, table, lens})) return kStatusInvalid;
+    if (any_overlap(outs[i], {outs[(i + 1) % 3]})) return kStatusInvalid;
+  }
+  a.Hq = q_heads;
+  a.o = static_cast<uint8_t*>(o);
+  a.lse = lse;
+  a.pages = pages;
+  a.n_pages = n_pages;
+  a.sl2 = scale * c->k_scale * 1.4426950408889634f;
+  a.x_type = x_type;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.ws = static_cast<uint8_t*>(workspace);
+  if ((rc = paged_device(&a.kv, &a.status))) return rc;
+  int launches = 0;
+  if ((rc = launch_paged_decode(a, &launches)) == kStatusOk) t_last_launches = launches;
+  return rc;
+}
+
+int paged_select_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_heads, int* pages, int n_select,
+                       int keep_first, int keep_last, int x_type, void* workspace, void* stream) {
+  PagedSelectArgs a = {};
+  Span ks, vs, qn;
+  int rc = paged_kv(c, x_type, &a.kv, &ks, &vs);
+  if (rc) return rc;
+  if (!c->k_min || !pages || (reinterpret_cast<uintptr_t>(pages) & 3u)) return kStatusInvalid;
+  if (n_select < 1 || keep_first < 0 || keep_last < 0 || static_cast<int64_t>(keep_first) + keep_last > n_select)
+    return kStatusInvalid;
+  if ((rc = query_heads_ok(q_heads, a.kv))) return rc;
+  if (static_cast<int64_t>(n_select) * c->page_size > (int64_t{1} << 30)) return kStatusUnsupported;
+  if ((rc = paged_rows(q, c->B, q_heads, c->head_dim, false, &a.q, &qn))) return rc;
+  const int64_t need = paged_select_workspace(c->B, c->kv_heads, c->max_pages);
+  if (need && (!workspace || !aligned16(workspace))) return kStatusInvalid;
+  const size_t sum = static_cast<size_t>(c->num_pages) * c->kv_heads * c->head_dim * type_bytes(c->type);
+  const Span table = {c->block_table, (static_cast<size_t>(c->B - 1) * c->table_stride + c->max_pages) * 4};
+  const Span lens = {c->seq_lens, static_cast<size_t>(c->B) * 4};
+  const Span out = {pages, static_cast<size_t>(c->B) * c->kv_heads * n_select * 4};
+  const Span ws = {need ? workspace : nullptr, static_cast<size_t>(need)};
+  for (const Span& s : {out, ws})
+    if (any_overlap(s, {qn, Span{c->k_min, sum}, Span{c->k_max, sum}, ks, vs, table, lens})) return kStatusInvalid;
+  if (any_overlap(out, {ws})) return kStatusInvalid;
+  a.Hq = q_heads;
+  a.pages = pages;
+  a.n_select = n_select;
+  a.keep_first = keep_first;
+  a.keep_last = keep_last;
+  a.x_type = x_type;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.ws = static_cast<uint8_t*>(workspace);
+  int* status = nullptr;
+  if ((rc = paged_device(&a.kv, &status))) return rc;
+  int launches = 0;
+  if ((rc = launch_paged_select(a, &launches)) == kStatusOk) t_last_launches = launches;
+  return rc;
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+int attn_paged_append(const attn_paged_kv_t* kv, const attn_rows_t* k, const attn_rows_t* v, const attn_rows_t* q,
+                      const attn_rows_t* q_out, int q_heads, int rows, const int* token_start, const float* cos,
+                      const float* sin, int table_rows, int rot_dim, int interleaved, int x_type, void* stream) {
+  return attn::paged_append_entry(kv, k, v, q, q_out, q_heads, rows, token_start, cos, sin, table_rows, rot_dim,
+                                  interleaved, x_type, stream);
+}
+
+int attn_paged_decode(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, void* o, float* lse,
+                      const int* pages, int n_pages, float scale, int x_type, void* workspace, void* stream) {
+  return attn::paged_decode_entry(kv, q, q_heads, o, lse, pages, n_pages, scale, x_type, workspace, stream);
+}
+
+int attn_paged_select(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, int* pages, int n_select,
+                      int keep_first, int keep_last, int x_type, void* workspace, void* stream) {
+  return attn::paged_select_entry(kv, q, q_heads, pages, n_select, keep_first, keep_last, x_type, workspace, stream);
+}
+
+long long attn_paged_decode_workspace(const attn_paged_kv_t* kv, int q_heads, int n_pages) {
+  if (!kv || kv->B < 1 || kv->kv_heads < 1 || kv->page_size < 1 || kv->head_dim < 1 || q_heads < 1 ||
+      q_heads % kv->kv_heads || (n_pages < 1 ? kv->max_pages : n_pages) < 1)
+    return 0;
+  return attn::paged_decode_workspace(kv->B, q_heads, kv->kv_heads, kv->head_dim, kv->page_size,
+                                      n_pages < 1 ? kv->max_pages : n_pages);
+}
+
+long long attn_paged_select_workspace(const attn_paged_kv_t* kv) {
+  if (!kv || kv->B < 1 || kv->kv_heads < 1 || kv->max_pages < 1) return 0;
+  return attn::paged_select_workspace(kv->B, kv->kv_heads, kv->max_pages);
+}
+
+}  // extern "C"
+
 extern "C" {
 
 int attn_fwd_dropout(const void* q, const void* k, const void* v, void* o, float* lse, int B,
@@ -600,12 +914,15 @@ int attn_sync_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return attn::kStatusCuda;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return attn::kStatusCuda;
-  int value = 0;
+  int value = 0, check = 0;
   const int zero = 0;
   if (cudaMemcpyFromSymbol(&value, g_attn_status, sizeof(int)) != cudaSuccess) return attn::kStatusCuda;
   if (value != 0 && cudaMemcpyToSymbol(g_attn_status, &zero, sizeof(int)) != cudaSuccess)
     return attn::kStatusCuda;
-  return value;
+  if (cudaMemcpyFromSymbol(&check, g_attn_check, sizeof(int)) != cudaSuccess) return attn::kStatusCuda;
+  if (check != 0 && cudaMemcpyToSymbol(g_attn_check, &zero, sizeof(int)) != cudaSuccess)
+    return attn::kStatusCuda;
+  return value ? value : check;
 }
 
 const char* attn_status_string(int status) {

@@ -1,0 +1,686 @@
+"""The paged cache on the GPU against plain float64 forms: appending rotated
+rows, decoding over all pages or over selected ones, selecting pages, and the
+three together as a server runs them.
+
+Tolerances come from the arithmetic.  A rounding to a type errs by at most half
+a step, finfo(t).eps / 2 of the value.
+  append: fp32 rotation of exact inputs errs by at most 3 roundings, 2^-22 of
+    |x1| + |x2|, then one rounding to the stored type (e4m3: after a
+    multiplication by 1 / scale, 2 more fp32 roundings; below 2^-6 its step is
+    2^-9 whatever the value).
+  decode: logits are fp32 sums of d products with the weights' argument rounded
+    once more, off by dt <= (d + 8) 2^-24 sum |q k| |scale| each; a weight then
+    by 2 dt + 2^-20 relative (exp2 and the sums); P is rounded to 16 bits with
+    the same rounded weights in the denominator, so by the 16-bit type's eps / 2
+    about a mean of w |v|.  O then has one rounding of its own.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, E4M3 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+NAN_BYTE = 0x7F
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from io_aware_exact_12_gb300 import build as b
+    b.build()
+    import io_aware_exact_12_gb300 as p
+    p.lib()
+    return p
+
+
+def _raw(t):
+    return t.view(torch.uint8) if t.dtype == E4M3 else t
+
+
+def _storage(P, H, page, d, dtype, layout):
+    """Two [P, H, page, d] views in the given memory order, every element NaN."""
+    def nans(shape):
+        if dtype == E4M3:
+            return torch.full(shape, NAN_BYTE, dtype=torch.uint8, device="cuda").view(E4M3)
+        return torch.full(shape, math.nan, dtype=dtype, device="cuda")
+    if layout == "heads":       # [P, H, page, d]
+        return nans((P, H, page, d)), nans((P, H, page, d))
+    if layout == "tokens":      # [P, page, H, d]
+        return nans((P, page, H, d)).permute(0, 2, 1, 3), nans((P, page, H, d)).permute(0, 2, 1, 3)
+    both = nans((P, 2, H, page, d))  # K and V of a page in turns
+    return both[:, 0], both[:, 1]
+
+
+class Case:
+    """A cache of sequences `lens`: random pages, NaN in every slot that no token fills, table entries behind a
+    sequence's pages that no kernel may follow."""
+
+    def __init__(self, pkg, lens, H=2, page=16, d=64, dtype=BF16, layout="heads", seed=0, scales=(1.0, 1.0), width=None,
+                 summaries=False, fill=True, spare=3):
+        g = torch.Generator().manual_seed(seed)
+        self.g, self.lens_list, self.H, self.page, self.d, self.dtype = g, list(lens), H, page, d, dtype
+        need = [-(-n // page) for n in lens]
+        width = max(need + [1]) + 1 if width is None else width
+        P = sum(need) + spare
+        ids = torch.randperm(P, generator=g).tolist()
+        self.table = torch.full((len(lens), width), 0x7FFFFFF0, dtype=torch.int32)
+        for b, n in enumerate(need):
+            for j in range(n):
+                self.table[b, j] = ids.pop()
+        self.free = ids
+        self.k, self.v = _storage(P, H, page, d, dtype, layout)
+        self.scales = scales if dtype == E4M3 else (1.0, 1.0)
+        self.k_ref = torch.zeros(len(lens), H, max(need + [1]) * page, d, dtype=torch.float64)  # as values
+        self.v_ref = self.k_ref.clone()
+        for b, n in enumerate(lens if fill else []):
+            for ref, to, s in ((self.k_ref, self.k, self.scales[0]), (self.v_ref, self.v, self.scales[1])):
+                x = torch.randn((H, n, d), generator=g) / s
+                x = x.clamp(-448, 448).to(dtype)
+                ref[b, :, :n] = x.double() * s
+                for j in range(need[b]):
+                    m = min(page, n - j * page)
+                    _raw(to)[int(self.table[b, j]), :, :m] = _raw(x[:, j * page:j * page + m].contiguous()).cuda()
+        self.k_min = self.k_max = None
+        if summaries:
+            self.k_min = torch.zeros(P, H, d, dtype=dtype, device="cuda")
+            self.k_max = torch.zeros(P, H, d, dtype=dtype, device="cuda")
+            for b, n in enumerate(lens if fill else []):
+                for j in range(need[b]):
+                    x = self.k_ref[b, :, j * page:min(n, (j + 1) * page)] / self.scales[0]
+                    _raw(self.k_min)[int(self.table[b, j])] = _raw(x.amin(1).to(dtype)).cuda()
+                    _raw(self.k_max)[int(self.table[b, j])] = _raw(x.amax(1).to(dtype)).cuda()
+        self.block_table = self.table.cuda()
+        self.seq_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.kv = pkg.PagedKV(self.k, self.v, self.block_table, self.seq_lens, k_scale=self.scales[0],
+                              v_scale=self.scales[1], k_min=self.k_min, k_max=self.k_max)
+
+    def randn(self, *shape, dtype=None):
+        return torch.randn(shape, generator=self.g).to(dtype or (BF16 if self.dtype == E4M3 else self.dtype))
+
+
+def _reference(c, q, scale, keys=None):
+    """float64 attention of q [B, Hq, d] over the cached values; keys[b][h]: the visible positions (None: all).
+    Also each output's tolerance."""
+    B, Hq, d = q.shape
+    G = Hq // c.H
+    o, lse = torch.zeros(B, Hq, d, dtype=torch.float64), torch.full((B, Hq), -math.inf, dtype=torch.float64)
+    tol_o, tol_l = torch.zeros(B, Hq, d, dtype=torch.float64), torch.zeros(B, Hq, dtype=torch.float64)
+    eps = torch.finfo(q.dtype).eps / 2
+    eps_p = eps if c.dtype != E4M3 else torch.finfo(F16).eps / 2  # an e4m3 cache is multiplied in fp16
+    for b, n in enumerate(c.lens_list):
+        for h in range(c.H):
+            at = torch.arange(n) if keys is None else torch.as_tensor(keys[b][h], dtype=torch.long)
+            if len(at) == 0:
+                continue
+            k, v = c.k_ref[b, h, at], c.v_ref[b, h, at]
+            x = q[b, h * G:(h + 1) * G].double()
+            t = scale * (x @ k.T)
+            w = torch.softmax(t, -1)
+            dt = ((d + 8) * 2.0 ** -24 * abs(scale) * (x.abs() @ k.abs().T)).amax(-1, keepdim=True)
+            rows = slice(h * G, (h + 1) * G)
+            o[b, rows], lse[b, rows] = w @ v, torch.logsumexp(t, -1)
+            spread = w @ v.abs() + (w @ v).abs()
+            tol_o[b, rows] = eps * (w @ v).abs() * (1 + 1e-3) + (eps_p + 2 * dt + 2.0 ** -20) * spread + 1e-30
+            if q.dtype == F16:
+                tol_o[b, rows] += 2.0 ** -25  # fp16 steps below its normal range
+            tol_l[b, rows] = dt[:, 0] + 2.0 ** -20 + 2.0 ** -22 * lse[b, rows].abs()
+    return o, lse, tol_o, tol_l
+
+
+def _check_decode(pkg, c, q, scale=None, pages=None, keys=None, **kw):
+    scale = 1 / math.sqrt(c.d) if scale is None else scale
+    o, lse = pkg.attn_paged_decode(c.kv, q.cuda() if not q.is_cuda else q, pages=pages, scale=scale, **kw)
+    assert pkg.sync_status() == 0
+    ro, rl, to, tl = _reference(c, q.cpu(), scale, keys)
+    err = (o.double().cpu() - ro).abs()
+    assert torch.isfinite(o.float()).all()
+    assert (err <= to).all(), "o off by %g of its tolerance" % (err / to).max()
+    l = lse.double().cpu()
+    none = rl == -math.inf
+    assert torch.equal(l == -math.inf, none)
+    lerr = (l[~none] - rl[~none]).abs()
+    assert (lerr <= tl[~none]).all(), "lse off by %g of its tolerance" % (lerr / tl[~none]).max()
+    assert (o.cpu()[none] == 0).all()
+    return o, lse
+
+
+TYPES = [(BF16, BF16, (1.0, 1.0)), (F16, F16, (1.0, 1.0)), (BF16, E4M3, (0.03, 0.011)), (F16, E4M3, (0.0625, 0.5))]
+
+
+# ------------------------------------------------------------------ decode
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+def test_decode_lengths_around_the_borders(pkg, x, dtype, scales, d):
+    lens = [0, 1, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 1000, 0]
+    c = Case(pkg, lens, H=2, page=16, d=d, dtype=dtype, scales=scales, seed=d)
+    _check_decode(pkg, c, c.randn(len(lens), 6, d, dtype=x))
+
+
+@pytest.mark.parametrize("page", [8, 24, 32, 56, 64, 128, 1024])
+@pytest.mark.parametrize("layout", ["heads", "tokens", "turns"])
+def test_decode_pages_and_layouts(pkg, page, layout):
+    lens = [700, 1, page, page + 1, 2 * page - 1]
+    c = Case(pkg, lens, H=3, page=page, d=128, layout=layout, seed=page)
+    _check_decode(pkg, c, c.randn(len(lens), 3, 128))
+    c = Case(pkg, lens, H=1, page=page, d=64, dtype=E4M3, layout=layout, seed=page, scales=(0.02, 0.03))
+    _check_decode(pkg, c, c.randn(len(lens), 4, 64, dtype=F16))
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 7, 8, 9, 15, 16, 17, 24, 33, 71])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_decode_group_sizes(pkg, group, dtype):
+    c = Case(pkg, [300, 41], H=2, d=64, dtype=dtype, seed=group, scales=(0.02, 0.03))
+    _check_decode(pkg, c, c.randn(2, 2 * group, 64))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 0.5])
+def test_decode_scales(pkg, scale):
+    c = Case(pkg, [900, 3], d=128, seed=4)
+    _check_decode(pkg, c, c.randn(2, 4, 128), scale=scale)
+
+
+def test_decode_large_logits(pkg):
+    """Logits of a few hundred: the running maximum moves by more than exp2's range between tiles."""
+    c = Case(pkg, [2000, 77], d=128, dtype=F16, seed=5)
+    _check_decode(pkg, c, c.randn(2, 8, 128) * 16, scale=1.0)
+
+
+def test_decode_tiny_and_huge_queries_over_an_8_bit_cache(pkg):
+    """bf16 queries outside fp16's range, with scales that bring the logits back."""
+    for power in (-100, 90):
+        c = Case(pkg, [500], H=1, d=64, dtype=E4M3, seed=6, scales=(2.0 ** -5, 0.1))
+        q = (c.randn(1, 4, 64).float() * 2.0 ** power).to(BF16)
+        _check_decode(pkg, c, q, scale=0.125 * 2.0 ** -power)
+
+
+def test_decode_one_long_sequence(pkg):
+    """Many splits of one (sequence, head)."""
+    c = Case(pkg, [70001], H=1, page=64, d=64, seed=7)
+    _check_decode(pkg, c, c.randn(1, 4, 64))
+
+
+@pytest.mark.parametrize("B", [1, 7, 200])
+def test_decode_ragged_batches(pkg, B):
+    g = torch.Generator().manual_seed(B)
+    lens = [int(x) for x in (torch.rand(B, generator=g) ** 3 * 1500)]
+    c = Case(pkg, lens, H=2, d=32, seed=B, width=200)
+    _check_decode(pkg, c, c.randn(B, 8, 32))
+
+
+def test_decode_a_slice_of_a_projection(pkg):
+    c = Case(pkg, [100, 200, 5], d=64, seed=8)
+    qkv = c.randn(3, 4 + 2 + 2, 64).cuda()
+    _check_decode(pkg, c, qkv[:, :4])
+    _check_decode(pkg, c, qkv.transpose(0, 1).contiguous().transpose(0, 1)[:, 2:6])
+
+
+def test_decode_writes_what_it_is_given(pkg):
+    c = Case(pkg, [50, 0], d=64, seed=9)
+    o = torch.full((4, 4, 64), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((4, 4), 7.0, device="cuda")
+    r = pkg.attn_paged_decode(c.kv, c.randn(2, 4, 64).cuda(), o=o[:2], lse=lse[:2])
+    assert pkg.sync_status() == 0
+    assert r[0].data_ptr() == o.data_ptr() and r[1].data_ptr() == lse.data_ptr()
+    assert (o[2:] == 7).all() and (lse[2:] == 7).all() and (o[1] == 0).all()
+
+
+def test_decode_past_32_bit_offsets(pkg):
+    """Pages more than 4 GB apart."""
+    d, page, H = 128, 64, 4
+    P = (5 << 30) // (H * page * d * 2)
+    k = torch.zeros((P, H, page, d), dtype=BF16, device="cuda")
+    v = torch.zeros((P, H, page, d), dtype=BF16, device="cuda")
+    c = Case(pkg, [150, 20], H=H, page=page, d=d, seed=10, spare=0)
+    far = torch.tensor([P - 1, 3, P - 2, P - 3])
+    near = torch.cat([c.table[0, :3], c.table[1, :1]]).long()
+    k[far.cuda()], v[far.cuda()] = c.k[near.cuda()], c.v[near.cuda()]
+    c.block_table[0, :3] = far[:3].int().cuda()
+    c.block_table[1, :1] = far[3:].int().cuda()
+    c.kv = pkg.PagedKV(k, v, c.block_table, c.seq_lens)
+    _check_decode(pkg, c, c.randn(2, 8, d))
+
+
+def test_decode_is_reproducible(pkg):
+    c = Case(pkg, [5000, 1, 1203], H=2, d=128, seed=11)
+    q = c.randn(3, 8, 128).cuda()
+    first = pkg.attn_paged_decode(c.kv, q)
+    for _ in range(5):
+        again = pkg.attn_paged_decode(c.kv, q)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert pkg.sync_status() == 0
+
+
+def test_bad_page_numbers_and_lengths_are_left_out(pkg):
+    c = Case(pkg, [100, 100], H=1, d=64, seed=12)
+    q = c.randn(2, 2, 64)
+    good = c.block_table.clone()
+    for bad in (-1, c.k.shape[0], 0x7FFFFFFF):
+        c.block_table.copy_(good)
+        c.block_table[0, 2] = bad
+        o, lse = pkg.attn_paged_decode(c.kv, q.cuda())
+        assert pkg.sync_status() == 6
+        ro, rl, to, tl = _reference(c, q, 0.125, [[[i for i in range(100) if i // 16 != 2]], [list(range(100))]])
+        assert ((o.double().cpu() - ro).abs() <= to).all() and ((lse.double().cpu() - rl).abs() <= tl).all()
+    c.block_table.copy_(good)
+    assert pkg.sync_status() == 0
+    c.seq_lens[1] = -5
+    o, lse = pkg.attn_paged_decode(c.kv, q.cuda())
+    assert pkg.sync_status() == 6
+    assert (o[1] == 0).all() and (lse[1] == -math.inf).all()
+    c.seq_lens[1] = 1 << 29  # more than the table row holds: cut to it, and the row's end holds no page
+    pkg.attn_paged_decode(c.kv, q.cuda())
+    assert pkg.sync_status() == 6
+    # an unrelated call is not disturbed
+    x = torch.randn(1, 2, 300, 64, dtype=BF16, device="cuda")
+    pkg.attn_fwd(x, x, x)
+    assert pkg.sync_status() == 0
+
+
+# ------------------------------------------------------------------ append
+
+def _rotated(x, pos, cos, sin, interleaved):
+    y, mag = x.double().clone(), x.double().abs()
+    if cos is None:
+        return y, mag
+    half = cos.shape[1]
+    cs, sn = cos[pos].double()[:, None], sin[pos].double()[:, None]
+    one, two = ((slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved
+                else (slice(0, half), slice(half, 2 * half)))
+    a, b = x[..., one].double(), x[..., two].double()
+    y[..., one], y[..., two] = a * cs - b * sn, b * cs + a * sn
+    mag[..., one] = mag[..., two] = a.abs() + b.abs()
+    return y, mag
+
+
+def _near(got, want, mag, dtype, scale=1.0):
+    """got, as stored, within one rounding of want / scale (and of the fp32 work before it)."""
+    want, mag = want / scale, mag / scale
+    tol = torch.finfo(dtype).eps / 2 * want.abs() * (1 + 1e-3) + 2.0 ** -21 * mag
+    if dtype == E4M3:
+        want = want.clamp(-448, 448)
+        tol = torch.maximum(tol * (1 + 1e-3), torch.tensor(2.0 ** -10)) + 2.0 ** -21 * mag
+    elif dtype == F16:
+        tol = tol + 2.0 ** -25
+    err = (got.double() - want).abs()
+    assert (err <= tol).all(), "off by %g of the tolerance" % (err / tol).max()
+
+
+def _check_append(pkg, c, new, x, Hq=4, rot=None, interleaved=False, pad=0, single=False, in_place=False, positions=None):
+    """Appends the last new[b] tokens of each sequence and compares everything that the call may touch."""
+    B, d, page = len(new), c.d, c.page
+    rot = d if rot is None else rot
+    T = sum(new) + pad
+    qkv = c.randn(T, Hq + 2 * c.H, d, dtype=x).cuda()
+    q, k, v = qkv.split([Hq, c.H, c.H], dim=1)
+    cos, sin = pkg.rotation_tables(positions or max(c.lens_list), rot, device="cuda") if rot else (None, None)
+    start = None if single else torch.tensor([sum(new[:b]) for b in range(B + 1)], dtype=torch.int32, device="cuda")
+    before = [_raw(t).clone() for t in (c.k, c.v)]
+    sums = [_raw(t).clone() for t in (c.k_min, c.k_max)] if c.k_min is not None else None
+    q_in, k_in, v_in = q.cpu(), k.cpu(), v.cpu()
+    q_out = q if in_place else torch.full((T, Hq, d), 3.0, dtype=x, device="cuda")
+    r = pkg.attn_paged_append(c.kv, k, v, q=q, q_out=q_out, token_start=start, cos=cos, sin=sin, interleaved=interleaved)
+    assert r is q_out
+    assert pkg.sync_status() == 0
+    cos, sin = (cos.cpu(), sin.cpu()) if rot else (None, None)
+    kc, vc = _raw(c.k).cpu(), _raw(c.v).cpu()
+    touched = torch.zeros(c.k.shape[0], page, dtype=torch.bool)
+    for b, n in enumerate(new):
+        t, s = c.lens_list[b], sum(new[:b])
+        if t == 0:
+            assert torch.equal(q_out[s:s + n].cpu(), q_in[s:s + n] if in_place else torch.full_like(q_in[s:s + n], 3.0))
+            continue
+        pos = torch.arange(t - n, t)
+        ids = c.table[b, pos // page].long()
+        touched[ids, pos % page] = True
+        y, mag = _rotated(q_in[s:s + n], pos, cos, sin, interleaved)
+        _near(q_out[s:s + n].cpu(), y, mag, x)
+        y, mag = _rotated(k_in[s:s + n], pos, cos, sin, interleaved)
+        got = kc[ids, :, pos % page]
+        _near(got.view(c.dtype), y, mag, c.dtype, c.scales[0])
+        c.k_ref[b, :, pos] = got.view(c.dtype).double().transpose(0, 1) * c.scales[0]
+        got = vc[ids, :, pos % page]
+        _near(got.view(c.dtype), v_in[s:s + n].double(), v_in[s:s + n].double().abs(), c.dtype, c.scales[1])
+        c.v_ref[b, :, pos] = got.view(c.dtype).double().transpose(0, 1) * c.scales[1]
+    rest = ~touched[:, None, :, None].expand(c.k.shape)
+    for got, old in ((kc, before[0].cpu()), (vc, before[1].cpu())):  # NaN included, bit for bit
+        assert torch.equal(got.view(torch.uint8 if c.dtype == E4M3 else torch.int16)[rest],
+                           old.view(torch.uint8 if c.dtype == E4M3 else torch.int16)[rest])
+    tail = slice(sum(new), T)
+    assert torch.equal(q_out[tail].cpu(), q_in[tail] if in_place else torch.full_like(q_in[tail], 3.0))
+    if sums is not None:
+        want = [t.cpu().view(c.dtype).float() for t in sums]
+        for b, n in enumerate(new):
+            t = c.lens_list[b]
+            for j in range((t - n) // page, -(-t // page)) if t and n else ():
+                id, first = int(c.table[b, j]), max(t - n, j * page)
+                x_ = c.kv.k_pages[id].cpu().float()[:, first - j * page:min(page, t - j * page)]
+                lo, hi = x_.amin(1), x_.amax(1)
+                fresh = first == j * page
+                want[0][id] = lo if fresh else torch.minimum(lo, want[0][id])
+                want[1][id] = hi if fresh else torch.maximum(hi, want[1][id])
+        assert torch.equal(c.k_min.cpu().float(), want[0]) and torch.equal(c.k_max.cpu().float(), want[1])
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_prompts(pkg, x, dtype, scales, d, interleaved):
+    new = [1, 33, 0, 16, 17, 100, 15, 2]
+    lens = [1, 33, 50, 48, 30, 117, 47, 40]
+    c = Case(pkg, lens, H=2, d=d, dtype=dtype, scales=scales, seed=d, summaries=True)
+    _check_append(pkg, c, new, x, interleaved=interleaved, pad=5)
+
+
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+def test_append_single_tokens(pkg, x, dtype, scales):
+    lens = [1, 0, 16, 17, 100, 0]
+    for summaries in (False, True):
+        c = Case(pkg, lens, H=3, d=64, dtype=dtype, scales=scales, seed=3, summaries=summaries)
+        _check_append(pkg, c, [1] * 6, x, Hq=9, single=True)
+
+
+@pytest.mark.parametrize("page", [8, 24, 64, 1024])
+@pytest.mark.parametrize("layout", ["heads", "tokens", "turns"])
+@pytest.mark.parametrize("summaries", [False, True])
+def test_append_pages_and_layouts(pkg, page, layout, summaries):
+    new = [page, page + 1, 1, 2 * page + 3]
+    lens = [page, 2 * page + 2, page + 1, 3 * page + 2]
+    c = Case(pkg, lens, H=1, page=page, d=32, layout=layout, seed=page, summaries=summaries)
+    _check_append(pkg, c, new, BF16, Hq=2)
+
+
+@pytest.mark.parametrize("rot", [0, 16, 48, 64])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_rotates_a_part_of_the_channels(pkg, rot, interleaved):
+    c = Case(pkg, [40, 9], H=2, d=64, seed=rot)
+    _check_append(pkg, c, [21, 9], BF16, rot=rot, interleaved=interleaved)
+
+
+def test_append_in_place(pkg):
+    c = Case(pkg, [40, 0, 9], H=2, d=64, seed=2)
+    _check_append(pkg, c, [21, 0, 9], BF16, in_place=True, pad=3)
+
+
+def test_append_many_sequences(pkg):
+    g = torch.Generator().manual_seed(1)
+    new = [int(x) for x in torch.randint(0, 20, (300,), generator=g)]
+    lens = [n + int(x) if n else 0 for n, x in zip(new, torch.randint(0, 40, (300,), generator=g))]
+    c = Case(pkg, lens, H=1, d=32, page=8, seed=1, summaries=True)
+    _check_append(pkg, c, new, BF16, Hq=1)
+
+
+def test_append_far_positions(pkg):
+    """Angles of far positions come from the tables; only they limit the position."""
+    c = Case(pkg, [100000], H=1, d=64, page=64, seed=1, fill=False)
+    _check_append(pkg, c, [70], BF16)
+
+
+def test_append_saturates_and_keeps_nan(pkg):
+    c = Case(pkg, [4], H=1, d=32, dtype=E4M3, seed=1, scales=(0.5, 0.25), summaries=True)
+    x = torch.zeros(4, 1, 32, dtype=BF16, device="cuda")
+    x[0], x[1], x[2, :, ::2] = 1e4, -1e4, math.nan
+    pkg.attn_paged_append(c.kv, x, x, token_start=torch.tensor([0, 4], dtype=torch.int32, device="cuda"))
+    assert pkg.sync_status() == 0
+    k = c.k[int(c.table[0, 0])].float().cpu()[0, :4]
+    assert (k[0] == 448).all() and (k[1] == -448).all() and k[2, ::2].isnan().all() and (k[3] == 0).all()
+    assert (c.k_max[int(c.table[0, 0])].float() == 448).all() and (c.k_min[int(c.table[0, 0])].float() == -448).all()
+
+
+def test_append_bad_tables_write_nothing(pkg):
+    c = Case(pkg, [20, 20], H=1, d=32, seed=1)
+    k = torch.ones(2, 1, 32, dtype=BF16, device="cuda")
+    before = (c.k.clone(), c.v.clone())
+    same = lambda: all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip((c.k, c.v), before))  # noqa: E731
+    c.block_table[:, 1] = torch.tensor([-3, c.k.shape[0]], dtype=torch.int32)
+    pkg.attn_paged_append(c.kv, k, k)
+    assert pkg.sync_status() == 6 and same()
+    for bad in ([0, 2, 1], [-1, 0, 2], [0, 0, 3], [2, 2, 1]):
+        pkg.attn_paged_append(c.kv, k, k, token_start=torch.tensor(bad, dtype=torch.int32, device="cuda"))
+        assert pkg.sync_status() == 6 and same(), bad
+    c.block_table.copy_(c.table)
+    cos, sin = pkg.rotation_tables(19, 32, device="cuda")  # one position short
+    pkg.attn_paged_append(c.kv, k, k, cos=cos, sin=sin)
+    assert pkg.sync_status() == 6 and same()
+    c.seq_lens.fill_(1 << 28)
+    pkg.attn_paged_append(c.kv, k, k)
+    assert pkg.sync_status() == 6 and same()
+
+
+def test_append_of_nothing(pkg):
+    c = Case(pkg, [20], H=1, d=32, seed=1)
+    k = torch.empty(0, 1, 32, dtype=BF16, device="cuda")
+    assert pkg.attn_paged_append(c.kv, k, k, token_start=torch.zeros(2, dtype=torch.int32, device="cuda")) is None
+    assert pkg.last_launch_count() == 0 and pkg.sync_status() == 0
+
+
+# ------------------------------------------------------------------ selection
+
+def _chosen(c, q, n, first, last):
+    """The definition in float64 on the CPU: [B][H] ascending page lists."""
+    B, Hq, d = q.shape
+    G, out = Hq // c.H, []
+    lo, hi = c.k_min.cpu().double(), c.k_max.cpu().double()
+    for b, t in enumerate(c.lens_list):
+        used, rows = -(-t // c.page), []
+        for h in range(c.H):
+            ids = c.table[b, :used].long()
+            x = q[b, h * G:(h + 1) * G].double()[:, None]
+            s = torch.maximum(x * lo[ids, h], x * hi[ids, h]).sum(-1).amax(0) if used else torch.zeros(0)
+            order = sorted(range(used), key=lambda j: (not (j < first or j >= used - last), -float(s[j]), j))
+            rows.append(sorted(order[:n]))
+        out.append(rows)
+    return out
+
+
+def _check_select(pkg, c, q, n, first=1, last=1):
+    pages = pkg.attn_paged_select(c.kv, q.cuda(), n, keep_first=first, keep_last=last)
+    assert pkg.sync_status() == 0
+    want = _chosen(c, q, n, first, last)
+    full = torch.full((len(c.lens_list), c.H, n), -1, dtype=torch.int32)
+    for b, rows in enumerate(want):
+        for h, row in enumerate(rows):
+            full[b, h, :len(row)] = torch.tensor(row, dtype=torch.int32)
+    assert torch.equal(pages.cpu(), full)
+    return pages, want
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+def test_select_and_decode(pkg, x, dtype, scales, d):
+    lens = [0, 1, 16 * 12, 16 * 12 + 1, 16 * 13, 1003, 2500]
+    c = Case(pkg, lens, H=2, d=d, dtype=dtype, scales=scales, seed=d + 1, summaries=True)
+    q = c.randn(len(lens), 6, d, dtype=x)
+    pages, want = _check_select(pkg, c, q, 12)
+    keys = [[[p * 16 + i for p in row for i in range(16) if p * 16 + i < lens[b]] for row in rows]
+            for b, rows in enumerate(want)]
+    _check_decode(pkg, c, q, pages=pages, keys=keys)
+
+
+@pytest.mark.parametrize("n,first,last", [(1, 0, 0), (1, 0, 1), (1, 1, 0), (2, 1, 1), (8, 4, 4), (31, 0, 0), (32, 0, 0),
+                                          (100, 3, 1), (700, 1, 1), (5000, 0, 0)])
+def test_select_counts(pkg, n, first, last):
+    c = Case(pkg, [8 * 31 + 3, 8 * 2000, 5], H=1, page=8, d=32, seed=n, summaries=True)
+    _check_select(pkg, c, c.randn(3, 5, 32), n, first, last)
+
+
+@pytest.mark.parametrize("group", [1, 4, 8, 16, 17, 40])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_select_group_sizes(pkg, group, dtype):
+    c = Case(pkg, [3000, 700], H=2, d=64, dtype=dtype, seed=group, summaries=True, scales=(0.02, 0.02))
+    _check_select(pkg, c, c.randn(2, 2 * group, 64), 20)
+
+
+def test_select_more_pages_than_a_block_has_threads(pkg):
+    c = Case(pkg, [8 * 9001], H=1, page=8, d=32, seed=1, summaries=True)
+    _check_select(pkg, c, c.randn(1, 4, 32), 333)
+
+
+def test_select_ties_go_to_the_lowest_page(pkg):
+    c = Case(pkg, [16 * 500], H=2, d=64, seed=1, summaries=True)
+    q = c.randn(1, 4, 64)
+    for t in (c.k_min, c.k_max):
+        t.zero_()
+    _check_select(pkg, c, q, 37)                 # every score is 0
+    some = torch.randint(0, 4, (c.k.shape[0],), generator=c.g)
+    kinds = torch.randn(4, 2, 64, generator=c.g).to(BF16)
+    c.k_min.copy_(kinds[some])
+    c.k_max.copy_(kinds[some])                   # four scores, each some hundred times
+    for n in (3, 100, 250, 499):
+        _check_select(pkg, c, q, n)
+
+
+def test_select_orders_scores_that_fp32_cannot_tell_apart(pkg):
+    """One large channel, the same on every page, and small ones that differ below its fp32 step."""
+    d, n = 64, 400
+    c = Case(pkg, [16 * n], H=1, d=d, seed=1, summaries=True)
+    q = torch.ones(1, 2, d, dtype=BF16)
+    lo = torch.zeros(c.k.shape[0], 1, d, dtype=BF16)
+    lo[..., 0] = 2.0 ** 13
+    lo[..., 1:] = (torch.randint(-8, 9, lo[..., 1:].shape, generator=c.g) * 2.0 ** -16).to(BF16)
+    c.k_min.copy_(lo)
+    c.k_max.copy_(lo)
+    for m in (2, 50, 200, 399):
+        _check_select(pkg, c, q, m)
+
+
+def test_select_cancelling_sums(pkg):
+    """Channels of opposite sign that cancel to a small score, in an order that a rounded sum would mistake."""
+    c = Case(pkg, [16 * 600], H=1, d=128, seed=3, summaries=True)
+    q = c.randn(1, 3, 128) * 8
+    big = (torch.randn(c.k.shape[0], 1, 128, generator=c.g) * 100).to(BF16)
+    c.k_min.copy_(big)
+    c.k_max.copy_(big)
+    for m in (2, 77, 300):
+        _check_select(pkg, c, q, m)
+
+
+def test_select_is_not_confused_by_bad_pages(pkg):
+    c = Case(pkg, [16 * 40], H=1, d=32, seed=1, summaries=True)
+    c.block_table[0, 7] = -1
+    pages = pkg.attn_paged_select(c.kv, c.randn(1, 2, 32).cuda(), 10)
+    assert pkg.sync_status() == 6
+    p = pages.cpu()[0, 0].tolist()
+    assert p == sorted(set(p)) and 0 <= p[0] and p[-1] < 40 and 7 not in p
+
+
+def test_decode_any_list_of_pages(pkg):
+    """Lists need not come from the selection: any order, gaps, entries behind the end."""
+    c = Case(pkg, [16 * 20 + 5, 30], H=2, d=64, seed=1)
+    q = c.randn(2, 4, 64)
+    lists = torch.tensor([[[20, -1, 3, 7, 0, -1], [5, 21, 19, 1000, -7, 2]], [[-1] * 6, [1, 2, -1, -1, -1, 0]]],
+                         dtype=torch.int32)
+    keys = [[[p * 16 + i for p in row if p >= 0 for i in range(16) if p * 16 + i < c.lens_list[b]]
+             for row in rows.tolist()] for b, rows in enumerate(lists)]
+    _check_decode(pkg, c, q, pages=lists.cuda(), keys=keys)
+    twice = torch.tensor([[[3, 3], [4, 0]], [[1, 1], [0, 1]]], dtype=torch.int32)
+    keys = [[[p * 16 + i for p in row for i in range(16) if p * 16 + i < c.lens_list[b]]
+             for row in rows.tolist()] for b, rows in enumerate(twice)]
+    _check_decode(pkg, c, q, pages=twice.cuda(), keys=keys)
+
+
+# ------------------------------------------------------------------ together
+
+def test_a_server_run(pkg):
+    """Prompts appended, then steps of append, select and decode, with a sequence that starts late and one that ends;
+    against float64 over what the cache holds, and the prompt's last token against the dense causal forward."""
+    H, Hq, d, page, B = 2, 8, 64, 16, 3
+    prompts, steps = [37, 0, 90], 6
+    final = [n + steps if n else 2 for n in prompts]
+    c = Case(pkg, final, H=H, d=d, page=page, seed=1, summaries=True, fill=False)
+    cos, sin = pkg.rotation_tables(256, d, device="cuda")
+    # prompts
+    T = sum(prompts)
+    q, k, v = (c.randn(T, h, d).cuda() for h in (Hq, H, H))
+    start = torch.tensor([0, 37, 37, 127], dtype=torch.int32, device="cuda")
+    c.seq_lens.copy_(torch.tensor(prompts, dtype=torch.int32))
+    qr = pkg.attn_paged_append(c.kv, k, v, q=q, token_start=start, cos=cos, sin=sin)
+    c.lens_list = list(prompts)
+
+    def read_back():
+        for b, t in enumerate(c.lens_list):
+            pos = torch.arange(t)
+            ids = c.table[b, pos // page].long()
+            c.k_ref[b, :, :t] = c.k.cpu()[ids, :, pos % page].double().transpose(0, 1)
+            c.v_ref[b, :, :t] = c.v.cpu()[ids, :, pos % page].double().transpose(0, 1)
+    read_back()
+    last = torch.stack([qr[36], qr[36], qr[126]])
+    o, lse = _check_decode(pkg, c, last)
+    dense_k = c.k_ref[2, :, :90].to(BF16).repeat_interleave(4, 0)[None].cuda()
+    dense_v = c.v_ref[2, :, :90].to(BF16).repeat_interleave(4, 0)[None].cuda()
+    of, lf = pkg.attn_fwd(qr[37:].transpose(0, 1).contiguous()[None], dense_k, dense_v, causal=True)
+    assert (of[0, :, 89].float() - o[2].float()).abs().max() <= 2e-2
+    assert (lf[0, :, 89] - lse[2]).abs().max() <= 1e-3
+    # steps
+    for s in range(steps):
+        c.lens_list = [37 + s + 1, max(0, s - steps + 3), 90 + s + 1 if s < 4 else 0]
+        c.seq_lens.copy_(torch.tensor(c.lens_list, dtype=torch.int32))
+        q, k, v = (c.randn(B, h, d).cuda() for h in (Hq, H, H))
+        qr = pkg.attn_paged_append(c.kv, k, v, q=q, cos=cos, sin=sin)
+        qr[torch.tensor(c.lens_list) == 0] = 0
+        pages = pkg.attn_paged_select(c.kv, qr, 3)
+        assert pkg.sync_status() == 0
+        read_back()
+        want = _chosen(c, qr.cpu(), 3, 1, 1)
+        assert [[[p for p in row if p >= 0] for row in rows] for rows in pages.tolist()] == want
+        _check_decode(pkg, c, qr)
+        keys = [[[p * page + i for p in row for i in range(page) if p * page + i < c.lens_list[b]] for row in rows]
+                for b, rows in enumerate(want)]
+        _check_decode(pkg, c, qr, pages=pages, keys=keys)
+
+
+def _step(pkg, c, q, k, v, cos, sin, n):
+    qr = pkg.attn_paged_append(c.kv, k, v, q=q, cos=cos, sin=sin)
+    pages = pkg.attn_paged_select(c.kv, qr, n)
+    return (qr, pages) + pkg.attn_paged_decode(c.kv, qr) + pkg.attn_paged_decode(c.kv, qr, pages=pages)
+
+
+def test_captured_step_replays_with_other_lengths(pkg):
+    lens = [200, 60, 333]
+    c = Case(pkg, lens, H=2, d=64, seed=1, summaries=True, width=40)
+    q, k, v = (c.randn(3, h, 64).cuda() for h in (4, 2, 2))
+    cos, sin = pkg.rotation_tables(1024, 64, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(pkg, c, q, k, v, cos, sin, 5)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):  # two graphs of the same step, replayed in turns
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(_step(pkg, c, q, k, v, cos, sin, 5))
+        graphs.append(graph)
+    for now in ([200, 60, 333], [16, 0, 170], [1, 64, 300]):
+        c.seq_lens.copy_(torch.tensor(now, dtype=torch.int32))
+        eager = [t.clone() for t in _step(pkg, c, q, k, v, cos, sin, 5)]
+        for graph, out in zip(graphs, outs):
+            out[2].fill_(5.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            live = [b for b, n in enumerate(now) if n]
+            for got, want in zip(out, eager):  # bit for bit: 64 tokens reach slots that nothing filled, and are NaN
+                bits = {2: torch.int16, 4: torch.int32}[got.element_size()]
+                assert torch.equal(got[live].view(bits), want[live].view(bits))
+    assert pkg.sync_status() == 0
+
+
+def test_two_streams_at_once(pkg):
+    cases = [Case(pkg, [900 + i, 33, 0, 2047], H=2, d=128, seed=i, summaries=True) for i in range(2)]
+    qs = [c.randn(4, 8, 128).cuda() for c in cases]
+    want = [(pkg.attn_paged_select(c.kv, q, 7),) + pkg.attn_paged_decode(c.kv, q) for c, q in zip(cases, qs)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, q, s) in enumerate(zip(cases, qs, streams)):
+            got[i].append((pkg.attn_paged_select(c.kv, q, 7, stream=s),) + pkg.attn_paged_decode(c.kv, q, stream=s))
+    torch.cuda.synchronize()
+    assert pkg.sync_status() == 0
+    for g, w in zip(got, want):
+        for r in g:
+            assert all(torch.equal(a, b) for a, b in zip(r, w))
