@@ -173,6 +173,12 @@ int launch_fwd_fp8(const Fp8Args& a);
 bool encode_map_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                    uint64_t stride1, uint64_t stride2, uint32_t b0, uint32_t b1);
 
+// 4-D map of a paged cache as bytes: dims (row bytes, tokens, heads, pages) with
+// byte strides of the last three, box (box_bytes, box_rows, 1, 1), swizzled over
+// box_bytes (32, 64 or 128), zero fill.
+bool encode_pages_map(CUtensorMap* map, const void* base, int row, int page, int heads, int pages, int64_t tok,
+                      int64_t head, int64_t page_stride, int box_bytes, int box_rows);
+
 // Number of key splits per (batch, head) for a decode problem.
 int decode_splits(int BH, int L);
 

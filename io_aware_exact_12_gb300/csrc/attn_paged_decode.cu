@@ -4,7 +4,26 @@
 //
 // FlashAttention (PKM page), "注意" section: decode has no N x N matrix, its
 // cost is reading the cache, and the variant for it splits the keys; the join
-// is exact by the online softmax of "三招" 2.
+// is exact by the online softmax of "三招" 2: with m = max_s m_s,
+//     l = sum_s e^{m_s - m} l_s,   O = sum_s e^{m_s - m} O_s / l.
+//
+// Every cached byte is read once, so HBM bounds it: G = Hq / Hkv query heads
+// make 2 G flops per 2-byte element (4 G for e4m3), beyond the fp32 units' rate
+// from G = 4 or so.  The products run as m16n8k16 matrix instructions with the
+// G query heads as rows: at the full HBM rate they take a fifth (e4m3: two
+// fifths) of that pipe, so the larger tcgen05 tiles, which want 64 rows at
+// least, would have nothing to gain from 1 to 16 rows.
+//
+//   attn_paged_decode_kernel : two CTAs per SM, each with an equal share of all
+//       tiles of keys (tile lists of the items (b, KV head, group of up to 16
+//       query heads) laid end to end; the lengths are on the device, so every
+//       CTA sums them and finds its own share).  One producer warp walks the
+//       page tables and keeps a ring of TMA loads in flight, boxes of rows that
+//       never cross a page; four consumer warps take tiles in turn, each with an
+//       online softmax of its own, and are merged in shared memory where an
+//       item ends.
+//   attn_paged_merge_kernel : joins the items that were cut by a CTA border.
+#include <atomic>
 #include <cmath>
 
 #include "attn_paged.h"
@@ -13,114 +32,664 @@
 namespace attn {
 namespace {
 
-constexpr int kPdThreads = 128;
+constexpr int kPdWarps = 4;  // consumers
+constexpr int kPdThreads = 32 * (kPdWarps + 1);
+constexpr int kPdRows = 16;  // query heads of an item
+constexpr int kPdRing = 80 * 1024;
 
-// Keys of one split of one query head; partial (m, l, O) to scratch.
+template <int C, int D>
+struct PdCfg {
+  static constexpr int CB = C == kTypeE4m3 ? 1 : 2;
+  static constexpr int ROW = D * CB;                   // bytes of a cached row
+  static constexpr int RBX = ROW < 128 ? ROW : 128;    // bytes of a row in one box (the swizzle's span)
+  static constexpr int NH = ROW / RBX;
+  static constexpr int TK = ROW >= 256 ? 32 : 64;      // keys of a tile
+  static constexpr int HALF = TK * ROW;                // K (or V) bytes of a stage
+  // A multiple of the warps, so that a stage always serves the same warp: loads
+  // land out of order, and a warp that looked at a stage whose previous tile,
+  // another warp's, had not landed yet would take the phase before for its own.
+  static constexpr int STAGES = (kPdRing / (2 * HALF) < 16 ? kPdRing / (2 * HALF) : 16) / kPdWarps * kPdWarps;
+  static_assert(STAGES >= kPdWarps && STAGES % kPdWarps == 0, "stages belong to warps");
+  static constexpr int OFF_O = STAGES * 2 * HALF;      // [warps][16][D] fp32
+  static constexpr int OFF_ML = OFF_O + kPdWarps * kPdRows * D * 4;  // [warps][3][16]
+  static constexpr int OFF_BAR = OFF_ML + kPdWarps * 3 * kPdRows * 4;
+  static constexpr int OFF_MASK = OFF_BAR + 2 * STAGES * 8;  // visible keys of a stage
+  static constexpr int OFF_SCHED = OFF_MASK + STAGES * 8;
+  static constexpr int SMEM = OFF_SCHED + 128;
+};
+
+struct Part {  // an item that CTA `first` begins and CTA `last` ends
+  int b, hr, first, last;
+};
+
+// Floats of one partial result: O [16][D], then m, l and the rounded l [16] each.
+__host__ __device__ constexpr int part_floats(int d) { return kPdRows * (d + 3); }
+
+// Weight of a part with maximum m in a join with maximum mm.  Without a maximum
+// the part's sums are 0 (no visible key) or NaN (nothing but NaN logits), and
+// either goes into the join as it is.
+__device__ __forceinline__ float part_weight(float m, float mm) { return m == -INFINITY ? 1.f : ex2_approx(m - mm); }
+
+struct Sched {
+  long long t0, total;
+  int b, hr, tile, n;  // first tile of the CTA and how many it has
+  int n_act, abort_flag;
+  long long warp_sum[kPdThreads / 32];
+};
+static_assert(sizeof(Sched) <= 128, "OFF_SCHED");
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 bytes (low half of the word) as two fp16 values; exact.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void consumer_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kPdWarps) : "memory");
+}
+
+template <int TK>
+__device__ __forceinline__ int tiles_of(const PagedDecodeArgs& a, int len) {
+  if (len <= 0) return 0;
+  return ((a.pages ? a.n_pages * a.kv.page : len) + TK - 1) / TK;
+}
+
+// Finds the CTA's share of the tiles.  All threads; B numbers are read once.
+template <int TK>
+__device__ __forceinline__ void find_share(const PagedDecodeArgs& a, int HR, Sched& s) {
+  const int tid = threadIdx.x, lane = tid & 31, B = a.kv.B;
+  const int per = (B + kPdThreads - 1) / kPdThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles_of<TK>(a, checked_len(a.kv, b));
+  mine *= HR;
+  long long upto = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, x);
+    if (lane >= x) upto += y;
+  }
+  if (lane == 31) s.warp_sum[tid >> 5] = upto;
+  if (tid == 0) s.n = 0, s.b = 0, s.hr = 0, s.tile = 0, s.t0 = 0;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int i = 0; i < kPdThreads / 32; ++i) {
+    if (i < (tid >> 5)) upto += s.warp_sum[i];
+    total += s.warp_sum[i];
+  }
+  // At least one tile per consumer warp, so that few tiles go to few CTAs.
+  const int n_act = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kPdWarps - 1) / kPdWarps));
+  const int c = blockIdx.x;
+  if (tid == 0) s.total = total, s.n_act = n_act;
+  if (c < n_act) {
+    const long long t0 = total * c / n_act, t1 = total * (c + 1) / n_act;
+    if (upto - mine <= t0 && t0 < upto) {
+      long long at = upto - mine;
+      for (int b = b0; b < b1; ++b) {
+        const long long t = tiles_of<TK>(a, checked_len(a.kv, b));
+        if (t0 < at + t * HR) {
+          s.b = b;
+          s.hr = static_cast<int>((t0 - at) / t);
+          s.tile = static_cast<int>((t0 - at) % t);
+          break;
+        }
+        at += t * HR;
+      }
+      s.t0 = t0;
+      s.n = static_cast<int>(t1 - t0);
+    }
+  }
+  __syncthreads();
+}
+
+// Position in the list of items.
+struct Item {
+  int b, hr, tiles, len;
+};
+template <int TK>
+__device__ __forceinline__ void next_item(const PagedDecodeArgs& a, int HR, Item& it) {
+  if (++it.hr < HR) return;
+  it.hr = 0;
+  do {
+    if (++it.b >= a.kv.B) {
+      it.tiles = 0;
+      return;
+    }
+    it.len = checked_len(a.kv, it.b);
+    it.tiles = tiles_of<TK>(a, it.len);
+  } while (it.tiles == 0);
+}
+
+template <int X>
+__device__ __forceinline__ void store_out4(uint8_t* p, const float (&o)[4]) {
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(pack2<X == kTypeBf16>(o[0], o[1]), pack2<X == kTypeBf16>(o[2], o[3]));
+}
+
 template <int X, int C, int D>
-__global__ void __launch_bounds__(kPdThreads) attn_paged_split_kernel(const PagedDecodeArgs a, float* part, int keys) {
+__global__ void __launch_bounds__(kPdThreads, 2)
+    attn_paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                             const PagedDecodeArgs a, int RT, int box_rows, int by_item, Part* parts, float* part) {
+  using F = PdCfg<C, D>;
+  constexpr int TK = F::TK;
+  constexpr bool BF = C == kTypeBf16;
+  constexpr bool E8 = C == kTypeE4m3;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const PagedKv& kv = a.kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int HR = kv.H * RT, G = a.Hq / kv.H;
+  Sched& s = *reinterpret_cast<Sched*>(smem + F::OFF_SCHED);
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t full = sbase + F::OFF_BAR, empty = full + F::STAGES * 8;
+  uint64_t* masks = reinterpret_cast<uint64_t*>(smem + F::OFF_MASK);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < F::STAGES; ++i) {
+      mbar_init(full + i * 8, 1);
+      mbar_init(empty + i * 8, 1);
+    }
+    s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&mk);
+    prefetch_tensormap(&mv);
+  }
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
-  const PagedKv& kv = a.kv;
-  constexpr int LPK = D / 8;  // lanes of a key
-  constexpr int GROUPS = kPdThreads / LPK;
-  constexpr int CB = C == kTypeE4m3 ? 1 : 2;
-  const int s = blockIdx.x, S = gridDim.x, b = blockIdx.y / a.Hq, hq = blockIdx.y % a.Hq;
-  const int h = hq / (a.Hq / kv.H);
-  const int g = threadIdx.x / LPK, c = (threadIdx.x % LPK) * 8;
-  const int len = checked_len(kv, b);
-  const int64_t entries = a.pages ? a.n_pages : (len + kv.page - 1) / kv.page;
-  const int64_t k0 = static_cast<int64_t>(s) * keys, k1 = min(entries * kv.page, k0 + keys);
+  find_share<TK>(a, HR, s);
+  const int n = s.n;
+  const int c = blockIdx.x;
 
-  float q[8];
-  load8<X>(a.q.p + b * a.q.row + hq * a.q.head + c * 2, q);
-  float m = -INFINITY, l = 0.f, acc[8] = {};
-  for (int64_t kk = k0; kk < k1; kk += GROUPS) {
-    const int64_t key = kk + g;
-    bool seen = key < k1;
-    float kf[8] = {}, vf[8] = {};
-    if (seen) {
-      const int e = static_cast<int>(key / kv.page), slot = static_cast<int>(key % kv.page);
-      const int j = a.pages ? a.pages[(static_cast<int64_t>(b) * kv.H + h) * a.n_pages + e] : e;
-      seen = j >= 0 && static_cast<int64_t>(j) * kv.page + slot < len;
-      if (seen) {
-        const int id = checked_page(kv, b, j);
-        seen = id >= 0;
-        if (seen) {
-          load8<C>(kv.k + id * kv.k_page + h * kv.k_head + slot * kv.k_tok + c * CB, kf);
-          load8<C>(kv.v + id * kv.v_page + h * kv.v_head + slot * kv.v_tok + c * CB, vf);
+  // Sequences without tokens: o = 0, lse = -inf.
+  for (int b = c; b < kv.B; b += gridDim.x) {
+    if (tiles_of<TK>(a, checked_len(kv, b))) continue;
+    for (int i = threadIdx.x; i < a.Hq * D / 8; i += kPdThreads)
+      reinterpret_cast<uint4*>(a.o + static_cast<int64_t>(b) * a.Hq * D * 2)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < a.Hq; i += kPdThreads) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
+    if (by_item)
+      for (int i = threadIdx.x; i < HR; i += kPdThreads) parts[b * HR + i] = Part{0, 0, 0, -1};
+  }
+  if (!by_item && threadIdx.x == 0) parts[c] = Part{0, 0, 0, -1};  // the last item may set it below
+  if (n == 0) return;
+  __syncthreads();
+
+  volatile int* abort_flag = &s.abort_flag;
+  Item it = {s.b, s.hr, 0, 0};
+  it.len = checked_len(kv, it.b);
+  it.tiles = tiles_of<TK>(a, it.len);
+
+  if (warp == kPdWarps) {  // ---------------------------------- producer warp
+    // Each lane looks up one box (box_rows keys of one page) of the next
+    // tiles, so one round trip through list and table serves 32 boxes.
+    const int nb = TK / box_rows, batch = 32 / nb;  // boxes of a tile, tiles of a batch
+    const int box = lane % nb;
+    int tile = s.tile;
+    bool ok = true;
+    int issued = 0;
+    for (int i0 = 0; ok && i0 < n; i0 += batch) {
+      Item mine = it;
+      int t = tile + lane / nb;
+      const bool live = i0 + lane / nb < n;
+      while (live && mine.tiles > 0 && t >= mine.tiles) {
+        t -= mine.tiles;
+        next_item<TK>(a, HR, mine);
+      }
+      int id = -1, h = 0, row = 0, seen = 0;
+      if (live) {
+        const int key = t * TK + box * box_rows;
+        const int e = key / kv.page;
+        row = key - e * kv.page;
+        h = mine.hr / RT;
+        int j = e;
+        if (a.pages) j = e < a.n_pages ? a.pages[(static_cast<int64_t>(mine.b) * kv.H + h) * a.n_pages + e] : -1;
+        const int64_t left = static_cast<int64_t>(mine.len) - (static_cast<int64_t>(j) * kv.page + row);
+        if (j >= 0 && left > 0) {
+          seen = static_cast<int>(min(left, static_cast<int64_t>(box_rows)));
+          id = checked_page(kv, mine.b, j);
+          if (id < 0) seen = 0;
+        }
+      }
+      // A box without a visible key is not loaded: its scores are masked and its
+      // V rows zeroed, whatever the stage held before.
+      int vis = id >= 0 ? 1 : 0;
+      uint64_t mask = (seen == 64 ? ~0ull : ((1ull << seen) - 1)) << (box * box_rows);
+      for (int x = 1; x < nb; x <<= 1) {
+        mask |= __shfl_xor_sync(0xffffffffu, mask, x);
+        vis += __shfl_xor_sync(0xffffffffu, vis, x);
+      }
+      for (int k = 0; k < batch && i0 + k < n; ++k) {
+        const int i = i0 + k, st = i % F::STAGES;
+        if (i >= F::STAGES) ok = mbar_wait(empty + st * 8, ((i / F::STAGES) - 1) & 1, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == k * nb) {
+          masks[st] = mask;
+          mbar_arrive_expect_tx(full + st * 8, vis * box_rows * F::ROW * 2);
+        }
+        __syncwarp();
+        if (lane / nb == k && id >= 0) {
+          const uint32_t dst = sbase + st * 2 * F::HALF + box * box_rows * F::RBX;
+#pragma unroll
+          for (int hf = 0; hf < F::NH; ++hf) {
+            tma_load_4d(dst + hf * TK * F::RBX, &mk, full + st * 8, hf * F::RBX, row, h, id);
+            tma_load_4d(dst + F::HALF + hf * TK * F::RBX, &mv, full + st * 8, hf * F::RBX, row, h, id);
+          }
+        }
+        issued = i + 1;
+      }
+      // The batch's end, for all lanes alike.
+      tile += batch;
+      while (it.tiles > 0 && tile >= it.tiles && i0 + batch < n) {
+        tile -= it.tiles;
+        next_item<TK>(a, HR, it);
+      }
+    }
+    // No copy may be in flight when the CTA ends, also where the consumers gave
+    // up: wait for the last ones here.
+    for (int i = max(0, issued - F::STAGES); i < issued; ++i) {
+      const uint64_t since = global_timer_ns();
+      while (!mbar_test(full + (i % F::STAGES) * 8, (i / F::STAGES) & 1) && global_timer_ns() - since < kWaitLimitNs) {
+      }
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------ consumer warps
+  float* so = reinterpret_cast<float*>(smem + F::OFF_O);
+  float* sml = reinterpret_cast<float*>(smem + F::OFF_ML);
+  const int g = lane >> 2, t4 = lane & 3, l8 = lane & 7, mi = lane >> 3;
+  const int swz = F::RBX == 128 ? l8 : F::RBX == 64 ? l8 >> 1 : l8 >> 2;
+  const uint32_t ones = BF ? 0x3f803f80u : 0x3c003c00u;
+  bool ok = true;
+  int i = warp, cur = 0, tile = s.tile;
+  long long g0 = s.t0 - tile;  // first tile of the item, counted from the start of all
+  while (cur < n && it.tiles > tile) {
+    const int end = min(n, cur + it.tiles - tile);
+    const int h = it.hr / RT, r0 = (it.hr % RT) * kPdRows;
+    const int rows = min(kPdRows, G - r0);
+    const int64_t head0 = static_cast<int64_t>(h) * G + r0;
+    // The query rows as A fragments.  An e4m3 cache is multiplied in fp16: its
+    // channels are taken in the order in which four bytes lie in a register,
+    // and bf16 queries are scaled by a power of two per row so that the largest
+    // lies in [2^8, 2^9) (what then falls below fp16's normal range is 2^-22 of
+    // it).
+    uint32_t qf[D / 16][4];
+    float mul0 = a.sl2, mul1 = a.sl2;
+    {
+      const uint8_t* q0 = a.q.p + it.b * a.q.row + (head0 + g) * a.q.head;
+      const uint8_t* q1 = q0 + 8 * a.q.head;
+      const bool v0 = g < rows, v1 = g + 8 < rows;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        if constexpr (E8) {
+          const uint2 x = v0 ? *reinterpret_cast<const uint2*>(q0 + ks * 32 + t4 * 8) : make_uint2(0u, 0u);
+          const uint2 y = v1 ? *reinterpret_cast<const uint2*>(q1 + ks * 32 + t4 * 8) : make_uint2(0u, 0u);
+          qf[ks][0] = x.x, qf[ks][2] = x.y, qf[ks][1] = y.x, qf[ks][3] = y.y;
+        } else {
+          qf[ks][0] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + ks * 32 + t4 * 4) : 0u;
+          qf[ks][2] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + ks * 32 + 16 + t4 * 4) : 0u;
+          qf[ks][1] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + ks * 32 + t4 * 4) : 0u;
+          qf[ks][3] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + ks * 32 + 16 + t4 * 4) : 0u;
+        }
+      }
+      if constexpr (E8 && X == kTypeBf16) {
+        float big0 = 0.f, big1 = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 f = unpack2<true>(qf[ks][x]);
+            float& big = (x & 1) ? big1 : big0;
+            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        float fac[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float big = x ? big1 : big0;
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          // 2^(8 - e) for a largest value of exponent e, within the normal range; 1 for an infinite one
+          const int e = max(20, static_cast<int>(__float_as_uint(big) >> 23));
+          fac[x] = e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
+          (x ? mul1 : mul0) *= e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(e - 8) << 23);
+        }
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 f = unpack2<true>(qf[ks][x]);
+            qf[ks][x] = pack2<false>(f.x * fac[x & 1], f.y * fac[x & 1]);
+          }
+      }
+    }
+
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float lr[4] = {0.f, 0.f, 0.f, 0.f};  // sums of the rounded weights
+    float o[D / 8][4];
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) o[x][y] = 0.f;
+
+    for (; i < end; i += kPdWarps) {
+      const int st = i % F::STAGES;
+      if (ok) ok = mbar_wait(full + st * 8, (i / F::STAGES) & 1, abort_flag, a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;
+      const uint64_t mask = masks[st];
+      const uint32_t kb = sbase + st * 2 * F::HALF, vb = kb + F::HALF;
+      const bool whole = mask == (TK == 64 ? ~0ull : (1ull << (TK & 63)) - 1);
+      if (!whole) {
+        // Slots behind the sequence's end may hold NaN: their V rows become 0.
+        for (int r = lane; r < TK; r += 32)
+          if (!((mask >> r) & 1))
+            for (int x = 0; x < F::NH; ++x)
+#pragma unroll
+              for (int y = 0; y < F::RBX; y += 16)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (x * TK + r) * F::RBX + y), "r"(0)
+                             : "memory");
+        fence_proxy_async_smem();  // before the stage's next load
+        __syncwarp();
+      }
+      // S = Q K^T
+      float sc[TK / 8][4];
+#pragma unroll
+      for (int x = 0; x < TK / 8; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) sc[x][y] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        if constexpr (E8) {
+          const uint32_t at = kb + (mi * 8 + l8) * F::RBX + ((ks ^ swz) << 4);
+#pragma unroll
+          for (int x = 0; x < TK / 32; ++x) {
+            uint32_t r[4];
+            ldsm4(at + x * 32 * F::RBX, r);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mma16<false>(sc[4 * x + y], qf[ks], e4m3_pair(r[y]), e4m3_pair(r[y] >> 16));
+          }
+        } else {
+          const int chunk = ks * 2 + (mi & 1);
+          const uint32_t at = kb + (chunk / (F::RBX / 16)) * TK * F::RBX + ((mi >> 1) * 8 + l8) * F::RBX +
+                              (((chunk % (F::RBX / 16)) ^ swz) << 4);
+#pragma unroll
+          for (int x = 0; x < TK / 16; ++x) {
+            uint32_t r[4];
+            ldsm4(at + x * 16 * F::RBX, r);
+            mma16<BF>(sc[2 * x], qf[ks], r[0], r[1]);
+            mma16<BF>(sc[2 * x + 1], qf[ks], r[2], r[3]);
+          }
+        }
+      }
+      // Online softmax, in units of log2.
+      float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < TK / 8; ++x) {
+        sc[x][0] *= mul0, sc[x][1] *= mul0, sc[x][2] *= mul1, sc[x][3] *= mul1;
+        if (!whole) {
+          const uint32_t two = static_cast<uint32_t>(mask >> (x * 8 + 2 * t4));
+          if (!(two & 1)) sc[x][0] = sc[x][2] = -INFINITY;
+          if (!(two & 2)) sc[x][1] = sc[x][3] = -INFINITY;
+        }
+        x0 = max3f(x0, sc[x][0], sc[x][1]);
+        x1 = max3f(x1, sc[x][2], sc[x][3]);
+      }
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {  // the maximum rises rarely once some tiles are seen
+        const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0), a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
+        m0 = n0, m1 = n1;
+        l0 *= a0, l1 *= a1;
+        lr[0] *= a0, lr[2] *= a1;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) o[x][0] *= a0, o[x][1] *= a0, o[x][2] *= a1, o[x][3] *= a1;
+      }
+      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;  // no key yet: weights 0
+      uint32_t pf[TK / 16][4];
+#pragma unroll
+      for (int x = 0; x < TK / 8; ++x) {
+        const float p0 = ex2_approx(sc[x][0] - z0), p1 = ex2_approx(sc[x][1] - z0);
+        const float p2 = ex2_approx(sc[x][2] - z1), p3 = ex2_approx(sc[x][3] - z1);
+        l0 += p0 + p1;
+        l1 += p2 + p3;
+        pf[x >> 1][(x & 1) * 2] = pack2<BF>(p0, p1);
+        pf[x >> 1][(x & 1) * 2 + 1] = pack2<BF>(p2, p3);
+      }
+      // O += P V; the weights that multiply V are rounded to 16 bits, and their
+      // sum (a column of ones) is what O is divided by.
+#pragma unroll
+      for (int kk = 0; kk < TK / 16; ++kk) {
+        mma16<BF>(lr, pf[kk], ones, ones);
+        const uint32_t at = vb + (kk * 16 + (mi & 1) * 8 + l8) * F::RBX;
+        if constexpr (E8) {
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
+            uint32_t r[4];
+            ldsm4_t(at + (((2 * x + (mi >> 1)) ^ swz) << 4), r);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {  // a register holds two channels of two keys
+              mma16<false>(o[4 * x + 2 * y], pf[kk], e4m3_pair(__byte_perm(r[2 * y], 0, 0x4420)),
+                           e4m3_pair(__byte_perm(r[2 * y + 1], 0, 0x4420)));
+              mma16<false>(o[4 * x + 2 * y + 1], pf[kk], e4m3_pair(__byte_perm(r[2 * y], 0, 0x4431)),
+                           e4m3_pair(__byte_perm(r[2 * y + 1], 0, 0x4431)));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const int chunk = 2 * x + (mi >> 1);
+            uint32_t r[4];
+            ldsm4_t(at + (chunk / (F::RBX / 16)) * TK * F::RBX + (((chunk % (F::RBX / 16)) ^ swz) << 4), r);
+            mma16<BF>(o[2 * x], pf[kk], r[0], r[1]);
+            mma16<BF>(o[2 * x + 1], pf[kk], r[2], r[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + st * 8);
+    }
+
+    // The item's end in this CTA: merge the four warps.  Columns are swizzled by
+    // the row, so that the fragments' stores meet no bank twice.
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    float* ml = sml + warp * 3 * kPdRows;
+    if (t4 == 0) {
+      ml[g] = m0, ml[kPdRows + g] = l0, ml[2 * kPdRows + g] = lr[0];
+      ml[g + 8] = m1, ml[kPdRows + g + 8] = l1, ml[2 * kPdRows + g + 8] = lr[2];
+    }
+    {
+      float* w0 = so + (warp * kPdRows + g) * D;
+      float* w1 = w0 + 8 * D;
+      const int sw = (g & 3) << 3;
+#pragma unroll
+      for (int x = 0; x < (E8 ? D / 16 : D / 8); ++x) {
+        if constexpr (E8) {
+          const int col = (x * 16 + t4 * 4) ^ sw;
+          *reinterpret_cast<float4*>(w0 + col) = make_float4(o[2 * x][0], o[2 * x + 1][0], o[2 * x][1], o[2 * x + 1][1]);
+          if (rows > 8)
+            *reinterpret_cast<float4*>(w1 + col) = make_float4(o[2 * x][2], o[2 * x + 1][2], o[2 * x][3], o[2 * x + 1][3]);
+        } else {
+          const int col = (x * 8 + t4 * 2) ^ sw;
+          *reinterpret_cast<float2*>(w0 + col) = make_float2(o[x][0], o[x][1]);
+          if (rows > 8) *reinterpret_cast<float2*>(w1 + col) = make_float2(o[x][2], o[x][3]);
         }
       }
     }
-    float t = 0.f;
+    consumer_sync();
+    const bool begins = tile == 0, ends = end - cur == it.tiles - tile;
+    const bool direct = begins && ends;
+    float* out = part + (static_cast<int64_t>(c) * 2 + (begins ? 1 : 0)) * part_floats(D);
+    for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kPdWarps) {
+      const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+      float mw[kPdWarps], mm = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t = fmaf(q[e], kf[e], t);
+      for (int w = 0; w < kPdWarps; ++w) mm = fmaxf(mm, mw[w] = sml[w * 3 * kPdRows + r]);
+      float l = 0.f, ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int x = LPK / 2; x; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-    if (!seen) continue;
-    t *= a.sl2;
-    const float mn = fmaxf(m, t);
-    if (mn == -INFINITY) continue;
-    const float alpha = exp2f(m - mn), p = exp2f(t - mn);
-    m = mn;
-    l = l * alpha + p;
+      for (int w = 0; w < kPdWarps; ++w) {
+        const float f = part_weight(mw[w], mm);
+        l += f * sml[w * 3 * kPdRows + kPdRows + r];
+        ls += f * sml[w * 3 * kPdRows + 2 * kPdRows + r];
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * kPdRows + r) * D + (col ^ ((r & 3) << 3)));
+        acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+      }
+      if (direct) {
+        const float inv = ls == 0.f ? 0.f : kv.v_scale / ls;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = acc[e] * alpha + p * vf[e];
+        for (int y = 0; y < 4; ++y) acc[y] *= inv;
+        const int64_t at = static_cast<int64_t>(it.b) * a.Hq + head0 + r;
+        store_out4<X>(a.o + (at * D + col) * 2, acc);
+        if (col == 0) a.lse[at] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+      } else {
+        *reinterpret_cast<float4*>(out + r * D + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (col == 0) {
+          out[kPdRows * D + r] = mm;
+          out[kPdRows * (D + 1) + r] = l;
+          out[kPdRows * (D + 2) + r] = ls;
+        }
+      }
+    }
+    if (begins && threadIdx.x == 0 && (by_item || !ends)) {
+      const long long e = g0 + it.tiles;  // CTA c starts at total * c / n_act
+      const int last = static_cast<int>((e * s.n_act + s.total - 1) / s.total - 1);
+      parts[by_item ? it.b * HR + it.hr : c] = Part{it.b, it.hr, c, ends ? -1 : last};
+    }
+    consumer_sync();  // the area is free for the next item
+    g0 += it.tiles;
+    cur = end;
+    tile = 0;
+    if (cur < n) next_item<TK>(a, HR, it);
   }
-  __shared__ float sm_m[GROUPS], sm_l[GROUPS], sm_o[GROUPS][D];
-  if (c == 0) sm_m[g] = m, sm_l[g] = l;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) sm_o[g][c + e] = acc[e];
-  __syncthreads();
-  float mm = -INFINITY;
-  for (int i = 0; i < GROUPS; ++i) mm = fmaxf(mm, sm_m[i]);
-  float* out = part + (static_cast<int64_t>(blockIdx.y) * S + s) * (D + 2);
-  for (int x = threadIdx.x; x < D + 1; x += kPdThreads) {
-    float sum = 0.f;
-    for (int i = 0; i < GROUPS; ++i)
-      if (sm_m[i] != -INFINITY) sum += exp2f(sm_m[i] - mm) * (x < D ? sm_o[i][x] : sm_l[i]);
-    out[x < D ? 2 + x : 1] = sum;
-  }
-  if (threadIdx.x == 0) out[0] = mm;
 }
 
+// One block per (cut item, query head): joins the parts in the order of the
+// CTAs, so the result does not depend on which finished first.
 template <int X, int D>
-__global__ void __launch_bounds__(128) attn_paged_merge_kernel(const PagedDecodeArgs a, const float* part, int S) {
+__global__ void __launch_bounds__(D) attn_paged_merge_kernel(const PagedDecodeArgs a, int RT, const Part* parts,
+                                                             const float* part) {
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
-  const float* p = part + static_cast<int64_t>(blockIdx.x) * S * (D + 2);
-  float mm = -INFINITY;
-  for (int s = 0; s < S; ++s) mm = fmaxf(mm, p[s * (D + 2)]);
-  float l = 0.f;
-  for (int s = 0; s < S; ++s)
-    if (p[s * (D + 2)] != -INFINITY) l += exp2f(p[s * (D + 2)] - mm) * p[s * (D + 2) + 1];
-  const int c = threadIdx.x;
-  if (c < D) {
-    float o = 0.f;
-    for (int s = 0; s < S; ++s)
-      if (p[s * (D + 2)] != -INFINITY) o += exp2f(p[s * (D + 2)] - mm) * p[s * (D + 2) + 2 + c];
-    o = l > 0.f ? o / l * a.kv.v_scale : l;  // no key: 0 (NaN stays NaN)
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * D + c;
-    if constexpr (X == kTypeBf16) reinterpret_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(o);
-    else reinterpret_cast<__half*>(a.o)[at] = __float2half_rn(o);
+  const Part p = parts[blockIdx.x];
+  if (p.last < 0) return;
+  const int G = a.Hq / a.kv.H, r = blockIdx.y;
+  const int r0 = (p.hr % RT) * kPdRows;
+  if (r >= min(kPdRows, G - r0)) return;
+  const int n = p.last - p.first + 1;
+  // CTA `first` has the item's beginning in its slot 1, the others theirs in slot 0.
+  const float* base = part + (static_cast<int64_t>(p.first) * 2) * part_floats(D) + r;
+  auto stat = [&](int i, int which) {
+    return base[(i ? static_cast<int64_t>(i) * 2 : 1) * part_floats(D) + kPdRows * (D + which)];
+  };
+  __shared__ float sm_m;
+  __shared__ float sm_f[1024];  // weights of the parts
+  if (threadIdx.x < 32) {
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += 32) m = fmaxf(m, stat(i, 0));
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    if (threadIdx.x == 0) sm_m = m;
   }
-  if (c == 0) a.lse[blockIdx.x] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+  __syncthreads();
+  const float m = sm_m;
+  for (int i = threadIdx.x; i < n; i += D) {
+    const float mi = stat(i, 0);
+    sm_f[i] = part_weight(mi, m);
+  }
+  __syncthreads();
+  float l = 0.f, ls = 0.f, o = 0.f;
+  const int c = threadIdx.x;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float f = sm_f[i];
+    const float* at = base - r + (i ? static_cast<int64_t>(i) * 2 : 1) * part_floats(D);
+    o += f * at[r * D + c];
+    l += f * at[kPdRows * (D + 1) + r];
+    ls += f * at[kPdRows * (D + 2) + r];
+  }
+  o = ls == 0.f ? 0.f : o * (a.kv.v_scale / ls);
+  const int64_t at = static_cast<int64_t>(p.b) * a.Hq + static_cast<int64_t>(p.hr / RT) * G + r0 + r;
+  if constexpr (X == kTypeBf16) reinterpret_cast<__nv_bfloat16*>(a.o)[at * D + c] = __float2bfloat16_rn(o);
+  else reinterpret_cast<__half*>(a.o)[at * D + c] = __float2half_rn(o);
+  if (c == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-int split_count(int B, int Hq, int64_t keys) {
-  const int64_t want = (152 * 8 + static_cast<int64_t>(B) * Hq - 1) / (static_cast<int64_t>(B) * Hq);
-  return static_cast<int>(std::max<int64_t>(1, std::min(std::min<int64_t>(want, (keys + 255) / 256), int64_t{256})));
-}
+constexpr int kMaxCtas = 1024;  // of the decode kernel; the merge kernel keeps a weight for each
+
+int row_tiles(int Hq, int H) { return (Hq / H + kPdRows - 1) / kPdRows; }
 
 template <int X, int C, int D>
 int launch_t(const PagedDecodeArgs& a) {
-  const int64_t keys = static_cast<int64_t>(a.pages ? a.n_pages : a.kv.max_pages) * a.kv.page;
-  const int S = split_count(a.kv.B, a.Hq, keys);
-  float* part = reinterpret_cast<float*>(a.ws);
-  if (launch_serialized(true, attn_paged_split_kernel<X, C, D>, dim3(S, a.kv.B * a.Hq), dim3(kPdThreads), 0, a.stream,
-                        a, part, static_cast<int>((keys + S - 1) / S)) != cudaSuccess)
+  using F = PdCfg<C, D>;
+  static_assert(F::SMEM <= 115712, "two CTAs per SM");
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kStatusCuda;
+  auto kern = attn_paged_decode_kernel<X, C, D>;
+  if (!((ready.load() >> dev) & 1)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM) != cudaSuccess) return kStatusCuda;
+    ready.fetch_or(1ull << dev);
+  }
+  const int RT = row_tiles(a.Hq, a.kv.H);
+  int box = 8;
+  while (box < F::TK && a.kv.page % (2 * box) == 0) box *= 2;
+  CUtensorMap mk, mv;
+  if (!encode_pages_map(&mk, a.kv.k, F::ROW, a.kv.page, a.kv.H, a.kv.num_pages, a.kv.k_tok, a.kv.k_head, a.kv.k_page, F::RBX,
+                        box) ||
+      !encode_pages_map(&mv, a.kv.v, F::ROW, a.kv.page, a.kv.H, a.kv.num_pages, a.kv.v_tok, a.kv.v_head, a.kv.v_page, F::RBX,
+                        box))
     return kStatusCuda;
-  return launch_serialized(true, attn_paged_merge_kernel<X, D>, dim3(a.kv.B * a.Hq), dim3(128), 0, a.stream, a, part,
-                           S) == cudaSuccess
+  const int sms = device_sm_count();
+  if (sms < 1) return kStatusCuda;
+  const int64_t keys = static_cast<int64_t>(a.pages ? a.n_pages : a.kv.max_pages) * a.kv.page;
+  const int64_t items = static_cast<int64_t>(a.kv.B) * a.kv.H * RT;
+  const int64_t most = items * ((keys + F::TK - 1) / F::TK);  // tiles, if every sequence fills its table
+  const int ctas = static_cast<int>(std::min<int64_t>(std::min(2 * sms, kMaxCtas), (most + kPdWarps - 1) / kPdWarps));
+  const int by_item = items <= ctas;
+  Part* parts = reinterpret_cast<Part*>(a.ws);
+  float* part = reinterpret_cast<float*>(a.ws + kMaxCtas * sizeof(Part));
+  if (launch_serialized(true, kern, dim3(ctas), dim3(kPdThreads), F::SMEM, a.stream, mk, mv, a, RT, box, by_item, parts,
+                        part) != cudaSuccess)
+    return kStatusCuda;
+  const dim3 grid(by_item ? static_cast<int>(items) : ctas, std::min(kPdRows, a.Hq / a.kv.H));
+  return launch_serialized(true, attn_paged_merge_kernel<X, D>, grid, dim3(D), 0, a.stream, a, RT, parts, part) ==
+                 cudaSuccess
              ? kStatusOk
              : kStatusCuda;
 }
@@ -137,8 +706,12 @@ int launch_d(const PagedDecodeArgs& a) {
 }  // namespace
 
 int64_t paged_decode_workspace(int B, int Hq, int H, int d, int page, int n_pages) {
-  const int64_t keys = static_cast<int64_t>(n_pages) * page;
-  return static_cast<int64_t>(B) * Hq * split_count(B, Hq, keys) * (d + 2) * 4;
+  // Two partial results for each CTA, as many as the largest GPU of the family
+  // could hold; a bound by the tiles keeps it small for small problems.
+  const int64_t items = static_cast<int64_t>(B) * H * row_tiles(Hq, H);
+  const int64_t most = items * ((static_cast<int64_t>(n_pages) * page + 31) / 32);
+  const int64_t ctas = std::min<int64_t>(kMaxCtas, (most + kPdWarps - 1) / kPdWarps);
+  return kMaxCtas * static_cast<int64_t>(sizeof(Part)) + ctas * 2 * part_floats(d) * 4;
 }
 
 int launch_paged_decode(const PagedDecodeArgs& a, int* launches) {

@@ -684,3 +684,13 @@ def test_two_streams_at_once(pkg):
     for g, w in zip(got, want):
         for r in g:
             assert all(torch.equal(a, b) for a, b in zip(r, w))
+
+
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+def test_decode_many_turns_of_the_ring(pkg, x, dtype, scales):
+    """Shares of some tens of tiles per CTA, cut items and lengths that end inside tiles and pages."""
+    g = torch.Generator().manual_seed(5)
+    lens = [2500] + [int(v) for v in torch.randint(0, 2500, (60,), generator=g)] + [0, 0, 0]
+    c = Case(pkg, lens, H=8, d=128, dtype=dtype, scales=scales, seed=5)
+    for _ in range(3):
+        _check_decode(pkg, c, c.randn(len(lens), 16, 128, dtype=x))
