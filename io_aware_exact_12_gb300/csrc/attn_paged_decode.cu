@@ -90,23 +90,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-template <bool BF16>
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Two e4m3 bytes (low half of the word) as two fp16 values; exact.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
-  return r;
-}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
                                             int c3) {
   asm volatile(
@@ -437,7 +420,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
             uint32_t r[4];
             ldsm4(at + x * 32 * F::RBX, r);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) mma16<false>(sc[4 * x + y], qf[ks], e4m3_pair(r[y]), e4m3_pair(r[y] >> 16));
+            for (int y = 0; y < 4; ++y) mma16<false>(sc[4 * x + y], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], e4m3_pair(r[y]), e4m3_pair(r[y] >> 16));
           }
         } else {
           const int chunk = ks * 2 + (mi & 1);
@@ -447,8 +430,8 @@ __global__ void __launch_bounds__(kPdThreads, 2)
           for (int x = 0; x < TK / 16; ++x) {
             uint32_t r[4];
             ldsm4(at + x * 16 * F::RBX, r);
-            mma16<BF>(sc[2 * x], qf[ks], r[0], r[1]);
-            mma16<BF>(sc[2 * x + 1], qf[ks], r[2], r[3]);
+            mma16<BF>(sc[2 * x], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], r[0], r[1]);
+            mma16<BF>(sc[2 * x + 1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], r[2], r[3]);
           }
         }
       }
@@ -493,7 +476,7 @@ __global__ void __launch_bounds__(kPdThreads, 2)
       // sum (a column of ones) is what O is divided by.
 #pragma unroll
       for (int kk = 0; kk < TK / 16; ++kk) {
-        mma16<BF>(lr, pf[kk], ones, ones);
+        mma16<BF>(lr, pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], ones, ones);
         const uint32_t at = vb + (kk * 16 + (mi & 1) * 8 + l8) * F::RBX;
         if constexpr (E8) {
 #pragma unroll
@@ -502,9 +485,9 @@ __global__ void __launch_bounds__(kPdThreads, 2)
             ldsm4_t(at + (((2 * x + (mi >> 1)) ^ swz) << 4), r);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {  // a register holds two channels of two keys
-              mma16<false>(o[4 * x + 2 * y], pf[kk], e4m3_pair(__byte_perm(r[2 * y], 0, 0x4420)),
+              mma16<false>(o[4 * x + 2 * y], pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], e4m3_pair(__byte_perm(r[2 * y], 0, 0x4420)),
                            e4m3_pair(__byte_perm(r[2 * y + 1], 0, 0x4420)));
-              mma16<false>(o[4 * x + 2 * y + 1], pf[kk], e4m3_pair(__byte_perm(r[2 * y], 0, 0x4431)),
+              mma16<false>(o[4 * x + 2 * y + 1], pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], e4m3_pair(__byte_perm(r[2 * y], 0, 0x4431)),
                            e4m3_pair(__byte_perm(r[2 * y + 1], 0, 0x4431)));
             }
           }
@@ -514,8 +497,8 @@ __global__ void __launch_bounds__(kPdThreads, 2)
             const int chunk = 2 * x + (mi >> 1);
             uint32_t r[4];
             ldsm4_t(at + (chunk / (F::RBX / 16)) * TK * F::RBX + (((chunk % (F::RBX / 16)) ^ swz) << 4), r);
-            mma16<BF>(o[2 * x], pf[kk], r[0], r[1]);
-            mma16<BF>(o[2 * x + 1], pf[kk], r[2], r[3]);
+            mma16<BF>(o[2 * x], pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], r[0], r[1]);
+            mma16<BF>(o[2 * x + 1], pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], r[2], r[3]);
           }
         }
       }

@@ -2,12 +2,27 @@
 // keys can have the largest logit with the new token's queries.
 //
 //   score(p) = max over the head's queries g of
-//              sum_c max(q_gc kmin_pc, q_gc kmax_pc),
+//              sum_c max(q_gc kmin_pc, q_gc kmax_pc)
+//            = max_g (q_g^+ . kmax_p + q_g^- . kmin_p),
 //
 // the least upper bound of q_g . k over the box that the page's summary spans.
 // The first and last pages of a sequence are always taken; the rest go by the
 // score, equal ones by the lower index.  Two pages next to the border must not
-// change places by rounding, so the order is that of scores in 64 bits.
+// change places by rounding, so the order is that of scores in 64 bits; but
+// reading and multiplying every summary in 64 bits would cost many times what
+// HBM needs to deliver it.  Hence two kernels:
+//
+//   attn_paged_score_kernel : every page's score as a matrix product of 2 d
+//       channels with fp32 sums (m16n8k16, the queries as rows; e4m3 summaries
+//       widened to fp16).  Reads 2 d elements per page and head once: HBM bound.
+//   attn_paged_pick_kernel : one CTA per (sequence, KV head).  A score s errs by
+//       at most eps = 2^-14 max_g |q_g|_1 max |k|: 2 d / 16 steps, each of which
+//       cuts 17 aligned terms at 2^-23 of the largest or less, stay below 2^-14.9
+//       of the sum of magnitudes at d = 128.  It brackets the border to [L, H)
+//       with H - L <= eps; pages at H + 2 eps or above are in, those below
+//       L - 2 eps out, and only those between (a few) are scored again in 64
+//       bits.  With eps = inf (a sum that overflowed or is NaN) that is all of
+//       them.
 #include <cmath>
 
 #include "attn_paged.h"
@@ -16,15 +31,217 @@
 namespace attn {
 namespace {
 
-constexpr int kSelThreads = 512;
+constexpr int kScoreWarps = 4;
+constexpr int kScorePages = 32;                       // pages of a warp, in groups of 8
+constexpr int kScoreChunk = kScoreWarps * kScorePages;  // pages of a CTA
+constexpr int kPickThreads = 1024;
+constexpr int kPickCap = 1024;  // candidates kept in shared memory
 
-// Order-preserving map of a score to an unsigned key; NaN ranks first.
+struct SelectScratch {  // per (sequence, head)
+  float* score;         // [max_pages]
+  float* kinf;          // [chunks] largest magnitude in a chunk's summaries
+  uint64_t* key;        // [max_pages] exact scores, used beyond kPickCap candidates
+};
+
+__host__ __device__ inline int64_t up16(int64_t x) { return (x + 15) & ~int64_t{15}; }
+
+__host__ __device__ inline int score_chunks(int max_pages) { return (max_pages + kScoreChunk - 1) / kScoreChunk; }
+__host__ __device__ inline int64_t select_scratch_bytes(int max_pages) {
+  return up16(int64_t{4} * max_pages) + up16(int64_t{4} * score_chunks(max_pages)) + int64_t{8} * max_pages + (max_pages & 1) * 8;
+}
+__device__ __forceinline__ SelectScratch scratch_of(uint8_t* ws, int64_t bh, int max_pages) {
+  uint8_t* p = ws + bh * select_scratch_bytes(max_pages);
+  SelectScratch s;
+  s.score = reinterpret_cast<float*>(p);
+  s.kinf = reinterpret_cast<float*>(p + up16(int64_t{4} * max_pages));
+  s.key = reinterpret_cast<uint64_t*>(p + up16(int64_t{4} * max_pages) + up16(int64_t{4} * score_chunks(max_pages)));
+  return s;
+}
+
+// ------------------------------------------------------------------- scores
+
+// Sign mask of two 16-bit floats: all ones in the halves that are negative.
+__device__ __forceinline__ uint32_t negative_halves(uint32_t x) { return ((x >> 15) & 0x00010001u) * 0xffffu; }
+
+// The larger magnitudes of two pairs, as 16-bit floats (their order is that of
+// their bits).
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t x) {
+  return __vmaxu2(m, x & 0x7fff7fffu);
+}
+template <bool BF16>
+__device__ __forceinline__ float magnitude(uint32_t m) {
+  const float2 f = unpack2<BF16>(m);
+  return fmaxf(f.x, f.y);
+}
+
+// A warp scores 8 pages at a time.  The sum over channels may run in any order,
+// so a thread loads whole 16-byte pieces of its page's summaries and the queries
+// are laid out to match: piece v of thread t4 holds bytes (4 v + t4) VB and on.
+template <int X, int C, int D, bool WIDE>  // WIDE: more than 8 query heads
+__global__ void __launch_bounds__(32 * kScoreWarps) attn_paged_score_kernel(const PagedSelectArgs a) {
+  griddep_wait();  // launched overlapped (launch_serialized)
+  griddep_launch_dependents();
+  constexpr bool E8 = C == kTypeE4m3;
+  constexpr bool BF = C == kTypeBf16;
+  constexpr int ROW = D * (E8 ? 1 : 2);
+  constexpr int VB = ROW / 4 < 16 ? ROW / 4 : 16;  // bytes of a piece
+  constexpr int NV = ROW / (4 * VB);
+  constexpr int WPV = VB / 4;                      // words of a piece
+  constexpr int NS = D / 16;                       // steps of 16 channels
+  const PagedKv& kv = a.kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int bh = blockIdx.y, b = bh / kv.H, h = bh % kv.H, G = a.Hq / kv.H;
+  const int used = (checked_len(kv, b) + kv.page - 1) / kv.page;
+  if (used <= a.n_select || static_cast<int>(blockIdx.x) * kScoreChunk >= used) return;
+  const SelectScratch sc = scratch_of(a.ws, bh, kv.max_pages);
+  const int p0 = blockIdx.x * kScoreChunk + warp * kScorePages;
+
+  int id[kScorePages / 8];
+#pragma unroll
+  for (int i = 0; i < kScorePages / 8; ++i) {
+    const int j = p0 + i * 8 + g;
+    id[i] = j < used ? checked_page(kv, b, j) : -1;
+  }
+  uint32_t big = 0;
+  for (int r0 = 0; r0 < G; r0 += WIDE ? 16 : 8) {
+    // q^+ and q^- of rows g and g + 8 as A fragments.
+    uint32_t qp[NS][WIDE ? 4 : 2], qn[NS][WIDE ? 4 : 2];
+    float mul[2] = {1.f, 1.f};
+    constexpr int NR = WIDE ? 2 : 1;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const bool live = r0 + g + 8 * r < G;
+      const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + r0 + g + 8 * r) * a.q.head;
+      uint32_t w[NS][2];
+      if constexpr (E8) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int i = 0; i < WPV; ++i) {
+            const uint2 x = live ? *reinterpret_cast<const uint2*>(q + 2 * ((v * 4 + t4) * VB + i * 4)) : make_uint2(0u, 0u);
+            w[v * WPV + i][0] = x.x, w[v * WPV + i][1] = x.y;
+          }
+        if constexpr (X == kTypeBf16) {  // into fp16's range by a power of two
+          float m = 0.f;
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 f = unpack2<true>(w[s][i]);
+              m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          const int e = max(20, static_cast<int>(__float_as_uint(m) >> 23));
+          const float fac = e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
+          mul[r] = e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(e - 8) << 23);
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 f = unpack2<true>(w[s][i]);
+              w[s][i] = pack2<false>(f.x * fac, f.y * fac);
+            }
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int i = 0; i < WPV; ++i)
+            w[(v * WPV + i) / 2][(v * WPV + i) % 2] =
+                live ? *reinterpret_cast<const uint32_t*>(q + (v * 4 + t4) * VB + i * 4) : 0u;
+      }
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t neg = negative_halves(w[s][i]);
+          qp[s][i * NR + r] = w[s][i] & ~neg;
+          qn[s][i * NR + r] = w[s][i] & neg;
+        }
+    }
+#pragma unroll 2
+    for (int i = 0; i < kScorePages / 8; ++i) {
+      uint32_t lo[NV * WPV], hi[NV * WPV];
+      const int64_t at = (static_cast<int64_t>(max(id[i], 0)) * kv.H + h) * ROW;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if constexpr (VB == 16) {
+          const uint4 x = id[i] >= 0 ? *reinterpret_cast<const uint4*>(kv.kmin + at + (v * 4 + t4) * 16) : make_uint4(0, 0, 0, 0);
+          const uint4 y = id[i] >= 0 ? *reinterpret_cast<const uint4*>(kv.kmax + at + (v * 4 + t4) * 16) : make_uint4(0, 0, 0, 0);
+          lo[4 * v] = x.x, lo[4 * v + 1] = x.y, lo[4 * v + 2] = x.z, lo[4 * v + 3] = x.w;
+          hi[4 * v] = y.x, hi[4 * v + 1] = y.y, hi[4 * v + 2] = y.z, hi[4 * v + 3] = y.w;
+        } else {
+          const uint2 x = id[i] >= 0 ? *reinterpret_cast<const uint2*>(kv.kmin + at + (v * 4 + t4) * 8) : make_uint2(0, 0);
+          const uint2 y = id[i] >= 0 ? *reinterpret_cast<const uint2*>(kv.kmax + at + (v * 4 + t4) * 8) : make_uint2(0, 0);
+          lo[2 * v] = x.x, lo[2 * v + 1] = x.y, hi[2 * v] = y.x, hi[2 * v + 1] = y.y;
+        }
+      }
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        uint32_t l0, l1, h0, h1;
+        if constexpr (E8) {
+          l0 = e4m3_pair(lo[s]), l1 = e4m3_pair(lo[s] >> 16), h0 = e4m3_pair(hi[s]), h1 = e4m3_pair(hi[s] >> 16);
+        } else {
+          l0 = lo[2 * s], l1 = lo[2 * s + 1], h0 = hi[2 * s], h1 = hi[2 * s + 1];
+        }
+        big = max_magnitude(max_magnitude(max_magnitude(max_magnitude(big, l0), l1), h0), h1);
+        if constexpr (WIDE) {
+          mma16<BF>(acc, qp[s][0], qp[s][1], qp[s][2], qp[s][3], h0, h1);
+          mma16<BF>(acc, qn[s][0], qn[s][1], qn[s][2], qn[s][3], l0, l1);
+        } else {
+          mma16<BF>(acc, qp[s][0], 0u, qp[s][1], 0u, h0, h1);
+          mma16<BF>(acc, qn[s][0], 0u, qn[s][1], 0u, l0, l1);
+        }
+      }
+      float best[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        best[x] = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          float s = acc[2 * r + x] * mul[r];
+          if (!(fabsf(s) <= 3.402823466e38f)) s = INFINITY;  // NaN too: the pick scores such pages anew
+          if (r0 + g + 8 * r < G) best[x] = fmaxf(best[x], s);
+        }
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], y));
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = p0 + i * 8 + 2 * t4 + x;
+        const int of = __shfl_sync(0xffffffffu, id[i], (2 * t4 + x) * 4);
+        if (g == 0 && j < used) {
+          const float s = of < 0 ? -3.402823466e38f : best[x];  // no page there: last
+          sc.score[j] = r0 ? fmaxf(sc.score[j], s) : s;
+        }
+      }
+    }
+  }
+  float m = magnitude<BF>(big);
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  __shared__ float sm[kScoreWarps];
+  if (lane == 0) sm[warp] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) sc.kinf[blockIdx.x] = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+}
+
+// --------------------------------------------------------------------- pick
+
+// Order-preserving maps of scores to unsigned keys; NaN ranks first.
 __device__ __forceinline__ uint64_t key64(double x) {
   if (isnan(x)) return ~0ull;
   x = x == 0.0 ? 0.0 : x;  // -0 equals +0
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
+__device__ __forceinline__ uint32_t key32(float x) {
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
+  return (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float of_key32(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
 
 template <int X>
 __device__ __forceinline__ double load1(const uint8_t* p, int i) {
@@ -33,108 +250,263 @@ __device__ __forceinline__ double load1(const uint8_t* p, int i) {
   else return __half2float(__half(__nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3)));
 }
 
-// Sum of one value per thread over the block, given to every thread.
-__device__ __forceinline__ int block_sum(int v, int* sm) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();  // sm is free again
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+struct PickShared {
+  int count[2][3][32];
+  float f[2][32];
+  int list[kPickCap];
+  uint64_t key[kPickCap];
+  int m;
+};
+
+// Sums over the block of up to three values, for every thread; `turn` alternates
+// so that one barrier per sum is enough.
+__device__ __forceinline__ int3 block_sum3(int3 v, PickShared& sm, int turn) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  v.x = __reduce_add_sync(0xffffffffu, v.x);
+  v.y = __reduce_add_sync(0xffffffffu, v.y);
+  v.z = __reduce_add_sync(0xffffffffu, v.z);
+  if (lane == 0) sm.count[turn][0][w] = v.x, sm.count[turn][1][w] = v.y, sm.count[turn][2][w] = v.z;
   __syncthreads();
-  int s = 0;
-  for (int i = 0; i < kSelThreads / 32; ++i) s += sm[i];
-  return s;
+  return make_int3(__reduce_add_sync(0xffffffffu, sm.count[turn][0][lane]),
+                   __reduce_add_sync(0xffffffffu, sm.count[turn][1][lane]),
+                   __reduce_add_sync(0xffffffffu, sm.count[turn][2][lane]));
 }
 
-template <int X, int C>
-__global__ void __launch_bounds__(kSelThreads) attn_paged_select_kernel(const PagedSelectArgs a) {
+// The definition, by one warp; every lane gets it.
+template <int X, int C, int D>
+__device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, int h, int G, int j) {
+  constexpr int CB = C == kTypeE4m3 ? 1 : 2;
+  const int lane = threadIdx.x & 31;
+  const int id = checked_page(a.kv, b, j);
+  if (id < 0) return 0;
+  const int64_t at = (static_cast<int64_t>(id) * a.kv.H + h) * D * CB;
+  double lo[D / 32], hi[D / 32], best = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) lo[i] = load1<C>(a.kv.kmin + at, lane + 32 * i), hi[i] = load1<C>(a.kv.kmax + at, lane + 32 * i);
+  for (int g = 0; g < G; ++g) {
+    const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + g) * a.q.head;
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const double x = load1<X>(q, lane + 32 * i);
+      s = fma(x, x >= 0.0 ? hi[i] : lo[i], s);
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    best = isnan(s) || isnan(best) ? NAN : fmax(best, s);
+  }
+  return key64(best);
+}
+
+template <int X, int C, int D>
+__global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const PagedSelectArgs a) {
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
+  __shared__ PickShared sm;
   const PagedKv& kv = a.kv;
-  constexpr int CB = C == kTypeE4m3 ? 1 : 2;
-  __shared__ int sm[kSelThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / kv.H, h = blockIdx.x % kv.H, G = a.Hq / kv.H;
   const int used = (checked_len(kv, b) + kv.page - 1) / kv.page;
   int* out = a.pages + static_cast<int64_t>(blockIdx.x) * a.n_select;
   if (used <= a.n_select) {
-    for (int i = threadIdx.x; i < a.n_select; i += kSelThreads) out[i] = i < used ? i : -1;
+    for (int i = tid; i < a.n_select; i += kPickThreads) out[i] = i < used ? i : -1;
     return;
   }
-  uint64_t* key = reinterpret_cast<uint64_t*>(a.ws) + static_cast<int64_t>(blockIdx.x) * kv.max_pages;
-  for (int j = threadIdx.x; j < used; j += kSelThreads) {
-    uint64_t k = ~0ull;
-    if (j >= a.keep_first && j < used - a.keep_last) {
-      const int id = checked_page(kv, b, j);
-      k = 0;
-      if (id >= 0) {
-        const int64_t at = (static_cast<int64_t>(id) * kv.H + h) * kv.d * CB;
-        double best = -INFINITY;
-        for (int g = 0; g < G; ++g) {
-          const uint8_t* q = a.q.p + b * a.q.row + (h * G + g) * a.q.head;
-          double s = 0.0;
-          for (int c = 0; c < kv.d; ++c) {
-            const double x = load1<X>(q, c);
-            s = fma(x, x >= 0.0 ? load1<C>(kv.kmax + at, c) : load1<C>(kv.kmin + at, c), s);
-          }
-          best = isnan(s) || isnan(best) ? NAN : fmax(best, s);
+  const SelectScratch sc = scratch_of(a.ws, blockIdx.x, kv.max_pages);
+  float* score = sc.score;
+  const int first = a.keep_first, end = used - a.keep_last;  // the pages that go by their score
+  const int want = a.n_select - a.keep_first - a.keep_last;
+  int turn = 0;
+  float sure = INFINITY;  // pages with this score or more are in
+  if (want > 0) {
+    // Range of the scores and their error.
+    float least = INFINITY, most = -INFINITY, kinf = 0.f, qsum = 0.f;
+    for (int j = first + tid; j < end; j += kPickThreads) least = fminf(least, score[j]), most = fmaxf(most, score[j]);
+    for (int i = tid; i < (used + kScoreChunk - 1) / kScoreChunk; i += kPickThreads) kinf = fmaxf(kinf, sc.kinf[i]);
+    for (int g = warp; g < G; g += kPickThreads / 32) {
+      const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + g) * a.q.head;
+      float s = 0.f;
+      for (int c = lane; c < D; c += 32) s += fabsf(static_cast<float>(load1<X>(q, c)));
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+      qsum = s > qsum || isnan(s) ? s : qsum;
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      least = fminf(least, __shfl_xor_sync(0xffffffffu, least, x));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+      kinf = fmaxf(kinf, __shfl_xor_sync(0xffffffffu, kinf, x));
+    }
+    if (lane == 0) {
+      sm.f[0][warp] = least, sm.f[1][warp] = most;
+      sm.count[0][0][warp] = __float_as_int(kinf), sm.count[0][1][warp] = __float_as_int(qsum);
+    }
+    if (tid == 0) sm.m = 0;
+    __syncthreads();
+    least = sm.f[0][lane], most = sm.f[1][lane];
+    kinf = __int_as_float(sm.count[0][0][lane]), qsum = __int_as_float(sm.count[0][1][lane]);
+    bool odd = isnan(qsum);
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      least = fminf(least, __shfl_xor_sync(0xffffffffu, least, x));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+      kinf = fmaxf(kinf, __shfl_xor_sync(0xffffffffu, kinf, x));
+      qsum = fmaxf(qsum, __shfl_xor_sync(0xffffffffu, qsum, x));
+    }
+    odd = __any_sync(0xffffffffu, odd) || most == INFINITY;
+    float eps = qsum * kinf * 6.2e-5f;  // 2^-14, and the rounding of this product and sum
+    if (odd || !(eps <= 1e37f)) eps = INFINITY;
+    float from = -INFINITY;  // candidates: from <= score < sure
+    if (eps < INFINITY) {
+      // [lo, hi): count(key >= lo) >= want > count(key >= hi); four parts a turn.
+      uint32_t lo = key32(least), hi = key32(most) + 1;
+      while (hi - lo > 1 && of_key32(hi) - of_key32(lo) > eps) {
+        turn ^= 1;
+        const uint32_t quarter = max((hi - lo) / 4, 1u);
+        const uint32_t k1 = lo + quarter, k2 = min(hi - 1, k1 + quarter), k3 = min(hi - 1, k2 + quarter);
+        int3 n = make_int3(0, 0, 0);
+        for (int j = first + tid; j < end; j += kPickThreads) {
+          const uint32_t k = key32(score[j]);
+          n.x += k >= k1, n.y += k >= k2, n.z += k >= k3;
         }
-        k = key64(best);
+        n = block_sum3(n, sm, turn);
+        if (n.z >= want) lo = k3;
+        else if (n.y >= want) lo = k2, hi = k3 > k2 ? k3 : hi;
+        else if (n.x >= want) lo = k1, hi = k2 > k1 ? k2 : hi;
+        else hi = k1;
+      }
+      from = of_key32(lo) - 2.f * eps;
+      sure = of_key32(hi) + 2.f * eps;
+      // rounding of the two sums
+      from -= fabsf(from) * 1e-6f;
+      sure += fabsf(sure) * 1e-6f;
+    }
+    // Pages that are in, and candidates.
+    turn ^= 1;
+    int3 n = make_int3(0, 0, 0);
+    for (int j = first + tid; j < end; j += kPickThreads) {
+      const float s = score[j];
+      const bool in = eps < INFINITY && s >= sure, cand = !in && s >= from;
+      n.x += in, n.y += cand;
+      if (cand) {
+        const int at = atomicAdd(&sm.m, 1);
+        if (at < kPickCap) sm.list[at] = j;
       }
     }
-    key[j] = k;
+    n = block_sum3(n, sm, turn);
+    const int m = n.y, r = want - n.x;  // r of the m candidates are in
+    const bool few = m <= kPickCap;
+    if (m > r) {
+      if (few) {
+        for (int i = warp; i < m; i += kPickThreads / 32) {
+          const uint64_t k = exact_key<X, C, D>(a, b, h, G, sm.list[i]);
+          if (lane == 0) sm.key[i] = k;
+        }
+        __syncthreads();
+        for (int i = tid; i < m; i += kPickThreads) {
+          const uint64_t k = sm.key[i];
+          const int j = sm.list[i];
+          int ahead = 0;
+          for (int y = 0; y < m; ++y) ahead += sm.key[y] > k || (sm.key[y] == k && sm.list[y] < j);
+          score[j] = ahead < r ? INFINITY : -INFINITY;
+        }
+      } else {
+        for (int j = first + warp; j < end; j += kPickThreads / 32) {
+          const float s = score[j];
+          if (s >= from && !(eps < INFINITY && s >= sure)) {
+            const uint64_t k = exact_key<X, C, D>(a, b, h, G, j);
+            if (lane == 0) sc.key[j] = k;
+          }
+        }
+        __syncthreads();
+        // The r-th largest key bit by bit, then equal keys by the r-th lowest page.
+        auto cand = [&](int j) {
+          const float s = score[j];
+          return s >= from && !(eps < INFINITY && s >= sure);
+        };
+        uint64_t border = 0;
+        for (int bit = 63; bit >= 0; --bit) {
+          turn ^= 1;
+          const uint64_t t = border | (1ull << bit);
+          int3 c = make_int3(0, 0, 0);
+          for (int j = first + tid; j < end; j += kPickThreads) c.x += cand(j) && sc.key[j] >= t;
+          if (block_sum3(c, sm, turn).x >= r) border = t;
+        }
+        turn ^= 1;
+        int3 c = make_int3(0, 0, 0);
+        for (int j = first + tid; j < end; j += kPickThreads) c.x += cand(j) && sc.key[j] > border;
+        const int equal = r - block_sum3(c, sm, turn).x;
+        int lo = first, hi = end;  // least j with `equal` pages at the border below it
+        while (lo < hi) {
+          turn ^= 1;
+          const int mid = lo + (hi - lo) / 2;
+          int3 e = make_int3(0, 0, 0);
+          for (int j = first + tid; j < mid; j += kPickThreads) e.x += cand(j) && sc.key[j] == border;
+          if (block_sum3(e, sm, turn).x >= equal) hi = mid;
+          else lo = mid + 1;
+        }
+        for (int j = first + tid; j < end; j += kPickThreads)
+          if (cand(j)) score[j] = sc.key[j] > border || (sc.key[j] == border && j < lo) ? INFINITY : -INFINITY;
+      }
+    } else {
+      for (int j = first + tid; j < end; j += kPickThreads) {
+        const float s = score[j];
+        if (s >= from) score[j] = INFINITY;
+      }
+    }
+    __syncthreads();
   }
+  // Ascending output: a run of pages per thread, places by a scan.
+  const int per = (used + kPickThreads - 1) / kPickThreads;
+  const int j0 = min(used, tid * per), j1 = min(used, j0 + per);
+  auto taken = [&](int j) { return j < first || j >= end || (want > 0 && score[j] >= sure); };
+  int mine = 0;
+  for (int j = j0; j < j1; ++j) mine += taken(j);
+  int upto = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, x);
+    if (lane >= x) upto += y;
+  }
+  turn ^= 1;
+  if (lane == 31) sm.count[turn][0][warp] = upto;
   __syncthreads();
-  // The n-th largest key, bit by bit from the top.
-  uint64_t border = 0;
-  for (int bit = 63; bit >= 0; --bit) {
-    const uint64_t t = border | (1ull << bit);
-    int n = 0;
-    for (int j = threadIdx.x; j < used; j += kSelThreads) n += key[j] >= t;
-    if (block_sum(n, sm) >= a.n_select) border = t;
-  }
-  int above = 0;
-  for (int j = threadIdx.x; j < used; j += kSelThreads) above += key[j] > border;
-  int equal = a.n_select - block_sum(above, sm);  // so many of those at the border, lowest first
-  // Ascending output: pages in chunks of the block, ranks by a scan.
-  int base = 0;
-  for (int j0 = 0; j0 < used; j0 += kSelThreads) {
-    const int j = j0 + threadIdx.x;
-    const uint64_t k = j < used ? key[j] : 0;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const bool eq = j < used && k == border;
-    const uint32_t be = __ballot_sync(0xffffffffu, eq);
-    __syncthreads();
-    if (lane == 0) sm[w] = __popc(be);
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int i = 0; i < kSelThreads / 32; ++i) before += i < w ? sm[i] : 0, total += sm[i];
-    const bool take = j < used && (k > border || (eq && before + __popc(be & ((1u << lane) - 1)) < equal));
-    equal = max(0, equal - total);
-    const uint32_t bt = __ballot_sync(0xffffffffu, take);
-    __syncthreads();
-    if (lane == 0) sm[w] = __popc(bt);
-    __syncthreads();
-    int rank = base;
-    for (int i = 0; i < kSelThreads / 32; ++i) rank += i < w ? sm[i] : 0, base += sm[i];
-    if (take) out[rank + __popc(bt & ((1u << lane) - 1))] = j;
-  }
+  int at = upto - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sm.count[turn][0][lane] : 0);
+  for (int j = j0; j < j1; ++j)
+    if (taken(j)) out[at++] = j;
 }
 
-template <int X, int C>
+template <int X, int C, int D>
 int launch_t(const PagedSelectArgs& a) {
-  return launch_serialized(true, attn_paged_select_kernel<X, C>, dim3(a.kv.B * a.kv.H), dim3(kSelThreads), 0, a.stream,
+  const dim3 grid(score_chunks(a.kv.max_pages), a.kv.B * a.kv.H);
+  auto score = a.Hq / a.kv.H > 8 ? attn_paged_score_kernel<X, C, D, true> : attn_paged_score_kernel<X, C, D, false>;
+  if (launch_serialized(true, score, grid, dim3(32 * kScoreWarps), 0, a.stream, a) != cudaSuccess) return kStatusCuda;
+  return launch_serialized(true, attn_paged_pick_kernel<X, C, D>, dim3(a.kv.B * a.kv.H), dim3(kPickThreads), 0, a.stream,
                            a) == cudaSuccess
              ? kStatusOk
              : kStatusCuda;
 }
 
+template <int X, int C>
+int launch_d(const PagedSelectArgs& a) {
+  switch (a.kv.d) {
+    case 32: return launch_t<X, C, 32>(a);
+    case 64: return launch_t<X, C, 64>(a);
+    default: return launch_t<X, C, 128>(a);
+  }
+}
+
 }  // namespace
 
-int64_t paged_select_workspace(int B, int H, int max_pages) { return static_cast<int64_t>(B) * H * max_pages * 8; }
+int64_t paged_select_workspace(int B, int H, int max_pages) {
+  return static_cast<int64_t>(B) * H * select_scratch_bytes(max_pages);
+}
 
 int launch_paged_select(const PagedSelectArgs& a, int* launches) {
-  *launches = 1;
+  *launches = 2;
   if (a.x_type == kTypeBf16)
-    return a.kv.type == kTypeE4m3 ? launch_t<kTypeBf16, kTypeE4m3>(a) : launch_t<kTypeBf16, kTypeBf16>(a);
-  return a.kv.type == kTypeE4m3 ? launch_t<kTypeF16, kTypeE4m3>(a) : launch_t<kTypeF16, kTypeF16>(a);
+    return a.kv.type == kTypeE4m3 ? launch_d<kTypeBf16, kTypeE4m3>(a) : launch_d<kTypeBf16, kTypeBf16>(a);
+  return a.kv.type == kTypeE4m3 ? launch_d<kTypeF16, kTypeE4m3>(a) : launch_d<kTypeF16, kTypeF16>(a);
 }
 
 }  // namespace attn
