@@ -117,74 +117,6 @@ __device__ __forceinline__ int checked_page(const PagedKv& kv, int b, int j) {
   return id;
 }
 
-// Eight consecutive elements as fp32.
-template <int TYPE>
-__device__ __forceinline__ void load8(const uint8_t* p, float (&f)[8]) {
-  if constexpr (TYPE == kTypeE4m3) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    const uint32_t u[2] = {w.x, w.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2_raw h =
-          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u[i >> 1] >> ((i & 1) * 16)), __NV_E4M3);
-      const float2 x = __half22float2(__half2(h));
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
-    }
-  } else {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 x;
-      if constexpr (TYPE == kTypeBf16)
-        x = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
-      else
-        x = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
-    }
-  }
-}
-
-// Rounds eight fp32 values to the element type (to nearest even; e4m3
-// saturates at +-448 and keeps NaN) and stores them.  f becomes the values
-// as stored.
-template <int TYPE>
-__device__ __forceinline__ void store8(uint8_t* p, float (&f)[8]) {
-  if constexpr (TYPE == kTypeE4m3) {
-    uint32_t u[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_fp8x2_storage_t s =
-          __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-      u[i >> 1] |= static_cast<uint32_t>(s) << ((i & 1) * 16);
-      const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(s, __NV_E4M3)));
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
-    }
-    *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
-  } else {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 x;
-      if constexpr (TYPE == kTypeBf16) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&b);
-        x = __bfloat1622float2(b);
-      } else {
-        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&h);
-        x = __half22float2(h);
-      }
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-  }
-}
-
 // D += A B of m16n8k16: rows are lane / 4 (a0, a2) and that + 8 (a1, a3), fp32 sums.
 template <bool BF16>
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,

@@ -12,7 +12,10 @@
 // positions (a page with summaries, else 8 tokens, which a page boundary never
 // cuts).  A thread owns sixteen channels of one head (an item: the two
 // 8-element chunks that the rotation couples) and walks the unit's tokens, so
-// the minima and maxima stay in its registers and need no exchange.
+// the minima and maxima stay in its registers and need no exchange.  Its next
+// kAppendDepth tokens are in flight as asynchronous copies into a slot of
+// shared memory that only it reads: no barrier, and no registers held while
+// they travel.
 #include <cmath>
 
 #include "attn_paged.h"
@@ -23,7 +26,91 @@ namespace {
 
 constexpr int kAppendThreads = 128;
 constexpr int kAppendSpan = 8;   // tokens of a unit without summaries
-constexpr int kAppendBatch = 4;  // tokens in flight per thread
+constexpr int kAppendDepth = 4;  // tokens in flight per thread
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 load_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// Minima and maxima of pairs in the 16-bit type that holds the stored values
+// exactly (fp16 for e4m3); a NaN gives way to the other operand.
+template <int C>
+__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (C == kTypeBf16) asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int C>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (C == kTypeBf16) asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Stored elements to pairs of that 16-bit type and back (exact).
+template <int C>
+__device__ __forceinline__ void load_pairs(const uint8_t* p, uint32_t (&w)[4]) {
+  if constexpr (C == kTypeE4m3) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = e4m3_pair(v.x), w[1] = e4m3_pair(v.x >> 16), w[2] = e4m3_pair(v.y), w[3] = e4m3_pair(v.y >> 16);
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+}
+template <int C>
+__device__ __forceinline__ void store_pairs(uint8_t* p, const uint32_t (&w)[4]) {
+  if constexpr (C == kTypeE4m3) {
+    uint32_t v[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(unpack2<false>(w[i]), __NV_SATFINITE, __NV_E4M3))
+                   << ((i & 1) * 16);
+    *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// Rounds to the stored type (nearest even; e4m3 saturates at +-448 and keeps
+// NaN) and stores; w becomes the stored values as pairs.
+template <int C>
+__device__ __forceinline__ void round_store(uint8_t* p, const float (&f)[8], uint32_t (&w)[4]) {
+  if constexpr (C == kTypeE4m3) {
+    uint32_t v[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i >> 1] |= static_cast<uint32_t>(
+                       __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3))
+                   << ((i & 1) * 16);
+    *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
+    w[0] = e4m3_pair(v[0]), w[1] = e4m3_pair(v[0] >> 16), w[2] = e4m3_pair(v[1]), w[3] = e4m3_pair(v[1] >> 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<C == kTypeBf16>(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+template <int X>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2<X == kTypeBf16>(w[i]);
+    f[2 * i] = x.x, f[2 * i + 1] = x.y;
+  }
+}
 
 template <int X, int C>
 __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const PagedAppendArgs a, int span) {
@@ -102,85 +189,100 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
   constexpr int CB = C == kTypeE4m3 ? 1 : 2;
   const float inv = 1.f / (kind ? kv.v_scale : kv.k_scale);
 
-  float lo0[8], lo1[8], hi0[8], hi1[8];
+  // Slot of token t: two 16-byte pieces per thread, a warp's pieces side by side.
+  __shared__ __align__(16) uint8_t ring[kAppendDepth * 2 * kAppendThreads * 16];
+  const uint32_t slots = smem_addr(ring) + threadIdx.x * 16;
+  auto fetch = [&](int t) {
+    if (t < n) {
+      const uint32_t at = slots + (t % kAppendDepth) * (2 * kAppendThreads * 16);
+      copy16_async(at, src + t * in.row + c0 * 2);
+      copy16_async(at + kAppendThreads * 16, src + t * in.row + c1 * 2);
+    }
+    copies_commit();
+  };
 #pragma unroll
-  for (int e = 0; e < 8; ++e) lo0[e] = lo1[e] = INFINITY, hi0[e] = hi1[e] = -INFINITY;
+  for (int t = 0; t < kAppendDepth; ++t) fetch(t);
+  const int half = a.rot / 2;
+  const float *cos = a.cos + static_cast<int64_t>(p0) * half + 8 * i, *sin = a.sin + static_cast<int64_t>(p0) * half + 8 * i;
+  float cs[8], sn[8];
+  auto angles = [&](int t) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      *reinterpret_cast<float4*>(cs + e) = __ldg(reinterpret_cast<const float4*>(cos + static_cast<int64_t>(t) * half + e));
+      *reinterpret_cast<float4*>(sn + e) = __ldg(reinterpret_cast<const float4*>(sin + static_cast<int64_t>(t) * half + e));
+    }
+  };
+  if (turn) angles(0);
+  const bool track = kind == 0 && kv.kmin != nullptr;
+  constexpr uint32_t kInf = C == kTypeBf16 ? 0x7f807f80u : 0x7c007c00u;
+  uint32_t lo[2][4], hi[2][4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) lo[0][e] = lo[1][e] = kInf, hi[0][e] = hi[1][e] = kInf | 0x80008000u;
 
-  for (int t0 = 0; t0 < n; t0 += kAppendBatch) {
-    float x[kAppendBatch][8], y[kAppendBatch][8];
+  for (int t = 0; t < n; ++t) {
+    copies_wait<kAppendDepth - 1>();
+    const uint32_t at = slots + (t % kAppendDepth) * (2 * kAppendThreads * 16);
+    float x[8], y[8];
+    unpack8<X>(load_shared16(at), x);
+    unpack8<X>(load_shared16(at + kAppendThreads * 16), y);
+    if (turn) {
+      if (a.interleaved) {
 #pragma unroll
-    for (int t = 0; t < kAppendBatch; ++t)
-      if (t0 + t < n) {
-        load8<X>(src + (t0 + t) * in.row + c0 * 2, x[t]);
-        load8<X>(src + (t0 + t) * in.row + c1 * 2, y[t]);
-      }
-#pragma unroll
-    for (int t = 0; t < kAppendBatch; ++t) {
-      if (t0 + t >= n) break;
-      if (turn) {
-        const int64_t at = static_cast<int64_t>(p0 + t0 + t) * (a.rot / 2) + 8 * i;
-        float cs[8], sn[8];
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          *reinterpret_cast<float4*>(cs + e) = __ldg(reinterpret_cast<const float4*>(a.cos + at + e));
-          *reinterpret_cast<float4*>(sn + e) = __ldg(reinterpret_cast<const float4*>(a.sin + at + e));
+        for (int e = 0; e < 8; ++e) {
+          float* z = e < 4 ? x + 2 * e : y + 2 * (e - 4);
+          const float u = z[0], w = z[1];
+          z[0] = u * cs[e] - w * sn[e];
+          z[1] = w * cs[e] + u * sn[e];
         }
-        if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float* z = e < 4 ? x[t] + 2 * e : y[t] + 2 * (e - 4);
-            const float u = z[0], w = z[1];
-            z[0] = u * cs[e] - w * sn[e];
-            z[1] = w * cs[e] + u * sn[e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float u = x[t][e], w = y[t][e];
-            x[t][e] = u * cs[e] - w * sn[e];
-            y[t][e] = w * cs[e] + u * sn[e];
-          }
-        }
-      }
-      uint8_t* to = dst + (t0 + t) * step;
-      if (kind == 2) {
-        store8<X>(to + c0 * 2, x[t]);
-        store8<X>(to + c1 * 2, y[t]);
       } else {
-        if constexpr (C == kTypeE4m3) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[t][e] *= inv, y[t][e] *= inv;
+        for (int e = 0; e < 8; ++e) {
+          const float u = x[e], w = y[e];
+          x[e] = u * cs[e] - w * sn[e];
+          y[e] = w * cs[e] + u * sn[e];
         }
-        store8<C>(to + c0 * CB, x[t]);
-        store8<C>(to + c1 * CB, y[t]);
-        if (kv.kmin && kind == 0) {
+      }
+      if (t + 1 < n) angles(t + 1);  // on their way while this token is stored
+    }
+    uint8_t* to = dst + t * step;
+    uint32_t w0[4], w1[4];
+    if (kind == 2) {
+      round_store<X>(to + c0 * 2, x, w0);
+      round_store<X>(to + c1 * 2, y, w1);
+    } else {
+      if constexpr (C == kTypeE4m3) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {  // fminf / fmaxf pass over a NaN
-            lo0[e] = fminf(lo0[e], x[t][e]), hi0[e] = fmaxf(hi0[e], x[t][e]);
-            lo1[e] = fminf(lo1[e], y[t][e]), hi1[e] = fmaxf(hi1[e], y[t][e]);
-          }
+        for (int e = 0; e < 8; ++e) x[e] *= inv, y[e] *= inv;
+      }
+      round_store<C>(to + c0 * CB, x, w0);
+      round_store<C>(to + c1 * CB, y, w1);
+      if (track) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          lo[0][e] = min_pair<C>(lo[0][e], w0[e]), hi[0][e] = max_pair<C>(hi[0][e], w0[e]);
+          lo[1][e] = min_pair<C>(lo[1][e], w1[e]), hi[1][e] = max_pair<C>(hi[1][e], w1[e]);
         }
       }
     }
+    fetch(t + kAppendDepth);  // the slot is read
   }
-  if (kv.kmin && kind == 0) {
+  if (track) {
     const int64_t at = (static_cast<int64_t>(id) * kv.H + h) * kv.d;
-    uint8_t *mn = kv.kmin + at * CB, *mx = kv.kmax + at * CB;
-    if (slot0 != 0) {  // earlier tokens of the page
-      float w[8];
-#define ATTN_JOIN(acc, ptr, c, op)         \
-  load8<C>(ptr + (c) * CB, w);             \
-  _Pragma("unroll") for (int e = 0; e < 8; ++e) acc[e] = op(acc[e], w[e]);
-      ATTN_JOIN(lo0, mn, c0, fminf)
-      ATTN_JOIN(lo1, mn, c1, fminf)
-      ATTN_JOIN(hi0, mx, c0, fmaxf)
-      ATTN_JOIN(hi1, mx, c1, fmaxf)
-#undef ATTN_JOIN
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint8_t *mn = kv.kmin + (at + (x ? c1 : c0)) * CB, *mx = kv.kmax + (at + (x ? c1 : c0)) * CB;
+      if (slot0 != 0) {  // earlier tokens of the page
+        uint32_t w[4];
+        load_pairs<C>(mn, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lo[x][e] = min_pair<C>(lo[x][e], w[e]);
+        load_pairs<C>(mx, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hi[x][e] = max_pair<C>(hi[x][e], w[e]);
+      }
+      store_pairs<C>(mn, lo[x]);
+      store_pairs<C>(mx, hi[x]);
     }
-    store8<C>(mn + c0 * CB, lo0);
-    store8<C>(mn + c1 * CB, lo1);
-    store8<C>(mx + c0 * CB, hi0);
-    store8<C>(mx + c1 * CB, hi1);
   }
 }
 
