@@ -9,8 +9,8 @@
 // Nothing is computed to speak of: 3 flops per rotated element against 4 bytes
 // moved, so HBM bounds prompts and the launch bounds single tokens.  Work is
 // cut into units: the tokens of one sequence inside one aligned span of
-// positions (a page with summaries, else 8 tokens, which a page boundary never
-// cuts).  A thread owns sixteen channels of one head (an item: the two
+// positions (a page with summaries, else 8 to 32 tokens, which a page boundary
+// never cuts).  A thread owns sixteen channels of one head (an item: the two
 // 8-element chunks that the rotation couples) and walks the unit's tokens, so
 // the minima and maxima stay in its registers and need no exchange.  Its next
 // kAppendDepth tokens are in flight as asynchronous copies into a slot of
@@ -25,7 +25,7 @@ namespace attn {
 namespace {
 
 constexpr int kAppendThreads = 128;
-constexpr int kAppendSpan = 8;   // tokens of a unit without summaries
+constexpr int kAppendSpan = 32;  // tokens of a unit without summaries, at most
 constexpr int kAppendDepth = 4;  // tokens in flight per thread
 
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
   if (item < k_items) kind = 0, h = item / per_head, i = item % per_head;
   else if (item < 2 * k_items) kind = 1, h = (item - k_items) / per_head, i = item % per_head;
   else if (item < 2 * k_items + a.Hq * per_head) kind = 2, h = (item - 2 * k_items) / per_head, i = item % per_head;
-  else return;
-  const bool turn = kind != 1 && i < a.rot / 16;
+  else kind = 3, h = 0, i = 0;  // only helps its warp to fetch the angles
+  const bool turn = (kind == 0 || kind == 2) && i < a.rot / 16;
   int c0 = 16 * i, c1 = 16 * i + 8;  // first channels of the two chunks
   if (turn && !a.interleaved) c0 = 8 * i, c1 = a.rot / 2 + 8 * i;
 
@@ -189,31 +189,33 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
   constexpr int CB = C == kTypeE4m3 ? 1 : 2;
   const float inv = 1.f / (kind ? kv.v_scale : kv.k_scale);
 
-  // Slot of token t: two 16-byte pieces per thread, a warp's pieces side by side.
-  __shared__ __align__(16) uint8_t ring[kAppendDepth * 2 * kAppendThreads * 16];
+  // Slot of token t: two 16-byte pieces per thread, a warp's pieces side by
+  // side, and the token's rows of cos and sin once per warp (its heads share them).
+  constexpr int kWarps = kAppendThreads / 32, kTable = 512;  // bytes of two table rows at most
+  __shared__ __align__(16) uint8_t ring[kAppendDepth * (2 * kAppendThreads * 16 + kWarps * kTable)];
+  const int lane = threadIdx.x & 31;
   const uint32_t slots = smem_addr(ring) + threadIdx.x * 16;
+  const uint32_t tables = smem_addr(ring) + kAppendDepth * 2 * kAppendThreads * 16 + (threadIdx.x >> 5) * kTable;
+  const int half = a.rot / 2;
+  // Lane l < rot / 4 fetches 16 bytes of a token's angles, cos before sin.
+  const float* angle = lane < half / 4 ? a.cos + lane * 4 : a.sin + (lane * 4 - half);
+  angle += static_cast<int64_t>(p0) * half;
   auto fetch = [&](int t) {
     if (t < n) {
       const uint32_t at = slots + (t % kAppendDepth) * (2 * kAppendThreads * 16);
-      copy16_async(at, src + t * in.row + c0 * 2);
-      copy16_async(at + kAppendThreads * 16, src + t * in.row + c1 * 2);
+      if (kind < 3) {
+        copy16_async(at, src + t * in.row + c0 * 2);
+        copy16_async(at + kAppendThreads * 16, src + t * in.row + c1 * 2);
+      }
+      if (lane < a.rot / 4)
+        copy16_async(tables + (t % kAppendDepth) * (kWarps * kTable) + lane * 16, angle + static_cast<int64_t>(t) * half);
     }
     copies_commit();
   };
 #pragma unroll
   for (int t = 0; t < kAppendDepth; ++t) fetch(t);
-  const int half = a.rot / 2;
-  const float *cos = a.cos + static_cast<int64_t>(p0) * half + 8 * i, *sin = a.sin + static_cast<int64_t>(p0) * half + 8 * i;
-  float cs[8], sn[8];
-  auto angles = [&](int t) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      *reinterpret_cast<float4*>(cs + e) = __ldg(reinterpret_cast<const float4*>(cos + static_cast<int64_t>(t) * half + e));
-      *reinterpret_cast<float4*>(sn + e) = __ldg(reinterpret_cast<const float4*>(sin + static_cast<int64_t>(t) * half + e));
-    }
-  };
-  if (turn) angles(0);
   const bool track = kind == 0 && kv.kmin != nullptr;
+  const bool plain = !turn && !track && (kind == 2 || C == X);
   constexpr uint32_t kInf = C == kTypeBf16 ? 0x7f807f80u : 0x7c007c00u;
   uint32_t lo[2][4], hi[2][4];
 #pragma unroll
@@ -221,10 +223,33 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
 
   for (int t = 0; t < n; ++t) {
     copies_wait<kAppendDepth - 1>();
+    __syncwarp();  // the other lanes' angles too
     const uint32_t at = slots + (t % kAppendDepth) * (2 * kAppendThreads * 16);
+    uint8_t* to = dst + t * step;
+    const uint4 xw = load_shared16(at), yw = load_shared16(at + kAppendThreads * 16);
+    float cs[8], sn[8];
+    if (turn) {
+      const uint32_t tb = tables + (t % kAppendDepth) * (kWarps * kTable) + 32 * i;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint4 u = load_shared16(tb + 16 * e), v = load_shared16(tb + half * 4 + 16 * e);
+        cs[4 * e] = __uint_as_float(u.x), cs[4 * e + 1] = __uint_as_float(u.y);
+        cs[4 * e + 2] = __uint_as_float(u.z), cs[4 * e + 3] = __uint_as_float(u.w);
+        sn[4 * e] = __uint_as_float(v.x), sn[4 * e + 1] = __uint_as_float(v.y);
+        sn[4 * e + 2] = __uint_as_float(v.z), sn[4 * e + 3] = __uint_as_float(v.w);
+      }
+    }
+    __syncwarp();  // every lane has its angles before the slot is fetched into again
+    fetch(t + kAppendDepth);
+    if (kind == 3) continue;
+    if (plain) {  // as it is
+      *reinterpret_cast<uint4*>(to + c0 * 2) = xw;
+      *reinterpret_cast<uint4*>(to + c1 * 2) = yw;
+      continue;
+    }
     float x[8], y[8];
-    unpack8<X>(load_shared16(at), x);
-    unpack8<X>(load_shared16(at + kAppendThreads * 16), y);
+    unpack8<X>(xw, x);
+    unpack8<X>(yw, y);
     if (turn) {
       if (a.interleaved) {
 #pragma unroll
@@ -242,9 +267,7 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
           y[e] = w * cs[e] + u * sn[e];
         }
       }
-      if (t + 1 < n) angles(t + 1);  // on their way while this token is stored
     }
-    uint8_t* to = dst + t * step;
     uint32_t w0[4], w1[4];
     if (kind == 2) {
       round_store<X>(to + c0 * 2, x, w0);
@@ -264,7 +287,6 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
         }
       }
     }
-    fetch(t + kAppendDepth);  // the slot is read
   }
   if (track) {
     const int64_t at = (static_cast<int64_t>(id) * kv.H + h) * kv.d;
@@ -288,10 +310,17 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
 
 template <int X, int C>
 int launch_append_t(const PagedAppendArgs& a) {
-  const int span = a.kv.kmin ? a.kv.page : kAppendSpan;
-  const int64_t units = a.token_start ? a.rows / span + 2 * static_cast<int64_t>(a.kv.B) : a.kv.B;
   const int items = (2 * a.kv.H + a.Hq) * (a.kv.d / 16);
-  const dim3 grid(static_cast<unsigned>(units), (items + kAppendThreads - 1) / kAppendThreads);
+  const int slices = (items + kAppendThreads - 1) / kAppendThreads;
+  int span = a.kv.page;
+  if (!a.kv.kmin) {  // longer walks amortise a unit's start, as long as they leave eight CTAs to an SM
+    span = 8;
+    while (span < kAppendSpan && a.kv.page % (2 * span) == 0 &&
+           static_cast<int64_t>(a.rows / (2 * span)) * slices >= 8 * std::max(1, device_sm_count()))
+      span *= 2;
+  }
+  const int64_t units = a.token_start ? a.rows / span + 2 * static_cast<int64_t>(a.kv.B) : a.kv.B;
+  const dim3 grid(static_cast<unsigned>(units), slices);
   return launch_serialized(true, attn_paged_append_kernel<X, C>, grid, dim3(kAppendThreads), 0, a.stream, a, span) ==
                  cudaSuccess
              ? kStatusOk
