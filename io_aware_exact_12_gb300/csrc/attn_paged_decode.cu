@@ -583,10 +583,13 @@ __global__ void __launch_bounds__(kPdThreads, 2)
 }
 
 // One block per (cut item, query head): joins the parts in the order of the
-// CTAs, so the result does not depend on which finished first.
+// CTAs, so the result does not depend on which finished first.  Every warp
+// works out the weights for itself; groups of D / 4 lanes take parts in turn.
+constexpr int kMergeThreads = 128;
+
 template <int X, int D>
-__global__ void __launch_bounds__(D) attn_paged_merge_kernel(const PagedDecodeArgs a, int RT, const Part* parts,
-                                                             const float* part) {
+__global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const PagedDecodeArgs a, int RT, const Part* parts,
+                                                                         const float* part) {
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
   const Part p = parts[blockIdx.x];
@@ -594,46 +597,53 @@ __global__ void __launch_bounds__(D) attn_paged_merge_kernel(const PagedDecodeAr
   const int G = a.Hq / a.kv.H, r = blockIdx.y;
   const int r0 = (p.hr % RT) * kPdRows;
   if (r >= min(kPdRows, G - r0)) return;
-  const int n = p.last - p.first + 1;
+  const int n = p.last - p.first + 1, lane = threadIdx.x & 31;
   // CTA `first` has the item's beginning in its slot 1, the others theirs in slot 0.
-  const float* base = part + (static_cast<int64_t>(p.first) * 2) * part_floats(D) + r;
-  auto stat = [&](int i, int which) {
-    return base[(i ? static_cast<int64_t>(i) * 2 : 1) * part_floats(D) + kPdRows * (D + which)];
-  };
-  __shared__ float sm_m;
-  __shared__ float sm_f[1024];  // weights of the parts
-  if (threadIdx.x < 32) {
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += 32) m = fmaxf(m, stat(i, 0));
+  const float* base = part + static_cast<int64_t>(p.first) * 2 * part_floats(D);
+  auto at = [&](int i) { return base + (i ? 2 * i : 1) * part_floats(D); };
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, at(i)[kPdRows * D + r]);
 #pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    if (threadIdx.x == 0) sm_m = m;
+  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  float l = 0.f, ls = 0.f;
+  for (int i = lane; i < n; i += 32) {
+    const float* s = at(i) + r;
+    const float f = part_weight(s[kPdRows * D], m);
+    l += f * s[kPdRows * (D + 1)];
+    ls += f * s[kPdRows * (D + 2)];
   }
-  __syncthreads();
-  const float m = sm_m;
-  for (int i = threadIdx.x; i < n; i += D) {
-    const float mi = stat(i, 0);
-    sm_f[i] = part_weight(mi, m);
+#pragma unroll
+  for (int x = 16; x; x >>= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, x);
+    ls += __shfl_xor_sync(0xffffffffu, ls, x);
   }
-  __syncthreads();
-  float l = 0.f, ls = 0.f, o = 0.f;
-  const int c = threadIdx.x;
+  constexpr int LPR = D / 4, GROUPS = kMergeThreads / LPR;
+  const int grp = threadIdx.x / LPR, c4 = threadIdx.x % LPR;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float f = sm_f[i];
-    const float* at = base - r + (i ? static_cast<int64_t>(i) * 2 : 1) * part_floats(D);
-    o += f * at[r * D + c];
-    l += f * at[kPdRows * (D + 1) + r];
-    ls += f * at[kPdRows * (D + 2) + r];
+  for (int i = grp; i < n; i += GROUPS) {
+    const float4 v = *reinterpret_cast<const float4*>(at(i) + r * D + c4 * 4);
+    const float f = part_weight(at(i)[kPdRows * D + r], m);
+    o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
   }
-  o = ls == 0.f ? 0.f : o * (a.kv.v_scale / ls);
-  const int64_t at = static_cast<int64_t>(p.b) * a.Hq + static_cast<int64_t>(p.hr / RT) * G + r0 + r;
-  if constexpr (X == kTypeBf16) reinterpret_cast<__nv_bfloat16*>(a.o)[at * D + c] = __float2bfloat16_rn(o);
-  else reinterpret_cast<__half*>(a.o)[at * D + c] = __float2half_rn(o);
-  if (c == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  __shared__ float4 sm[GROUPS][LPR];
+  sm[grp][c4] = o;
+  __syncthreads();
+  const int64_t out = static_cast<int64_t>(p.b) * a.Hq + static_cast<int64_t>(p.hr / RT) * G + r0 + r;
+  if (grp == 0) {
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) {
+      const float4 v = sm[i][c4];
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const float inv = ls == 0.f ? 0.f : a.kv.v_scale / ls;
+    const float w[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    store_out4<X>(a.o + (out * D + c4 * 4) * 2, w);
+  }
+  if (threadIdx.x == 0) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-constexpr int kMaxCtas = 1024;  // of the decode kernel; the merge kernel keeps a weight for each
+constexpr int kMaxCtas = 1024;  // of the decode kernel
 
 int row_tiles(int Hq, int H) { return (Hq / H + kPdRows - 1) / kPdRows; }
 
@@ -671,7 +681,7 @@ int launch_t(const PagedDecodeArgs& a) {
                         part) != cudaSuccess)
     return kStatusCuda;
   const dim3 grid(by_item ? static_cast<int>(items) : ctas, std::min(kPdRows, a.Hq / a.kv.H));
-  return launch_serialized(true, attn_paged_merge_kernel<X, D>, grid, dim3(D), 0, a.stream, a, RT, parts, part) ==
+  return launch_serialized(true, attn_paged_merge_kernel<X, D>, grid, dim3(kMergeThreads), 0, a.stream, a, RT, parts, part) ==
                  cudaSuccess
              ? kStatusOk
              : kStatusCuda;

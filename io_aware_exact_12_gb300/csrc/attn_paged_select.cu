@@ -20,9 +20,9 @@
 //       cuts 17 aligned terms at 2^-23 of the largest or less, stay below 2^-14.9
 //       of the sum of magnitudes at d = 128.  It brackets the border to [L, H)
 //       with H - L <= eps; pages at H + 2 eps or above are in, those below
-//       L - 2 eps out, and only those between (a few) are scored again in 64
+//       L - 2 eps out, and only those between (a few) are scored again, to 48
 //       bits.  With eps = inf (a sum that overflowed or is NaN) that is all of
-//       them.
+//       them, in fp64.
 #include <cmath>
 
 #include "attn_paged.h"
@@ -31,15 +31,16 @@
 namespace attn {
 namespace {
 
-constexpr int kScoreWarps = 4;
-constexpr int kScorePages = 32;                       // pages of a warp, in groups of 8
-constexpr int kScoreChunk = kScoreWarps * kScorePages;  // pages of a CTA
+constexpr int kScoreWarps = 2;
+constexpr int kScoreThreads = 32 * kScoreWarps;
+constexpr int kScoreDepth = 4;                  // groups of 8 pages in flight per warp
+constexpr int kScoreChunk = 8 * kScoreWarps * 4;  // pages of a CTA, times 1 to 8
 constexpr int kPickThreads = 1024;
 constexpr int kPickCap = 1024;  // candidates kept in shared memory
 
 struct SelectScratch {  // per (sequence, head)
   float* score;         // [max_pages]
-  float* kinf;          // [chunks] largest magnitude in a chunk's summaries
+  float* kinf;          // [chunks] largest magnitude in a CTA's summaries
   uint64_t* key;        // [max_pages] exact scores, used beyond kPickCap candidates
 };
 
@@ -74,11 +75,19 @@ __device__ __forceinline__ float magnitude(uint32_t m) {
   return fmaxf(f.x, f.y);
 }
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // A warp scores 8 pages at a time.  The sum over channels may run in any order,
-// so a thread loads whole 16-byte pieces of its page's summaries and the queries
+// so a thread takes whole 16-byte pieces of its page's summaries and the queries
 // are laid out to match: piece v of thread t4 holds bytes (4 v + t4) VB and on.
+// The pieces of the next groups travel as asynchronous copies into slots of
+// shared memory that only their thread reads.
 template <int X, int C, int D, bool WIDE>  // WIDE: more than 8 query heads
-__global__ void __launch_bounds__(32 * kScoreWarps) attn_paged_score_kernel(const PagedSelectArgs a) {
+__global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const PagedSelectArgs a, int chunk) {
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
   constexpr bool E8 = C == kTypeE4m3;
@@ -88,22 +97,43 @@ __global__ void __launch_bounds__(32 * kScoreWarps) attn_paged_score_kernel(cons
   constexpr int NV = ROW / (4 * VB);
   constexpr int WPV = VB / 4;                      // words of a piece
   constexpr int NS = D / 16;                       // steps of 16 channels
+  constexpr int SLOT = 2 * NV * kScoreThreads * 16;
+  __shared__ __align__(16) uint8_t ring[kScoreDepth * SLOT];
   const PagedKv& kv = a.kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int bh = blockIdx.y, b = bh / kv.H, h = bh % kv.H, G = a.Hq / kv.H;
   const int used = (checked_len(kv, b) + kv.page - 1) / kv.page;
-  if (used <= a.n_select || static_cast<int>(blockIdx.x) * kScoreChunk >= used) return;
+  const int p0 = blockIdx.x * chunk + warp * 8;     // the warp's first page
+  const int p1 = min(used, static_cast<int>(blockIdx.x + 1) * chunk);
+  if (used <= a.n_select || static_cast<int>(blockIdx.x) * chunk >= used) return;
   const SelectScratch sc = scratch_of(a.ws, bh, kv.max_pages);
-  const int p0 = blockIdx.x * kScoreChunk + warp * kScorePages;
+  const int groups = p1 > p0 ? (p1 - p0 + 8 * kScoreWarps - 1) / (8 * kScoreWarps) : 0;
+  const uint32_t slots = smem_addr(ring) + threadIdx.x * 16;
 
-  int id[kScorePages / 8];
-#pragma unroll
-  for (int i = 0; i < kScorePages / 8; ++i) {
-    const int j = p0 + i * 8 + g;
-    id[i] = j < used ? checked_page(kv, b, j) : -1;
-  }
+  auto look_up = [&](int i) {  // page of this lane in the warp's group i
+    const int j = p0 + i * 8 * kScoreWarps + g;
+    return i < groups && j < p1 ? checked_page(kv, b, j) : -1;
+  };
   uint32_t big = 0;
   for (int r0 = 0; r0 < G; r0 += WIDE ? 16 : 8) {
+    int next = look_up(0);
+    uint32_t found = 0;  // bit i % 32: the page of group i exists
+    auto fetch = [&](int i) {
+      if (next >= 0) {
+        const int64_t at = (static_cast<int64_t>(next) * kv.H + h) * ROW + t4 * VB;
+        const uint32_t to = slots + (i % kScoreDepth) * SLOT;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          copy_async<VB>(to + v * (kScoreThreads * 16), kv.kmin + at + v * 4 * VB);
+          copy_async<VB>(to + (NV + v) * (kScoreThreads * 16), kv.kmax + at + v * 4 * VB);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      found = (found & ~(1u << (i & 31))) | ((next >= 0 ? 1u : 0u) << (i & 31));
+      next = look_up(i + 1);
+    };
+#pragma unroll 1
+    for (int i = 0; i < kScoreDepth; ++i) fetch(i);
     // q^+ and q^- of rows g and g + 8 as A fragments.
     uint32_t qp[NS][WIDE ? 4 : 2], qn[NS][WIDE ? 4 : 2];
     float mul[2] = {1.f, 1.f};
@@ -160,22 +190,29 @@ __global__ void __launch_bounds__(32 * kScoreWarps) attn_paged_score_kernel(cons
           qn[s][i * NR + r] = w[s][i] & neg;
         }
     }
-#pragma unroll 2
-    for (int i = 0; i < kScorePages / 8; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < groups; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kScoreDepth - 1) : "memory");
+      const bool there = (found >> (i & 31)) & 1;
       uint32_t lo[NV * WPV], hi[NV * WPV];
-      const int64_t at = (static_cast<int64_t>(max(id[i], 0)) * kv.H + h) * ROW;
+      const uint32_t at = slots + (i % kScoreDepth) * SLOT;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         if constexpr (VB == 16) {
-          const uint4 x = id[i] >= 0 ? *reinterpret_cast<const uint4*>(kv.kmin + at + (v * 4 + t4) * 16) : make_uint4(0, 0, 0, 0);
-          const uint4 y = id[i] >= 0 ? *reinterpret_cast<const uint4*>(kv.kmax + at + (v * 4 + t4) * 16) : make_uint4(0, 0, 0, 0);
-          lo[4 * v] = x.x, lo[4 * v + 1] = x.y, lo[4 * v + 2] = x.z, lo[4 * v + 3] = x.w;
-          hi[4 * v] = y.x, hi[4 * v + 1] = y.y, hi[4 * v + 2] = y.z, hi[4 * v + 3] = y.w;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(lo[4 * v]), "=r"(lo[4 * v + 1]), "=r"(lo[4 * v + 2]),
+                       "=r"(lo[4 * v + 3]) : "r"(at + v * (kScoreThreads * 16)) : "memory");
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(hi[4 * v]), "=r"(hi[4 * v + 1]), "=r"(hi[4 * v + 2]),
+                       "=r"(hi[4 * v + 3]) : "r"(at + (NV + v) * (kScoreThreads * 16)) : "memory");
         } else {
-          const uint2 x = id[i] >= 0 ? *reinterpret_cast<const uint2*>(kv.kmin + at + (v * 4 + t4) * 8) : make_uint2(0, 0);
-          const uint2 y = id[i] >= 0 ? *reinterpret_cast<const uint2*>(kv.kmax + at + (v * 4 + t4) * 8) : make_uint2(0, 0);
-          lo[2 * v] = x.x, lo[2 * v + 1] = x.y, hi[2 * v] = y.x, hi[2 * v + 1] = y.y;
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(lo[2 * v]), "=r"(lo[2 * v + 1])
+                       : "r"(at + v * (kScoreThreads * 16)) : "memory");
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(hi[2 * v]), "=r"(hi[2 * v + 1])
+                       : "r"(at + (NV + v) * (kScoreThreads * 16)) : "memory");
         }
+      }
+      if (!there) {  // what the slot held before
+#pragma unroll
+        for (int v = 0; v < NV * WPV; ++v) lo[v] = hi[v] = 0u;
       }
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -210,14 +247,16 @@ __global__ void __launch_bounds__(32 * kScoreWarps) attn_paged_score_kernel(cons
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int j = p0 + i * 8 + 2 * t4 + x;
-        const int of = __shfl_sync(0xffffffffu, id[i], (2 * t4 + x) * 4);
-        if (g == 0 && j < used) {
-          const float s = of < 0 ? -3.402823466e38f : best[x];  // no page there: last
+        const int j = p0 + i * 8 * kScoreWarps + 2 * t4 + x;
+        const bool of = __shfl_sync(0xffffffffu, there, (2 * t4 + x) * 4);
+        if (g == 0 && j < p1) {
+          const float s = of ? best[x] : -3.402823466e38f;  // no page there: last
           sc.score[j] = r0 ? fmaxf(sc.score[j], s) : s;
         }
       }
+      fetch(i + kScoreDepth);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   float m = magnitude<BF>(big);
 #pragma unroll
@@ -225,7 +264,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) attn_paged_score_kernel(cons
   __shared__ float sm[kScoreWarps];
   if (lane == 0) sm[warp] = m;
   __syncthreads();
-  if (threadIdx.x == 0) sc.kinf[blockIdx.x] = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  if (threadIdx.x == 0) sc.kinf[blockIdx.x] = fmaxf(sm[0], sm[1]);
 }
 
 // --------------------------------------------------------------------- pick
@@ -244,7 +283,7 @@ __device__ __forceinline__ uint32_t key32(float x) {
 __device__ __forceinline__ float of_key32(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
 
 template <int X>
-__device__ __forceinline__ double load1(const uint8_t* p, int i) {
+__device__ __forceinline__ float load1(const uint8_t* p, int i) {
   if constexpr (X == kTypeBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
   else if constexpr (X == kTypeF16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
   else return __half2float(__half(__nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3)));
@@ -272,34 +311,73 @@ __device__ __forceinline__ int3 block_sum3(int3 v, PickShared& sm, int turn) {
                    __reduce_add_sync(0xffffffffu, sm.count[turn][2][lane]));
 }
 
-// The definition, by one warp; every lane gets it.
-template <int X, int C, int D>
+// A sum in two fp32 words, hi + lo with |lo| <= ulp(hi) / 2 (Knuth's and
+// Dekker's error-free sums): 48 bits, as good as 128 terms summed in fp64.
+// The fp64 units have a sixtieth of the fp32 rate: some tens of candidates took
+// 20 us there.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two two_add(Two a, Two b) {
+  const Two h = two_sum(a.hi, b.hi), l = two_sum(a.lo, b.lo);
+  float c = __fadd_rn(h.lo, l.hi);
+  float s = __fadd_rn(h.hi, c);
+  c = __fadd_rn(l.lo, __fsub_rn(c, __fsub_rn(s, h.hi)));
+  const float r = __fadd_rn(s, c);
+  return {r, __fsub_rn(c, __fsub_rn(r, s))};
+}
+
+// The definition, by one warp; every lane gets it.  Products of two 16-bit
+// floats are exact in fp32 (WORDS: none of them near the ends of its range).
+template <int X, int C, int D, bool WORDS>
 __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, int h, int G, int j) {
   constexpr int CB = C == kTypeE4m3 ? 1 : 2;
   const int lane = threadIdx.x & 31;
   const int id = checked_page(a.kv, b, j);
   if (id < 0) return 0;
   const int64_t at = (static_cast<int64_t>(id) * a.kv.H + h) * D * CB;
-  double lo[D / 32], hi[D / 32], best = -INFINITY;
+  float lo[D / 32], hi[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) lo[i] = load1<C>(a.kv.kmin + at, lane + 32 * i), hi[i] = load1<C>(a.kv.kmax + at, lane + 32 * i);
+  double best = -INFINITY;
+  Two top = {-INFINITY, 0.f};
+#pragma unroll 4
   for (int g = 0; g < G; ++g) {
     const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + g) * a.q.head;
-    double s = 0.0;
+    if constexpr (WORDS) {
+      Two s = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const double x = load1<X>(q, lane + 32 * i);
-      s = fma(x, x >= 0.0 ? hi[i] : lo[i], s);
+      for (int i = 0; i < D / 32; ++i) {
+        const float x = load1<X>(q, lane + 32 * i), p = __fmul_rn(x, x >= 0.f ? hi[i] : lo[i]);
+        const Two t = two_sum(s.hi, p);
+        s = {t.hi, __fadd_rn(s.lo, t.lo)};
+      }
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1)
+        s = two_add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, x), __shfl_xor_sync(0xffffffffu, s.lo, x)});
+      if (s.hi > top.hi || (s.hi == top.hi && s.lo > top.lo)) top = s;
+    } else {
+      double s = 0.0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const float x = load1<X>(q, lane + 32 * i);
+        s = fma(static_cast<double>(x), static_cast<double>(x >= 0.f ? hi[i] : lo[i]), s);
+      }
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+      best = isnan(s) || isnan(best) ? NAN : fmax(best, s);
     }
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    best = isnan(s) || isnan(best) ? NAN : fmax(best, s);
   }
+  if constexpr (WORDS) return (static_cast<uint64_t>(key32(top.hi)) << 32) | key32(top.lo);
   return key64(best);
 }
 
 template <int X, int C, int D>
-__global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const PagedSelectArgs a) {
+__global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const PagedSelectArgs a, int chunk) {
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
   __shared__ PickShared sm;
@@ -322,11 +400,11 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
     // Range of the scores and their error.
     float least = INFINITY, most = -INFINITY, kinf = 0.f, qsum = 0.f;
     for (int j = first + tid; j < end; j += kPickThreads) least = fminf(least, score[j]), most = fmaxf(most, score[j]);
-    for (int i = tid; i < (used + kScoreChunk - 1) / kScoreChunk; i += kPickThreads) kinf = fmaxf(kinf, sc.kinf[i]);
+    for (int i = tid; i < (used + chunk - 1) / chunk; i += kPickThreads) kinf = fmaxf(kinf, sc.kinf[i]);
     for (int g = warp; g < G; g += kPickThreads / 32) {
       const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + g) * a.q.head;
       float s = 0.f;
-      for (int c = lane; c < D; c += 32) s += fabsf(static_cast<float>(load1<X>(q, c)));
+      for (int c = lane; c < D; c += 32) s += fabsf(load1<X>(q, c));
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
       qsum = s > qsum || isnan(s) ? s : qsum;
@@ -356,6 +434,9 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
     odd = __any_sync(0xffffffffu, odd) || most == INFINITY;
     float eps = qsum * kinf * 6.2e-5f;  // 2^-14, and the rounding of this product and sum
     if (odd || !(eps <= 1e37f)) eps = INFINITY;
+    // Two-word sums where sums of the scores' magnitude neither overflow nor lose
+    // their last bits below fp32's range.
+    const bool words = eps < INFINITY && eps > 1e-24f;
     float from = -INFINITY;  // candidates: from <= score < sure
     if (eps < INFINITY) {
       // [lo, hi): count(key >= lo) >= want > count(key >= hi); four parts a turn.
@@ -399,7 +480,8 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
     if (m > r) {
       if (few) {
         for (int i = warp; i < m; i += kPickThreads / 32) {
-          const uint64_t k = exact_key<X, C, D>(a, b, h, G, sm.list[i]);
+          const int j = sm.list[i];
+          const uint64_t k = words ? exact_key<X, C, D, true>(a, b, h, G, j) : exact_key<X, C, D, false>(a, b, h, G, j);
           if (lane == 0) sm.key[i] = k;
         }
         __syncthreads();
@@ -414,7 +496,7 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
         for (int j = first + warp; j < end; j += kPickThreads / 32) {
           const float s = score[j];
           if (s >= from && !(eps < INFINITY && s >= sure)) {
-            const uint64_t k = exact_key<X, C, D>(a, b, h, G, j);
+            const uint64_t k = words ? exact_key<X, C, D, true>(a, b, h, G, j) : exact_key<X, C, D, false>(a, b, h, G, j);
             if (lane == 0) sc.key[j] = k;
           }
         }
@@ -478,11 +560,16 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
 
 template <int X, int C, int D>
 int launch_t(const PagedSelectArgs& a) {
-  const dim3 grid(score_chunks(a.kv.max_pages), a.kv.B * a.kv.H);
+  // Long walks amortise a CTA's start, as long as they leave eight CTAs to an SM.
+  int chunk = kScoreChunk;
+  while (chunk < 8 * kScoreChunk && static_cast<int64_t>(a.kv.max_pages / (2 * chunk)) * a.kv.B * a.kv.H >=
+                                        8 * std::max(1, device_sm_count()))
+    chunk *= 2;
+  const dim3 grid((a.kv.max_pages + chunk - 1) / chunk, a.kv.B * a.kv.H);
   auto score = a.Hq / a.kv.H > 8 ? attn_paged_score_kernel<X, C, D, true> : attn_paged_score_kernel<X, C, D, false>;
-  if (launch_serialized(true, score, grid, dim3(32 * kScoreWarps), 0, a.stream, a) != cudaSuccess) return kStatusCuda;
+  if (launch_serialized(true, score, grid, dim3(kScoreThreads), 0, a.stream, a, chunk) != cudaSuccess) return kStatusCuda;
   return launch_serialized(true, attn_paged_pick_kernel<X, C, D>, dim3(a.kv.B * a.kv.H), dim3(kPickThreads), 0, a.stream,
-                           a) == cudaSuccess
+                           a, chunk) == cudaSuccess
              ? kStatusOk
              : kStatusCuda;
 }
