@@ -34,11 +34,12 @@ namespace {
 
 constexpr int kPdWarps = 4;  // consumers
 constexpr int kPdThreads = 32 * (kPdWarps + 1);
-constexpr int kPdRows = 16;  // query heads of an item
+constexpr int kPdRows = 16;  // query heads of an item, at most
 constexpr int kPdRing = 80 * 1024;
 
-template <int C, int D>
+template <int C, int D, int NT>  // NT: groups of 8 query heads
 struct PdCfg {
+  static constexpr int ROWS = 8 * NT;
   static constexpr int CB = C == kTypeE4m3 ? 1 : 2;
   static constexpr int ROW = D * CB;                   // bytes of a cached row
   static constexpr int RBX = ROW < 128 ? ROW : 128;    // bytes of a row in one box (the swizzle's span)
@@ -50,9 +51,9 @@ struct PdCfg {
   // another warp's, had not landed yet would take the phase before for its own.
   static constexpr int STAGES = (kPdRing / (2 * HALF) < 16 ? kPdRing / (2 * HALF) : 16) / kPdWarps * kPdWarps;
   static_assert(STAGES >= kPdWarps && STAGES % kPdWarps == 0, "stages belong to warps");
-  static constexpr int OFF_O = STAGES * 2 * HALF;      // [warps][16][D] fp32
-  static constexpr int OFF_ML = OFF_O + kPdWarps * kPdRows * D * 4;  // [warps][3][16]
-  static constexpr int OFF_BAR = OFF_ML + kPdWarps * 3 * kPdRows * 4;
+  static constexpr int OFF_O = STAGES * 2 * HALF;      // [warps][ROWS][D] fp32
+  static constexpr int OFF_ML = OFF_O + kPdWarps * ROWS * D * 4;  // [warps][3][ROWS]
+  static constexpr int OFF_BAR = OFF_ML + kPdWarps * 3 * ROWS * 4;
   static constexpr int OFF_MASK = OFF_BAR + 2 * STAGES * 8;  // visible keys of a stage
   static constexpr int OFF_SCHED = OFF_MASK + STAGES * 8;
   static constexpr int SMEM = OFF_SCHED + 128;
@@ -62,8 +63,8 @@ struct Part {  // an item that CTA `first` begins and CTA `last` ends
   int b, hr, first, last;
 };
 
-// Floats of one partial result: O [16][D], then m, l and the rounded l [16] each.
-__host__ __device__ constexpr int part_floats(int d) { return kPdRows * (d + 3); }
+// Floats of one partial result: O [rows][D], then m, l and the rounded l [rows] each.
+__host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 3); }
 
 // Weight of a part with maximum m in a join with maximum mm.  Without a maximum
 // the part's sums are 0 (no visible key) or NaN (nothing but NaN logits), and
@@ -89,6 +90,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// Transposes an 8 x 8 matrix of 16-bit elements, two of a row per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
                                             int c3) {
@@ -182,12 +189,12 @@ __device__ __forceinline__ void store_out4(uint8_t* p, const float (&o)[4]) {
       make_uint2(pack2<X == kTypeBf16>(o[0], o[1]), pack2<X == kTypeBf16>(o[2], o[3]));
 }
 
-template <int X, int C, int D>
+template <int X, int C, int D, int NT>
 __global__ void __launch_bounds__(kPdThreads, 2)
     attn_paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                              const PagedDecodeArgs a, int RT, int box_rows, int by_item, Part* parts, float* part) {
-  using F = PdCfg<C, D>;
-  constexpr int TK = F::TK;
+  using F = PdCfg<C, D, NT>;
+  constexpr int TK = F::TK, ROWS = F::ROWS;
   constexpr bool BF = C == kTypeBf16;
   constexpr bool E8 = C == kTypeE4m3;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -309,81 +316,86 @@ __global__ void __launch_bounds__(kPdThreads, 2)
   }
 
   // ------------------------------------------------------------ consumer warps
+  // Both products have the cache as the 16-row operand and the query heads as
+  // the 8 (NT = 2: 16) columns, so that few heads waste little:
+  //   S^T [keys, heads] = K Q^T,  O^T [channels, heads] += V^T P^T.
+  // In fragments: key or channel by g = lane / 4, heads 2 t4 and 2 t4 + 1.
   float* so = reinterpret_cast<float*>(smem + F::OFF_O);
   float* sml = reinterpret_cast<float*>(smem + F::OFF_ML);
   const int g = lane >> 2, t4 = lane & 3, l8 = lane & 7, mi = lane >> 3;
   const int swz = F::RBX == 128 ? l8 : F::RBX == 64 ? l8 >> 1 : l8 >> 2;
+  constexpr int CPB = F::RBX / 16;  // 16-byte chunks of a box row
   const uint32_t ones = BF ? 0x3f803f80u : 0x3c003c00u;
   bool ok = true;
   int i = warp, cur = 0, tile = s.tile;
   long long g0 = s.t0 - tile;  // first tile of the item, counted from the start of all
   while (cur < n && it.tiles > tile) {
     const int end = min(n, cur + it.tiles - tile);
-    const int h = it.hr / RT, r0 = (it.hr % RT) * kPdRows;
-    const int rows = min(kPdRows, G - r0);
+    const int h = it.hr / RT, r0 = (it.hr % RT) * ROWS;
+    const int rows = min(ROWS, G - r0);
     const int64_t head0 = static_cast<int64_t>(h) * G + r0;
-    // The query rows as A fragments.  An e4m3 cache is multiplied in fp16: its
-    // channels are taken in the order in which four bytes lie in a register,
-    // and bf16 queries are scaled by a power of two per row so that the largest
-    // lies in [2^8, 2^9) (what then falls below fp16's normal range is 2^-22 of
-    // it).
-    uint32_t qf[D / 16][4];
-    float mul0 = a.sl2, mul1 = a.sl2;
-    {
-      const uint8_t* q0 = a.q.p + it.b * a.q.row + (head0 + g) * a.q.head;
-      const uint8_t* q1 = q0 + 8 * a.q.head;
-      const bool v0 = g < rows, v1 = g + 8 < rows;
+    // The queries as B fragments, head 8 nt + g.  An e4m3 cache is multiplied in
+    // fp16: its channels are taken in the order in which four bytes lie in a
+    // register, and bf16 queries are scaled by a power of two per head so that
+    // the largest lies in [2^8, 2^9) (what then falls below fp16's normal range
+    // is 2^-22 of it).
+    uint32_t qf[NT][D / 16][2];
+    float mul[NT][2];  // of heads 2 t4 and 2 t4 + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint8_t* q = a.q.p + it.b * a.q.row + (head0 + nt * 8 + g) * a.q.head;
+      const bool live = nt * 8 + g < rows;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         if constexpr (E8) {
-          const uint2 x = v0 ? *reinterpret_cast<const uint2*>(q0 + ks * 32 + t4 * 8) : make_uint2(0u, 0u);
-          const uint2 y = v1 ? *reinterpret_cast<const uint2*>(q1 + ks * 32 + t4 * 8) : make_uint2(0u, 0u);
-          qf[ks][0] = x.x, qf[ks][2] = x.y, qf[ks][1] = y.x, qf[ks][3] = y.y;
+          const uint2 x = live ? *reinterpret_cast<const uint2*>(q + ks * 32 + t4 * 8) : make_uint2(0u, 0u);
+          qf[nt][ks][0] = x.x, qf[nt][ks][1] = x.y;
         } else {
-          qf[ks][0] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + ks * 32 + t4 * 4) : 0u;
-          qf[ks][2] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + ks * 32 + 16 + t4 * 4) : 0u;
-          qf[ks][1] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + ks * 32 + t4 * 4) : 0u;
-          qf[ks][3] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + ks * 32 + 16 + t4 * 4) : 0u;
+          qf[nt][ks][0] = live ? *reinterpret_cast<const uint32_t*>(q + ks * 32 + t4 * 4) : 0u;
+          qf[nt][ks][1] = live ? *reinterpret_cast<const uint32_t*>(q + ks * 32 + 16 + t4 * 4) : 0u;
         }
       }
+      mul[nt][0] = mul[nt][1] = a.sl2;
       if constexpr (E8 && X == kTypeBf16) {
-        float big0 = 0.f, big1 = 0.f;
+        float big = 0.f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 f = unpack2<true>(qf[ks][x]);
-            float& big = (x & 1) ? big1 : big0;
+          for (int x = 0; x < 2; ++x) {
+            const float2 f = unpack2<true>(qf[nt][ks][x]);
             big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
-        float fac[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float big = x ? big1 : big0;
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          // 2^(8 - e) for a largest value of exponent e, within the normal range; 1 for an infinite one
-          const int e = max(20, static_cast<int>(__float_as_uint(big) >> 23));
-          fac[x] = e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
-          (x ? mul1 : mul0) *= e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(e - 8) << 23);
-        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^(8 - e) for a largest value of exponent e, within the normal range; 1 for an infinite one
+        const int e = max(20, static_cast<int>(__float_as_uint(big) >> 23));
+        const float fac = e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
+        const float back = a.sl2 * (e == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(e - 8) << 23));
+        mul[nt][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
+        mul[nt][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 f = unpack2<true>(qf[ks][x]);
-            qf[ks][x] = pack2<false>(f.x * fac[x & 1], f.y * fac[x & 1]);
+          for (int x = 0; x < 2; ++x) {
+            const float2 f = unpack2<true>(qf[nt][ks][x]);
+            qf[nt][ks][x] = pack2<false>(f.x * fac, f.y * fac);
           }
       }
     }
 
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float lr[4] = {0.f, 0.f, 0.f, 0.f};  // sums of the rounded weights
-    float o[D / 8][4];
+    float m[NT][2], l[NT][2];  // maximum and this thread's share of the sum
+    float lr[NT][4];           // sums of the rounded weights
+    float o[NT][D / 16][4];
 #pragma unroll
-    for (int x = 0; x < D / 8; ++x)
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) o[x][y] = 0.f;
+      for (int y = 0; y < 4; ++y) {
+        lr[nt][y] = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) o[nt][x][y] = 0.f;
+      }
+    }
 
     for (; i < end; i += kPdWarps) {
       const int st = i % F::STAGES;
@@ -405,100 +417,120 @@ __global__ void __launch_bounds__(kPdThreads, 2)
         fence_proxy_async_smem();  // before the stage's next load
         __syncwarp();
       }
-      // S = Q K^T
-      float sc[TK / 8][4];
+      // S^T = K Q^T
+      float sc[NT][TK / 16][4];
 #pragma unroll
-      for (int x = 0; x < TK / 8; ++x)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) sc[x][y] = 0.f;
+        for (int x = 0; x < TK / 16; ++x)
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        if constexpr (E8) {
-          const uint32_t at = kb + (mi * 8 + l8) * F::RBX + ((ks ^ swz) << 4);
+          for (int y = 0; y < 4; ++y) sc[nt][x][y] = 0.f;
 #pragma unroll
-          for (int x = 0; x < TK / 32; ++x) {
-            uint32_t r[4];
-            ldsm4(at + x * 32 * F::RBX, r);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) mma16<false>(sc[4 * x + y], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], e4m3_pair(r[y]), e4m3_pair(r[y] >> 16));
-          }
-        } else {
-          const int chunk = ks * 2 + (mi & 1);
-          const uint32_t at = kb + (chunk / (F::RBX / 16)) * TK * F::RBX + ((mi >> 1) * 8 + l8) * F::RBX +
-                              (((chunk % (F::RBX / 16)) ^ swz) << 4);
-#pragma unroll
-          for (int x = 0; x < TK / 16; ++x) {
-            uint32_t r[4];
-            ldsm4(at + x * 16 * F::RBX, r);
-            mma16<BF>(sc[2 * x], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], r[0], r[1]);
-            mma16<BF>(sc[2 * x + 1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], r[2], r[3]);
-          }
-        }
-      }
-      // Online softmax, in units of log2.
-      float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < TK / 8; ++x) {
-        sc[x][0] *= mul0, sc[x][1] *= mul0, sc[x][2] *= mul1, sc[x][3] *= mul1;
-        if (!whole) {
-          const uint32_t two = static_cast<uint32_t>(mask >> (x * 8 + 2 * t4));
-          if (!(two & 1)) sc[x][0] = sc[x][2] = -INFINITY;
-          if (!(two & 2)) sc[x][1] = sc[x][3] = -INFINITY;
-        }
-        x0 = max3f(x0, sc[x][0], sc[x][1]);
-        x1 = max3f(x1, sc[x][2], sc[x][3]);
-      }
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {  // the maximum rises rarely once some tiles are seen
-        const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0), a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
-        m0 = n0, m1 = n1;
-        l0 *= a0, l1 *= a1;
-        lr[0] *= a0, lr[2] *= a1;
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x) o[x][0] *= a0, o[x][1] *= a0, o[x][2] *= a1, o[x][3] *= a1;
-      }
-      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;  // no key yet: weights 0
-      uint32_t pf[TK / 16][4];
-#pragma unroll
-      for (int x = 0; x < TK / 8; ++x) {
-        const float p0 = ex2_approx(sc[x][0] - z0), p1 = ex2_approx(sc[x][1] - z0);
-        const float p2 = ex2_approx(sc[x][2] - z1), p3 = ex2_approx(sc[x][3] - z1);
-        l0 += p0 + p1;
-        l1 += p2 + p3;
-        pf[x >> 1][(x & 1) * 2] = pack2<BF>(p0, p1);
-        pf[x >> 1][(x & 1) * 2 + 1] = pack2<BF>(p2, p3);
-      }
-      // O += P V; the weights that multiply V are rounded to 16 bits, and their
-      // sum (a column of ones) is what O is divided by.
-#pragma unroll
-      for (int kk = 0; kk < TK / 16; ++kk) {
-        mma16<BF>(lr, pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], ones, ones);
-        const uint32_t at = vb + (kk * 16 + (mi & 1) * 8 + l8) * F::RBX;
+      for (int x = 0; x < TK / 16; ++x) {
+        const uint32_t at = kb + (x * 16 + (mi & 1) * 8 + l8) * F::RBX;
         if constexpr (E8) {
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
+          for (int ks = 0; ks < D / 16; ks += 2) {
             uint32_t r[4];
-            ldsm4_t(at + (((2 * x + (mi >> 1)) ^ swz) << 4), r);
+            ldsm4(at + (((ks + (mi >> 1)) ^ swz) << 4), r);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {  // a register holds two channels of two keys
-              mma16<false>(o[4 * x + 2 * y], pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], e4m3_pair(__byte_perm(r[2 * y], 0, 0x4420)),
-                           e4m3_pair(__byte_perm(r[2 * y + 1], 0, 0x4420)));
-              mma16<false>(o[4 * x + 2 * y + 1], pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], e4m3_pair(__byte_perm(r[2 * y], 0, 0x4431)),
-                           e4m3_pair(__byte_perm(r[2 * y + 1], 0, 0x4431)));
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t a0 = e4m3_pair(r[2 * y]), a2 = e4m3_pair(r[2 * y] >> 16);
+              const uint32_t a1 = e4m3_pair(r[2 * y + 1]), a3 = e4m3_pair(r[2 * y + 1] >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16<false>(sc[nt][x], a0, a1, a2, a3, qf[nt][ks + y][0], qf[nt][ks + y][1]);
             }
           }
         } else {
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
-            const int chunk = 2 * x + (mi >> 1);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const int chunk = ks * 2 + (mi >> 1);
             uint32_t r[4];
-            ldsm4_t(at + (chunk / (F::RBX / 16)) * TK * F::RBX + (((chunk % (F::RBX / 16)) ^ swz) << 4), r);
-            mma16<BF>(o[2 * x], pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], r[0], r[1]);
-            mma16<BF>(o[2 * x + 1], pf[kk][0], pf[kk][1], pf[kk][2], pf[kk][3], r[2], r[3]);
+            ldsm4(at + (chunk / CPB) * TK * F::RBX + (((chunk % CPB) ^ swz) << 4), r);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16<BF>(sc[nt][x], r[0], r[1], r[2], r[3], qf[nt][ks][0], qf[nt][ks][1]);
+          }
+        }
+      }
+      // Online softmax, in units of log2.
+      uint32_t pf[NT][TK / 16][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < TK / 16; ++x) {
+          float(&v)[4] = sc[nt][x];
+          v[0] *= mul[nt][0], v[1] *= mul[nt][1], v[2] *= mul[nt][0], v[3] *= mul[nt][1];
+          if (!whole) {
+            const uint32_t two = static_cast<uint32_t>(mask >> (x * 16 + g));
+            if (!(two & 1)) v[0] = v[1] = -INFINITY;
+            if (!(two & 256)) v[2] = v[3] = -INFINITY;
+          }
+          x0 = max3f(x0, v[0], v[2]);
+          x1 = max3f(x1, v[1], v[3]);
+        }
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, y));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, y));
+        }
+        const float n0 = fmaxf(m[nt][0], x0), n1 = fmaxf(m[nt][1], x1);
+        if (__any_sync(0xffffffffu, n0 > m[nt][0] || n1 > m[nt][1])) {  // rare once some tiles are seen
+          const float a0 = m[nt][0] == -INFINITY ? 0.f : ex2_approx(m[nt][0] - n0);
+          const float a1 = m[nt][1] == -INFINITY ? 0.f : ex2_approx(m[nt][1] - n1);
+          m[nt][0] = n0, m[nt][1] = n1;
+          l[nt][0] *= a0, l[nt][1] *= a1;
+          lr[nt][0] *= a0, lr[nt][1] *= a1;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) o[nt][x][0] *= a0, o[nt][x][1] *= a1, o[nt][x][2] *= a0, o[nt][x][3] *= a1;
+        }
+        // No key yet: weights 0.
+        const float z0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], z1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int x = 0; x < TK / 16; ++x) {
+          const float(&v)[4] = sc[nt][x];
+          const float p0 = ex2_approx(v[0] - z0), p1 = ex2_approx(v[1] - z1);
+          const float p2 = ex2_approx(v[2] - z0), p3 = ex2_approx(v[3] - z1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          pf[nt][x][0] = transpose8(pack2<BF>(p0, p1));
+          pf[nt][x][1] = transpose8(pack2<BF>(p2, p3));
+        }
+      }
+      // O^T += V^T P^T; the weights that multiply V are rounded to 16 bits, and
+      // their sum (a row of ones) is what O is divided by.
+#pragma unroll
+      for (int kk = 0; kk < TK / 16; ++kk) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16<BF>(lr[nt], ones, ones, ones, ones, pf[nt][kk][0], pf[nt][kk][1]);
+        if constexpr (E8) {
+          const uint32_t at = vb + (kk * 16 + (mi & 1) * 8 + l8) * F::RBX;
+#pragma unroll
+          for (int x = 0; x < D / 16; x += 2) {
+            uint32_t r[4];
+            ldsm4_t(at + (((x + (mi >> 1)) ^ swz) << 4), r);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {  // two channels of two keys each: rows g and g + 8 are channels 2 g and 2 g + 1
+              const uint32_t a0 = e4m3_pair(__byte_perm(r[2 * y], 0, 0x4420)), a1 = e4m3_pair(__byte_perm(r[2 * y], 0, 0x4431));
+              const uint32_t a2 = e4m3_pair(__byte_perm(r[2 * y + 1], 0, 0x4420));
+              const uint32_t a3 = e4m3_pair(__byte_perm(r[2 * y + 1], 0, 0x4431));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16<false>(o[nt][x + y], a0, a1, a2, a3, pf[nt][kk][0], pf[nt][kk][1]);
+            }
+          }
+        } else {
+          const uint32_t at = vb + (kk * 16 + (mi >> 1) * 8 + l8) * F::RBX;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const int chunk = 2 * x + (mi & 1);
+            uint32_t r[4];
+            ldsm4_t(at + (chunk / CPB) * TK * F::RBX + (((chunk % CPB) ^ swz) << 4), r);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16<BF>(o[nt][x], r[0], r[1], r[2], r[3], pf[nt][kk][0], pf[nt][kk][1]);
           }
         }
       }
@@ -507,50 +539,50 @@ __global__ void __launch_bounds__(kPdThreads, 2)
     }
 
     // The item's end in this CTA: merge the four warps.  Columns are swizzled by
-    // the row, so that the fragments' stores meet no bank twice.
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    float* ml = sml + warp * 3 * kPdRows;
-    if (t4 == 0) {
-      ml[g] = m0, ml[kPdRows + g] = l0, ml[2 * kPdRows + g] = lr[0];
-      ml[g + 8] = m1, ml[kPdRows + g + 8] = l1, ml[2 * kPdRows + g + 8] = lr[2];
-    }
-    {
-      float* w0 = so + (warp * kPdRows + g) * D;
-      float* w1 = w0 + 8 * D;
-      const int sw = (g & 3) << 3;
+    // the head, so that the fragments' stores meet no bank twice.
+    float* ml = sml + warp * 3 * ROWS;
 #pragma unroll
-      for (int x = 0; x < (E8 ? D / 16 : D / 8); ++x) {
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int y = 4; y < 32; y <<= 1) {
+        l[nt][0] += __shfl_xor_sync(0xffffffffu, l[nt][0], y);
+        l[nt][1] += __shfl_xor_sync(0xffffffffu, l[nt][1], y);
+      }
+      if (g < 2) {
+        const int r = nt * 8 + 2 * t4 + g;
+        ml[r] = m[nt][g], ml[ROWS + r] = l[nt][g], ml[2 * ROWS + r] = lr[nt][g];
+      }
+      float* w0 = so + (warp * ROWS + nt * 8 + 2 * t4) * D;  // heads 2 t4 and 2 t4 + 1
+      const int sw = t4 << 3;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const float(&v)[4] = o[nt][x];
         if constexpr (E8) {
-          const int col = (x * 16 + t4 * 4) ^ sw;
-          *reinterpret_cast<float4*>(w0 + col) = make_float4(o[2 * x][0], o[2 * x + 1][0], o[2 * x][1], o[2 * x + 1][1]);
-          if (rows > 8)
-            *reinterpret_cast<float4*>(w1 + col) = make_float4(o[2 * x][2], o[2 * x + 1][2], o[2 * x][3], o[2 * x + 1][3]);
+          const int col = (x * 16 + 2 * g) ^ sw;
+          *reinterpret_cast<float2*>(w0 + col) = make_float2(v[0], v[2]);
+          *reinterpret_cast<float2*>(w0 + D + col) = make_float2(v[1], v[3]);
         } else {
-          const int col = (x * 8 + t4 * 2) ^ sw;
-          *reinterpret_cast<float2*>(w0 + col) = make_float2(o[x][0], o[x][1]);
-          if (rows > 8) *reinterpret_cast<float2*>(w1 + col) = make_float2(o[x][2], o[x][3]);
+          const int c0 = (x * 16 + g) ^ sw, c1 = (x * 16 + 8 + g) ^ sw;
+          w0[c0] = v[0], w0[D + c0] = v[1], w0[c1] = v[2], w0[D + c1] = v[3];
         }
       }
     }
     consumer_sync();
     const bool begins = tile == 0, ends = end - cur == it.tiles - tile;
     const bool direct = begins && ends;
-    float* out = part + (static_cast<int64_t>(c) * 2 + (begins ? 1 : 0)) * part_floats(D);
+    float* out = part + (static_cast<int64_t>(c) * 2 + (begins ? 1 : 0)) * part_floats(D, ROWS);
     for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kPdWarps) {
       const int r = x / (D / 4), col = (x % (D / 4)) * 4;
       float mw[kPdWarps], mm = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kPdWarps; ++w) mm = fmaxf(mm, mw[w] = sml[w * 3 * kPdRows + r]);
-      float l = 0.f, ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < kPdWarps; ++w) mm = fmaxf(mm, mw[w] = sml[w * 3 * ROWS + r]);
+      float ll = 0.f, ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kPdWarps; ++w) {
         const float f = part_weight(mw[w], mm);
-        l += f * sml[w * 3 * kPdRows + kPdRows + r];
-        ls += f * sml[w * 3 * kPdRows + 2 * kPdRows + r];
-        const float4 v = *reinterpret_cast<const float4*>(so + (w * kPdRows + r) * D + (col ^ ((r & 3) << 3)));
+        ll += f * sml[w * 3 * ROWS + ROWS + r];
+        ls += f * sml[w * 3 * ROWS + 2 * ROWS + r];
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * D + (col ^ (((r >> 1) & 3) << 3)));
         acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
       }
       if (direct) {
@@ -559,13 +591,13 @@ __global__ void __launch_bounds__(kPdThreads, 2)
         for (int y = 0; y < 4; ++y) acc[y] *= inv;
         const int64_t at = static_cast<int64_t>(it.b) * a.Hq + head0 + r;
         store_out4<X>(a.o + (at * D + col) * 2, acc);
-        if (col == 0) a.lse[at] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+        if (col == 0) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
       } else {
         *reinterpret_cast<float4*>(out + r * D + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (col == 0) {
-          out[kPdRows * D + r] = mm;
-          out[kPdRows * (D + 1) + r] = l;
-          out[kPdRows * (D + 2) + r] = ls;
+          out[ROWS * D + r] = mm;
+          out[ROWS * (D + 1) + r] = ll;
+          out[ROWS * (D + 2) + r] = ls;
         }
       }
     }
@@ -588,29 +620,29 @@ __global__ void __launch_bounds__(kPdThreads, 2)
 constexpr int kMergeThreads = 128;
 
 template <int X, int D>
-__global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const PagedDecodeArgs a, int RT, const Part* parts,
-                                                                         const float* part) {
+__global__ void __launch_bounds__(kMergeThreads)
+    attn_paged_merge_kernel(const PagedDecodeArgs a, int RT, int ROWS, const Part* parts, const float* part) {
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
   const Part p = parts[blockIdx.x];
   if (p.last < 0) return;
   const int G = a.Hq / a.kv.H, r = blockIdx.y;
-  const int r0 = (p.hr % RT) * kPdRows;
-  if (r >= min(kPdRows, G - r0)) return;
+  const int r0 = (p.hr % RT) * ROWS;
+  if (r >= min(ROWS, G - r0)) return;
   const int n = p.last - p.first + 1, lane = threadIdx.x & 31;
   // CTA `first` has the item's beginning in its slot 1, the others theirs in slot 0.
-  const float* base = part + static_cast<int64_t>(p.first) * 2 * part_floats(D);
-  auto at = [&](int i) { return base + (i ? 2 * i : 1) * part_floats(D); };
+  const float* base = part + static_cast<int64_t>(p.first) * 2 * part_floats(D, ROWS);
+  auto at = [&](int i) { return base + (i ? 2 * i : 1) * part_floats(D, ROWS); };
   float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, at(i)[kPdRows * D + r]);
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, at(i)[ROWS * D + r]);
 #pragma unroll
   for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   float l = 0.f, ls = 0.f;
   for (int i = lane; i < n; i += 32) {
     const float* s = at(i) + r;
-    const float f = part_weight(s[kPdRows * D], m);
-    l += f * s[kPdRows * (D + 1)];
-    ls += f * s[kPdRows * (D + 2)];
+    const float f = part_weight(s[ROWS * D], m);
+    l += f * s[ROWS * (D + 1)];
+    ls += f * s[ROWS * (D + 2)];
   }
 #pragma unroll
   for (int x = 16; x; x >>= 1) {
@@ -623,7 +655,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const P
 #pragma unroll 4
   for (int i = grp; i < n; i += GROUPS) {
     const float4 v = *reinterpret_cast<const float4*>(at(i) + r * D + c4 * 4);
-    const float f = part_weight(at(i)[kPdRows * D + r], m);
+    const float f = part_weight(at(i)[ROWS * D + r], m);
     o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
   }
   __shared__ float4 sm[GROUPS][LPR];
@@ -647,14 +679,14 @@ constexpr int kMaxCtas = 1024;  // of the decode kernel
 
 int row_tiles(int Hq, int H) { return (Hq / H + kPdRows - 1) / kPdRows; }
 
-template <int X, int C, int D>
+template <int X, int C, int D, int NT>
 int launch_t(const PagedDecodeArgs& a) {
-  using F = PdCfg<C, D>;
+  using F = PdCfg<C, D, NT>;
   static_assert(F::SMEM <= 115712, "two CTAs per SM");
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kStatusCuda;
-  auto kern = attn_paged_decode_kernel<X, C, D>;
+  auto kern = attn_paged_decode_kernel<X, C, D, NT>;
   if (!((ready.load() >> dev) & 1)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM) != cudaSuccess) return kStatusCuda;
     ready.fetch_or(1ull << dev);
@@ -680,8 +712,9 @@ int launch_t(const PagedDecodeArgs& a) {
   if (launch_serialized(true, kern, dim3(ctas), dim3(kPdThreads), F::SMEM, a.stream, mk, mv, a, RT, box, by_item, parts,
                         part) != cudaSuccess)
     return kStatusCuda;
-  const dim3 grid(by_item ? static_cast<int>(items) : ctas, std::min(kPdRows, a.Hq / a.kv.H));
-  return launch_serialized(true, attn_paged_merge_kernel<X, D>, grid, dim3(kMergeThreads), 0, a.stream, a, RT, parts, part) ==
+  const dim3 grid(by_item ? static_cast<int>(items) : ctas, std::min(F::ROWS, a.Hq / a.kv.H));
+  return launch_serialized(true, attn_paged_merge_kernel<X, D>, grid, dim3(kMergeThreads), 0, a.stream, a, RT, F::ROWS,
+                           parts, part) ==
                  cudaSuccess
              ? kStatusOk
              : kStatusCuda;
@@ -689,10 +722,11 @@ int launch_t(const PagedDecodeArgs& a) {
 
 template <int X, int C>
 int launch_d(const PagedDecodeArgs& a) {
+  const bool wide = a.Hq / a.kv.H > 8;
   switch (a.kv.d) {
-    case 32: return launch_t<X, C, 32>(a);
-    case 64: return launch_t<X, C, 64>(a);
-    default: return launch_t<X, C, 128>(a);
+    case 32: return wide ? launch_t<X, C, 32, 2>(a) : launch_t<X, C, 32, 1>(a);
+    case 64: return wide ? launch_t<X, C, 64, 2>(a) : launch_t<X, C, 64, 1>(a);
+    default: return wide ? launch_t<X, C, 128, 2>(a) : launch_t<X, C, 128, 1>(a);
   }
 }
 
@@ -704,7 +738,7 @@ int64_t paged_decode_workspace(int B, int Hq, int H, int d, int page, int n_page
   const int64_t items = static_cast<int64_t>(B) * H * row_tiles(Hq, H);
   const int64_t most = items * ((static_cast<int64_t>(n_pages) * page + 31) / 32);
   const int64_t ctas = std::min<int64_t>(kMaxCtas, (most + kPdWarps - 1) / kPdWarps);
-  return kMaxCtas * static_cast<int64_t>(sizeof(Part)) + ctas * 2 * part_floats(d) * 4;
+  return kMaxCtas * static_cast<int64_t>(sizeof(Part)) + ctas * 2 * part_floats(d, kPdRows) * 4;
 }
 
 int launch_paged_decode(const PagedDecodeArgs& a, int* launches) {
