@@ -16,13 +16,12 @@
 //       channels with fp32 sums (m16n8k16, the queries as rows; e4m3 summaries
 //       widened to fp16).  Reads 2 d elements per page and head once: HBM bound.
 //   attn_paged_pick_kernel : one CTA per (sequence, KV head).  A score s errs by
-//       at most eps = 2^-14 max_g |q_g|_1 max |k|: 2 d / 16 steps, each of which
-//       cuts 17 aligned terms at 2^-23 of the largest or less, stay below 2^-14.9
-//       of the sum of magnitudes at d = 128.  It brackets the border to [L, H)
-//       with H - L <= eps; pages at H + 2 eps or above are in, those below
-//       L - 2 eps out, and only those between (a few) are scored again, to 48
-//       bits.  With eps = inf (a sum that overflowed or is NaN) that is all of
-//       them, in fp64.
+//       at most eps = 2.125 d 2^-23 max_g |q_g|_1 max |k|: each of the 2 d / 16
+//       steps cuts 17 aligned terms at 2^-23 of the largest or less.  A histogram
+//       brackets the border to [L, H) with H - L <= 4 eps; pages at H + 2 eps or
+//       above are in, those below L - 2 eps out, and only those between (a few)
+//       are scored again, to 48 bits.  With eps = inf (a sum that overflowed or is
+//       NaN) that is all of them, in fp64.
 #include <cmath>
 
 #include "attn_paged.h"
@@ -40,7 +39,7 @@ constexpr int kPickCap = 1024;  // candidates kept in shared memory
 
 struct SelectScratch {  // per (sequence, head)
   float* score;         // [max_pages]
-  float* kinf;          // [chunks] largest magnitude in a CTA's summaries
+  float* eps;           // [chunks] error of a score CTA's scores
   uint64_t* key;        // [max_pages] exact scores, used beyond kPickCap candidates
 };
 
@@ -54,7 +53,7 @@ __device__ __forceinline__ SelectScratch scratch_of(uint8_t* ws, int64_t bh, int
   uint8_t* p = ws + bh * select_scratch_bytes(max_pages);
   SelectScratch s;
   s.score = reinterpret_cast<float*>(p);
-  s.kinf = reinterpret_cast<float*>(p + up16(int64_t{4} * max_pages));
+  s.eps = reinterpret_cast<float*>(p + up16(int64_t{4} * max_pages));
   s.key = reinterpret_cast<uint64_t*>(p + up16(int64_t{4} * max_pages) + up16(int64_t{4} * score_chunks(max_pages)));
   return s;
 }
@@ -101,26 +100,32 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
   __shared__ __align__(16) uint8_t ring[kScoreDepth * SLOT];
   const PagedKv& kv = a.kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const int bh = blockIdx.y, b = bh / kv.H, h = bh % kv.H, G = a.Hq / kv.H;
+  // Heads in turn, so that a page's summaries, side by side in memory, are read
+  // at about the same time.
+  const int b = blockIdx.y, h = blockIdx.x % kv.H, part = blockIdx.x / kv.H, G = a.Hq / kv.H;
   const int used = (checked_len(kv, b) + kv.page - 1) / kv.page;
-  const int p0 = blockIdx.x * chunk + warp * 8;     // the warp's first page
-  const int p1 = min(used, static_cast<int>(blockIdx.x + 1) * chunk);
-  if (used <= a.n_select || static_cast<int>(blockIdx.x) * chunk >= used) return;
-  const SelectScratch sc = scratch_of(a.ws, bh, kv.max_pages);
+  const int p0 = part * chunk + warp * 8;           // the warp's first page
+  const int p1 = min(used, (part + 1) * chunk);
+  if (used <= a.n_select || part * chunk >= used) return;
+  const SelectScratch sc = scratch_of(a.ws, static_cast<int64_t>(b) * kv.H + h, kv.max_pages);
   const int groups = p1 > p0 ? (p1 - p0 + 8 * kScoreWarps - 1) / (8 * kScoreWarps) : 0;
   const uint32_t slots = smem_addr(ring) + threadIdx.x * 16;
 
-  auto look_up = [&](int i) {  // page of this lane in the warp's group i
-    const int j = p0 + i * 8 * kScoreWarps + g;
-    return i < groups && j < p1 ? checked_page(kv, b, j) : -1;
+  // Page numbers of four groups in one load: lane (g, t4) has page g of group i + t4.
+  static_assert(kScoreDepth == 4, "a batch of page numbers is as long as the ring");
+  auto look_up = [&](int i) {
+    const int j = p0 + (i + t4) * 8 * kScoreWarps + g;
+    return j < p1 ? checked_page(kv, b, j) : -1;
   };
   uint32_t big = 0;
+  float qmost = 0.f;  // largest |q|_1
   for (int r0 = 0; r0 < G; r0 += WIDE ? 16 : 8) {
-    int next = look_up(0);
+    int ids = look_up(0), more = look_up(4);
     uint32_t found = 0;  // bit i % 32: the page of group i exists
     auto fetch = [&](int i) {
-      if (next >= 0) {
-        const int64_t at = (static_cast<int64_t>(next) * kv.H + h) * ROW + t4 * VB;
+      const int id = __shfl_sync(0xffffffffu, ids, (lane & ~3) | (i & 3));
+      if (id >= 0) {
+        const int64_t at = (static_cast<int64_t>(id) * kv.H + h) * ROW + t4 * VB;
         const uint32_t to = slots + (i % kScoreDepth) * SLOT;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -129,8 +134,11 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      found = (found & ~(1u << (i & 31))) | ((next >= 0 ? 1u : 0u) << (i & 31));
-      next = look_up(i + 1);
+      found = (found & ~(1u << (i & 31))) | ((id >= 0 ? 1u : 0u) << (i & 31));
+      if ((i & 3) == 3) {
+        ids = more;
+        more = look_up(i + 5);
+      }
     };
 #pragma unroll 1
     for (int i = 0; i < kScoreDepth; ++i) fetch(i);
@@ -181,14 +189,21 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
             w[(v * WPV + i) / 2][(v * WPV + i) % 2] =
                 live ? *reinterpret_cast<const uint32_t*>(q + (v * 4 + t4) * VB + i * 4) : 0u;
       }
+      float sum = 0.f;
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          const float2 f = unpack2<BF>(w[s][i]);
+          sum += fabsf(f.x) + fabsf(f.y);
           const uint32_t neg = negative_halves(w[s][i]);
           qp[s][i * NR + r] = w[s][i] & ~neg;
           qn[s][i * NR + r] = w[s][i] & neg;
         }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum *= mul[r];
+      qmost = sum <= qmost ? qmost : sum;  // a NaN stays
     }
 #pragma unroll 1
     for (int i = 0; i < groups; ++i) {
@@ -261,10 +276,16 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
   float m = magnitude<BF>(big);
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const bool odd = __any_sync(0xffffffffu, isnan(qmost));
+#pragma unroll
+  for (int x = 4; x < 32; x <<= 1) qmost = fmaxf(qmost, __shfl_xor_sync(0xffffffffu, qmost, x));
   __shared__ float sm[kScoreWarps];
   if (lane == 0) sm[warp] = m;
   __syncthreads();
-  if (threadIdx.x == 0) sc.kinf[blockIdx.x] = fmaxf(sm[0], sm[1]);
+  if (threadIdx.x == 0) {
+    const float eps = D * 2.6e-7f * qmost * fmaxf(sm[0], sm[1]);  // 2.125 d 2^-23, and the rounding of sum and product
+    sc.eps[part] = odd || !(eps <= 1e37f) ? INFINITY : eps;
+  }
 }
 
 // --------------------------------------------------------------------- pick
@@ -290,25 +311,22 @@ __device__ __forceinline__ float load1(const uint8_t* p, int i) {
 }
 
 struct PickShared {
-  int count[2][3][32];
-  float f[2][32];
+  int count[2][32];
+  float f[3][32];
+  int hist[kPickThreads];
   int list[kPickCap];
   uint64_t key[kPickCap];
-  int m;
+  int m, bin;
 };
 
-// Sums over the block of up to three values, for every thread; `turn` alternates
-// so that one barrier per sum is enough.
-__device__ __forceinline__ int3 block_sum3(int3 v, PickShared& sm, int turn) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  v.x = __reduce_add_sync(0xffffffffu, v.x);
-  v.y = __reduce_add_sync(0xffffffffu, v.y);
-  v.z = __reduce_add_sync(0xffffffffu, v.z);
-  if (lane == 0) sm.count[turn][0][w] = v.x, sm.count[turn][1][w] = v.y, sm.count[turn][2][w] = v.z;
+// Sum over the block, for every thread; `turn` alternates so that one barrier
+// per sum is enough.
+__device__ __forceinline__ int block_sum(int v, PickShared& sm, int turn) {
+  const int lane = threadIdx.x & 31;
+  v = __reduce_add_sync(0xffffffffu, v);
+  if (lane == 0) sm.count[turn][threadIdx.x >> 5] = v;
   __syncthreads();
-  return make_int3(__reduce_add_sync(0xffffffffu, sm.count[turn][0][lane]),
-                   __reduce_add_sync(0xffffffffu, sm.count[turn][1][lane]),
-                   __reduce_add_sync(0xffffffffu, sm.count[turn][2][lane]));
+  return __reduce_add_sync(0xffffffffu, sm.count[turn][lane]);
 }
 
 // A sum in two fp32 words, hi + lo with |lo| <= ulp(hi) / 2 (Knuth's and
@@ -331,45 +349,55 @@ __device__ __forceinline__ Two two_add(Two a, Two b) {
   return {r, __fsub_rn(c, __fsub_rn(r, s))};
 }
 
-// The definition, by one warp; every lane gets it.  Products of two 16-bit
-// floats are exact in fp32 (WORDS: none of them near the ends of its range).
+// The definition, by one warp; every lane gets it.  Eight lanes take a head,
+// four heads at a time.  Products of two 16-bit floats are exact in fp32
+// (WORDS: none of them near the ends of its range).
 template <int X, int C, int D, bool WORDS>
 __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, int h, int G, int j) {
   constexpr int CB = C == kTypeE4m3 ? 1 : 2;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, c0 = (lane & 7) * (D / 8);
   const int id = checked_page(a.kv, b, j);
   if (id < 0) return 0;
   const int64_t at = (static_cast<int64_t>(id) * a.kv.H + h) * D * CB;
-  float lo[D / 32], hi[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) lo[i] = load1<C>(a.kv.kmin + at, lane + 32 * i), hi[i] = load1<C>(a.kv.kmax + at, lane + 32 * i);
   double best = -INFINITY;
   Two top = {-INFINITY, 0.f};
-#pragma unroll 4
-  for (int g = 0; g < G; ++g) {
+  for (int g0 = 0; g0 < G; g0 += 4) {
+    const int g = min(g0 + (lane >> 3), G - 1);  // the last head again where there is none
     const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + g) * a.q.head;
-    if constexpr (WORDS) {
-      Two s = {0.f, 0.f};
+    Two s = {0.f, 0.f};
+    double d = 0.0;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const float x = load1<X>(q, lane + 32 * i), p = __fmul_rn(x, x >= 0.f ? hi[i] : lo[i]);
-        const Two t = two_sum(s.hi, p);
+    for (int i = 0; i < D / 8; ++i) {
+      const float x = load1<X>(q, c0 + i);
+      const float k = x >= 0.f ? load1<C>(a.kv.kmax + at, c0 + i) : load1<C>(a.kv.kmin + at, c0 + i);
+      if constexpr (WORDS) {
+        const Two t = two_sum(s.hi, __fmul_rn(x, k));
         s = {t.hi, __fadd_rn(s.lo, t.lo)};
+      } else {
+        d = fma(static_cast<double>(x), static_cast<double>(k), d);
       }
+    }
 #pragma unroll
-      for (int x = 1; x < 32; x <<= 1)
+    for (int x = 1; x < 8; x <<= 1) {
+      if constexpr (WORDS)
         s = two_add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, x), __shfl_xor_sync(0xffffffffu, s.lo, x)});
+      else
+        d += __shfl_xor_sync(0xffffffffu, d, x);
+    }
+    if constexpr (WORDS) {
       if (s.hi > top.hi || (s.hi == top.hi && s.lo > top.lo)) top = s;
     } else {
-      double s = 0.0;
+      best = isnan(d) || isnan(best) ? NAN : fmax(best, d);
+    }
+  }
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const float x = load1<X>(q, lane + 32 * i);
-        s = fma(static_cast<double>(x), static_cast<double>(x >= 0.f ? hi[i] : lo[i]), s);
-      }
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      best = isnan(s) || isnan(best) ? NAN : fmax(best, s);
+  for (int x = 8; x < 32; x <<= 1) {
+    if constexpr (WORDS) {
+      const Two s = {__shfl_xor_sync(0xffffffffu, top.hi, x), __shfl_xor_sync(0xffffffffu, top.lo, x)};
+      if (s.hi > top.hi || (s.hi == top.hi && s.lo > top.lo)) top = s;
+    } else {
+      const double d = __shfl_xor_sync(0xffffffffu, best, x);
+      best = isnan(d) || isnan(best) ? NAN : fmax(best, d);
     }
   }
   if constexpr (WORDS) return (static_cast<uint64_t>(key32(top.hi)) << 32) | key32(top.lo);
@@ -397,85 +425,93 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
   int turn = 0;
   float sure = INFINITY;  // pages with this score or more are in
   if (want > 0) {
-    // Range of the scores and their error.
-    float least = INFINITY, most = -INFINITY, kinf = 0.f, qsum = 0.f;
-    for (int j = first + tid; j < end; j += kPickThreads) least = fminf(least, score[j]), most = fmaxf(most, score[j]);
-    for (int i = tid; i < (used + chunk - 1) / chunk; i += kPickThreads) kinf = fmaxf(kinf, sc.kinf[i]);
-    for (int g = warp; g < G; g += kPickThreads / 32) {
-      const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + g) * a.q.head;
-      float s = 0.f;
-      for (int c = lane; c < D; c += 32) s += fabsf(load1<X>(q, c));
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      qsum = s > qsum || isnan(s) ? s : qsum;
+    // Range of the scores and their error.  Pages that the table does not have
+    // count for nothing here: they are out, or the last resort.
+    constexpr float kNone = -3.402823466e38f;
+    float least = INFINITY, most = -INFINITY, eps = 0.f;
+    int none = 0;
+    for (int j = first + tid; j < end; j += kPickThreads) {
+      const float s = score[j];
+      none += s <= kNone;
+      least = fminf(least, s <= kNone ? INFINITY : s), most = fmaxf(most, s);
     }
+    for (int i = tid; i < (used + chunk - 1) / chunk; i += kPickThreads) eps = fmaxf(eps, sc.eps[i]);
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       least = fminf(least, __shfl_xor_sync(0xffffffffu, least, x));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-      kinf = fmaxf(kinf, __shfl_xor_sync(0xffffffffu, kinf, x));
+      eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, x));
     }
-    if (lane == 0) {
-      sm.f[0][warp] = least, sm.f[1][warp] = most;
-      sm.count[0][0][warp] = __float_as_int(kinf), sm.count[0][1][warp] = __float_as_int(qsum);
-    }
+    if (lane == 0) sm.f[0][warp] = least, sm.f[1][warp] = most, sm.f[2][warp] = eps;
     if (tid == 0) sm.m = 0;
-    __syncthreads();
-    least = sm.f[0][lane], most = sm.f[1][lane];
-    kinf = __int_as_float(sm.count[0][0][lane]), qsum = __int_as_float(sm.count[0][1][lane]);
-    bool odd = isnan(qsum);
+    sm.hist[tid] = 0;
+    none = block_sum(none, sm, turn);
+    least = sm.f[0][lane], most = sm.f[1][lane], eps = sm.f[2][lane];
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
       least = fminf(least, __shfl_xor_sync(0xffffffffu, least, x));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-      kinf = fmaxf(kinf, __shfl_xor_sync(0xffffffffu, kinf, x));
-      qsum = fmaxf(qsum, __shfl_xor_sync(0xffffffffu, qsum, x));
+      eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, x));
     }
-    odd = __any_sync(0xffffffffu, odd) || most == INFINITY;
-    float eps = qsum * kinf * 6.2e-5f;  // 2^-14, and the rounding of this product and sum
-    if (odd || !(eps <= 1e37f)) eps = INFINITY;
+    if (!(most - least <= 1e37f) || end - first - none < want) eps = INFINITY;
     // Two-word sums where sums of the scores' magnitude neither overflow nor lose
     // their last bits below fp32's range.
     const bool words = eps < INFINITY && eps > 1e-24f;
     float from = -INFINITY;  // candidates: from <= score < sure
     if (eps < INFINITY) {
-      // [lo, hi): count(key >= lo) >= want > count(key >= hi); four parts a turn.
-      uint32_t lo = key32(least), hi = key32(most) + 1;
-      while (hi - lo > 1 && of_key32(hi) - of_key32(lo) > eps) {
-        turn ^= 1;
-        const uint32_t quarter = max((hi - lo) / 4, 1u);
-        const uint32_t k1 = lo + quarter, k2 = min(hi - 1, k1 + quarter), k3 = min(hi - 1, k2 + quarter);
-        int3 n = make_int3(0, 0, 0);
+      // The border lies in [lo, hi]: less than `want` scores are above, at least
+      // `want` reach lo.  A turn cuts that to a bin of 1024 and a rounding.
+      float lo = least, hi = most;
+      for (int n = 0; n < 64; ++n) {
+        const float width = hi - lo, scale = 1024.f / width;
+        if (width <= 4.f * eps || !(scale <= 1e37f)) break;
+        int above = 0;
         for (int j = first + tid; j < end; j += kPickThreads) {
-          const uint32_t k = key32(score[j]);
-          n.x += k >= k1, n.y += k >= k2, n.z += k >= k3;
+          const float s = score[j];
+          above += s > hi;
+          if (s >= lo && s <= hi) atomicAdd(&sm.hist[min(1023, static_cast<int>((s - lo) * scale))], 1);
         }
-        n = block_sum3(n, sm, turn);
-        if (n.z >= want) lo = k3;
-        else if (n.y >= want) lo = k2, hi = k3 > k2 ? k3 : hi;
-        else if (n.x >= want) lo = k1, hi = k2 > k1 ? k2 : hi;
-        else hi = k1;
+        turn ^= 1;
+        above = block_sum(above, sm, turn);  // its barrier completes the histogram
+        const int mine = sm.hist[1023 - tid];  // thread 0 has the highest bin
+        int upto = mine;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, x);
+          if (lane >= x) upto += y;
+        }
+        turn ^= 1;
+        if (lane == 31) sm.count[turn][warp] = upto;
+        __syncthreads();
+        upto += above + __reduce_add_sync(0xffffffffu, lane < warp ? sm.count[turn][lane] : 0);
+        if (upto - mine < want && want <= upto) sm.bin = 1023 - tid;
+        sm.hist[1023 - tid] = 0;  // for the next turn
+        __syncthreads();
+        const float l = lo + sm.bin * (width / 1024.f), h = lo + (sm.bin + 1) * (width / 1024.f);
+        const float slack = 4e-7f * (fabsf(lo) + fabsf(hi));  // of these sums and of the bins' rounding
+        const float nl = fmaxf(lo, l - slack), nh = fminf(hi, h + slack);
+        if (nh - nl > 0.5f * width) break;  // as narrow as fp32 can tell
+        lo = nl, hi = nh;
       }
-      from = of_key32(lo) - 2.f * eps;
-      sure = of_key32(hi) + 2.f * eps;
-      // rounding of the two sums
+      from = lo - 2.f * eps;
+      sure = hi + 2.f * eps;
+      // Rounding of the two sums; and more than hi, whatever eps.
       from -= fabsf(from) * 1e-6f;
-      sure += fabsf(sure) * 1e-6f;
+      sure += fabsf(sure) * 1e-6f + 2e-38f;
     }
     // Pages that are in, and candidates.
-    turn ^= 1;
-    int3 n = make_int3(0, 0, 0);
+    int in_all = 0;
     for (int j = first + tid; j < end; j += kPickThreads) {
       const float s = score[j];
-      const bool in = eps < INFINITY && s >= sure, cand = !in && s >= from;
-      n.x += in, n.y += cand;
-      if (cand) {
+      const bool in = eps < INFINITY && s >= sure;
+      in_all += in;
+      if (!in && s >= from) {
         const int at = atomicAdd(&sm.m, 1);
         if (at < kPickCap) sm.list[at] = j;
       }
     }
-    n = block_sum3(n, sm, turn);
-    const int m = n.y, r = want - n.x;  // r of the m candidates are in
+    turn ^= 1;
+    const int r = want - block_sum(in_all, sm, turn), m = sm.m;  // r of the m candidates are in
     const bool few = m <= kPickCap;
     if (m > r) {
       if (few) {
@@ -485,12 +521,15 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
           if (lane == 0) sm.key[i] = k;
         }
         __syncthreads();
-        for (int i = tid; i < m; i += kPickThreads) {
+        for (int i = warp; i < m; i += kPickThreads / 32) {
           const uint64_t k = sm.key[i];
           const int j = sm.list[i];
           int ahead = 0;
-          for (int y = 0; y < m; ++y) ahead += sm.key[y] > k || (sm.key[y] == k && sm.list[y] < j);
-          score[j] = ahead < r ? INFINITY : -INFINITY;
+          for (int y0 = 0; y0 < m; y0 += 32) {
+            const int y = y0 + lane;
+            ahead += __popc(__ballot_sync(0xffffffffu, y < m && (sm.key[y] > k || (sm.key[y] == k && sm.list[y] < j))));
+          }
+          if (lane == 0) score[j] = ahead < r ? INFINITY : -INFINITY;
         }
       } else {
         for (int j = first + warp; j < end; j += kPickThreads / 32) {
@@ -510,21 +549,21 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
         for (int bit = 63; bit >= 0; --bit) {
           turn ^= 1;
           const uint64_t t = border | (1ull << bit);
-          int3 c = make_int3(0, 0, 0);
-          for (int j = first + tid; j < end; j += kPickThreads) c.x += cand(j) && sc.key[j] >= t;
-          if (block_sum3(c, sm, turn).x >= r) border = t;
+          int c = 0;
+          for (int j = first + tid; j < end; j += kPickThreads) c += cand(j) && sc.key[j] >= t;
+          if (block_sum(c, sm, turn) >= r) border = t;
         }
         turn ^= 1;
-        int3 c = make_int3(0, 0, 0);
-        for (int j = first + tid; j < end; j += kPickThreads) c.x += cand(j) && sc.key[j] > border;
-        const int equal = r - block_sum3(c, sm, turn).x;
+        int c = 0;
+        for (int j = first + tid; j < end; j += kPickThreads) c += cand(j) && sc.key[j] > border;
+        const int equal = r - block_sum(c, sm, turn);
         int lo = first, hi = end;  // least j with `equal` pages at the border below it
         while (lo < hi) {
           turn ^= 1;
           const int mid = lo + (hi - lo) / 2;
-          int3 e = make_int3(0, 0, 0);
-          for (int j = first + tid; j < mid; j += kPickThreads) e.x += cand(j) && sc.key[j] == border;
-          if (block_sum3(e, sm, turn).x >= equal) hi = mid;
+          int e = 0;
+          for (int j = first + tid; j < mid; j += kPickThreads) e += cand(j) && sc.key[j] == border;
+          if (block_sum(e, sm, turn) >= equal) hi = mid;
           else lo = mid + 1;
         }
         for (int j = first + tid; j < end; j += kPickThreads)
@@ -538,24 +577,21 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
     }
     __syncthreads();
   }
-  // Ascending output: a run of pages per thread, places by a scan.
-  const int per = (used + kPickThreads - 1) / kPickThreads;
-  const int j0 = min(used, tid * per), j1 = min(used, j0 + per);
-  auto taken = [&](int j) { return j < first || j >= end || (want > 0 && score[j] >= sure); };
+  // Ascending output: a run of pages per warp, places by a scan over the warps.
+  const int per = (used + 32 * (kPickThreads / 32) - 1) / (32 * (kPickThreads / 32)) * 32;
+  const int j0 = min(used, warp * per), j1 = min(used, j0 + per);
+  auto taken = [&](int j) { return j < j1 && (j < first || j >= end || (want > 0 && score[j] >= sure)); };
   int mine = 0;
-  for (int j = j0; j < j1; ++j) mine += taken(j);
-  int upto = mine;
-#pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, upto, x);
-    if (lane >= x) upto += y;
-  }
+  for (int j = j0; j < j1; j += 32) mine += __popc(__ballot_sync(0xffffffffu, taken(j + lane)));
   turn ^= 1;
-  if (lane == 31) sm.count[turn][0][warp] = upto;
+  if (lane == 0) sm.count[turn][warp] = mine;
   __syncthreads();
-  int at = upto - mine + __reduce_add_sync(0xffffffffu, lane < warp ? sm.count[turn][0][lane] : 0);
-  for (int j = j0; j < j1; ++j)
-    if (taken(j)) out[at++] = j;
+  int at = __reduce_add_sync(0xffffffffu, lane < warp ? sm.count[turn][lane] : 0);
+  for (int j = j0; j < j1; j += 32) {
+    const uint32_t who = __ballot_sync(0xffffffffu, taken(j + lane));
+    if ((who >> lane) & 1) out[at + __popc(who & ((1u << lane) - 1))] = j + lane;
+    at += __popc(who);
+  }
 }
 
 template <int X, int C, int D>
@@ -565,7 +601,7 @@ int launch_t(const PagedSelectArgs& a) {
   while (chunk < 8 * kScoreChunk && static_cast<int64_t>(a.kv.max_pages / (2 * chunk)) * a.kv.B * a.kv.H >=
                                         8 * std::max(1, device_sm_count()))
     chunk *= 2;
-  const dim3 grid((a.kv.max_pages + chunk - 1) / chunk, a.kv.B * a.kv.H);
+  const dim3 grid((a.kv.max_pages + chunk - 1) / chunk * a.kv.H, a.kv.B);
   auto score = a.Hq / a.kv.H > 8 ? attn_paged_score_kernel<X, C, D, true> : attn_paged_score_kernel<X, C, D, false>;
   if (launch_serialized(true, score, grid, dim3(kScoreThreads), 0, a.stream, a, chunk) != cudaSuccess) return kStatusCuda;
   return launch_serialized(true, attn_paged_pick_kernel<X, C, D>, dim3(a.kv.B * a.kv.H), dim3(kPickThreads), 0, a.stream,
