@@ -47,6 +47,10 @@ class _PagedKvStruct(ctypes.Structure):  # attn_paged_kv_t
                 ("type", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
+class _CacheStruct(ctypes.Structure):  # what the compiled binding reads
+    _fields_ = [("kv", _PagedKvStruct), ("device", ctypes.c_int)]
+
+
 class _RowsStruct(ctypes.Structure):  # attn_rows_t
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
 
@@ -337,7 +341,7 @@ class PagedKV:
     The object holds references to the tensors and no data of its own."""
 
     __slots__ = ("k_pages", "v_pages", "block_table", "seq_lens", "k_min", "k_max", "k_scale", "v_scale", "device",
-                 "index", "_scale", "B", "kv_heads", "page_size", "head_dim", "max_pages", "dtype", "_struct", "_ref", "_ws")
+                 "B", "kv_heads", "page_size", "head_dim", "max_pages", "dtype", "_struct", "_address")
 
     def __init__(self, k_pages, v_pages, block_table, seq_lens, k_scale=1.0, v_scale=1.0, k_min=None, k_max=None):
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
@@ -369,79 +373,60 @@ class PagedKV:
                 raise ValueError("%s must be a contiguous [num_pages, kv_heads, d]" % name)
         self.k_pages, self.v_pages, self.block_table, self.seq_lens = k_pages, v_pages, block_table, seq_lens
         self.k_min, self.k_max, self.k_scale, self.v_scale = k_min, k_max, float(k_scale), float(v_scale)
-        self.device, self.index, self.dtype = dev, dev.index, k_pages.dtype
-        self._scale = 1.0 / math.sqrt(d) if d else 0.0
+        self.device, self.dtype = dev, k_pages.dtype
         self.B, self.max_pages = int(block_table.shape[0]), int(block_table.shape[1])
         self.kv_heads, self.page_size, self.head_dim = H, page, d
         three = ctypes.c_longlong * 3
-        self._struct = _PagedKvStruct(
+        self._struct = _CacheStruct(_PagedKvStruct(
             k_pages.data_ptr(), v_pages.data_ptr(), three(*k_pages.stride()[:3]), three(*v_pages.stride()[:3]),
             k_min.data_ptr() if k_min is not None else None, k_max.data_ptr() if k_max is not None else None,
             block_table.data_ptr(), seq_lens.data_ptr(), int(block_table.stride(0)), P, page, H, d, self.max_pages,
-            self.B, _TYPE_CODES[k_pages.dtype], self.k_scale, self.v_scale)
-        self._ref = ctypes.byref(self._struct)
-        self._ws = {}  # workspace bytes by (query heads, listed pages), None: selection; functions of the sizes
+            self.B, _TYPE_CODES[k_pages.dtype], self.k_scale, self.v_scale), dev.index)
+        self._address = ctypes.addressof(self._struct)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # a tenth of the cost of torch.cuda.current_stream()
+_native_module = None
 
 
-def _bad_rows(name, t, kv, heads, rows, dtype):
-    """Raises what is wrong with rows that _paged_rows refused."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != kv.device:
-        raise TypeError("%s must be a tensor on the cache's device" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s" % (name, dtype))
-    raise ValueError("%s must be [%s, %s, %d] with contiguous channels" % (
-        name, "rows" if rows is None else rows, "heads" if heads is None else heads, kv.head_dim))
+def _native():
+    """The compiled marshalling of the paged calls (raises if it has not been built)."""
+    global _native_module
+    if _native_module is None:
+        lib()  # says how to build where that has not been done
+        from . import _paged
+        _native_module = _paged
+    return _native_module
 
 
-def _paged_rows(name, t, kv, heads, rows, dtype):
-    """attn_rows_t of a [rows, heads, d] tensor, by reference."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != kv.index:
-        _bad_rows(name, t, kv, heads, rows, dtype)
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[2] != kv.head_dim or stride[2] != 1 or (rows is not None and shape[0] != rows) or (
-            heads is not None and shape[1] != heads):
-        _bad_rows(name, t, kv, heads, rows, dtype)
-    return ctypes.byref(_RowsStruct(t.data_ptr(), stride[0], stride[1]))
-
-
-def _paged_x(kv, x):
-    """Element type code of new rows; the cache's own type, or either for e4m3."""
-    if not isinstance(kv, PagedKV):
-        raise TypeError("kv must be a PagedKV")
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("rows must be a tensor on the cache's device")
-    if x.dtype != kv.dtype and (kv.dtype != torch.float8_e4m3fn or x.dtype not in (torch.bfloat16, torch.float16)):
-        raise TypeError("a %s cache takes bf16 or fp16 rows%s" % (kv.dtype, "" if kv.dtype.itemsize == 1 else
-                                                                  " of its own type"))
-    return 1 if x.dtype == torch.float16 else 0
-
-
-def _elsewhere(kv, stream):
-    """True where a call must switch the current device or stream first."""
-    return stream is not None or kv.index != torch.cuda.current_device()
-
-
-class _Switched:
-    """The cache's device and the call's stream as the current ones: what a call
-    allocates then belongs to the stream that it runs on."""
+class _OnStream:
+    """A stream of the cache's device as the current one: what a call allocates
+    then belongs to the stream that it runs on."""
 
     def __init__(self, kv, stream):
-        if stream is not None and stream.device != kv.device:
+        if stream.device != kv.device:
             raise ValueError("the stream must be of the cache's device")
-        self.device = torch.cuda.device(kv.device)
-        self.stream = _NOTHING if stream is None else torch.cuda.stream(stream)
+        self.stream = torch.cuda.stream(stream)
 
     def __enter__(self):
-        self.device.__enter__()
         self.stream.__enter__()
 
     def __exit__(self, *exc):
         self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
         return False
+
+
+def _paged_call(name, kv, stream, *args):
+    if not isinstance(kv, PagedKV):
+        raise TypeError("kv must be a PagedKV")
+    f = getattr(_native_module or _native(), name)
+    if stream is None:
+        r = f(kv._address, *args)
+    else:
+        with _OnStream(kv, stream):
+            r = f(kv._address, *args)
+    if type(r) is int:
+        raise AttnError("attn_paged_" + name, r)
+    return r
 
 
 def rotation_tables(positions, rot_dim, base=10000.0, device=None):
@@ -460,59 +445,7 @@ def attn_paged_append(kv, k, v, q=None, q_out=None, token_start=None, cos=None, 
     token_start [B + 1] int32 gives each sequence's rows (None: one row per
     sequence).  Returns q_out (allocated where None; may be q itself), or None
     without q.  Rows of padding and empty slots are left as they are."""
-    x = _paged_x(kv, k)
-    if _elsewhere(kv, stream):
-        with _Switched(kv, stream):
-            return attn_paged_append(kv, k, v, q, q_out, token_start, cos, sin, interleaved)
-    dtype, rows = k.dtype, k.shape[0] if k.dim() else 0
-    rk = _paged_rows("k", k, kv, kv.kv_heads, None, dtype)
-    rv = _paged_rows("v", v, kv, kv.kv_heads, rows, dtype)
-    start = None
-    if token_start is not None:
-        if (not isinstance(token_start, torch.Tensor) or token_start.get_device() != kv.index
-                or token_start.dtype != torch.int32 or token_start.shape != (kv.B + 1,)
-                or not token_start.is_contiguous()):
-            raise ValueError("token_start must be a contiguous int32 [%d] on the cache's device" % (kv.B + 1))
-        start = token_start.data_ptr()
-    elif rows != kv.B:
-        raise ValueError("without token_start k and v must have one row per sequence (%d)" % kv.B)
-    table_rows = rot = 0
-    pc = ps = None
-    if cos is not None or sin is not None:
-        if cos is None or sin is None:
-            raise ValueError("cos and sin come together")
-        for name, t in (("cos", cos), ("sin", sin)):
-            if not isinstance(t, torch.Tensor) or t.get_device() != kv.index or t.dtype != torch.float32:
-                raise TypeError("%s must be a float32 tensor on the cache's device" % name)
-            if t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
-                raise ValueError("cos and sin must be contiguous [positions, rot_dim / 2] of one shape")
-        table_rows, rot = cos.shape
-        rot *= 2
-        pc, ps = cos.data_ptr(), sin.data_ptr()
-    rq = ro = None
-    heads = 0
-    if q is not None:
-        rq = _paged_rows("q", q, kv, None, rows, dtype)
-        heads = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=kv.device)
-        ro = _paged_rows("q_out", q_out, kv, heads, rows, dtype)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rc = lib().attn_paged_append(kv._ref, rk, rv, rq, ro, heads, rows, start, pc, ps, table_rows, rot,
-                                 1 if interleaved else 0, x, _raw_stream(kv.index))
-    if rc:
-        raise AttnError("attn_paged_append", rc)
-    return q_out
-
-
-def _paged_pages(kv, pages):
-    if (not isinstance(pages, torch.Tensor) or pages.get_device() != kv.index or pages.dtype != torch.int32
-            or pages.dim() != 3 or pages.shape[0] != kv.B or pages.shape[1] != kv.kv_heads or pages.shape[2] < 1
-            or not pages.is_contiguous()):
-        raise ValueError("pages must be a contiguous int32 [%d, %d, n >= 1] on the cache's device"
-                         % (kv.B, kv.kv_heads))
-    return pages.shape[2]
+    return _paged_call("append", kv, stream, k, v, q, q_out, token_start, cos, sin, interleaved)
 
 
 def attn_paged_decode(kv, q, pages=None, scale=None, o=None, lse=None, stream=None):
@@ -521,34 +454,7 @@ def attn_paged_decode(kv, q, pages=None, scale=None, o=None, lse=None, stream=No
     sequence's seq_lens tokens, or the tokens of the listed ``pages``
     [B, kv_heads, n] (attn_paged_select).  Returns (o [B, q_heads, d],
     lse [B, q_heads]); an empty sequence gets o = 0, lse = -inf."""
-    x = _paged_x(kv, q)
-    if _elsewhere(kv, stream):
-        with _Switched(kv, stream):
-            return attn_paged_decode(kv, q, pages, scale, o, lse)
-    rq = _paged_rows("q", q, kv, None, kv.B, q.dtype)
-    heads = q.shape[1]
-    n = 0 if pages is None else _paged_pages(kv, pages)
-    need = kv._ws.get((heads, n))
-    if need is None:
-        need = kv._ws[(heads, n)] = lib().attn_paged_decode_workspace(kv._ref, heads, n)
-    if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=kv.device)
-    else:
-        _check("o", o, q, q.dtype)
-    if lse is None:
-        lse = torch.empty((kv.B, heads), dtype=torch.float32, device=kv.device)
-    else:
-        _check("lse", lse, None, torch.float32)
-        if lse.shape != (kv.B, heads) or lse.device != kv.device:
-            raise ValueError("lse must be [B, q_heads] on the cache's device")
-    ws = torch.empty(need, dtype=torch.uint8, device=kv.device) if need else None
-    rc = lib().attn_paged_decode(kv._ref, rq, heads, o.data_ptr(), lse.data_ptr(),
-                                 None if pages is None else pages.data_ptr(), n,
-                                 kv._scale if scale is None else float(scale), x,
-                                 ws.data_ptr() if need else None, _raw_stream(kv.index))
-    if rc:
-        raise AttnError("attn_paged_decode", rc)
-    return o, lse
+    return _paged_call("decode", kv, stream, q, pages, scale, o, lse)
 
 
 def attn_paged_select(kv, q, n_select, keep_first=1, keep_last=1, pages=None, stream=None):
@@ -558,29 +464,9 @@ def attn_paged_select(kv, q, n_select, keep_first=1, keep_last=1, pages=None, st
     pages always, equal scores by the lower index.  Returns int32
     [B, kv_heads, n_select] page indices, ascending, -1 behind the pages of a
     shorter sequence, for attn_paged_decode."""
-    x = _paged_x(kv, q)
-    if kv.k_min is None:
+    if isinstance(kv, PagedKV) and kv.k_min is None:
         raise ValueError("the cache has no key summaries (k_min, k_max)")
-    n = int(n_select)
-    if n < 1 or keep_first < 0 or keep_last < 0 or keep_first + keep_last > n:
-        raise ValueError("n_select must be at least 1 and keep_first + keep_last, both at least 0")
-    if _elsewhere(kv, stream):
-        with _Switched(kv, stream):
-            return attn_paged_select(kv, q, n_select, keep_first, keep_last, pages)
-    rq = _paged_rows("q", q, kv, None, kv.B, q.dtype)
-    need = kv._ws.get(None)
-    if need is None:
-        need = kv._ws[None] = lib().attn_paged_select_workspace(kv._ref)
-    if pages is None:
-        pages = torch.empty((kv.B, kv.kv_heads, n), dtype=torch.int32, device=kv.device)
-    elif _paged_pages(kv, pages) != n:
-        raise ValueError("pages must be [B, kv_heads, n_select]")
-    ws = torch.empty(need, dtype=torch.uint8, device=kv.device) if need else None
-    rc = lib().attn_paged_select(kv._ref, rq, q.shape[1], pages.data_ptr(), n, int(keep_first), int(keep_last), x,
-                                 ws.data_ptr() if need else None, _raw_stream(kv.index))
-    if rc:
-        raise AttnError("attn_paged_select", rc)
-    return pages
+    return _paged_call("select", kv, stream, q, n_select, keep_first, keep_last, pages)
 
 
 def _check_block_mask(block_mask, H, N):

@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kScoreWarps = 2;
 constexpr int kScoreThreads = 32 * kScoreWarps;
+constexpr int kScoreFill = 8;
 constexpr int kScoreDepth = 4;                  // groups of 8 pages in flight per warp
 constexpr int kScoreChunk = 8 * kScoreWarps * 4;  // pages of a CTA, times 1 to 8
 constexpr int kPickThreads = 1024;
@@ -63,15 +64,18 @@ __device__ __forceinline__ SelectScratch scratch_of(uint8_t* ws, int64_t bh, int
 // Sign mask of two 16-bit floats: all ones in the halves that are negative.
 __device__ __forceinline__ uint32_t negative_halves(uint32_t x) { return ((x >> 15) & 0x00010001u) * 0xffffu; }
 
-// The larger magnitudes of two pairs, as 16-bit floats (their order is that of
-// their bits).
+// The larger magnitudes of two pairs, with some sign; a NaN gives way.
+template <bool BF16>
 __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t x) {
-  return __vmaxu2(m, x & 0x7fff7fffu);
+  uint32_t r;
+  if constexpr (BF16) asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x));
+  else asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x));
+  return r;
 }
 template <bool BF16>
 __device__ __forceinline__ float magnitude(uint32_t m) {
   const float2 f = unpack2<BF16>(m);
-  return fmaxf(f.x, f.y);
+  return fmaxf(fabsf(f.x), fabsf(f.y));
 }
 
 template <int BYTES>
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
         } else {
           l0 = lo[2 * s], l1 = lo[2 * s + 1], h0 = hi[2 * s], h1 = hi[2 * s + 1];
         }
-        big = max_magnitude(max_magnitude(max_magnitude(max_magnitude(big, l0), l1), h0), h1);
+        big = max_magnitude<BF>(max_magnitude<BF>(max_magnitude<BF>(max_magnitude<BF>(big, l0), l1), h0), h1);
         if constexpr (WIDE) {
           mma16<BF>(acc, qp[s][0], qp[s][1], qp[s][2], qp[s][3], h0, h1);
           mma16<BF>(acc, qn[s][0], qn[s][1], qn[s][2], qn[s][3], l0, l1);
@@ -599,7 +603,7 @@ int launch_t(const PagedSelectArgs& a) {
   // Long walks amortise a CTA's start, as long as they leave eight CTAs to an SM.
   int chunk = kScoreChunk;
   while (chunk < 8 * kScoreChunk && static_cast<int64_t>(a.kv.max_pages / (2 * chunk)) * a.kv.B * a.kv.H >=
-                                        8 * std::max(1, device_sm_count()))
+                                        kScoreFill * std::max(1, device_sm_count()))
     chunk *= 2;
   const dim3 grid((a.kv.max_pages + chunk - 1) / chunk * a.kv.H, a.kv.B);
   auto score = a.Hq / a.kv.H > 8 ? attn_paged_score_kernel<X, C, D, true> : attn_paged_score_kernel<X, C, D, false>;

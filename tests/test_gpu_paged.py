@@ -694,3 +694,59 @@ def test_decode_many_turns_of_the_ring(pkg, x, dtype, scales):
     c = Case(pkg, lens, H=8, d=128, dtype=dtype, scales=scales, seed=5)
     for _ in range(3):
         _check_decode(pkg, c, c.randn(len(lens), 16, 128, dtype=x))
+
+
+# ------------------------------------------------------------------ the binding's own checks
+
+def test_the_binding_refuses(pkg):
+    c = Case(pkg, [20, 3], H=2, d=64, summaries=True, seed=1)
+    q, k = c.randn(2, 4, 64).cuda(), c.randn(2, 2, 64).cuda()
+    cos, sin = pkg.rotation_tables(64, 64, device="cuda")
+    start = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    before = (c.k.clone(), c.v.clone())
+    app, dec, sel = pkg.attn_paged_append, pkg.attn_paged_decode, pkg.attn_paged_select
+    wrong = [
+        (TypeError, lambda: dec(c.kv, q.cpu())), (TypeError, lambda: dec(c.kv, q.half())), (TypeError, lambda: dec(c.kv, q.float())),
+        (TypeError, lambda: dec(c.kv, None)), (TypeError, lambda: dec(None, q)), (ValueError, lambda: dec(c.kv, q[:1])),
+        (ValueError, lambda: dec(c.kv, q[..., :32])), (ValueError, lambda: dec(c.kv, q[:, 0])),
+        (ValueError, lambda: dec(c.kv, q.transpose(1, 2).contiguous().transpose(1, 2))),
+        (pkg.AttnError, lambda: dec(c.kv, q[:, :3])), (pkg.AttnError, lambda: dec(c.kv, q, scale=math.inf)),
+        (TypeError, lambda: dec(c.kv, q, scale="x")), (ValueError, lambda: dec(c.kv, q, o=torch.empty(2, 4, 32, dtype=BF16, device="cuda"))),
+        (TypeError, lambda: dec(c.kv, q, o=torch.empty(2, 4, 64, device="cuda"))), (pkg.AttnError, lambda: dec(c.kv, q, o=q)),
+        (ValueError, lambda: dec(c.kv, q, lse=torch.empty(2, 3, device="cuda"))), (TypeError, lambda: dec(c.kv, q, lse=q)),
+        (ValueError, lambda: dec(c.kv, q, pages=torch.zeros(2, 2, 0, dtype=torch.int32, device="cuda"))),
+        (ValueError, lambda: dec(c.kv, q, pages=torch.zeros(2, 1, 3, dtype=torch.int32, device="cuda"))),
+        (ValueError, lambda: dec(c.kv, q, pages=torch.zeros(2, 2, 3, dtype=torch.int64, device="cuda"))),
+        (TypeError, lambda: dec(c.kv, q, pages=[0])),
+        (ValueError, lambda: sel(c.kv, q, 0)), (ValueError, lambda: sel(c.kv, q, 1)), (ValueError, lambda: sel(c.kv, q, 4, keep_first=-1)),
+        (ValueError, lambda: sel(c.kv, q, 4, pages=torch.zeros(2, 2, 3, dtype=torch.int32, device="cuda"))),
+        (ValueError, lambda: sel(pkg.PagedKV(c.k, c.v, c.block_table, c.seq_lens), q, 4)), (TypeError, lambda: sel(c.kv, q, "x")),
+        (TypeError, lambda: app(c.kv, k, k.half())), (TypeError, lambda: app(c.kv, k.half(), k.half())), (ValueError, lambda: app(c.kv, q, q)),
+        (ValueError, lambda: app(c.kv, k[:1], k[:1])), (ValueError, lambda: app(c.kv, k, k, token_start=start[:2])),
+        (ValueError, lambda: app(c.kv, k, k, token_start=start.long())), (ValueError, lambda: app(c.kv, k, k, cos=cos)),
+        (TypeError, lambda: app(c.kv, k, k, cos=cos.half(), sin=sin.half())), (ValueError, lambda: app(c.kv, k, k, cos=cos, sin=sin[:3])),
+        (pkg.AttnError, lambda: app(c.kv, k, k, cos=cos[:, :4].contiguous(), sin=sin[:, :4].contiguous())),
+        (ValueError, lambda: app(c.kv, k, k, q_out=q)), (ValueError, lambda: app(c.kv, k, k, q=q[:1], token_start=start)),
+        (pkg.AttnError, lambda: app(c.kv, k, k, q=q, q_out=torch.empty(8, 4, 64, dtype=BF16, device="cuda")[::1][:1].expand(2, 4, 64))),
+    ]
+    for i, (error, call) in enumerate(wrong):
+        with pytest.raises(error):
+            call()
+            pytest.fail("call %d was taken" % i)
+    assert pkg.sync_status() == 0
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip((c.k, c.v), before))
+
+
+def test_calls_on_a_side_stream_allocate_there(pkg):
+    """Outputs and workspace of a call with a stream come from that stream's pool, and the current stream stays."""
+    c = Case(pkg, [500, 30], H=2, d=64, summaries=True, seed=2)
+    q = c.randn(2, 4, 64).cuda()
+    want = pkg.attn_paged_decode(c.kv, q)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    here = torch.cuda.current_stream()
+    got = pkg.attn_paged_decode(c.kv, q, stream=side)
+    assert torch.cuda.current_stream() == here
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert pkg.sync_status() == 0
