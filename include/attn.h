@@ -329,9 +329,10 @@ int attn_paged_append(const attn_paged_kv_t* kv, const attn_rows_t* k, const att
  *   lse  : out, [B, q_heads] fp32
  *   pages: NULL (all seq_lens[b] tokens), or [B, kv_heads, n_pages] int32 page
  *          indices within the sequence (attn_paged_select's output): attention
- *          over the tokens of those pages only.  Negative entries are skipped,
- *          as are indices at or past the sequence's last page; a page that is
- *          listed twice counts twice.
+ *          over the tokens of those pages only, in any order, no page twice,
+ *          negative entries behind the others (of a sequence of fewer than
+ *          n_pages pages only as many entries are read as it has pages).
+ *          Indices past the sequence's last page are skipped.
  * A sequence without visible tokens gets o = 0, lse = -inf.  Slots behind a
  * sequence's end may hold anything (NaN too).
  *   workspace : attn_paged_decode_workspace() bytes of device memory, 16-byte

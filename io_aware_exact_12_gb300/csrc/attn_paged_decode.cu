@@ -35,7 +35,7 @@ namespace {
 constexpr int kPdWarps = 4;  // consumers
 constexpr int kPdThreads = 32 * (kPdWarps + 1);
 constexpr int kPdRows = 16;  // query heads of an item, at most
-constexpr int kPdRing = 80 * 1024;
+constexpr int kPdSolo = 4;  // tiles up to which a warp takes a whole item
 
 template <int C, int D, int NT>  // NT: groups of 8 query heads
 struct PdCfg {
@@ -44,19 +44,24 @@ struct PdCfg {
   static constexpr int ROW = D * CB;                   // bytes of a cached row
   static constexpr int RBX = ROW < 128 ? ROW : 128;    // bytes of a row in one box (the swizzle's span)
   static constexpr int NH = ROW / RBX;
+  static constexpr int MINB = NT == 1 && ROW <= 64 ? 3 : 2;  // CTAs per SM
   static constexpr int TK = ROW >= 256 ? 32 : 64;      // keys of a tile
   static constexpr int HALF = TK * ROW;                // K (or V) bytes of a stage
+  static constexpr int OTHER = kPdWarps * ROWS * D * 4 + kPdWarps * 3 * ROWS * 4 + 1024;
+  static constexpr int RING = 227 * 1024 / MINB - 1024 - OTHER;
   // A multiple of the warps, so that a stage always serves the same warp: loads
   // land out of order, and a warp that looked at a stage whose previous tile,
   // another warp's, had not landed yet would take the phase before for its own.
-  static constexpr int STAGES = (kPdRing / (2 * HALF) < 16 ? kPdRing / (2 * HALF) : 16) / kPdWarps * kPdWarps;
+  static constexpr int STAGES = (RING / (2 * HALF) < 16 ? RING / (2 * HALF) : 16) / kPdWarps * kPdWarps;
   static_assert(STAGES >= kPdWarps && STAGES % kPdWarps == 0, "stages belong to warps");
+  static constexpr int SPW = STAGES / kPdWarps;        // stages of a warp
   static constexpr int OFF_O = STAGES * 2 * HALF;      // [warps][ROWS][D] fp32
   static constexpr int OFF_ML = OFF_O + kPdWarps * ROWS * D * 4;  // [warps][3][ROWS]
   static constexpr int OFF_BAR = OFF_ML + kPdWarps * 3 * ROWS * 4;
   static constexpr int OFF_MASK = OFF_BAR + 2 * STAGES * 8;  // visible keys of a stage
   static constexpr int OFF_SCHED = OFF_MASK + STAGES * 8;
-  static constexpr int SMEM = OFF_SCHED + 128;
+  static constexpr int SMEM = OFF_SCHED + 192;
+  static_assert(MINB * (SMEM + 1024) <= 228 * 1024, "MINB CTAs fit an SM");
 };
 
 struct Part {  // an item that CTA `first` begins and CTA `last` ends
@@ -74,10 +79,12 @@ __device__ __forceinline__ float part_weight(float m, float mm) { return m == -I
 struct Sched {
   long long t0, total;
   int b, hr, tile, n;  // first tile of the CTA and how many it has
-  int n_act, abort_flag;
+  int n_act, solo, abort_flag;
+  int up[2];  // tiles from a bound of the share to the next item's start
   long long warp_sum[kPdThreads / 32];
+  int warp_most[kPdThreads / 32], warp_live[kPdThreads / 32];
 };
-static_assert(sizeof(Sched) <= 128, "OFF_SCHED");
+static_assert(sizeof(Sched) <= 192, "OFF_SCHED");
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -113,54 +120,70 @@ __device__ __forceinline__ void consumer_sync() {
 template <int TK>
 __device__ __forceinline__ int tiles_of(const PagedDecodeArgs& a, int len) {
   if (len <= 0) return 0;
-  return ((a.pages ? a.n_pages * a.kv.page : len) + TK - 1) / TK;
+  // A list without repetitions has no more entries than the sequence has pages.
+  return ((a.pages ? min(a.n_pages, (len + a.kv.page - 1) / a.kv.page) * a.kv.page : len) + TK - 1) / TK;
 }
 
 // Finds the CTA's share of the tiles.  All threads; B numbers are read once.
+// Where every item is short and there are many, items are not cut ("solo"): a
+// CTA has those that begin in its share, and a warp takes each for itself.
 template <int TK>
 __device__ __forceinline__ void find_share(const PagedDecodeArgs& a, int HR, Sched& s) {
   const int tid = threadIdx.x, lane = tid & 31, B = a.kv.B;
   const int per = (B + kPdThreads - 1) / kPdThreads;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of<TK>(a, checked_len(a.kv, b));
+  int most = 0, live = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int t = tiles_of<TK>(a, checked_len(a.kv, b));
+    mine += t, most = max(most, t), live += t > 0;
+  }
   mine *= HR;
   long long upto = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, upto, x);
     if (lane >= x) upto += y;
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
+    live += __shfl_xor_sync(0xffffffffu, live, x);
   }
-  if (lane == 31) s.warp_sum[tid >> 5] = upto;
-  if (tid == 0) s.n = 0, s.b = 0, s.hr = 0, s.tile = 0, s.t0 = 0;
+  if (lane == 31) s.warp_sum[tid >> 5] = upto, s.warp_most[tid >> 5] = most, s.warp_live[tid >> 5] = live;
+  if (tid == 0) s.n = 0, s.b = 0, s.hr = 0, s.tile = 0, s.t0 = 0, s.up[0] = s.up[1] = 0;
   __syncthreads();
   long long total = 0;
+  most = live = 0;
 #pragma unroll
   for (int i = 0; i < kPdThreads / 32; ++i) {
     if (i < (tid >> 5)) upto += s.warp_sum[i];
     total += s.warp_sum[i];
+    most = max(most, s.warp_most[i]), live += s.warp_live[i];
   }
-  // At least one tile per consumer warp, so that few tiles go to few CTAs.
-  const int n_act = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + kPdWarps - 1) / kPdWarps));
+  // Few tiles: a tile per consumer warp, in as many CTAs to every item.
+  const long long items = static_cast<long long>(live) * HR;
+  const long long want = items ? items * ((total + items * kPdWarps - 1) / (items * kPdWarps)) : 0;
+  const int n_act = static_cast<int>(min(static_cast<long long>(gridDim.x), want));
+  const bool solo = most <= kPdSolo && items >= kPdWarps * static_cast<long long>(gridDim.x);
   const int c = blockIdx.x;
-  if (tid == 0) s.total = total, s.n_act = n_act;
+  if (tid == 0) s.total = total, s.n_act = n_act, s.solo = solo;
   if (c < n_act) {
-    const long long t0 = total * c / n_act, t1 = total * (c + 1) / n_act;
-    if (upto - mine <= t0 && t0 < upto) {
+    const long long bound[2] = {total * c / n_act, total * (c + 1) / n_act};
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const long long t0 = bound[x];
+      if (!(upto - mine <= t0 && t0 < upto)) continue;
       long long at = upto - mine;
       for (int b = b0; b < b1; ++b) {
         const long long t = tiles_of<TK>(a, checked_len(a.kv, b));
         if (t0 < at + t * HR) {
-          s.b = b;
-          s.hr = static_cast<int>((t0 - at) / t);
-          s.tile = static_cast<int>((t0 - at) % t);
+          const int tile = static_cast<int>((t0 - at) % t);
+          s.up[x] = tile ? static_cast<int>(t) - tile : 0;
+          if (x == 0) s.b = b, s.hr = static_cast<int>((t0 - at) / t), s.tile = tile;
           break;
         }
         at += t * HR;
       }
-      s.t0 = t0;
-      s.n = static_cast<int>(t1 - t0);
     }
+    if (tid == 0) s.t0 = bound[0], s.n = static_cast<int>(bound[1] - bound[0]);
   }
   __syncthreads();
 }
@@ -190,7 +213,7 @@ __device__ __forceinline__ void store_out4(uint8_t* p, const float (&o)[4]) {
 }
 
 template <int X, int C, int D, int NT>
-__global__ void __launch_bounds__(kPdThreads, 2)
+__global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     attn_paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                              const PagedDecodeArgs a, int RT, int box_rows, int by_item, Part* parts, float* part) {
   using F = PdCfg<C, D, NT>;
@@ -218,7 +241,9 @@ __global__ void __launch_bounds__(kPdThreads, 2)
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
   find_share<TK>(a, HR, s);
-  const int n = s.n;
+  const bool solo = s.solo;
+  // Solo: from the first item that begins here to the end of the last one.
+  const int n = solo && s.n > 0 ? s.n - s.up[0] + s.up[1] : s.n;
   const int c = blockIdx.x;
 
   // Sequences without tokens: o = 0, lse = -inf.
@@ -238,15 +263,21 @@ __global__ void __launch_bounds__(kPdThreads, 2)
   Item it = {s.b, s.hr, 0, 0};
   it.len = checked_len(kv, it.b);
   it.tiles = tiles_of<TK>(a, it.len);
+  int tile = s.tile;
+  if (solo && tile) {
+    next_item<TK>(a, HR, it);
+    tile = 0;
+  }
 
   if (warp == kPdWarps) {  // ---------------------------------- producer warp
     // Each lane looks up one box (box_rows keys of one page) of the next
     // tiles, so one round trip through list and table serves 32 boxes.
     const int nb = TK / box_rows, batch = 32 / nb;  // boxes of a tile, tiles of a batch
     const int box = lane % nb;
-    int tile = s.tile;
     bool ok = true;
-    int issued = 0;
+    // Tile i goes to warp i % 4, or (solo) the j-th item to warp j % 4; `taken`
+    // counts each warp's tiles.
+    int w = kPdWarps - 1, taken[kPdWarps] = {};
     for (int i0 = 0; ok && i0 < n; i0 += batch) {
       Item mine = it;
       int t = tile + lane / nb;
@@ -278,11 +309,22 @@ __global__ void __launch_bounds__(kPdThreads, 2)
         mask |= __shfl_xor_sync(0xffffffffu, mask, x);
         vis += __shfl_xor_sync(0xffffffffu, vis, x);
       }
+      const uint32_t begin = __ballot_sync(0xffffffffu, t == 0);
       for (int k = 0; k < batch && i0 + k < n; ++k) {
-        const int i = i0 + k, st = i % F::STAGES;
-        if (i >= F::STAGES) ok = mbar_wait(empty + st * 8, ((i / F::STAGES) - 1) & 1, abort_flag, a.status);
+        if (!solo || ((begin >> (k * nb)) & 1)) w = (w + 1) % kPdWarps;
+        int turn = 0;  // the warp's tiles so far
+#pragma unroll
+        for (int x = 0; x < kPdWarps; ++x)
+          if (x == w) turn = taken[x]++;
+        const int st = w + kPdWarps * (turn % F::SPW);
+        if (turn >= F::SPW) ok = mbar_wait(empty + st * 8, (turn / F::SPW - 1) & 1, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (!ok) {
+#pragma unroll
+          for (int x = 0; x < kPdWarps; ++x)
+            if (x == w) --taken[x];  // not issued
+          break;
+        }
         if (lane == k * nb) {
           masks[st] = mask;
           mbar_arrive_expect_tx(full + st * 8, vis * box_rows * F::ROW * 2);
@@ -296,7 +338,6 @@ __global__ void __launch_bounds__(kPdThreads, 2)
             tma_load_4d(dst + F::HALF + hf * TK * F::RBX, &mv, full + st * 8, hf * F::RBX, row, h, id);
           }
         }
-        issued = i + 1;
       }
       // The batch's end, for all lanes alike.
       tile += batch;
@@ -307,11 +348,14 @@ __global__ void __launch_bounds__(kPdThreads, 2)
     }
     // No copy may be in flight when the CTA ends, also where the consumers gave
     // up: wait for the last ones here.
-    for (int i = max(0, issued - F::STAGES); i < issued; ++i) {
-      const uint64_t since = global_timer_ns();
-      while (!mbar_test(full + (i % F::STAGES) * 8, (i / F::STAGES) & 1) && global_timer_ns() - since < kWaitLimitNs) {
+#pragma unroll
+    for (int x = 0; x < kPdWarps; ++x)
+      for (int k = max(0, taken[x] - F::SPW); k < taken[x]; ++k) {
+        const uint64_t since = global_timer_ns();
+        while (!mbar_test(full + (x + kPdWarps * (k % F::SPW)) * 8, (k / F::SPW) & 1) &&
+               global_timer_ns() - since < kWaitLimitNs) {
+        }
       }
-    }
     return;
   }
 
@@ -327,10 +371,20 @@ __global__ void __launch_bounds__(kPdThreads, 2)
   constexpr int CPB = F::RBX / 16;  // 16-byte chunks of a box row
   const uint32_t ones = BF ? 0x3f803f80u : 0x3c003c00u;
   bool ok = true;
-  int i = warp, cur = 0, tile = s.tile;
+  int cur = 0, turn = 0;       // tiles of the CTA that are done, and of this warp
   long long g0 = s.t0 - tile;  // first tile of the item, counted from the start of all
-  while (cur < n && it.tiles > tile) {
+  for (int item = 0; cur < n && it.tiles > tile; ++item) {
     const int end = min(n, cur + it.tiles - tile);
+    // This warp's tiles of the item.
+    int tiles = (end - warp + kPdWarps - 1) / kPdWarps - (cur - warp + kPdWarps - 1) / kPdWarps;
+    if (solo) {
+      tiles = end - cur;
+      if (item % kPdWarps != warp) {
+        cur = end;
+        if (cur < n) next_item<TK>(a, HR, it);
+        continue;
+      }
+    }
     const int h = it.hr / RT, r0 = (it.hr % RT) * ROWS;
     const int rows = min(ROWS, G - r0);
     const int64_t head0 = static_cast<int64_t>(h) * G + r0;
@@ -397,12 +451,17 @@ __global__ void __launch_bounds__(kPdThreads, 2)
       }
     }
 
-    for (; i < end; i += kPdWarps) {
-      const int st = i % F::STAGES;
-      if (ok) ok = mbar_wait(full + st * 8, (i / F::STAGES) & 1, abort_flag, a.status);
+    for (; tiles > 0; --tiles, ++turn) {
+      const int st = warp + kPdWarps * (turn % F::SPW);
+      if (ok) ok = mbar_wait(full + st * 8, (turn / F::SPW) & 1, abort_flag, a.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;
       const uint64_t mask = masks[st];
+      if (mask == 0) {  // nothing to see, nothing was loaded
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + st * 8);
+        continue;
+      }
       const uint32_t kb = sbase + st * 2 * F::HALF, vb = kb + F::HALF;
       const bool whole = mask == (TK == 64 ? ~0ull : (1ull << (TK & 63)) - 1);
       if (!whole) {
@@ -538,8 +597,9 @@ __global__ void __launch_bounds__(kPdThreads, 2)
       if (lane == 0) mbar_arrive(empty + st * 8);
     }
 
-    // The item's end in this CTA: merge the four warps.  Columns are swizzled by
-    // the head, so that the fragments' stores meet no bank twice.
+    // The item's end in this CTA: the four warps are merged (solo: one is all).
+    // Columns are swizzled by the head, so that the fragments' stores meet no bank
+    // twice.
     float* ml = sml + warp * 3 * ROWS;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -567,19 +627,22 @@ __global__ void __launch_bounds__(kPdThreads, 2)
         }
       }
     }
-    consumer_sync();
+    if (solo) __syncwarp();
+    else consumer_sync();
     const bool begins = tile == 0, ends = end - cur == it.tiles - tile;
     const bool direct = begins && ends;
     float* out = part + (static_cast<int64_t>(c) * 2 + (begins ? 1 : 0)) * part_floats(D, ROWS);
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kPdWarps) {
+    for (int x = solo ? lane : threadIdx.x; x < rows * (D / 4); x += solo ? 32 : 32 * kPdWarps) {
       const int r = x / (D / 4), col = (x % (D / 4)) * 4;
       float mw[kPdWarps], mm = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kPdWarps; ++w) mm = fmaxf(mm, mw[w] = sml[w * 3 * ROWS + r]);
+      for (int w = 0; w < kPdWarps; ++w) mm = fmaxf(mm, mw[w] = sml[(solo ? warp : w) * 3 * ROWS + r]);
       float ll = 0.f, ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kPdWarps; ++w) {
-        const float f = part_weight(mw[w], mm);
+      for (int x = 0; x < kPdWarps; ++x) {
+        if (solo && x) break;
+        const int w = solo ? warp : x;
+        const float f = part_weight(mw[x], mm);
         ll += f * sml[w * 3 * ROWS + ROWS + r];
         ls += f * sml[w * 3 * ROWS + 2 * ROWS + r];
         const float4 v = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * D + (col ^ (((r >> 1) & 3) << 3)));
@@ -601,12 +664,13 @@ __global__ void __launch_bounds__(kPdThreads, 2)
         }
       }
     }
-    if (begins && threadIdx.x == 0 && (by_item || !ends)) {
+    if (!solo && begins && threadIdx.x == 0 && (by_item || !ends)) {
       const long long e = g0 + it.tiles;  // CTA c starts at total * c / n_act
       const int last = static_cast<int>((e * s.n_act + s.total - 1) / s.total - 1);
       parts[by_item ? it.b * HR + it.hr : c] = Part{it.b, it.hr, c, ends ? -1 : last};
     }
-    consumer_sync();  // the area is free for the next item
+    if (solo) __syncwarp();  // the area is free for the next item
+    else consumer_sync();
     g0 += it.tiles;
     cur = end;
     tile = 0;
@@ -677,12 +741,14 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 constexpr int kMaxCtas = 1024;  // of the decode kernel
 
+// CTAs that find a tile for each of their warps, if every sequence fills its table.
+int64_t most_ctas(int64_t items, int64_t keys, int tk) { return items * (((keys + tk - 1) / tk + kPdWarps - 1) / kPdWarps); }
+
 int row_tiles(int Hq, int H) { return (Hq / H + kPdRows - 1) / kPdRows; }
 
 template <int X, int C, int D, int NT>
 int launch_t(const PagedDecodeArgs& a) {
   using F = PdCfg<C, D, NT>;
-  static_assert(F::SMEM <= 115712, "two CTAs per SM");
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kStatusCuda;
@@ -704,8 +770,7 @@ int launch_t(const PagedDecodeArgs& a) {
   if (sms < 1) return kStatusCuda;
   const int64_t keys = static_cast<int64_t>(a.pages ? a.n_pages : a.kv.max_pages) * a.kv.page;
   const int64_t items = static_cast<int64_t>(a.kv.B) * a.kv.H * RT;
-  const int64_t most = items * ((keys + F::TK - 1) / F::TK);  // tiles, if every sequence fills its table
-  const int ctas = static_cast<int>(std::min<int64_t>(std::min(2 * sms, kMaxCtas), (most + kPdWarps - 1) / kPdWarps));
+  const int ctas = static_cast<int>(std::min<int64_t>(std::min(F::MINB * sms, kMaxCtas), most_ctas(items, keys, F::TK)));
   const int by_item = items <= ctas;
   Part* parts = reinterpret_cast<Part*>(a.ws);
   float* part = reinterpret_cast<float*>(a.ws + kMaxCtas * sizeof(Part));
@@ -736,8 +801,7 @@ int64_t paged_decode_workspace(int B, int Hq, int H, int d, int page, int n_page
   // Two partial results for each CTA, as many as the largest GPU of the family
   // could hold; a bound by the tiles keeps it small for small problems.
   const int64_t items = static_cast<int64_t>(B) * H * row_tiles(Hq, H);
-  const int64_t most = items * ((static_cast<int64_t>(n_pages) * page + 31) / 32);
-  const int64_t ctas = std::min<int64_t>(kMaxCtas, (most + kPdWarps - 1) / kPdWarps);
+  const int64_t ctas = std::min<int64_t>(kMaxCtas, most_ctas(items, static_cast<int64_t>(n_pages) * page, 32));
   return kMaxCtas * static_cast<int64_t>(sizeof(Part)) + ctas * 2 * part_floats(d, kPdRows) * 4;
 }
 

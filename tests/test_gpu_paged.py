@@ -568,18 +568,34 @@ def test_select_is_not_confused_by_bad_pages(pkg):
 
 
 def test_decode_any_list_of_pages(pkg):
-    """Lists need not come from the selection: any order, gaps, entries behind the end."""
+    """Lists need not come from the selection: any order, gaps, indices behind the end."""
     c = Case(pkg, [16 * 20 + 5, 30], H=2, d=64, seed=1)
     q = c.randn(2, 4, 64)
-    lists = torch.tensor([[[20, -1, 3, 7, 0, -1], [5, 21, 19, 1000, -7, 2]], [[-1] * 6, [1, 2, -1, -1, -1, 0]]],
+    lists = torch.tensor([[[20, -1, 3, 7, 0, -1], [5, 21, 19, 1000, -7, 2]], [[-1] * 6, [1, 2, -1, -1, -1, -1]]],
                          dtype=torch.int32)
     keys = [[[p * 16 + i for p in row if p >= 0 for i in range(16) if p * 16 + i < c.lens_list[b]]
              for row in rows.tolist()] for b, rows in enumerate(lists)]
     _check_decode(pkg, c, q, pages=lists.cuda(), keys=keys)
-    twice = torch.tensor([[[3, 3], [4, 0]], [[1, 1], [0, 1]]], dtype=torch.int32)
-    keys = [[[p * 16 + i for p in row for i in range(16) if p * 16 + i < c.lens_list[b]]
-             for row in rows.tolist()] for b, rows in enumerate(twice)]
-    _check_decode(pkg, c, q, pages=twice.cuda(), keys=keys)
+
+
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+@pytest.mark.parametrize("longest", [1, 60, 128, 256])
+def test_many_short_sequences(pkg, x, dtype, scales, longest):
+    """More items than warps, each a few tiles: a warp takes an item for itself."""
+    g = torch.Generator().manual_seed(longest)
+    lens = [int(v) for v in torch.randint(0, longest + 1, (230,), generator=g)]
+    for d, heads, Hq in ((64, 16, 32), (128, 8, 96)):
+        c = Case(pkg, lens, H=heads, d=d, dtype=dtype, scales=scales, seed=longest)
+        _check_decode(pkg, c, c.randn(len(lens), Hq, d, dtype=x))
+
+
+def test_many_short_sequences_through_lists(pkg):
+    lens = [i % 40 for i in range(200)]
+    c = Case(pkg, lens, H=16, page=8, d=32, dtype=F16, seed=1, summaries=True)
+    q = c.randn(200, 32, 32)
+    pages, want = _check_select(pkg, c, q, 3)
+    keys = [[[p * 8 + i for p in row for i in range(8) if p * 8 + i < lens[b]] for row in rows] for b, rows in enumerate(want)]
+    _check_decode(pkg, c, q, pages=pages, keys=keys)
 
 
 # ------------------------------------------------------------------ together
