@@ -35,6 +35,8 @@ namespace {
 constexpr int kPdWarps = 4;  // consumers
 constexpr int kPdThreads = 32 * (kPdWarps + 1);
 constexpr int kPdRows = 16;  // query heads of an item, at most
+constexpr int kPdExtra = 4;  // tiles that an item's start and end are worth, where shares have
+constexpr int kPdShare = 16; // this many tiles or more
 constexpr int kPdSolo = 4;  // tiles up to which a warp takes a whole item
 
 template <int C, int D, int NT>  // NT: groups of 8 query heads
@@ -77,9 +79,9 @@ __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (
 __device__ __forceinline__ float part_weight(float m, float mm) { return m == -INFINITY ? 1.f : ex2_approx(m - mm); }
 
 struct Sched {
-  long long t0, total;
-  int b, hr, tile, n;  // first tile of the CTA and how many it has
-  int n_act, solo, abort_flag;
+  long long w0, total, bound_tile[2];  // share's start and the whole, in weights; tiles before the share's bounds
+  int b, hr, tile;  // first tile of the CTA
+  int n_act, extra, solo, abort_flag;
   int up[2];  // tiles from a bound of the share to the next item's start
   long long warp_sum[kPdThreads / 32];
   int warp_most[kPdThreads / 32], warp_live[kPdThreads / 32];
@@ -124,7 +126,14 @@ __device__ __forceinline__ int tiles_of(const PagedDecodeArgs& a, int len) {
   return ((a.pages ? min(a.n_pages, (len + a.kv.page - 1) / a.kv.page) * a.kv.page : len) + TK - 1) / TK;
 }
 
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Finds the CTA's share of the tiles.  All threads; B numbers are read once.
+// An item costs its tiles and a start and an end (queries, merge): `extra` tiles'
+// worth, laid before its tiles, so that a share of many short items gets fewer.
 // Where every item is short and there are many, items are not cut ("solo"): a
 // CTA has those that begin in its share, and a warp takes each for itself.
 template <int TK>
@@ -133,57 +142,70 @@ __device__ __forceinline__ void find_share(const PagedDecodeArgs& a, int HR, Sch
   const int per = (B + kPdThreads - 1) / kPdThreads;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   long long mine = 0;
-  int most = 0, live = 0;
+  int most = 0, alive = 0;  // longest item, sequences with tokens
   for (int b = b0; b < b1; ++b) {
     const int t = tiles_of<TK>(a, checked_len(a.kv, b));
-    mine += t, most = max(most, t), live += t > 0;
+    mine += t, most = max(most, t), alive += t > 0;
   }
   mine *= HR;
   long long upto = mine;
+  int before = alive;  // up to and with this thread's
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, upto, x);
-    if (lane >= x) upto += y;
+    const int z = __shfl_up_sync(0xffffffffu, before, x);
+    if (lane >= x) upto += y, before += z;
     most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
-    live += __shfl_xor_sync(0xffffffffu, live, x);
   }
-  if (lane == 31) s.warp_sum[tid >> 5] = upto, s.warp_most[tid >> 5] = most, s.warp_live[tid >> 5] = live;
-  if (tid == 0) s.n = 0, s.b = 0, s.hr = 0, s.tile = 0, s.t0 = 0, s.up[0] = s.up[1] = 0;
+  if (lane == 31) s.warp_sum[tid >> 5] = upto, s.warp_most[tid >> 5] = most, s.warp_live[tid >> 5] = before;
+  if (tid == 0) s.b = s.hr = s.tile = 0, s.w0 = 0, s.bound_tile[0] = s.bound_tile[1] = 0, s.up[0] = s.up[1] = 0;
   __syncthreads();
   long long total = 0;
-  most = live = 0;
+  int live = 0;
+  most = 0;
 #pragma unroll
   for (int i = 0; i < kPdThreads / 32; ++i) {
-    if (i < (tid >> 5)) upto += s.warp_sum[i];
+    if (i < (tid >> 5)) upto += s.warp_sum[i], before += s.warp_live[i];
     total += s.warp_sum[i];
     most = max(most, s.warp_most[i]), live += s.warp_live[i];
   }
   // Few tiles: a tile per consumer warp, in as many CTAs to every item.
   const long long items = static_cast<long long>(live) * HR;
-  const long long want = items ? items * ((total + items * kPdWarps - 1) / (items * kPdWarps)) : 0;
+  const long long want = items ? items * divide(total + items * kPdWarps - 1, items * kPdWarps) : 0;
   const int n_act = static_cast<int>(min(static_cast<long long>(gridDim.x), want));
   const bool solo = most <= kPdSolo && items >= kPdWarps * static_cast<long long>(gridDim.x);
+  const int extra = total >= kPdShare * static_cast<long long>(n_act) ? kPdExtra : 0;
+  total += items * extra;
+  mine += static_cast<long long>(alive) * HR * extra;
+  upto += static_cast<long long>(before) * HR * extra;
   const int c = blockIdx.x;
-  if (tid == 0) s.total = total, s.n_act = n_act, s.solo = solo;
+  if (tid == 0) s.total = total, s.n_act = n_act, s.extra = extra, s.solo = solo;
   if (c < n_act) {
-    const long long bound[2] = {total * c / n_act, total * (c + 1) / n_act};
+    const long long bound[2] = {divide(total * c, n_act), divide(total * (c + 1), n_act)};
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const long long t0 = bound[x];
-      if (!(upto - mine <= t0 && t0 < upto)) continue;
-      long long at = upto - mine;
+      const long long w = bound[x];
+      if (x == 1 && w == total) {  // the last share ends with all
+        if (tid == 0) s.bound_tile[1] = total - items * extra;
+        continue;
+      }
+      if (!(upto - mine <= w && w < upto)) continue;
+      long long at = upto - mine, tiles = at - static_cast<long long>(before - alive) * HR * extra;
       for (int b = b0; b < b1; ++b) {
-        const long long t = tiles_of<TK>(a, checked_len(a.kv, b));
-        if (t0 < at + t * HR) {
-          const int tile = static_cast<int>((t0 - at) % t);
-          s.up[x] = tile ? static_cast<int>(t) - tile : 0;
-          if (x == 0) s.b = b, s.hr = static_cast<int>((t0 - at) / t), s.tile = tile;
+        const int t = tiles_of<TK>(a, checked_len(a.kv, b));
+        if (t == 0) continue;
+        if (w < at + static_cast<long long>(t + extra) * HR) {
+          const int hr = static_cast<int>(divide(w - at, t + extra));
+          const int tile = max(0, static_cast<int>(w - at - static_cast<long long>(hr) * (t + extra)) - extra);
+          s.up[x] = tile ? t - tile : 0;
+          s.bound_tile[x] = tiles + static_cast<long long>(hr) * t + tile;
+          if (x == 0) s.b = b, s.hr = hr, s.tile = tile, s.w0 = at + static_cast<long long>(hr) * (t + extra);
           break;
         }
-        at += t * HR;
+        at += static_cast<long long>(t + extra) * HR;
+        tiles += static_cast<long long>(t) * HR;
       }
     }
-    if (tid == 0) s.t0 = bound[0], s.n = static_cast<int>(bound[1] - bound[0]);
   }
   __syncthreads();
 }
@@ -243,7 +265,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   find_share<TK>(a, HR, s);
   const bool solo = s.solo;
   // Solo: from the first item that begins here to the end of the last one.
-  const int n = solo && s.n > 0 ? s.n - s.up[0] + s.up[1] : s.n;
+  const int share = static_cast<int>(s.bound_tile[1] - s.bound_tile[0]);
+  const int n = solo ? share - s.up[0] + s.up[1] : share;
   const int c = blockIdx.x;
 
   // Sequences without tokens: o = 0, lse = -inf.
@@ -372,7 +395,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   const uint32_t ones = BF ? 0x3f803f80u : 0x3c003c00u;
   bool ok = true;
   int cur = 0, turn = 0;       // tiles of the CTA that are done, and of this warp
-  long long g0 = s.t0 - tile;  // first tile of the item, counted from the start of all
+  long long w0 = s.w0;         // start of the item, in weights
   for (int item = 0; cur < n && it.tiles > tile; ++item) {
     const int end = min(n, cur + it.tiles - tile);
     // This warp's tiles of the item.
@@ -665,13 +688,13 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       }
     }
     if (!solo && begins && threadIdx.x == 0 && (by_item || !ends)) {
-      const long long e = g0 + it.tiles;  // CTA c starts at total * c / n_act
-      const int last = static_cast<int>((e * s.n_act + s.total - 1) / s.total - 1);
+      const long long e = w0 + s.extra + it.tiles;  // CTA c starts at total * c / n_act
+      const int last = static_cast<int>(divide(e * s.n_act + s.total - 1, s.total) - 1);
       parts[by_item ? it.b * HR + it.hr : c] = Part{it.b, it.hr, c, ends ? -1 : last};
     }
     if (solo) __syncwarp();  // the area is free for the next item
     else consumer_sync();
-    g0 += it.tiles;
+    w0 += s.extra + it.tiles;
     cur = end;
     tile = 0;
     if (cur < n) next_item<TK>(a, HR, it);
