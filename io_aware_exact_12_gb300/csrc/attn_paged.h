@@ -131,10 +131,15 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 bytes (low half of the word) as two fp16 values; exact.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
+// Two e4m3 bytes (the low or high half of a word) as two fp16 values; exact.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t four) {
   uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(four));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_pair_hi(uint32_t four) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(four));
   return r;
 }
 

@@ -64,7 +64,7 @@ template <int C>
 __device__ __forceinline__ void load_pairs(const uint8_t* p, uint32_t (&w)[4]) {
   if constexpr (C == kTypeE4m3) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = e4m3_pair(v.x), w[1] = e4m3_pair(v.x >> 16), w[2] = e4m3_pair(v.y), w[3] = e4m3_pair(v.y >> 16);
+    w[0] = e4m3_pair(v.x), w[1] = e4m3_pair_hi(v.x), w[2] = e4m3_pair(v.y), w[3] = e4m3_pair_hi(v.y);
   } else {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
@@ -95,7 +95,7 @@ __device__ __forceinline__ void round_store(uint8_t* p, const float (&f)[8], uin
                        __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3))
                    << ((i & 1) * 16);
     *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
-    w[0] = e4m3_pair(v[0]), w[1] = e4m3_pair(v[0] >> 16), w[2] = e4m3_pair(v[1]), w[3] = e4m3_pair(v[1] >> 16);
+    w[0] = e4m3_pair(v[0]), w[1] = e4m3_pair_hi(v[0]), w[2] = e4m3_pair(v[1]), w[3] = e4m3_pair_hi(v[1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack2<C == kTypeBf16>(f[2 * i], f[2 * i + 1]);

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
       for (int s = 0; s < NS; ++s) {
         uint32_t l0, l1, h0, h1;
         if constexpr (E8) {
-          l0 = e4m3_pair(lo[s]), l1 = e4m3_pair(lo[s] >> 16), h0 = e4m3_pair(hi[s]), h1 = e4m3_pair(hi[s] >> 16);
+          l0 = e4m3_pair(lo[s]), l1 = e4m3_pair_hi(lo[s]), h0 = e4m3_pair(hi[s]), h1 = e4m3_pair_hi(hi[s]);
         } else {
           l0 = lo[2 * s], l1 = lo[2 * s + 1], h0 = hi[2 * s], h1 = hi[2 * s + 1];
         }
