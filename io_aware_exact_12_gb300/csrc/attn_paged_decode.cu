@@ -269,21 +269,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   const int n = solo ? share - s.up[0] + s.up[1] : share;
   const int c = blockIdx.x;
 
-  // Sequences without tokens: o = 0, lse = -inf.
-  for (int b = c; b < kv.B; b += gridDim.x) {
-    if (tiles_of<TK>(a, checked_len(kv, b))) continue;
-    for (int i = threadIdx.x; i < a.Hq * D / 8; i += kPdThreads)
-      reinterpret_cast<uint4*>(a.o + static_cast<int64_t>(b) * a.Hq * D * 2)[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = threadIdx.x; i < a.Hq; i += kPdThreads) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
-    if (by_item)
-      for (int i = threadIdx.x; i < HR; i += kPdThreads) parts[b * HR + i] = Part{0, 0, 0, -1};
-  }
-  if (!by_item && threadIdx.x == 0) parts[c] = Part{0, 0, 0, -1};  // the last item may set it below
-  if (n == 0) return;
-  __syncthreads();
-
   volatile int* abort_flag = &s.abort_flag;
-  Item it = {s.b, s.hr, 0, 0};
+  Item it = {s.b, s.hr, 0, 0};  // sequence 0 where there is no tile
   it.len = checked_len(kv, it.b);
   it.tiles = tiles_of<TK>(a, it.len);
   int tile = s.tile;
@@ -293,6 +280,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   }
 
   if (warp == kPdWarps) {  // ---------------------------------- producer warp
+    if (n == 0) return;
     // Each lane looks up one box (box_rows keys of one page) of the next
     // tiles, so one round trip through list and table serves 32 boxes.
     const int nb = TK / box_rows, batch = 32 / nb;  // boxes of a tile, tiles of a batch
@@ -383,6 +371,17 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   }
 
   // ------------------------------------------------------------ consumer warps
+  // Sequences without tokens: o = 0, lse = -inf; while the first loads travel.
+  for (int b = c; b < kv.B; b += gridDim.x) {
+    if (tiles_of<TK>(a, checked_len(kv, b))) continue;
+    for (int i = threadIdx.x; i < a.Hq * D / 8; i += 32 * kPdWarps)
+      reinterpret_cast<uint4*>(a.o + static_cast<int64_t>(b) * a.Hq * D * 2)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < a.Hq; i += 32 * kPdWarps) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
+    if (by_item)
+      for (int i = threadIdx.x; i < HR; i += 32 * kPdWarps) parts[b * HR + i] = Part{0, 0, 0, -1};
+  }
+  if (!by_item && threadIdx.x == 0) parts[c] = Part{0, 0, 0, -1};  // the last item may set it below
+
   // Both products have the cache as the 16-row operand and the query heads as
   // the 8 (NT = 2: 16) columns, so that few heads waste little:
   //   S^T [keys, heads] = K Q^T,  O^T [channels, heads] += V^T P^T.

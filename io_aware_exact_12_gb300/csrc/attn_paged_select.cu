@@ -22,6 +22,7 @@
 //       above are in, those below L - 2 eps out, and only those between (a few)
 //       are scored again, to 48 bits.  With eps = inf (a sum that overflowed or is
 //       NaN) that is all of them, in fp64.
+#include <atomic>
 #include <cmath>
 
 #include "attn_paged.h"
@@ -32,9 +33,9 @@ namespace {
 
 constexpr int kScoreWarps = 2;
 constexpr int kScoreThreads = 32 * kScoreWarps;
-constexpr int kScoreFill = 8;
 constexpr int kScoreDepth = 4;                  // groups of 8 pages in flight per warp
-constexpr int kScoreChunk = 8 * kScoreWarps * 4;  // pages of a CTA, times 1 to 8
+constexpr int kScoreStep = 8 * kScoreWarps;     // pages of a CTA's turn
+constexpr int kScoreChunk = 4 * kScoreStep;     // pages of a CTA, at least
 constexpr int kPickThreads = 1024;
 constexpr int kPickCap = 1024;  // candidates kept in shared memory
 
@@ -600,13 +601,23 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
 
 template <int X, int C, int D>
 int launch_t(const PagedSelectArgs& a) {
-  // Long walks amortise a CTA's start, as long as they leave eight CTAs to an SM.
-  int chunk = kScoreChunk;
-  while (chunk < 8 * kScoreChunk && static_cast<int64_t>(a.kv.max_pages / (2 * chunk)) * a.kv.B * a.kv.H >=
-                                        kScoreFill * std::max(1, device_sm_count()))
-    chunk *= 2;
-  const dim3 grid((a.kv.max_pages + chunk - 1) / chunk * a.kv.H, a.kv.B);
+  // A CTA takes 4 us to its first result and 0.6 us a turn from there, so the
+  // walks are as long as it takes for all CTAs to be resident at once, and not
+  // shorter than four turns (against runs of 128 pages: selection and decode of 8
+  // sequences of 4096 pages 131 -> 129 us, 4 of 8192 in e4m3 46 -> 44).
   auto score = a.Hq / a.kv.H > 8 ? attn_paged_score_kernel<X, C, D, true> : attn_paged_score_kernel<X, C, D, false>;
+  static std::atomic<int> per_sm[2];
+  int fit = per_sm[a.Hq / a.kv.H > 8].load();
+  if (fit < 1) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, score, kScoreThreads, 0) != cudaSuccess || fit < 1)
+      return kStatusCuda;
+    per_sm[a.Hq / a.kv.H > 8].store(fit);
+  }
+  const int64_t heads = static_cast<int64_t>(a.kv.B) * a.kv.H;
+  const int64_t each = std::max<int64_t>(1, static_cast<int64_t>(fit) * std::max(1, device_sm_count()) / heads);  // CTAs of a head
+  const int64_t steps = (a.kv.max_pages + kScoreStep - 1) / kScoreStep;
+  const int chunk = static_cast<int>(std::max<int64_t>(kScoreChunk, (steps + each - 1) / each * kScoreStep));
+  const dim3 grid((a.kv.max_pages + chunk - 1) / chunk * a.kv.H, a.kv.B);
   if (launch_serialized(true, score, grid, dim3(kScoreThreads), 0, a.stream, a, chunk) != cudaSuccess) return kStatusCuda;
   return launch_serialized(true, attn_paged_pick_kernel<X, C, D>, dim3(a.kv.B * a.kv.H), dim3(kPickThreads), 0, a.stream,
                            a, chunk) == cudaSuccess
