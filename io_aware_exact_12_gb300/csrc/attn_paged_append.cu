@@ -171,8 +171,10 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
   else if (item < 2 * k_items + a.Hq * per_head) kind = 2, h = (item - 2 * k_items) / per_head, i = item % per_head;
   else kind = 3, h = 0, i = 0;  // only helps its warp to fetch the angles
   const bool turn = (kind == 0 || kind == 2) && i < a.rot / 16;
-  int c0 = 16 * i, c1 = 16 * i + 8;  // first channels of the two chunks
-  if (turn && !a.interleaved) c0 = 8 * i, c1 = a.rot / 2 + 8 * i;
+  // First channels of the two chunks: halves of the rotated channels, or of the
+  // others, apart, so that neighbouring threads' chunks are neighbours in memory.
+  const int base = kind == 1 || turn ? 0 : a.rot, range = kind == 1 ? kv.d : turn ? a.rot : kv.d - a.rot;
+  const int c0 = base + 8 * (i - base / 16), c1 = c0 + range / 2;
 
   const PagedRows& in = kind == 0 ? a.k : kind == 1 ? a.v : a.q;
   const uint8_t* src = in.p + r0 * in.row + h * in.head;
@@ -229,10 +231,12 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
     const uint4 xw = load_shared16(at), yw = load_shared16(at + kAppendThreads * 16);
     float cs[8], sn[8];
     if (turn) {
-      const uint32_t tb = tables + (t % kAppendDepth) * (kWarps * kTable) + 32 * i;
+      // Eight angles: of channels c0 .. c0 + 7, or of four pairs in either chunk.
+      const uint32_t tb = tables + (t % kAppendDepth) * (kWarps * kTable);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint4 u = load_shared16(tb + 16 * e), v = load_shared16(tb + half * 4 + 16 * e);
+        const uint32_t from = tb + (a.interleaved ? (e ? c1 : c0) * 2 : c0 * 4 + 16 * e);
+        const uint4 u = load_shared16(from), v = load_shared16(from + half * 4);
         cs[4 * e] = __uint_as_float(u.x), cs[4 * e + 1] = __uint_as_float(u.y);
         cs[4 * e + 2] = __uint_as_float(u.z), cs[4 * e + 3] = __uint_as_float(u.w);
         sn[4 * e] = __uint_as_float(v.x), sn[4 * e + 1] = __uint_as_float(v.y);
