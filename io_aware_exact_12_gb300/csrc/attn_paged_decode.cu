@@ -21,7 +21,8 @@
 //       page tables and keeps a ring of TMA loads in flight, boxes of rows that
 //       never cross a page; four consumer warps take tiles in turn, each with an
 //       online softmax of its own, and are merged in shared memory where an
-//       item ends.
+//       item ends.  Short items go whole to clusters of CTAs instead, which join
+//       their results through shared memory.
 //   attn_paged_merge_kernel : joins the items that were cut by a CTA border.
 #include <atomic>
 #include <cmath>
@@ -105,6 +106,27 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
+}
+// Barrier over the cluster's threads; what they wrote before it, also to shared
+// memory, is visible to all behind it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of another CTA's shared memory in the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_cluster16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_cluster4(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
                                             int c3) {
@@ -237,7 +259,8 @@ __device__ __forceinline__ void store_out4(uint8_t* p, const float (&o)[4]) {
 template <int X, int C, int D, int NT>
 __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     attn_paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                             const PagedDecodeArgs a, int RT, int box_rows, int by_item, Part* parts, float* part) {
+                             const PagedDecodeArgs a, int RT, int box_rows, int cluster, int by_item, Part* parts,
+                             float* part) {
   using F = PdCfg<C, D, NT>;
   constexpr int TK = F::TK, ROWS = F::ROWS;
   constexpr bool BF = C == kTypeBf16;
@@ -262,7 +285,19 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   }
   griddep_wait();  // launched overlapped (launch_serialized)
   griddep_launch_dependents();
-  find_share<TK>(a, HR, s);
+  if (cluster) {
+    // An item to each cluster, its tiles in equal runs to the CTAs.
+    if (threadIdx.x == 0) {
+      const int item = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+      s.b = item / HR, s.hr = item % HR;
+      const long long t = tiles_of<TK>(a, checked_len(kv, s.b));
+      s.bound_tile[0] = s.tile = static_cast<int>(t * rank / cluster), s.bound_tile[1] = t * (rank + 1) / cluster;
+      s.w0 = 0, s.total = 1, s.n_act = 1, s.extra = 0, s.solo = 0, s.up[0] = s.up[1] = 0;
+    }
+    __syncthreads();
+  } else {
+    find_share<TK>(a, HR, s);
+  }
   const bool solo = s.solo;
   // Solo: from the first item that begins here to the end of the last one.
   const int share = static_cast<int>(s.bound_tile[1] - s.bound_tile[0]);
@@ -280,7 +315,6 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   }
 
   if (warp == kPdWarps) {  // ---------------------------------- producer warp
-    if (n == 0) return;
     // Each lane looks up one box (box_rows keys of one page) of the next
     // tiles, so one round trip through list and table serves 32 boxes.
     const int nb = TK / box_rows, batch = 32 / nb;  // boxes of a tile, tiles of a batch
@@ -367,12 +401,16 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
                global_timer_ns() - since < kWaitLimitNs) {
         }
       }
+    if (cluster) {
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
   // ------------------------------------------------------------ consumer warps
   // Sequences without tokens: o = 0, lse = -inf; while the first loads travel.
-  for (int b = c; b < kv.B; b += gridDim.x) {
+  for (int b = c; b < kv.B && !cluster; b += gridDim.x) {
     if (tiles_of<TK>(a, checked_len(kv, b))) continue;
     for (int i = threadIdx.x; i < a.Hq * D / 8; i += 32 * kPdWarps)
       reinterpret_cast<uint4*>(a.o + static_cast<int64_t>(b) * a.Hq * D * 2)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -380,7 +418,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     if (by_item)
       for (int i = threadIdx.x; i < HR; i += 32 * kPdWarps) parts[b * HR + i] = Part{0, 0, 0, -1};
   }
-  if (!by_item && threadIdx.x == 0) parts[c] = Part{0, 0, 0, -1};  // the last item may set it below
+  if (!by_item && !cluster && threadIdx.x == 0) parts[c] = Part{0, 0, 0, -1};  // the last item may set it below
 
   // Both products have the cache as the 16-row operand and the query heads as
   // the 8 (NT = 2: 16) columns, so that few heads waste little:
@@ -651,8 +689,10 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     if (solo) __syncwarp();
     else consumer_sync();
     const bool begins = tile == 0, ends = end - cur == it.tiles - tile;
-    const bool direct = begins && ends;
-    float* out = part + (static_cast<int64_t>(c) * 2 + (begins ? 1 : 0)) * part_floats(D, ROWS);
+    const bool direct = begins && ends && !cluster;
+    // In a cluster the partial result stays in shared memory, where the ring was.
+    float* out = cluster ? reinterpret_cast<float*>(smem)
+                         : part + (static_cast<int64_t>(c) * 2 + (begins ? 1 : 0)) * part_floats(D, ROWS);
     for (int x = solo ? lane : threadIdx.x; x < rows * (D / 4); x += solo ? 32 : 32 * kPdWarps) {
       const int r = x / (D / 4), col = (x % (D / 4)) * 4;
       float mw[kPdWarps], mm = -INFINITY;
@@ -685,7 +725,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
         }
       }
     }
-    if (!solo && begins && threadIdx.x == 0 && (by_item || !ends)) {
+    if (!cluster && !solo && begins && threadIdx.x == 0 && (by_item || !ends)) {
       const long long e = w0 + s.extra + it.tiles;  // CTA c starts at total * c / n_act
       const int last = static_cast<int>(divide(e * s.n_act + s.total - 1, s.total) - 1);
       parts[by_item ? it.b * HR + it.hr : c] = Part{it.b, it.hr, c, ends ? -1 : last};
@@ -696,6 +736,40 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     cur = end;
     tile = 0;
     if (cur < n) next_item<TK>(a, HR, it);
+  }
+  if (cluster) {
+    // Join of the cluster's partial results, in the order of the CTAs.
+    const float* mine = reinterpret_cast<const float*>(smem);
+    if (n == 0 && threadIdx.x < ROWS) const_cast<float*>(mine)[ROWS * (D + 1) + threadIdx.x] = 0.f;  // l: nothing seen
+    cluster_sync();
+    const int h = s.hr / RT, r0 = (s.hr % RT) * ROWS, rows = min(ROWS, G - r0), rank = blockIdx.x % cluster;
+    for (int x = rank * 32 * kPdWarps + threadIdx.x; x < rows * (D / 4); x += cluster * 32 * kPdWarps) {
+      const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+      const uint32_t at = smem_addr(mine);
+      float mm = -INFINITY;
+      for (int k = 0; k < cluster; ++k) {
+        const uint32_t p = in_cta(at, k);
+        if (load_cluster4(p + (ROWS * (D + 1) + r) * 4) != 0.f) mm = fmaxf(mm, load_cluster4(p + (ROWS * D + r) * 4));
+      }
+      float ll = 0.f, ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < cluster; ++k) {
+        const uint32_t p = in_cta(at, k);
+        const float l = load_cluster4(p + (ROWS * (D + 1) + r) * 4);
+        if (l == 0.f) continue;
+        const float f = part_weight(load_cluster4(p + (ROWS * D + r) * 4), mm);
+        const float4 v = load_cluster16(p + (r * D + col) * 4);
+        ll += f * l;
+        ls += f * load_cluster4(p + (ROWS * (D + 2) + r) * 4);
+        acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+      }
+      const float inv = ls == 0.f ? 0.f : kv.v_scale / ls;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) acc[y] *= inv;
+      const int64_t to = static_cast<int64_t>(s.b) * a.Hq + static_cast<int64_t>(h) * G + r0 + r;
+      store_out4<X>(a.o + (to * D + col) * 2, acc);
+      if (col == 0) a.lse[to] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+    }
+    cluster_sync();  // nobody's shared memory goes before it is read
   }
 }
 
@@ -767,8 +841,42 @@ int64_t most_ctas(int64_t items, int64_t keys, int tk) { return items * (((keys 
 
 int row_tiles(int Hq, int H) { return (Hq / H + kPdRows - 1) / kPdRows; }
 
+// CTAs of a cluster for short items, or 0: the join through shared memory saves
+// the partial results' way through L2 and the merge kernel (one sequence of 1000
+// 10.2 -> 8.7 us, 16 of up to 200 16.4 -> 8.4).  A warp has one tile, or two where
+// the clusters have more CTAs than the GPU has SMs (else cutting the items finer is
+// faster: one sequence of 2000 10.5 against 10.3 us).  The clusters may be twice
+// what is resident at once (64 sequences of up to 100 13.6 against 16.6 us; four
+// times: 32 of up to 300 25.6 against 17.2), unless most warps would have nothing
+// to do (64 of up to 20 12.6 against 10.9).
+int cluster_size(int64_t items, int64_t tiles, int sms) {
+  for (int k = 1; k <= 8; k *= 2)
+    if (k * kPdWarps >= tiles || (k == 8 && 2 * k * kPdWarps >= tiles && items * k > sms))
+      return items * k <= (2 * tiles > kPdWarps ? 4 : 2) * sms ? k : 0;
+  return 0;
+}
+
+template <typename Kernel>
+cudaError_t launch_clusters(Kernel kern, int ctas, int cluster, size_t smem, cudaStream_t stream, const CUtensorMap& mk,
+                            const CUtensorMap& mv, const PagedDecodeArgs& a, int RT, int box, int size) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, mk, mv, a, RT, box, size, 0, static_cast<Part*>(nullptr), static_cast<float*>(nullptr));
+}
+
 template <int X, int C, int D, int NT>
-int launch_t(const PagedDecodeArgs& a) {
+int launch_t(const PagedDecodeArgs& a, int* launches) {
   using F = PdCfg<C, D, NT>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
@@ -791,6 +899,14 @@ int launch_t(const PagedDecodeArgs& a) {
   if (sms < 1) return kStatusCuda;
   const int64_t keys = static_cast<int64_t>(a.pages ? a.n_pages : a.kv.max_pages) * a.kv.page;
   const int64_t items = static_cast<int64_t>(a.kv.B) * a.kv.H * RT;
+  const int cluster = cluster_size(items, (keys + F::TK - 1) / F::TK, sms);
+  if (cluster) {
+    *launches = 1;
+    return launch_clusters(kern, static_cast<int>(items) * cluster, cluster, F::SMEM, a.stream, mk, mv, a, RT, box, cluster) ==
+                   cudaSuccess
+               ? kStatusOk
+               : kStatusCuda;
+  }
   const int ctas = static_cast<int>(std::min<int64_t>(std::min(F::MINB * sms, kMaxCtas), most_ctas(items, keys, F::TK)));
   const int by_item = items <= ctas;
   Part* parts = reinterpret_cast<Part*>(a.ws);
@@ -799,7 +915,7 @@ int launch_t(const PagedDecodeArgs& a) {
   // one's last blocks: two per SM.  Of three per SM some did not, and started not
   // when those blocks ended but when a CTA of their own kernel did (e4m3 heads 119
   // against 97 us); for the others it saves up to 1 us.
-  if (launch_serialized(ctas <= 2 * sms, kern, dim3(ctas), dim3(kPdThreads), F::SMEM, a.stream, mk, mv, a, RT, box, by_item, parts,
+  if (launch_serialized(ctas <= 2 * sms, kern, dim3(ctas), dim3(kPdThreads), F::SMEM, a.stream, mk, mv, a, RT, box, 0, by_item, parts,
                         part) != cudaSuccess)
     return kStatusCuda;
   const dim3 grid(by_item ? static_cast<int>(items) : ctas, std::min(F::ROWS, a.Hq / a.kv.H));
@@ -811,12 +927,12 @@ int launch_t(const PagedDecodeArgs& a) {
 }
 
 template <int X, int C>
-int launch_d(const PagedDecodeArgs& a) {
+int launch_d(const PagedDecodeArgs& a, int* launches) {
   const bool wide = a.Hq / a.kv.H > 8;
   switch (a.kv.d) {
-    case 32: return wide ? launch_t<X, C, 32, 2>(a) : launch_t<X, C, 32, 1>(a);
-    case 64: return wide ? launch_t<X, C, 64, 2>(a) : launch_t<X, C, 64, 1>(a);
-    default: return wide ? launch_t<X, C, 128, 2>(a) : launch_t<X, C, 128, 1>(a);
+    case 32: return wide ? launch_t<X, C, 32, 2>(a, launches) : launch_t<X, C, 32, 1>(a, launches);
+    case 64: return wide ? launch_t<X, C, 64, 2>(a, launches) : launch_t<X, C, 64, 1>(a, launches);
+    default: return wide ? launch_t<X, C, 128, 2>(a, launches) : launch_t<X, C, 128, 1>(a, launches);
   }
 }
 
@@ -833,8 +949,8 @@ int64_t paged_decode_workspace(int B, int Hq, int H, int d, int page, int n_page
 int launch_paged_decode(const PagedDecodeArgs& a, int* launches) {
   *launches = 2;
   if (a.x_type == kTypeBf16)
-    return a.kv.type == kTypeE4m3 ? launch_d<kTypeBf16, kTypeE4m3>(a) : launch_d<kTypeBf16, kTypeBf16>(a);
-  return a.kv.type == kTypeE4m3 ? launch_d<kTypeF16, kTypeE4m3>(a) : launch_d<kTypeF16, kTypeF16>(a);
+    return a.kv.type == kTypeE4m3 ? launch_d<kTypeBf16, kTypeE4m3>(a, launches) : launch_d<kTypeBf16, kTypeBf16>(a, launches);
+  return a.kv.type == kTypeE4m3 ? launch_d<kTypeF16, kTypeE4m3>(a, launches) : launch_d<kTypeF16, kTypeF16>(a, launches);
 }
 
 }  // namespace attn

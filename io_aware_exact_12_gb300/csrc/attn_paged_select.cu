@@ -38,6 +38,7 @@ constexpr int kScoreStep = 8 * kScoreWarps;     // pages of a CTA's turn
 constexpr int kScoreChunk = 4 * kScoreStep;     // pages of a CTA, at least
 constexpr int kPickThreads = 1024;
 constexpr int kPickCap = 1024;  // candidates kept in shared memory
+constexpr int kPickHeld = 8;    // scores that a thread keeps in registers
 
 struct SelectScratch {  // per (sequence, head)
   float* score;         // [max_pages]
@@ -308,11 +309,30 @@ __device__ __forceinline__ uint32_t key32(float x) {
 }
 __device__ __forceinline__ float of_key32(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
 
-template <int X>
-__device__ __forceinline__ float load1(const uint8_t* p, int i) {
-  if constexpr (X == kTypeBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-  else if constexpr (X == kTypeF16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
-  else return __half2float(__half(__nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3)));
+// N consecutive elements as fp32, 4 to 32 bytes.
+template <int TYPE, int N>
+__device__ __forceinline__ void load_channels(const uint8_t* p, float (&f)[N]) {
+  constexpr int W = N * (TYPE == kTypeE4m3 ? 1 : 2) / 4;  // words
+  uint32_t w[W];
+  if constexpr (W >= 4) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  } else if constexpr (W == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float2 x;
+    if constexpr (TYPE == kTypeE4m3) x = unpack2<false>((i & 1) ? e4m3_pair_hi(w[i / 2]) : e4m3_pair(w[i / 2]));
+    else x = unpack2<TYPE == kTypeBf16>(w[i]);
+    f[2 * i] = x.x, f[2 * i + 1] = x.y;
+  }
 }
 
 struct PickShared {
@@ -363,7 +383,10 @@ __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, i
   const int lane = threadIdx.x & 31, c0 = (lane & 7) * (D / 8);
   const int id = checked_page(a.kv, b, j);
   if (id < 0) return 0;
-  const int64_t at = (static_cast<int64_t>(id) * a.kv.H + h) * D * CB;
+  const int64_t at = ((static_cast<int64_t>(id) * a.kv.H + h) * D + c0) * CB;
+  float lo[D / 8], hi[D / 8];
+  load_channels<C>(a.kv.kmin + at, lo);
+  load_channels<C>(a.kv.kmax + at, hi);
   double best = -INFINITY;
   Two top = {-INFINITY, 0.f};
   for (int g0 = 0; g0 < G; g0 += 4) {
@@ -371,10 +394,11 @@ __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, i
     const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + g) * a.q.head;
     Two s = {0.f, 0.f};
     double d = 0.0;
+    float qf[D / 8];
+    load_channels<X>(q + c0 * 2, qf);
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
-      const float x = load1<X>(q, c0 + i);
-      const float k = x >= 0.f ? load1<C>(a.kv.kmax + at, c0 + i) : load1<C>(a.kv.kmin + at, c0 + i);
+      const float x = qf[i], k = x >= 0.f ? hi[i] : lo[i];
       if constexpr (WORDS) {
         const Two t = two_sum(s.hi, __fmul_rn(x, k));
         s = {t.hi, __fadd_rn(s.lo, t.lo)};
@@ -417,16 +441,34 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
   const PagedKv& kv = a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / kv.H, h = blockIdx.x % kv.H, G = a.Hq / kv.H;
+  // The first scores of each thread, before it is known how many there are; the
+  // scratch behind them is there, and what it holds is not looked at.
+  const SelectScratch sc = scratch_of(a.ws, blockIdx.x, kv.max_pages);
+  float* score = sc.score;
+  float held[kPickHeld];
+#pragma unroll
+  for (int i = 0; i < kPickHeld; ++i) {
+    const int j = i * kPickThreads + tid;
+    held[i] = j < kv.max_pages ? score[j] : 0.f;
+  }
   const int used = (checked_len(kv, b) + kv.page - 1) / kv.page;
   int* out = a.pages + static_cast<int64_t>(blockIdx.x) * a.n_select;
   if (used <= a.n_select) {
     for (int i = tid; i < a.n_select; i += kPickThreads) out[i] = i < used ? i : -1;
     return;
   }
-  const SelectScratch sc = scratch_of(a.ws, blockIdx.x, kv.max_pages);
-  float* score = sc.score;
   const int first = a.keep_first, end = used - a.keep_last;  // the pages that go by their score
   const int want = a.n_select - a.keep_first - a.keep_last;
+  // All scored pages of this thread, as they came.
+  auto each = [&](auto&& body) {
+#pragma unroll
+    for (int i = 0; i < kPickHeld; ++i) {
+      const int j = i * kPickThreads + tid;
+      if (j >= first && j < end) body(j, held[i]);
+    }
+    for (int j = kPickHeld * kPickThreads + tid; j < end; j += kPickThreads)
+      if (j >= first) body(j, score[j]);
+  };
   int turn = 0;
   float sure = INFINITY;  // pages with this score or more are in
   if (want > 0) {
@@ -435,11 +477,10 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
     constexpr float kNone = -3.402823466e38f;
     float least = INFINITY, most = -INFINITY, eps = 0.f;
     int none = 0;
-    for (int j = first + tid; j < end; j += kPickThreads) {
-      const float s = score[j];
+    each([&](int, float s) {
       none += s <= kNone;
       least = fminf(least, s <= kNone ? INFINITY : s), most = fmaxf(most, s);
-    }
+    });
     for (int i = tid; i < (used + chunk - 1) / chunk; i += kPickThreads) eps = fmaxf(eps, sc.eps[i]);
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -471,11 +512,10 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
         const float width = hi - lo, scale = 1024.f / width;
         if (width <= 4.f * eps || !(scale <= 1e37f)) break;
         int above = 0;
-        for (int j = first + tid; j < end; j += kPickThreads) {
-          const float s = score[j];
+        each([&](int, float s) {
           above += s > hi;
           if (s >= lo && s <= hi) atomicAdd(&sm.hist[min(1023, static_cast<int>((s - lo) * scale))], 1);
-        }
+        });
         turn ^= 1;
         above = block_sum(above, sm, turn);  // its barrier completes the histogram
         const int mine = sm.hist[1023 - tid];  // thread 0 has the highest bin
@@ -506,15 +546,14 @@ __global__ void __launch_bounds__(kPickThreads) attn_paged_pick_kernel(const Pag
     }
     // Pages that are in, and candidates.
     int in_all = 0;
-    for (int j = first + tid; j < end; j += kPickThreads) {
-      const float s = score[j];
+    each([&](int j, float s) {
       const bool in = eps < INFINITY && s >= sure;
       in_all += in;
       if (!in && s >= from) {
         const int at = atomicAdd(&sm.m, 1);
         if (at < kPickCap) sm.list[at] = j;
       }
-    }
+    });
     turn ^= 1;
     const int r = want - block_sum(in_all, sm, turn), m = sm.m;  // r of the m candidates are in
     const bool few = m <= kPickCap;

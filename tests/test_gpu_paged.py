@@ -766,3 +766,17 @@ def test_calls_on_a_side_stream_allocate_there(pkg):
     side.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert pkg.sync_status() == 0
+
+
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+@pytest.mark.parametrize("B,longest,d", [(1, 1000, 128), (1, 500, 64), (3, 250, 128), (5, 120, 32), (16, 200, 128), (2, 30, 64)])
+def test_short_items_in_clusters(pkg, x, dtype, scales, B, longest, d):
+    """Tables as wide as the longest sequence: an item goes to 1, 2, 4 or 8 CTAs, some of them without a tile."""
+    g = torch.Generator().manual_seed(B)
+    lens = [longest] + [int(v) for v in torch.randint(0, longest + 1, (B - 1,), generator=g)]
+    c = Case(pkg, lens, H=4, d=d, dtype=dtype, scales=scales, seed=B, width=-(-longest // 16))
+    _check_decode(pkg, c, c.randn(B, 12, d, dtype=x))
+    _check_decode(pkg, c, c.randn(B, 44, d, dtype=x))
+    c.lens_list = [0] * B
+    c.seq_lens.zero_()
+    _check_decode(pkg, c, c.randn(B, 12, d, dtype=x))
