@@ -38,7 +38,8 @@ constexpr int kScoreStep = 8 * kScoreWarps;     // pages of a CTA's turn
 constexpr int kScoreChunk = 4 * kScoreStep;     // pages of a CTA, at least
 constexpr int kPickThreads = 1024;
 constexpr int kPickCap = 1024;  // candidates kept in shared memory
-constexpr int kPickHeld = 8;    // scores that a thread keeps in registers
+constexpr int kPickHeld = 4;    // scores that a thread keeps in registers (1, 2, 4, 8 of them: 22.2, 22.5,
+                                // 22.5, 23.5 us for one of 16001; 42.6, 42.5, 41.7, 41.7 for 4 of 131072)
 
 struct SelectScratch {  // per (sequence, head)
   float* score;         // [max_pages]

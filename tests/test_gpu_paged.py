@@ -780,3 +780,171 @@ def test_short_items_in_clusters(pkg, x, dtype, scales, B, longest, d):
     c.lens_list = [0] * B
     c.seq_lens.zero_()
     _check_decode(pkg, c, c.randn(B, 12, d, dtype=x))
+
+
+# ------------------------------------------------------------------ what the documentation allows and is easily forgotten
+
+def test_sequences_share_pages(pkg):
+    """A common prefix stands in the cache once."""
+    c = Case(pkg, [100, 90, 70], H=2, d=64, seed=1)
+    for b, n in ((1, 4), (2, 3)):  # whole pages of sequence 0
+        c.block_table[b, :n] = c.block_table[0, :n]
+        c.k_ref[b, :, :n * 16], c.v_ref[b, :, :n * 16] = c.k_ref[0, :, :n * 16], c.v_ref[0, :, :n * 16]
+    _check_decode(pkg, c, c.randn(3, 4, 64))
+
+
+def test_thousands_of_sequences(pkg):
+    g = torch.Generator().manual_seed(1)
+    lens = [int(v) for v in torch.randint(0, 20, (3000,), generator=g)]
+    c = Case(pkg, lens, H=1, page=8, d=32, seed=1, summaries=True)
+    _check_decode(pkg, c, c.randn(3000, 2, 32))
+    _check_select(pkg, c, c.randn(3000, 2, 32), 2)
+    c = Case(pkg, lens, H=1, page=8, d=32, seed=1, summaries=True)
+    _check_append(pkg, c, [1] * 3000, BF16, Hq=2, single=True)
+    c = Case(pkg, lens, H=1, page=8, d=32, seed=1)
+    _check_append(pkg, c, [n // 2 for n in lens], BF16, Hq=2)
+
+
+def test_rows_before_the_first_sequence_are_padding(pkg):
+    c = Case(pkg, [9, 30], H=1, d=32, seed=1, fill=False)
+    k, v, q = c.randn(20, 1, 32).cuda(), c.randn(20, 1, 32).cuda(), c.randn(20, 2, 32).cuda()
+    out = torch.full((20, 2, 32), 3.0, dtype=BF16, device="cuda")
+    pkg.attn_paged_append(c.kv, k, v, q=q, q_out=out, token_start=torch.tensor([5, 7, 17], dtype=torch.int32, device="cuda"))
+    assert pkg.sync_status() == 0
+    assert (out[:5] == 3).all() and (out[17:] == 3).all() and torch.equal(out[5:17], q[5:17])
+    for b, (rows, first) in enumerate(((range(5, 7), 7), (range(7, 17), 20))):
+        for i, r in enumerate(rows):
+            pos = first + i
+            assert torch.equal(c.k[int(c.table[b, pos // 16]), :, pos % 16], k[r])
+            assert torch.equal(c.v[int(c.table[b, pos // 16]), :, pos % 16], v[r])
+
+
+def test_append_past_32_bit_offsets(pkg):
+    d, page, H = 128, 64, 4
+    P = (5 << 30) // (H * page * d * 2)
+    k = torch.zeros((P, H, page, d), dtype=BF16, device="cuda")
+    v = torch.zeros((P, H, page, d), dtype=BF16, device="cuda")
+    table = torch.tensor([[P - 1, P - 2]], dtype=torch.int32, device="cuda")
+    kv = pkg.PagedKV(k, v, table, torch.tensor([100], dtype=torch.int32, device="cuda"))
+    x = torch.randn(100, 2 * H, d, device="cuda").to(BF16)
+    pkg.attn_paged_append(kv, x[:, :H], x[:, H:], token_start=torch.tensor([0, 100], dtype=torch.int32, device="cuda"))
+    assert pkg.sync_status() == 0
+    for pages, new in ((k, x[:, :H]), (v, x[:, H:])):
+        assert torch.equal(pages[P - 1].transpose(0, 1), new[:64]) and torch.equal(pages[P - 2, :, :36].transpose(0, 1), new[64:])
+        assert (pages[P - 2, :, 36:] == 0).all() and (pages[:P - 2].view(torch.int16) != 0).sum() == 0
+
+
+@pytest.mark.parametrize("pages", [3000, 9000])
+def test_select_more_ties_than_shared_memory_holds(pkg, pages):
+    c = Case(pkg, [8 * pages], H=1, page=8, d=32, seed=1, summaries=True)
+    q = c.randn(1, 3, 32)
+    c.k_min.zero_()
+    c.k_max.zero_()
+    _check_select(pkg, c, q, 37)
+    kinds = torch.randn(2, 1, 32, generator=c.g).to(BF16)
+    some = kinds[torch.randint(0, 2, (c.k.shape[0],), generator=c.g)]
+    c.k_min.copy_(some)
+    c.k_max.copy_(some)
+    for n in (5, pages // 3, pages - 100):
+        _check_select(pkg, c, q, n)
+
+
+def test_select_scores_beyond_fp32(pkg):
+    """Sums that overflow fp32, or vanish in it, are ordered all the same."""
+    for power, scale in ((100, 100), (-100, -60)):
+        c = Case(pkg, [16 * 1500], H=1, d=64, seed=2, summaries=True)
+        q = (c.randn(1, 4, 64).float() * 2.0 ** power).to(BF16)
+        for t in (c.k_min, c.k_max):
+            t.copy_((t.float() * 2.0 ** scale).to(BF16))
+        _check_select(pkg, c, q, 70)
+
+
+def test_select_takes_nan_and_infinite_scores_first(pkg):
+    c = Case(pkg, [16 * 300], H=1, d=32, seed=3, summaries=True)
+    q = c.randn(1, 2, 32)
+    ids = c.table[0].long()
+    c.k_max[ids[50], 0, 4] = math.nan
+    c.k_min[ids[50], 0, 4] = math.nan
+    c.k_max[ids[70]] = math.inf
+    c.k_min[ids[70]] = -math.inf
+    got = pkg.attn_paged_select(c.kv, q.cuda(), 2, keep_first=0, keep_last=0)
+    assert pkg.sync_status() == 0 and got[0, 0].tolist() == [50, 70]
+    got = pkg.attn_paged_select(c.kv, q.cuda(), 12, keep_first=1, keep_last=1)[0, 0].tolist()
+    assert pkg.sync_status() == 0 and {0, 50, 70, 299} <= set(got) and got == sorted(set(got))
+
+
+def test_select_with_hardly_a_page_in_the_table(pkg):
+    c = Case(pkg, [16 * 100], H=2, d=32, seed=4, summaries=True)
+    good = [3, 60, 61]
+    for j in range(100):
+        if j not in good:
+            c.block_table[0, j] = -1
+    got = pkg.attn_paged_select(c.kv, c.randn(1, 4, 32).cuda(), 10)
+    assert pkg.sync_status() == 6
+    for row in got[0].tolist():
+        assert row == sorted(set(row)) and row[0] == 0 and row[-1] == 99 and set(good) <= set(row)
+
+
+def test_nan_queries_give_nan(pkg):
+    """A NaN in a query is not an empty sequence."""
+    for lens in ([100], [40000], [3] * 700):
+        c = Case(pkg, lens, H=1, d=32, seed=5)
+        q = c.randn(len(lens), 2, 32).cuda()
+        q[:, 1, 7] = math.nan
+        o, lse = pkg.attn_paged_decode(c.kv, q)
+        assert pkg.sync_status() == 0
+        assert o[:, 1].isnan().all() and lse[:, 1].isnan().all() and o[:, 0].isfinite().all() and lse[:, 0].isfinite().all()
+
+
+def test_two_threads_at_once(pkg):
+    import threading
+    cases = [Case(pkg, [900 + i, 33, 2047], H=2, d=64, seed=i, summaries=True) for i in range(4)]
+    qs = [c.randn(3, 8, 64).cuda() for c in cases]
+    want = [(pkg.attn_paged_select(c.kv, q, 7),) + pkg.attn_paged_decode(c.kv, q) for c, q in zip(cases, qs)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(c, q, w):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                got = (pkg.attn_paged_select(c.kv, q, 7),) + pkg.attn_paged_decode(c.kv, q)
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                    wrong.append(c)
+    threads = [threading.Thread(target=work, args=x) for x in zip(cases, qs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and pkg.sync_status() == 0
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import torch, sys
+sys.path.insert(0, %r)
+import io_aware_exact_12_gb300 as p
+x = lambda *s: torch.randn(s, device="cuda").to(torch.bfloat16)
+k, v, lo, hi, q, new = x(40, 2, 16, 64), x(40, 2, 16, 64), x(40, 2, 64) - 1, x(40, 2, 64) + 1, x(2, 4, 64), x(2, 2, 64)
+kv = p.PagedKV(k, v, torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20), torch.tensor([300, 17], dtype=torch.int32, device="cuda"), k_min=lo, k_max=hi)
+def step():
+    p.attn_paged_append(kv, new, new)
+    return p.attn_paged_decode(kv, q, pages=p.attn_paged_select(kv, q, 5)) + p.attn_paged_decode(kv, q)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = step()
+g.replay()
+torch.cuda.synchronize()
+assert p.sync_status() == 0
+assert all(torch.equal(a, b) for a, b in zip(out, step()))
+print("ok")
+"""
+
+
+def test_first_call_of_a_process_in_a_capture(pkg):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE % root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
