@@ -81,10 +81,18 @@ __device__ __forceinline__ float magnitude(uint32_t m) {
   return fmaxf(fabsf(f.x), fabsf(f.y));
 }
 
+// Copies the first `size` bytes and fills the rest with zeros.
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t size) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+// The larger one, or NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // A warp scores 8 pages at a time.  The sum over channels may run in any order,
@@ -124,6 +132,8 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
     const int j = p0 + (i + t4) * 8 * kScoreWarps + g;
     return j < p1 ? checked_page(kv, b, j) : -1;
   };
+  const int64_t page_bytes = static_cast<int64_t>(kv.H) * ROW;
+  const uint8_t *kmin = kv.kmin + h * ROW + t4 * VB, *kmax = kv.kmax + h * ROW + t4 * VB;
   uint32_t big = 0;
   float qmost = 0.f;  // largest |q|_1
   for (int r0 = 0; r0 < G; r0 += WIDE ? 16 : 8) {
@@ -131,14 +141,12 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
     uint32_t found = 0;  // bit i % 32: the page of group i exists
     auto fetch = [&](int i) {
       const int id = __shfl_sync(0xffffffffu, ids, (lane & ~3) | (i & 3));
-      if (id >= 0) {
-        const int64_t at = (static_cast<int64_t>(id) * kv.H + h) * ROW + t4 * VB;
-        const uint32_t to = slots + (i % kScoreDepth) * SLOT;
+      const int64_t at = static_cast<int64_t>(max(id, 0)) * page_bytes;
+      const uint32_t to = slots + (i % kScoreDepth) * SLOT, size = id >= 0 ? VB : 0;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          copy_async<VB>(to + v * (kScoreThreads * 16), kv.kmin + at + v * 4 * VB);
-          copy_async<VB>(to + (NV + v) * (kScoreThreads * 16), kv.kmax + at + v * 4 * VB);
-        }
+      for (int v = 0; v < NV; ++v) {
+        copy_async<VB>(to + v * (kScoreThreads * 16), kmin + at + v * 4 * VB, size);
+        copy_async<VB>(to + (NV + v) * (kScoreThreads * 16), kmax + at + v * 4 * VB, size);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       found = (found & ~(1u << (i & 31))) | ((id >= 0 ? 1u : 0u) << (i & 31));
@@ -232,10 +240,6 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
                        : "r"(at + (NV + v) * (kScoreThreads * 16)) : "memory");
         }
       }
-      if (!there) {  // what the slot held before
-#pragma unroll
-        for (int v = 0; v < NV * WPV; ++v) lo[v] = hi[v] = 0u;
-      }
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
@@ -254,26 +258,23 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
           mma16<BF>(acc, qn[s][0], 0u, qn[s][1], 0u, l0, l1);
         }
       }
-      float best[2];
+      const uint32_t have = __ballot_sync(0xffffffffu, there);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        best[x] = -INFINITY;
+        float best = -INFINITY;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          float s = acc[2 * r + x] * mul[r];
-          if (!(fabsf(s) <= 3.402823466e38f)) s = INFINITY;  // NaN too: the pick scores such pages anew
-          if (r0 + g + 8 * r < G) best[x] = fmaxf(best[x], s);
+          float s = acc[2 * r + x];
+          if constexpr (E8 && X == kTypeBf16) s *= mul[r];
+          if (r0 + g + 8 * r < G) best = max_nan(best, s);
         }
 #pragma unroll
-        for (int y = 4; y < 32; y <<= 1) best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], y));
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
+        for (int y = 4; y < 32; y <<= 1) best = max_nan(best, __shfl_xor_sync(0xffffffffu, best, y));
         const int j = p0 + i * 8 * kScoreWarps + 2 * t4 + x;
-        const bool of = __shfl_sync(0xffffffffu, there, (2 * t4 + x) * 4);
         if (g == 0 && j < p1) {
-          const float s = of ? best[x] : -3.402823466e38f;  // no page there: last
-          sc.score[j] = r0 ? fmaxf(sc.score[j], s) : s;
+          if (!(fabsf(best) <= 3.402823466e38f)) best = INFINITY;                // NaN too: the pick scores all anew
+          if (!((have >> ((2 * t4 + x) * 4)) & 1)) best = -3.402823466e38f;     // no page there: last
+          sc.score[j] = r0 ? fmaxf(sc.score[j], best) : best;
         }
       }
       fetch(i + kScoreDepth);
