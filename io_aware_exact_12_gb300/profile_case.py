@@ -11,6 +11,10 @@ capture can skip them with ``-s``.
   --op fwd_blocksparse / bwd_blocksparse: a seeded random 25 %-dense per-head
       block mask (diagonal on), as in bench.py
   --op fwd_fp8: the e4m3 forward (d = 128) on per-tensor-quantised inputs
+  --op paged_append / paged_decode / paged_select: B sequences of N tokens in pages
+      of 16, H key/value heads and 4 H query heads; append writes all N tokens with
+      rotation and summaries, select takes an eighth of the pages; --dtype e4m3 for
+      an 8-bit cache
 """
 from __future__ import annotations
 
@@ -20,10 +24,42 @@ import math
 import torch
 
 
+def paged(attn, a):
+    """The paged-cache ops on a cache whose pages lie in random order."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    page, pages = 16, (a.N + 15) // 16
+    x = torch.bfloat16 if a.dtype == "e4m3" else {"bf16": torch.bfloat16, "f16": torch.float16}[a.dtype]
+    cache = torch.float8_e4m3fn if a.dtype == "e4m3" else x
+    randn = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=x)  # noqa: E731
+    k, v = (randn(a.B * pages, a.H, page, a.d).to(cache) for _ in range(2))
+    lo, hi = (f(k.to(x), 2).to(cache) for f in (torch.amin, torch.amax))
+    table = torch.randperm(a.B * pages, generator=g, device="cuda").to(torch.int32).view(a.B, pages)
+    kv = attn.PagedKV(k, v, table, torch.full((a.B,), a.N, dtype=torch.int32, device="cuda"), k_min=lo, k_max=hi)
+    q = randn(a.B, 4 * a.H, a.d)
+    if a.op == "paged_append":
+        rows = randn(a.B * a.N, 6 * a.H, a.d)
+        cos, sin = attn.rotation_tables(a.N, a.d, device="cuda")
+        start = torch.arange(0, a.B * a.N + 1, a.N, dtype=torch.int32, device="cuda")
+        out = torch.empty(a.B * a.N, 4 * a.H, a.d, dtype=x, device="cuda")
+        run = lambda: attn.attn_paged_append(kv, rows[:, :a.H], rows[:, a.H:2 * a.H], q=rows[:, 2 * a.H:], q_out=out,  # noqa: E731
+                                             token_start=start, cos=cos, sin=sin)
+    elif a.op == "paged_decode":
+        run = lambda: attn.attn_paged_decode(kv, q)  # noqa: E731
+    else:
+        run = lambda: attn.attn_paged_select(kv, q, max(2, pages // 8))  # noqa: E731
+    for _ in range(a.warmup + a.launches):
+        run()
+    torch.cuda.synchronize()
+    st = attn.sync_status()
+    print("done op=%s status=%d" % (a.op, st))
+    return 1 if st else 0
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", choices=["fwd", "bwd", "naive", "fwd_dropout", "bwd_dropout", "decode",
-                                     "fwd_blocksparse", "bwd_blocksparse", "fwd_fp8"], default="fwd")
+                                     "fwd_blocksparse", "bwd_blocksparse", "fwd_fp8", "paged_append",
+                                     "paged_decode", "paged_select"], default="fwd")
     ap.add_argument("--B", type=int, default=2)
     ap.add_argument("--H", type=int, default=16)
     ap.add_argument("--N", type=int, default=8192)
@@ -35,6 +71,8 @@ def main(argv=None):
     a = ap.parse_args(argv)
 
     import io_aware_exact_12_gb300 as attn
+    if a.op.startswith("paged"):
+        return paged(attn, a)
     from io_aware_exact_12_gb300.synth import AttnShape, make_inputs
     x = make_inputs(AttnShape(a.B, a.H, a.N, a.d), a.dtype, seed=4, device="cuda")
     q, k, v, do = x["q"], x["k"], x["v"], x["do"]
