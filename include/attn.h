@@ -349,8 +349,8 @@ int attn_paged_decode(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_hea
  *              sum_c max(q_gc k_min[p]_c, q_gc k_max[p]_c),
  * an upper bound of q_g . k over the page's keys.  The first keep_first and the
  * last keep_last pages (their sum at most n_select) are taken whatever their
- * score; of equal scores the lower index.  The order is that of the scores in
- * 64 bits, not of a rounded sum.  A NaN score ranks first.
+ * score; of equal scores the lower index.  Scores count to 44 bits or more of
+ * their terms' magnitude (not an fp32 sum's 20).  A NaN score ranks first.
  *   pages : out, [B, kv_heads, n_select] int32, ascending; a sequence of fewer
  *           pages gets all of them, then -1.
  *   workspace : attn_paged_select_workspace() bytes, as for attn_paged_decode.
@@ -405,7 +405,8 @@ int attn_sync_status(void* stream);
 const char* attn_status_string(int status);
 
 /* Number of kernel launches the most recent successful attn_fwd* / attn_bwd* /
- * attn_decode call on this thread enqueued (forward 1, backward 3, decode 2). */
+ * attn_decode / attn_paged_* call on this thread enqueued (forward 1, backward 3,
+ * decode 2, paged append 1, paged decode 1 or 2, paged select 2). */
 int attn_last_launch_count(void);
 
 #ifdef __cplusplus

@@ -8,13 +8,13 @@
 //     l = sum_s e^{m_s - m} l_s,   O = sum_s e^{m_s - m} O_s / l.
 //
 // Every cached byte is read once, so HBM bounds it: G = Hq / Hkv query heads
-// make 2 G flops per 2-byte element (4 G for e4m3), beyond the fp32 units' rate
-// from G = 4 or so.  The products run as m16n8k16 matrix instructions with the
-// G query heads as rows: at the full HBM rate they take a fifth (e4m3: two
-// fifths) of that pipe, so the larger tcgen05 tiles, which want 64 rows at
-// least, would have nothing to gain from 1 to 16 rows.
+// make 2 G flops per element, beyond the fp32 units' rate from G = 4 or so.  The
+// products run as m16n8k16 matrix instructions, 16 rows of the cache times 8 or 16
+// query heads.  At 6 TB/s they keep the tensor pipe 9 % busy (e4m3, widened to fp16
+// in registers: 17 %), so tcgen05, whose operands would have to lie in shared
+// memory as 64 rows at least and widened, has nothing to gain.
 //
-//   attn_paged_decode_kernel : two CTAs per SM, each with an equal share of all
+//   attn_paged_decode_kernel : two or three CTAs per SM, each with a share of all
 //       tiles of keys (tile lists of the items (b, KV head, group of up to 16
 //       query heads) laid end to end; the lengths are on the device, so every
 //       CTA sums them and finds its own share).  One producer warp walks the
@@ -24,6 +24,14 @@
 //       item ends.  Short items go whole to clusters of CTAs instead, which join
 //       their results through shared memory.
 //   attn_paged_merge_kernel : joins the items that were cut by a CTA border.
+//
+// Measured (GB300; the copy's rate is 6.8 TB/s): two sequences of 131071 tokens,
+// 64 / 8 heads of 128, fp16, 1074 MB: 157 us (6.8 TB/s); 61 sequences of up to 8192,
+// 32 / 8 heads of 128, bf16, 965 MB: 152 us (6.3 TB/s); 128 of up to 4096, 16 / 16
+// heads of 64, e4m3, 511 MB: 93 us (5.5 TB/s; its items are short, an item's start
+// and end cost as much as four tiles); one of 1000 tokens: 8.7 us, of which 4 us
+// pass until the first tile has come (length, page table and tile are three trips
+// to memory, one after the other).
 #include <atomic>
 #include <cmath>
 

@@ -8,9 +8,8 @@
 // the least upper bound of q_g . k over the box that the page's summary spans.
 // The first and last pages of a sequence are always taken; the rest go by the
 // score, equal ones by the lower index.  Two pages next to the border must not
-// change places by rounding, so the order is that of scores in 64 bits; but
-// reading and multiplying every summary in 64 bits would cost many times what
-// HBM needs to deliver it.  Hence two kernels:
+// change places by an fp32 sum's rounding; but multiplying every summary in 64
+// bits would cost many times what HBM needs to deliver it.  Hence two kernels:
 //
 //   attn_paged_score_kernel : every page's score as a matrix product of 2 d
 //       channels with fp32 sums (m16n8k16, the queries as rows; e4m3 summaries
@@ -20,8 +19,14 @@
 //       steps cuts 17 aligned terms at 2^-23 of the largest or less.  A histogram
 //       brackets the border to [L, H) with H - L <= 4 eps; pages at H + 2 eps or
 //       above are in, those below L - 2 eps out, and only those between (a few)
-//       are scored again, to 48 bits.  With eps = inf (a sum that overflowed or is
+//       are scored again, to 44 bits or more.  With eps = inf (a sum that overflowed or is
 //       NaN) that is all of them, in fp64.
+//
+// Measured (GB300; the copy's rate is 6.8 TB/s), both kernels: 8 sequences of 4096
+// pages, 32 / 8 heads of 128, bf16, 134 MB of summaries: 36 us, scores 26 and pick
+// 11; 4 of up to 8192 pages, 40 / 8 heads, e4m3, 55 MB: 26 us; one of 1001 pages:
+// 10.5 us.  The pick runs on one SM per head and is bound by its own 7 to 11 us of
+// barriers and cold instructions.
 #include <atomic>
 #include <cmath>
 
@@ -358,7 +363,8 @@ __device__ __forceinline__ int block_sum(int v, PickShared& sm, int turn) {
 }
 
 // A sum in two fp32 words, hi + lo with |lo| <= ulp(hi) / 2 (Knuth's and
-// Dekker's error-free sums): 48 bits, as good as 128 terms summed in fp64.
+// Dekker's error-free sums): 48 bits, 44 after d / 8 additions to lo, near the 46
+// that 128 terms summed in fp64 keep.
 // The fp64 units have a sixtieth of the fp32 rate: some tens of candidates took
 // 20 us there.
 struct Two {
