@@ -948,3 +948,11 @@ def test_first_call_of_a_process_in_a_capture(pkg):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE % root], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_one_item_in_hundreds_of_parts(pkg, x, dtype, scales, d):
+    c = Case(pkg, [90001], H=1, page=64, d=d, dtype=dtype, scales=scales, seed=d)
+    _check_decode(pkg, c, c.randn(1, 5, d, dtype=x))
+    _check_decode(pkg, c, c.randn(1, 17, d, dtype=x))
