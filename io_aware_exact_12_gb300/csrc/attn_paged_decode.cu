@@ -996,10 +996,10 @@ int launch_t(const PagedDecodeArgs& a, int* launches) {
   if (launch_serialized(ctas <= 2 * sms, kern, dim3(ctas), dim3(kPdThreads), F::SMEM, a.stream, mk, mv, a, RT, box, 0, by_item, parts,
                         part) != cudaSuccess)
     return kStatusCuda;
-  // Around 64 parts and more (one sequence of 131071 and one KV head, 304 parts: 36.7
-  // -> 25.2 us, of 64000 27.8 -> 17.1; eight heads of 16000, 38 parts: 22.0 against
-  // 22.9) the wide form is faster.
-  const bool many = items * 64 <= ctas;
+  // The wide form is faster from about 32 parts on (one sequence of 131071 and one KV
+  // head, 304 parts: 36 -> 22 us; eight heads of 16000, 38 parts: 22.0 -> 20.1; of
+  // 2000, 16 parts: 10.5 -> 11.0).
+  const bool many = items * 32 <= ctas;
   const dim3 grid(by_item ? static_cast<int>(items) : ctas, std::min(F::ROWS, a.Hq / a.kv.H), many ? D / 32 : 1);
   return launch_serialized(true, many ? attn_paged_merge_many_kernel<X, D> : attn_paged_merge_kernel<X, D>, grid,
                            dim3(many ? kManyThreads : kMergeThreads), 0, a.stream, a, RT, F::ROWS, parts, part) == cudaSuccess
