@@ -45,8 +45,9 @@ constexpr int kPdWarps = 4;  // consumers
 constexpr int kPdThreads = 32 * (kPdWarps + 1);
 constexpr int kPdRows = 16;  // query heads of an item, at most
 // An item's start and end are worth kPdExtra tiles in the shares, where items are
-// more than CTAs (64 sequences of 8 heads of up to 300 keys 26.2 -> 17.9 us, of up
-// to 500 34.3 -> 21.1) or shares have kPdShare tiles or more. Up to kPdSolo tiles
+// more than half the CTAs (64 sequences of 8 heads of up to 500 keys 34.3 -> 21.1 us,
+// 32 of up to 300 16.8 -> 13.0; with fewer items they cost one sequence of 2000 10.5
+// -> 11.0) or shares have kPdShare tiles or more. Up to kPdSolo tiles
 // and with more items than CTAs a warp takes a whole item: 128 sequences of up to
 // 100 24.3 -> 19.3 us; with 6 tiles instead of 4, 250 of up to 180 33.5 -> 45.5.
 constexpr int kPdExtra = 4;
@@ -209,7 +210,7 @@ __device__ __forceinline__ void find_share(const PagedDecodeArgs& a, int HR, Sch
   const long long want = items ? items * divide(total + items * kPdWarps - 1, items * kPdWarps) : 0;
   const int n_act = static_cast<int>(min(static_cast<long long>(gridDim.x), want));
   const bool solo = most <= kPdSolo && items > gridDim.x;
-  const int extra = total >= kPdShare * static_cast<long long>(n_act) || (!solo && items > gridDim.x) ? kPdExtra : 0;
+  const int extra = total >= kPdShare * static_cast<long long>(n_act) || (!solo && 2 * items > gridDim.x) ? kPdExtra : 0;
   total += items * extra;
   mine += static_cast<long long>(alive) * HR * extra;
   upto += static_cast<long long>(before) * HR * extra;
@@ -930,7 +931,7 @@ int row_tiles(int Hq, int H) { return (Hq / H + kPdRows - 1) / kPdRows; }
 // the clusters have more CTAs than the GPU has SMs (else cutting the items finer is
 // faster: one sequence of 2000 10.5 against 10.3 us).  The clusters may be twice
 // what is resident at once (64 sequences of up to 100 13.6 against 16.6 us; four
-// times: 32 of up to 300 25.6 against 17.2), unless most warps would have nothing
+// times: 32 of up to 300 25.6 against 13.0), unless most warps would have nothing
 // to do (64 of up to 20 12.6 against 10.9).
 int cluster_size(int64_t items, int64_t tiles, int sms) {
   for (int k = 1; k <= 8; k *= 2)
