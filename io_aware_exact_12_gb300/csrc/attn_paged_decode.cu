@@ -666,6 +666,11 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
           }
         }
       }
+      // The next load writes where these lanes have just read, by another path: only
+      // the fence orders it behind the reads.  Without it the last fragments of V were
+      // now and then the next tile's (one item of 600 in every fifth call); it costs
+      // nothing that can be measured.
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + st * 8);
     }

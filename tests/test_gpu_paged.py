@@ -589,6 +589,24 @@ def test_many_short_sequences(pkg, x, dtype, scales, longest):
         _check_decode(pkg, c, c.randn(len(lens), Hq, d, dtype=x))
 
 
+@pytest.mark.parametrize("per_sm", [1, 2, 3, 4])
+@pytest.mark.parametrize("more", [-1, 0, 1, 30])
+@pytest.mark.parametrize("longest", [100, 400])
+def test_about_as_many_items_as_blocks(pkg, per_sm, more, longest):
+    """Items a little fewer and more than the blocks that the GPU holds at one, two, three and four per SM, under a
+    wide table, all with tokens and some without."""
+    g = torch.Generator().manual_seed(per_sm)
+    n = per_sm * torch.cuda.get_device_properties(0).multi_processor_count + more
+    lens = [1 + int(v) for v in torch.randint(0, longest, (n,), generator=g)]
+    c = Case(pkg, lens, H=1, page=64, d=128, seed=1, width=200)
+    q = c.randn(n, 2, 128)
+    _check_decode(pkg, c, q)
+    for b in (0, n // 2, n - 1):
+        c.lens_list[b] = 0
+    c.seq_lens.copy_(torch.tensor(c.lens_list, dtype=torch.int32))
+    _check_decode(pkg, c, q)
+
+
 def test_many_short_sequences_through_lists(pkg):
     lens = [i % 40 for i in range(200)]
     c = Case(pkg, lens, H=16, page=8, d=32, dtype=F16, seed=1, summaries=True)
