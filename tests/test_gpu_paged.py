@@ -618,6 +618,32 @@ def test_many_short_sequences_through_lists(pkg):
 
 # ------------------------------------------------------------------ together
 
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_calls_are_right_and_repeat_bit_for_bit(pkg, seed):
+    g = torch.Generator().manual_seed(1000 + seed)
+
+    def pick(*of):
+        return of[int(torch.randint(0, len(of), (1,), generator=g))]
+
+    x, dtype, scales = pick(*TYPES)
+    B, H, G, n = pick(1, 5, 40, 200, 400), pick(1, 2, 8), pick(1, 4, 16, 20), pick(2, 7, 32)
+    top = pick(20, 130, 600) if B * H < 1000 else pick(5, 30, 60)
+    lens = [int(v) for v in torch.randint(0, top + 1, (B,), generator=g)]
+    c = Case(pkg, lens, H=H, page=pick(8, 16, 64), d=pick(32, 64, 128), dtype=dtype, scales=scales, seed=seed,
+             width=pick(None, 80), summaries=True, layout=pick("heads", "tokens", "turns"))
+    q = c.randn(B, H * G, c.d, dtype=x).cuda()
+    o, lse = _check_decode(pkg, c, q)
+    pages = pkg.attn_paged_select(c.kv, q, n)
+    first = pkg.attn_paged_decode(c.kv, q, pages=pages)
+    for _ in range(10):
+        again = pkg.attn_paged_decode(c.kv, q)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+        listed = pkg.attn_paged_select(c.kv, q, n)
+        again = pkg.attn_paged_decode(c.kv, q, pages=listed)
+        assert torch.equal(listed, pages) and torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    assert pkg.sync_status() == 0
+
+
 def test_a_server_run(pkg):
     """Prompts appended, then steps of append, select and decode, with a sequence that starts late and one that ends;
     against float64 over what the cache holds, and the prompt's last token against the dense causal forward."""
