@@ -122,8 +122,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 // Barrier over the cluster's threads; what they wrote before it, also to shared
-// memory, is visible to all behind it.
+// memory, is visible to all behind it.  `.aligned` wants a warp's lanes together,
+// and callers come out of loops and spins that lanes leave apart.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Address of another CTA's shared memory in the cluster.
@@ -548,8 +550,8 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (x * TK + r) * F::RBX + y), "r"(0)
                              : "memory");
         fence_proxy_async_smem();  // before the stage's next load
-        __syncwarp();
       }
+      __syncwarp();  // the zeros are there, and the lanes together for the matrix steps
       // S^T = K Q^T
       float sc[NT][TK / 16][4];
 #pragma unroll

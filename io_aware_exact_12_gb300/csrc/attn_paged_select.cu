@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kScoreThreads) attn_paged_score_kernel(const P
                        : "r"(at + (NV + v) * (kScoreThreads * 16)) : "memory");
         }
       }
+      __syncwarp();  // look-ups part the lanes, the matrix steps want them together
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < NS; ++s) {

@@ -1000,3 +1000,21 @@ def test_one_item_in_hundreds_of_parts(pkg, x, dtype, scales, d):
     c = Case(pkg, [90001], H=1, page=64, d=d, dtype=dtype, scales=scales, seed=d)
     _check_decode(pkg, c, c.randn(1, 5, d, dtype=x))
     _check_decode(pkg, c, c.randn(1, 17, d, dtype=x))
+
+
+# ------------------------------------------------------------------ lanes that part
+
+@pytest.mark.parametrize("group,d", [(1, 32), (3, 32), (5, 32), (1, 64), (3, 64), (7, 128), (9, 32), (11, 64)])
+@pytest.mark.parametrize("longest", [40, 250, 500])
+def test_clusters_whose_warps_have_lanes_without_work(pkg, group, d, longest):
+    """Rows that fill no warp in the join, CTAs without a tile, and a producer that waits for a stage: the barrier over the
+    cluster comes behind all of them."""
+    g = torch.Generator().manual_seed(group)
+    lens = [longest, 0, 1] + [int(v) for v in torch.randint(0, longest + 1, (3,), generator=g)]
+    c = Case(pkg, lens, H=2, d=d, seed=longest, width=-(-longest // 16))
+    q = c.randn(len(lens), 2 * group, d).cuda()
+    o, lse = _check_decode(pkg, c, q)
+    for _ in range(20):
+        again = pkg.attn_paged_decode(c.kv, q)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    assert pkg.sync_status() == 0
