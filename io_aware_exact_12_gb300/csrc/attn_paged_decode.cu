@@ -88,6 +88,25 @@ struct Part {  // an item that CTA `first` begins and CTA `last` ends
 // Floats of one partial result: O [rows][D], then m, l and the rounded l [rows] each.
 __host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 3); }
 
+// The reference point of the weights 2^(s - m) for a maximum x.  Weights that multiply
+// V as fp16 have the largest at 2^15, not 1: then those down to 2^-29 of it are normal
+// numbers (10 and more bits) and those down to 2^-40 not nothing.  With the largest at
+// 1, keys 2^-25 of it and less were dropped, and with a sink whose value is 0 they are all
+// that O consists of.  The factor cancels in O and is part of m in lse.  From 2^20 on m
+// stays the maximum itself: there the shift would be rounded, up to an overflow.
+template <bool FP16>
+__device__ __forceinline__ float weight_origin(float x) {
+  if constexpr (FP16) return fabsf(x) < 1048576.f ? x - 15.f : x;
+  else return x;
+}
+
+// ln of the sum of 2^s for weights that add to l.  The shift is taken out of both
+// sides first: log2 of a sum about 1, not 2^15, has the smaller step.
+__device__ __forceinline__ float log_sum(float m, float l, bool fp16) {
+  if (l == 0.f) return -INFINITY;
+  return (fp16 ? (m + 15.f) + log2f(l * 0x1p-15f) : m + log2f(l)) * 0.69314718055994531f;
+}
+
 // Weight of a part with maximum m in a join with maximum mm.  Without a maximum
 // the part's sums are 0 (no visible key) or NaN (nothing but NaN logits), and
 // either goes into the join as it is.
@@ -513,7 +532,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       }
     }
 
-    float m[NT][2], l[NT][2];  // maximum and this thread's share of the sum
+    float m[NT][2], l[NT][2];  // maximum (weight_origin of it) and this thread's share of the sum
     float lr[NT][4];           // sums of the rounded weights
     float o[NT][D / 16][4];
 #pragma unroll
@@ -611,7 +630,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
           x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, y));
           x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, y));
         }
-        const float n0 = fmaxf(m[nt][0], x0), n1 = fmaxf(m[nt][1], x1);
+        const float n0 = fmaxf(m[nt][0], weight_origin<!BF>(x0)), n1 = fmaxf(m[nt][1], weight_origin<!BF>(x1));
         if (__any_sync(0xffffffffu, n0 > m[nt][0] || n1 > m[nt][1])) {  // rare once some tiles are seen
           const float a0 = m[nt][0] == -INFINITY ? 0.f : ex2_approx(m[nt][0] - n0);
           const float a1 = m[nt][1] == -INFINITY ? 0.f : ex2_approx(m[nt][1] - n1);
@@ -736,7 +755,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
         for (int y = 0; y < 4; ++y) acc[y] *= inv;
         const int64_t at = static_cast<int64_t>(it.b) * a.Hq + head0 + r;
         store_out4<X>(a.o + (at * D + col) * 2, acc);
-        if (col == 0) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+        if (col == 0) a.lse[at] = log_sum(mm, ll, !BF);
       } else {
         *reinterpret_cast<float4*>(out + r * D + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (col == 0) {
@@ -788,7 +807,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       for (int y = 0; y < 4; ++y) acc[y] *= inv;
       const int64_t to = static_cast<int64_t>(s.b) * a.Hq + static_cast<int64_t>(h) * G + r0 + r;
       store_out4<X>(a.o + (to * D + col) * 2, acc);
-      if (col == 0) a.lse[to] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+      if (col == 0) a.lse[to] = log_sum(mm, ll, !BF);
     }
     cluster_sync();  // nobody's shared memory goes before it is read
   }
@@ -852,7 +871,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     const float w[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     store_out4<X>(a.o + (out * D + c4 * 4) * 2, w);
   }
-  if (threadIdx.x == 0) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  if (threadIdx.x == 0) a.lse[out] = log_sum(m, l, a.kv.type != kTypeBf16);
 }
 
 // The same for items cut into many parts: a block to every 32 columns, whose
@@ -922,7 +941,7 @@ __global__ void __launch_bounds__(kManyThreads)
     const float w[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     store_out4<X>(a.o + (out * D + c) * 2, w);
   }
-  if (threadIdx.x == 0 && blockIdx.z == 0) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  if (threadIdx.x == 0 && blockIdx.z == 0) a.lse[out] = log_sum(m, l, a.kv.type != kTypeBf16);
 }
 
 constexpr int kMaxCtas = kMergeParts;  // of the decode kernel

@@ -1018,3 +1018,47 @@ def test_clusters_whose_warps_have_lanes_without_work(pkg, group, d, longest):
         again = pkg.attn_paged_decode(c.kv, q)
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
     assert pkg.sync_status() == 0
+
+
+# ------------------------------------------------------------------ small weights
+
+@pytest.mark.parametrize("x,dtype,scales", [(BF16, BF16, (1.0, 1.0)), (F16, F16, (1.0, 1.0)), (BF16, E4M3, (1.0, 0.5)), (F16, E4M3, (1.0, 0.5))])
+@pytest.mark.parametrize("above", [8.0, 12.0, 15.0, 16.5, 17.2, 17.5, 20.0])
+@pytest.mark.parametrize("n,d", [(500, 64), (4000, 128), (70000, 64)])
+def test_decode_one_key_far_above_the_others(pkg, x, dtype, scales, above, n, d):
+    """A key that takes nearly all of the weight and whose value is 0 (an attention sink): O is what the others leave, so
+    they must keep their bits, down to 2^-29 of the largest weight (20 in the exponent; fp16 weights with the largest at
+    2^15 are normal numbers down to there)."""
+    c = Case(pkg, [n], H=1, page=16, d=d, dtype=dtype, scales=scales, seed=1)
+    q = c.randn(1, 4, d, dtype=x) * 0.03
+    q[..., 0] = 1.0
+    at = 77
+    c.k_ref[0, 0, :n, 0] = 0.0
+    c.k_ref[0, 0, at] = 0.0
+    c.k_ref[0, 0, at, 0] = (torch.tensor(above * math.sqrt(d)).to(dtype)).double()
+    c.v_ref[0, 0, at] = 0.0
+    ids = c.table[0, :-(-n // 16)].long().cuda()
+    slots = torch.arange(len(ids) * 16, device="cuda")
+    live = slots < n
+    for to, ref, s in ((c.k, c.k_ref, scales[0]), (c.v, c.v_ref, scales[1])):
+        rows = (ref[0, 0, :n] / s).to(dtype).cuda()
+        _raw(to)[ids[slots[live] // 16], 0, slots[live] % 16] = _raw(rows)
+    assert (q[0].double() @ c.k_ref[0, 0, :n].T / math.sqrt(d)).sort(-1).values[:, -2].max() < 1.0
+    _check_decode(pkg, c, q)
+
+
+@pytest.mark.parametrize("dtype", [F16, E4M3])
+@pytest.mark.parametrize("power", [3, 8, 12])
+def test_decode_logits_far_from_zero(pkg, dtype, power):
+    """All logits near +-2^power (and beyond 2^20 with fp16), where a shift of the exponent is a rounding of its own."""
+    for sign in (1, -1):
+        c = Case(pkg, [900], H=1, d=64, dtype=dtype, seed=power, scales=(1.0, 1.0))
+        q = c.randn(1, 4, 64, dtype=F16) * 0.05
+        q[..., 0] = 16.0
+        kx = torch.tensor(sign * 2.0 ** min(power, 8))
+        c.k_ref[0, 0, :900, 0] = kx.double()
+        slots = torch.arange(900)
+        _raw(c.k)[c.table[0, slots // 16].long().cuda(), 0, (slots % 16).cuda(), 0] = _raw(kx.to(dtype).reshape(1)).cuda()
+        _check_decode(pkg, c, q, scale=2.0 ** (power - 4 - min(power, 8)))
+        if dtype == F16:
+            _check_decode(pkg, c, q, scale=2.0 ** (21 - 4 - min(power, 8)))
