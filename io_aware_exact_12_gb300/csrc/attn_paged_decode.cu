@@ -23,6 +23,8 @@
 //       online softmax of its own, and are merged in shared memory where an
 //       item ends.  Short items go whole to clusters of CTAs instead, which join
 //       their results through shared memory.
+//   The weights multiply V as two 16-bit words (rounding and remainder), so O keeps
+//   what fp32 weights give up to 2^-16 and l is the fp32 sum of the weights as they are.
 //   attn_paged_merge_kernel : joins the items that were cut by a CTA border.
 //
 // Measured (GB300; the copy's rate is 6.8 TB/s): two sequences of 131071 tokens,
@@ -64,7 +66,7 @@ struct PdCfg {
   static constexpr int MINB = NT == 1 && ROW <= 64 ? 3 : 2;  // CTAs per SM
   static constexpr int TK = ROW >= 256 ? 32 : 64;      // keys of a tile
   static constexpr int HALF = TK * ROW;                // K (or V) bytes of a stage
-  static constexpr int OTHER = kPdWarps * ROWS * D * 4 + kPdWarps * 3 * ROWS * 4 + 1024;
+  static constexpr int OTHER = kPdWarps * ROWS * D * 4 + kPdWarps * 2 * ROWS * 4 + 1024;
   static constexpr int RING = 227 * 1024 / MINB - 1024 - OTHER;
   // A multiple of the warps, so that a stage always serves the same warp: loads
   // land out of order, and a warp that looked at a stage whose previous tile,
@@ -73,8 +75,8 @@ struct PdCfg {
   static_assert(STAGES >= kPdWarps && STAGES % kPdWarps == 0, "stages belong to warps");
   static constexpr int SPW = STAGES / kPdWarps;        // stages of a warp
   static constexpr int OFF_O = STAGES * 2 * HALF;      // [warps][ROWS][D] fp32
-  static constexpr int OFF_ML = OFF_O + kPdWarps * ROWS * D * 4;  // [warps][3][ROWS]
-  static constexpr int OFF_BAR = OFF_ML + kPdWarps * 3 * ROWS * 4;
+  static constexpr int OFF_ML = OFF_O + kPdWarps * ROWS * D * 4;  // [warps][2][ROWS]
+  static constexpr int OFF_BAR = OFF_ML + kPdWarps * 2 * ROWS * 4;
   static constexpr int OFF_MASK = OFF_BAR + 2 * STAGES * 8;  // visible keys of a stage
   static constexpr int OFF_SCHED = OFF_MASK + STAGES * 8;
   static constexpr int SMEM = OFF_SCHED + 192;
@@ -85,8 +87,8 @@ struct Part {  // an item that CTA `first` begins and CTA `last` ends
   int b, hr, first, last;
 };
 
-// Floats of one partial result: O [rows][D], then m, l and the rounded l [rows] each.
-__host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 3); }
+// Floats of one partial result: O [rows][D], then m and l [rows] each.
+__host__ __device__ constexpr int part_floats(int d, int rows) { return rows * (d + 2); }
 
 // The reference point of the weights 2^(s - m) for a maximum x.  Weights that multiply
 // V as fp16 have the largest at 2^15, not 1: then those down to 2^-29 of it are normal
@@ -464,7 +466,6 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   const int g = lane >> 2, t4 = lane & 3, l8 = lane & 7, mi = lane >> 3;
   const int swz = F::RBX == 128 ? l8 : F::RBX == 64 ? l8 >> 1 : l8 >> 2;
   constexpr int CPB = F::RBX / 16;  // 16-byte chunks of a box row
-  const uint32_t ones = BF ? 0x3f803f80u : 0x3c003c00u;
   bool ok = true;
   int cur = 0, turn = 0;       // tiles of the CTA that are done, and of this warp
   long long w0 = s.w0;         // start of the item, in weights
@@ -533,14 +534,12 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     }
 
     float m[NT][2], l[NT][2];  // maximum (weight_origin of it) and this thread's share of the sum
-    float lr[NT][4];           // sums of the rounded weights
     float o[NT][D / 16][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        lr[nt][y] = 0.f;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) o[nt][x][y] = 0.f;
       }
@@ -609,7 +608,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
         }
       }
       // Online softmax, in units of log2.
-      uint32_t pf[NT][TK / 16][2];
+      uint32_t pf[NT][TK / 16][2], pr[NT][TK / 16][2];  // weights, remainders
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x0 = -INFINITY, x1 = -INFINITY;
@@ -636,7 +635,6 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
           const float a1 = m[nt][1] == -INFINITY ? 0.f : ex2_approx(m[nt][1] - n1);
           m[nt][0] = n0, m[nt][1] = n1;
           l[nt][0] *= a0, l[nt][1] *= a1;
-          lr[nt][0] *= a0, lr[nt][1] *= a1;
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) o[nt][x][0] *= a0, o[nt][x][1] *= a1, o[nt][x][2] *= a0, o[nt][x][3] *= a1;
         }
@@ -649,16 +647,21 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
           const float p2 = ex2_approx(v[2] - z0), p3 = ex2_approx(v[3] - z1);
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
-          pf[nt][x][0] = transpose8(pack2<BF>(p0, p1));
-          pf[nt][x][1] = transpose8(pack2<BF>(p2, p3));
+          const uint32_t u = pack2<BF>(p0, p1), w = pack2<BF>(p2, p3);
+          const float2 uf = unpack2<BF>(u), wf = unpack2<BF>(w);
+          pf[nt][x][0] = transpose8(u);
+          pf[nt][x][1] = transpose8(w);
+          pr[nt][x][0] = transpose8(pack2<BF>(p0 - uf.x, p1 - uf.y));
+          pr[nt][x][1] = transpose8(pack2<BF>(p2 - wf.x, p3 - wf.y));
         }
       }
-      // O^T += V^T P^T; the weights that multiply V are rounded to 16 bits, and
-      // their sum (a row of ones) is what O is divided by.
+      // O^T += V^T P^T, with every weight as two 16-bit words, its rounding and the
+      // remainder: 2^-16 (fp16: 2^-22) of it is lost, against 2^-8 (2^-11) in one word,
+      // which was an O with up to 1.3 times the error of fp32 weights.  The matrix pipe has
+      // room for the second product (two sequences of 131071 tokens 155.3 -> 155.2 us, 16 of
+      // 16384 in e4m3 94.3 -> 95.3, one of 1000 8.84 -> 8.97).
 #pragma unroll
       for (int kk = 0; kk < TK / 16; ++kk) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16<BF>(lr[nt], ones, ones, ones, ones, pf[nt][kk][0], pf[nt][kk][1]);
         if constexpr (E8) {
           const uint32_t at = vb + (kk * 16 + (mi & 1) * 8 + l8) * F::RBX;
 #pragma unroll
@@ -670,8 +673,10 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
               const uint32_t lo = __byte_perm(r[2 * y], 0, 0x3120), hi = __byte_perm(r[2 * y + 1], 0, 0x3120);
               const uint32_t a0 = e4m3_pair(lo), a1 = e4m3_pair_hi(lo), a2 = e4m3_pair(hi), a3 = e4m3_pair_hi(hi);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+              for (int nt = 0; nt < NT; ++nt) {
                 mma16<false>(o[nt][x + y], a0, a1, a2, a3, pf[nt][kk][0], pf[nt][kk][1]);
+                mma16<false>(o[nt][x + y], a0, a1, a2, a3, pr[nt][kk][0], pr[nt][kk][1]);
+              }
             }
           }
         } else {
@@ -682,8 +687,10 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
             uint32_t r[4];
             ldsm4_t(at + (chunk / CPB) * TK * F::RBX + (((chunk % CPB) ^ swz) << 4), r);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
               mma16<BF>(o[nt][x], r[0], r[1], r[2], r[3], pf[nt][kk][0], pf[nt][kk][1]);
+              mma16<BF>(o[nt][x], r[0], r[1], r[2], r[3], pr[nt][kk][0], pr[nt][kk][1]);
+            }
           }
         }
       }
@@ -699,7 +706,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     // The item's end in this CTA: the four warps are merged (solo: one is all).
     // Columns are swizzled by the head, so that the fragments' stores meet no bank
     // twice.
-    float* ml = sml + warp * 3 * ROWS;
+    float* ml = sml + warp * 2 * ROWS;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       }
       if (g < 2) {
         const int r = nt * 8 + 2 * t4 + g;
-        ml[r] = m[nt][g], ml[ROWS + r] = l[nt][g], ml[2 * ROWS + r] = lr[nt][g];
+        ml[r] = m[nt][g], ml[ROWS + r] = l[nt][g];
       }
       float* w0 = so + (warp * ROWS + nt * 8 + 2 * t4) * D;  // heads 2 t4 and 2 t4 + 1
       const int sw = t4 << 3;
@@ -737,20 +744,19 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       const int r = x / (D / 4), col = (x % (D / 4)) * 4;
       float mw[kPdWarps], mm = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kPdWarps; ++w) mm = fmaxf(mm, mw[w] = sml[(solo ? warp : w) * 3 * ROWS + r]);
-      float ll = 0.f, ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < kPdWarps; ++w) mm = fmaxf(mm, mw[w] = sml[(solo ? warp : w) * 2 * ROWS + r]);
+      float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < kPdWarps; ++x) {
         if (solo && x) break;
         const int w = solo ? warp : x;
         const float f = part_weight(mw[x], mm);
-        ll += f * sml[w * 3 * ROWS + ROWS + r];
-        ls += f * sml[w * 3 * ROWS + 2 * ROWS + r];
+        ll += f * sml[w * 2 * ROWS + ROWS + r];
         const float4 v = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * D + (col ^ (((r >> 1) & 3) << 3)));
         acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
       }
       if (direct) {
-        const float inv = ls == 0.f ? 0.f : kv.v_scale / ls;
+        const float inv = ll == 0.f ? 0.f : kv.v_scale / ll;
 #pragma unroll
         for (int y = 0; y < 4; ++y) acc[y] *= inv;
         const int64_t at = static_cast<int64_t>(it.b) * a.Hq + head0 + r;
@@ -761,7 +767,6 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
         if (col == 0) {
           out[ROWS * D + r] = mm;
           out[ROWS * (D + 1) + r] = ll;
-          out[ROWS * (D + 2) + r] = ls;
         }
       }
     }
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
         const uint32_t p = in_cta(at, k);
         if (load_cluster4(p + (ROWS * (D + 1) + r) * 4) != 0.f) mm = fmaxf(mm, load_cluster4(p + (ROWS * D + r) * 4));
       }
-      float ll = 0.f, ls = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float ll = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
       for (int k = 0; k < cluster; ++k) {
         const uint32_t p = in_cta(at, k);
         const float l = load_cluster4(p + (ROWS * (D + 1) + r) * 4);
@@ -799,10 +804,9 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
         const float f = part_weight(load_cluster4(p + (ROWS * D + r) * 4), mm);
         const float4 v = load_cluster16(p + (r * D + col) * 4);
         ll += f * l;
-        ls += f * load_cluster4(p + (ROWS * (D + 2) + r) * 4);
         acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
       }
-      const float inv = ls == 0.f ? 0.f : kv.v_scale / ls;
+      const float inv = ll == 0.f ? 0.f : kv.v_scale / ll;
 #pragma unroll
       for (int y = 0; y < 4; ++y) acc[y] *= inv;
       const int64_t to = static_cast<int64_t>(s.b) * a.Hq + static_cast<int64_t>(h) * G + r0 + r;
@@ -836,17 +840,15 @@ __global__ void __launch_bounds__(kMergeThreads)
   for (int i = lane; i < n; i += 32) m = fmaxf(m, at(i)[ROWS * D + r]);
 #pragma unroll
   for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  float l = 0.f, ls = 0.f;
+  float l = 0.f;
   for (int i = lane; i < n; i += 32) {
     const float* s = at(i) + r;
     const float f = part_weight(s[ROWS * D], m);
     l += f * s[ROWS * (D + 1)];
-    ls += f * s[ROWS * (D + 2)];
   }
 #pragma unroll
   for (int x = 16; x; x >>= 1) {
     l += __shfl_xor_sync(0xffffffffu, l, x);
-    ls += __shfl_xor_sync(0xffffffffu, ls, x);
   }
   constexpr int LPR = D / 4, GROUPS = kMergeThreads / LPR;
   const int grp = threadIdx.x / LPR, c4 = threadIdx.x % LPR;
@@ -867,7 +869,7 @@ __global__ void __launch_bounds__(kMergeThreads)
       const float4 v = sm[i][c4];
       o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
     }
-    const float inv = ls == 0.f ? 0.f : a.kv.v_scale / ls;
+    const float inv = l == 0.f ? 0.f : a.kv.v_scale / l;
     const float w[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     store_out4<X>(a.o + (out * D + c4 * 4) * 2, w);
   }
@@ -894,7 +896,7 @@ __global__ void __launch_bounds__(kManyThreads)
   // CTA `first` has the item's beginning in its slot 1, the others theirs in slot 0.
   const float* base = part + static_cast<int64_t>(p.first) * 2 * part_floats(D, ROWS);
   auto at = [&](int i) { return base + (i ? 2 * i : 1) * part_floats(D, ROWS); };
-  __shared__ float weight[kMergeParts], sums[3][kManyThreads / 32];
+  __shared__ float weight[kMergeParts], sums[2][kManyThreads / 32];
   __shared__ float4 sm[kManyThreads];
   float m = -INFINITY;
   for (int i = threadIdx.x; i < n; i += T) m = fmaxf(m, at(i)[ROWS * D + r]);
@@ -903,23 +905,21 @@ __global__ void __launch_bounds__(kManyThreads)
   if (lane == 0) sums[0][warp] = m;
   __syncthreads();
   for (int i = 0; i < warps; ++i) m = fmaxf(m, sums[0][i]);
-  float l = 0.f, ls = 0.f;
+  float l = 0.f;
   for (int i = threadIdx.x; i < n; i += T) {
     const float* s = at(i) + r;
     const float f = part_weight(s[ROWS * D], m);
     weight[i] = f;
     l += f * s[ROWS * (D + 1)];
-    ls += f * s[ROWS * (D + 2)];
   }
 #pragma unroll
   for (int x = 16; x; x >>= 1) {
     l += __shfl_xor_sync(0xffffffffu, l, x);
-    ls += __shfl_xor_sync(0xffffffffu, ls, x);
   }
-  if (lane == 0) sums[1][warp] = l, sums[2][warp] = ls;
+  if (lane == 0) sums[1][warp] = l;
   __syncthreads();
-  l = ls = 0.f;
-  for (int i = 0; i < warps; ++i) l += sums[1][i], ls += sums[2][i];
+  l = 0.f;
+  for (int i = 0; i < warps; ++i) l += sums[1][i];
   constexpr int LPR = 8, GROUPS = T / LPR;  // eight lanes take a part's 32 columns
   const int grp = threadIdx.x / LPR, c = blockIdx.z * 32 + (threadIdx.x % LPR) * 4;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(kManyThreads)
       const float4 v = sm[threadIdx.x + i * LPR];
       o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
     }
-    const float inv = ls == 0.f ? 0.f : a.kv.v_scale / ls;
+    const float inv = l == 0.f ? 0.f : a.kv.v_scale / l;
     const float w[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     store_out4<X>(a.o + (out * D + c) * 2, w);
   }

@@ -1062,3 +1062,30 @@ def test_decode_logits_far_from_zero(pkg, dtype, power):
         _check_decode(pkg, c, q, scale=2.0 ** (power - 4 - min(power, 8)))
         if dtype == F16:
             _check_decode(pkg, c, q, scale=2.0 ** (21 - 4 - min(power, 8)))
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+@pytest.mark.parametrize("group", [2, 12])
+def test_decode_weights_keep_more_than_16_bits(pkg, x, dtype, scales, d, group):
+    """Values of alternating sign: O is a small difference, and a weight's error shows in it undivided.  A weight in two
+    16-bit words errs by the square of one word's half step; the rest of the tolerance is _reference's."""
+    lens = [2, 4, 16, 64, 300, 3000]
+    c = Case(pkg, lens, H=1, d=d, dtype=dtype, scales=scales, seed=d + group)
+    for b, n in enumerate(lens):
+        pos = torch.arange(n)
+        sign = (1.0 - 2.0 * (pos % 2)).to(dtype)
+        c.v_ref[b, 0, :n] = sign.double()[:, None] * scales[1]
+        _raw(c.v)[c.table[b, pos // 16].long().cuda(), 0, (pos % 16).cuda()] = _raw(sign[:, None].expand(n, d).contiguous()).cuda()
+    q = c.randn(len(lens), group, d, dtype=x)
+    scale = 1 / math.sqrt(d)
+    o, lse = _check_decode(pkg, c, q)
+    eps, word = torch.finfo(x).eps / 2, torch.finfo(F16 if dtype == E4M3 else dtype).eps / 2
+    for b, n in enumerate(lens):
+        k, v, y = c.k_ref[b, 0, :n], c.v_ref[b, 0, :n], q[b].double()
+        w = torch.softmax(scale * (y @ k.T), -1)
+        dt = ((d + 8) * 2.0 ** -24 * scale * (y.abs() @ k.abs().T)).amax(-1, keepdim=True)
+        want = w @ v
+        tol = eps * want.abs() * (1 + 1e-3) + (word ** 2 + 2 * dt + 2.0 ** -20) * (w @ v.abs() + want.abs())
+        err = (o[b].double().cpu() - want).abs()
+        assert (err <= tol).all(), "sequence of %d: off by %g of its tolerance" % (n, (err / tol).max())
