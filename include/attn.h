@@ -307,8 +307,9 @@ typedef struct {
  *             multiple of 16 up to head_dim (0: no rotation).  Channels (i,
  *             i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved, turn by angle i
  *             in fp32: x1 cos - x2 sin, x2 cos + x1 sin; one rounding.
- * An e4m3 cache holds x / scale rounded to nearest even, saturated at +-448
- * (NaN stays NaN).  Summaries, where the cache has them: a page's is started
+ * An e4m3 cache holds the fp32 quotient x / scale (x the row's element, or what
+ * the rotation gives in fp32) rounded to nearest even, saturated at +-448 (NaN
+ * stays NaN).  Summaries, where the cache has them: a page's is started
  * by the token in its first slot and widened by later ones (a NaN is passed
  * over); after a sequence was cut back it still covers the dropped tokens.
  * Slots with seq_lens[b] = 0 and rows of padding write nothing, nor do

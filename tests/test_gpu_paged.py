@@ -1089,3 +1089,26 @@ def test_decode_weights_keep_more_than_16_bits(pkg, x, dtype, scales, d, group):
         tol = eps * want.abs() * (1 + 1e-3) + (word ** 2 + 2 * dt + 2.0 ** -20) * (w @ v.abs() + want.abs())
         err = (o[b].double().cpu() - want).abs()
         assert (err <= tol).all(), "sequence of %d: off by %g of its tolerance" % (n, (err / tol).max())
+
+
+# ------------------------------------------------------------------ 8-bit scales
+
+@pytest.mark.parametrize("x", [BF16, F16])
+@pytest.mark.parametrize("scale", [math.exp(0.37 * i - 3) for i in range(12)] + [448.0 / 3 * 2.0 ** -i for i in (9, 30)] + [1.9999 * 2.0 ** -83, 1e-25, 1e25,
+                                   1.0, 2.0 ** -6, 7.0, 0.21875, 0.4375, 0.03, 448.0 / 3, 2.0 ** -126, 2.0 ** -127, 2.0 ** -140, 1.5 * 2.0 ** -133,
+                                   2.0 ** 127, 3e38])
+def test_append_stores_the_quotient_bit_for_bit(pkg, x, scale):
+    """Every 16-bit value through each scale, against fp32 division."""
+    d, n = 128, 512
+    c = Case(pkg, [n], H=1, page=32, d=d, dtype=E4M3, scales=(scale, scale * 0.75), seed=1, fill=False)
+    every = torch.arange(-32768, 32768).to(torch.int16).view(x).reshape(n, 1, d)
+    back = every.flip(0).contiguous()
+    pkg.attn_paged_append(c.kv, every.cuda(), back.cuda(), token_start=torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    assert pkg.sync_status() == 0
+    pos = torch.arange(n)
+    for cache, rows, s in ((c.k, every, scale), (c.v, back, scale * 0.75)):
+        got = _raw(cache).cpu()[c.table[0, pos // 32].long(), :, pos % 32].view(E4M3)
+        want = (rows.float() / torch.tensor(s, dtype=torch.float32)).clamp(-448, 448).to(E4M3)
+        nan = want.float().isnan()
+        assert torch.equal(got.float().isnan(), nan)
+        assert torch.equal(_raw(got)[~nan], _raw(want)[~nan])
