@@ -1112,3 +1112,21 @@ def test_append_stores_the_quotient_bit_for_bit(pkg, x, scale):
         nan = want.float().isnan()
         assert torch.equal(got.float().isnan(), nan)
         assert torch.equal(_raw(got)[~nan], _raw(want)[~nan])
+
+
+# ------------------------------------------------------------------ lists longer than their sequences
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("page", [8, 16, 64])
+def test_list_entries_past_the_number_of_pages_are_not_read(pkg, d, dtype, page):
+    """As many entries count as the sequence has pages, whatever the tile that they lie in."""
+    lens = [2 * page, 2 * page - 3, 1, 3 * page + 1, 0]
+    c = Case(pkg, lens, H=1, page=page, d=d, dtype=dtype, seed=page, scales=(0.02, 0.03))
+    lists = torch.tensor([[1, -1, 0, 0, 1, 1, 0, 0], [0, 1, 0, 1, 0, 1, 0, 1], [0, 0, 0, 0, 0, 0, 0, 0], [3, 0, 2, -1, 1, 1, 1, 1],
+                          [0, 0, 0, 0, 0, 0, 0, 0]], dtype=torch.int32)[:, None]
+    keys = []
+    for n, row in zip(lens, lists[:, 0].tolist()):
+        row = [p for p in row[:-(-n // page)] if p >= 0]
+        keys.append([[p * page + i for p in row for i in range(page) if p * page + i < n]])
+    _check_decode(pkg, c, c.randn(len(lens), 4, d), pages=lists.cuda(), keys=keys)
