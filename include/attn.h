@@ -350,7 +350,7 @@ int attn_paged_decode(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_hea
  *              sum_c max(q_gc k_min[p]_c, q_gc k_max[p]_c),
  * an upper bound of q_g . k over the page's keys.  The first keep_first and the
  * last keep_last pages (their sum at most n_select) are taken whatever their
- * score; of equal scores the lower index.  Scores count to 44 bits or more of
+ * score; of equal scores the lower index.  Scores count to 53 bits or more of
  * their terms' magnitude (not an fp32 sum's 20).  A NaN score ranks first.
  *   pages : out, [B, kv_heads, n_select] int32, ascending; a sequence of fewer
  *           pages gets all of them, then -1.

@@ -19,7 +19,7 @@
 //       steps cuts 17 aligned terms at 2^-23 of the largest or less.  A histogram
 //       brackets the border to [L, H) with H - L <= 4 eps; pages at H + 2 eps or
 //       above are in, those below L - 2 eps out, and only those between (a few)
-//       are scored again, to 44 bits or more.  With eps = inf (a sum that overflowed or is
+//       are scored again, to 53 bits or more.  With eps = inf (a sum that overflowed or is
 //       NaN) that is all of them, in fp64.
 //
 // Measured (GB300; the copy's rate is 6.8 TB/s), both kernels: 8 sequences of 4096
@@ -363,11 +363,13 @@ __device__ __forceinline__ int block_sum(int v, PickShared& sm, int turn) {
   return __reduce_add_sync(0xffffffffu, lane < T / 32 ? sm.count[turn][lane] : 0);
 }
 
-// A sum in two fp32 words, hi + lo with |lo| <= ulp(hi) / 2 (Knuth's and
-// Dekker's error-free sums): 48 bits, 44 after d / 8 additions to lo, near the 46
-// that 128 terms summed in fp64 keep.
-// The fp64 units have a sixtieth of the fp32 rate: some tens of candidates took
-// 20 us there.
+// A sum in three fp32 words: the running sum, the sum of what its additions round off
+// (exact, by Knuth's error-free sum) and the sum of what those round off.  Only the last
+// one's own roundings are lost, 2^-59 of the terms' magnitude for d = 128.  The fp64 units
+// have a sixtieth of the fp32 rate: some tens of candidates took 20 us there.
+struct Sum3 {
+  float hi, mid, lo;
+};
 struct Two {
   float hi, lo;
 };
@@ -375,13 +377,22 @@ __device__ __forceinline__ Two two_sum(float a, float b) {
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ Two two_add(Two a, Two b) {
-  const Two h = two_sum(a.hi, b.hi), l = two_sum(a.lo, b.lo);
-  float c = __fadd_rn(h.lo, l.hi);
-  float s = __fadd_rn(h.hi, c);
-  c = __fadd_rn(l.lo, __fsub_rn(c, __fsub_rn(s, h.hi)));
-  const float r = __fadd_rn(s, c);
-  return {r, __fsub_rn(c, __fsub_rn(r, s))};
+__device__ __forceinline__ Sum3 add(const Sum3& s, float x) {
+  const Two h = two_sum(s.hi, x), m = two_sum(s.mid, h.lo);
+  return {h.hi, m.hi, __fadd_rn(s.lo, m.lo)};
+}
+__device__ __forceinline__ Sum3 add(const Sum3& a, const Sum3& b) {  // the same for (b, a)
+  const Two h = two_sum(a.hi, b.hi), m = two_sum(a.mid, b.mid), n = two_sum(m.hi, h.lo);
+  return {h.hi, n.hi, __fadd_rn(__fadd_rn(a.lo, b.lo), __fadd_rn(m.lo, n.lo))};
+}
+// Order-preserving key of a finite sum: the leading word's, 2^32 to a step of it, and the
+// rest in such units: 56 bits.
+__device__ __forceinline__ uint64_t key_of(const Sum3& s) {
+  const Two v = two_sum(s.mid, s.lo), w = two_sum(s.hi, v.hi), x = two_sum(w.lo, v.lo), r = two_sum(w.hi, x.hi);
+  const int e = max(static_cast<int>((__float_as_uint(r.hi) >> 23) & 255u), 60);  // below 2^-67 the rest counts for less
+  const float unit = __uint_as_float(static_cast<uint32_t>(309 - e) << 23);       // 2^32 steps of r.hi
+  const long long rest = __float2ll_rn(r.lo * unit) + __float2ll_rn(x.lo * unit);
+  return (static_cast<uint64_t>(key32(r.hi)) << 32) + static_cast<uint64_t>(rest);
 }
 
 // The definition, by one warp; every lane gets it.  Eight lanes take a head,
@@ -398,11 +409,11 @@ __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, i
   load_channels<C>(a.kv.kmin + at, lo);
   load_channels<C>(a.kv.kmax + at, hi);
   double best = -INFINITY;
-  Two top = {-INFINITY, 0.f};
+  uint64_t top = 0;
   for (int g0 = 0; g0 < G; g0 += 4) {
     const int g = min(g0 + (lane >> 3), G - 1);  // the last head again where there is none
     const uint8_t* q = a.q.p + b * a.q.row + (static_cast<int64_t>(h) * G + g) * a.q.head;
-    Two s = {0.f, 0.f};
+    Sum3 s = {0.f, 0.f, 0.f};
     double d = 0.0;
     float qf[D / 8];
     load_channels<X>(q + c0 * 2, qf);
@@ -410,8 +421,7 @@ __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, i
     for (int i = 0; i < D / 8; ++i) {
       const float x = qf[i], k = x >= 0.f ? hi[i] : lo[i];
       if constexpr (WORDS) {
-        const Two t = two_sum(s.hi, __fmul_rn(x, k));
-        s = {t.hi, __fadd_rn(s.lo, t.lo)};
+        s = add(s, __fmul_rn(x, k));
       } else {
         d = fma(static_cast<double>(x), static_cast<double>(k), d);
       }
@@ -419,12 +429,13 @@ __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, i
 #pragma unroll
     for (int x = 1; x < 8; x <<= 1) {
       if constexpr (WORDS)
-        s = two_add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, x), __shfl_xor_sync(0xffffffffu, s.lo, x)});
+        s = add(s, Sum3{__shfl_xor_sync(0xffffffffu, s.hi, x), __shfl_xor_sync(0xffffffffu, s.mid, x),
+                        __shfl_xor_sync(0xffffffffu, s.lo, x)});
       else
         d += __shfl_xor_sync(0xffffffffu, d, x);
     }
     if constexpr (WORDS) {
-      if (s.hi > top.hi || (s.hi == top.hi && s.lo > top.lo)) top = s;
+      top = max(top, key_of(s));
     } else {
       best = isnan(d) || isnan(best) ? NAN : fmax(best, d);
     }
@@ -432,14 +443,13 @@ __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, i
 #pragma unroll
   for (int x = 8; x < 32; x <<= 1) {
     if constexpr (WORDS) {
-      const Two s = {__shfl_xor_sync(0xffffffffu, top.hi, x), __shfl_xor_sync(0xffffffffu, top.lo, x)};
-      if (s.hi > top.hi || (s.hi == top.hi && s.lo > top.lo)) top = s;
+      top = max(top, static_cast<uint64_t>(__shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(top), x)));
     } else {
       const double d = __shfl_xor_sync(0xffffffffu, best, x);
       best = isnan(d) || isnan(best) ? NAN : fmax(best, d);
     }
   }
-  if constexpr (WORDS) return (static_cast<uint64_t>(key32(top.hi)) << 32) | key32(top.lo);
+  if constexpr (WORDS) return top;
   return key64(best);
 }
 
@@ -511,9 +521,9 @@ __global__ void __launch_bounds__(T) attn_paged_pick_kernel(const PagedSelectArg
       eps = fmaxf(eps, __shfl_xor_sync(0xffffffffu, eps, x));
     }
     if (!(most - least <= 1e37f) || end - first - none < want) eps = INFINITY;
-    // Two-word sums where sums of the scores' magnitude neither overflow nor lose
-    // their last bits below fp32's range.
-    const bool words = eps < INFINITY && eps > 1e-24f;
+    // Sums in fp32 words where no product overflows (the terms' magnitude is at most
+    // eps / (d 2.6e-7)), nor the last bits vanish below fp32's range.
+    const bool words = eps < 1e32f && eps > 1e-24f;
     float from = -INFINITY;  // candidates: from <= score < sure
     if (eps < INFINITY) {
       // The border lies in [lo, hi]: less than `want` scores are above, at least

@@ -1130,3 +1130,35 @@ def test_list_entries_past_the_number_of_pages_are_not_read(pkg, d, dtype, page)
         row = [p for p in row[:-(-n // page)] if p >= 0]
         keys.append([[p * page + i for p in row for i in range(page) if p * page + i < n]])
     _check_decode(pkg, c, c.randn(len(lens), 4, d), pages=lists.cuda(), keys=keys)
+
+
+# ------------------------------------------------------------------ scores that differ in their last bits
+
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+@pytest.mark.parametrize("n,group", [(600, 1), (600, 6), (1500, 3)])
+def test_select_equal_and_nearly_equal_sums_of_other_terms(pkg, x, dtype, scales, n, group):
+    """Pages whose summaries are permutations of one set of values under queries of one value in all channels: equal scores
+    from other running sums.  On some pages the smallest term is a step of its own larger or smaller, 2^-40 to 2^-52 of the
+    terms' magnitude.  All sums fit 53 bits, so float64 has them exactly, in any order."""
+    d, t = 128, torch
+    g = t.Generator().manual_seed(n + group)
+    # large, middling and small values: what the running sums round off spans more than 24 bits
+    top, mid, step = {BF16: (2.0 ** 10, 2.0 ** -4, 2.0 ** -27), F16: (2.0 ** 10, 2.0 ** -2, 2.0 ** -24), E4M3: (2.0 ** 7, 2.0 ** -2, 2.0 ** -9)}[dtype]
+    bits = {BF16: 128, F16: 1024, E4M3: 8}[dtype]
+    large, middle = ((1 + t.randint(0, bits, (k,), generator=g).double() / bits) * v for k, v in ((40, top), (48, mid)))
+    small = t.randint(2, 8, (40,), generator=g).double() * step
+    large, middle = large.to(dtype).double(), middle.to(dtype).double()
+    sign = 1.0 - 2.0 * t.randint(0, 2, (d,), generator=g)
+    values = t.cat([large, middle, small]) * sign
+    c = Case(pkg, [16 * n], H=1, d=d, dtype=dtype, scales=scales, seed=1, summaries=True, fill=False)
+    pages = t.stack([values[t.randperm(d, generator=g)] for _ in range(c.k.shape[0])])
+    odd = t.randint(0, c.k.shape[0], (n // 10,), generator=g)
+    at = pages[odd].abs().argmin(1)
+    pages[odd, at] += step * (1.0 - 2.0 * t.randint(0, 2, (len(odd),), generator=g))
+    assert t.equal(pages.to(dtype).double(), pages)
+    for s in (c.k_min, c.k_max):
+        _raw(s).copy_(_raw(pages.to(dtype))[:, None].cuda())
+    q = t.full((1, group, d), 1.0 + 2.0 ** -7 * 37, dtype=x)
+    q[0, group // 2:] *= -1  # the other half of the heads ranks the other way round
+    for m in (2, n // 15, n // 2, n - 7):
+        _check_select(pkg, c, q, m)
