@@ -309,9 +309,11 @@ typedef struct {
  *             in fp32: x1 cos - x2 sin, x2 cos + x1 sin; one rounding.
  * An e4m3 cache holds the fp32 quotient x / scale (x the row's element, or what
  * the rotation gives in fp32) rounded to nearest even, saturated at +-448 (NaN
- * stays NaN).  Summaries, where the cache has them: a page's is started
- * by the token in its first slot and widened by later ones (a NaN is passed
- * over); after a sequence was cut back it still covers the dropped tokens.
+ * stays NaN).  Summaries, where the cache has them: a page's is started by the
+ * token in its first slot and widened by later ones (a NaN is passed over; a
+ * channel of nothing but NaN keeps k_min = inf and k_max = -inf, in e4m3 NaN for
+ * both, and so ranks its page first); after a sequence was cut back it still
+ * covers the dropped tokens.
  * Slots with seq_lens[b] = 0 and rows of padding write nothing, nor do
  * positions at or past table_rows (ATTN_ERR_DEVICE_CHECK through
  * attn_sync_status, as for a token_start that is not ascending within rows

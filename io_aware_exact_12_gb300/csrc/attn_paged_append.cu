@@ -81,9 +81,13 @@ __device__ __forceinline__ void store_pairs(uint8_t* p, const uint32_t (&w)[4]) 
   if constexpr (C == kTypeE4m3) {
     uint32_t v[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(unpack2<false>(w[i]), __NV_SATFINITE, __NV_E4M3))
-                   << ((i & 1) * 16);
+    for (int i = 0; i < 4; ++i) {
+      // Infinite where every key was NaN; e4m3 has no infinity, and 448 would pass for a key.
+      float2 f = unpack2<false>(w[i]);
+      if (isinf(f.x)) f.x = NAN;
+      if (isinf(f.y)) f.y = NAN;
+      v[i >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << ((i & 1) * 16);
+    }
     *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
   } else {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);

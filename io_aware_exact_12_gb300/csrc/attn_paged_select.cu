@@ -419,11 +419,14 @@ __device__ __forceinline__ uint64_t exact_key(const PagedSelectArgs& a, int b, i
     load_channels<X>(q + c0 * 2, qf);
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
-      const float x = qf[i], k = x >= 0.f ? hi[i] : lo[i];
+      const float x = qf[i];
       if constexpr (WORDS) {
-        s = add(s, __fmul_rn(x, k));
+        s = add(s, __fmul_rn(x, x >= 0.f ? hi[i] : lo[i]));
       } else {
-        d = fma(static_cast<double>(x), static_cast<double>(k), d);
+        // Both products, as the definition has it: where every key of a page was NaN, append
+        // leaves kmin = inf and kmax = -inf, and 0 times an infinite one is NaN.
+        const double u = static_cast<double>(x) * lo[i], v = static_cast<double>(x) * hi[i];
+        d += isnan(u) || isnan(v) ? NAN : fmax(u, v);
       }
     }
 #pragma unroll

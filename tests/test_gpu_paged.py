@@ -1162,3 +1162,26 @@ def test_select_equal_and_nearly_equal_sums_of_other_terms(pkg, x, dtype, scales
     q[0, group // 2:] *= -1  # the other half of the heads ranks the other way round
     for m in (2, n // 15, n // 2, n - 7):
         _check_select(pkg, c, q, m)
+
+
+@pytest.mark.parametrize("x,dtype,scales", TYPES)
+def test_select_takes_pages_of_nan_keys_first(pkg, x, dtype, scales):
+    """Append passes NaN over in the summaries, so a page of nothing else keeps what a summary starts with; its logits are
+    NaN, and so it ranks first.  The same for an infinite bound under a query of 0."""
+    n = 100
+    c = Case(pkg, [16 * n], H=1, d=32, dtype=dtype, scales=scales, seed=3, summaries=True, fill=False)
+    rows = c.randn(16 * n, 1, 32, dtype=x)
+    rows[16 * 41:16 * 42] = math.nan
+    rows[16 * 60:16 * 61, :, 5] = math.nan  # one channel of a page
+    pkg.attn_paged_append(c.kv, rows.cuda(), rows.cuda(), token_start=torch.tensor([0, 16 * n], dtype=torch.int32, device="cuda"))
+    for sign in (1, -1):
+        q = sign * (c.randn(1, 3, 32, dtype=x).abs() + 0.1)
+        got = pkg.attn_paged_select(c.kv, q.cuda(), 2, keep_first=0, keep_last=0)
+        assert pkg.sync_status() == 0 and got[0, 0].tolist() == [41, 60]
+    if dtype == E4M3:
+        return  # has no infinities
+    c.k_min[int(c.table[0, 70]), 0, 9] = -math.inf
+    q = c.randn(1, 3, 32, dtype=x).abs() + 0.1
+    q[..., 9] = 0
+    got = pkg.attn_paged_select(c.kv, q.cuda(), 3, keep_first=0, keep_last=0)
+    assert pkg.sync_status() == 0 and got[0, 0].tolist() == [41, 60, 70]
