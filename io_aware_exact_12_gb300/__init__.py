@@ -338,7 +338,10 @@ class PagedKV:
     k_min, k_max : [num_pages, kv_heads, d] of the cache's type, contiguous: key
         summaries for attn_paged_select, kept by attn_paged_append.
 
-    The object holds references to the tensors and no data of its own."""
+    The object holds references to the tensors and no data of its own.  Its
+    attributes cannot be assigned: the calls go by what it was built with, so new
+    lengths or tables are written into the tensors, and other tensors want
+    another PagedKV."""
 
     __slots__ = ("k_pages", "v_pages", "block_table", "seq_lens", "k_min", "k_max", "k_scale", "v_scale", "device",
                  "B", "kv_heads", "page_size", "head_dim", "max_pages", "dtype", "_struct", "_address")
@@ -371,18 +374,27 @@ class PagedKV:
                 raise TypeError("%s must be of the cache's type on its device" % name)
             if tuple(t.shape) != (P, H, d) or not t.is_contiguous():
                 raise ValueError("%s must be a contiguous [num_pages, kv_heads, d]" % name)
-        self.k_pages, self.v_pages, self.block_table, self.seq_lens = k_pages, v_pages, block_table, seq_lens
-        self.k_min, self.k_max, self.k_scale, self.v_scale = k_min, k_max, float(k_scale), float(v_scale)
-        self.device, self.dtype = dev, k_pages.dtype
-        self.B, self.max_pages = int(block_table.shape[0]), int(block_table.shape[1])
-        self.kv_heads, self.page_size, self.head_dim = H, page, d
         three = ctypes.c_longlong * 3
-        self._struct = _CacheStruct(_PagedKvStruct(
+        B, max_pages, k_scale, v_scale = int(block_table.shape[0]), int(block_table.shape[1]), float(k_scale), float(v_scale)
+        struct = _CacheStruct(_PagedKvStruct(
             k_pages.data_ptr(), v_pages.data_ptr(), three(*k_pages.stride()[:3]), three(*v_pages.stride()[:3]),
             k_min.data_ptr() if k_min is not None else None, k_max.data_ptr() if k_max is not None else None,
-            block_table.data_ptr(), seq_lens.data_ptr(), int(block_table.stride(0)), P, page, H, d, self.max_pages,
-            self.B, _TYPE_CODES[k_pages.dtype], self.k_scale, self.v_scale), dev.index)
-        self._address = ctypes.addressof(self._struct)
+            block_table.data_ptr(), seq_lens.data_ptr(), int(block_table.stride(0)), P, page, H, d, max_pages,
+            B, _TYPE_CODES[k_pages.dtype], k_scale, v_scale), dev.index)
+        for name, value in (("k_pages", k_pages), ("v_pages", v_pages), ("block_table", block_table), ("seq_lens", seq_lens),
+                            ("k_min", k_min), ("k_max", k_max), ("k_scale", k_scale), ("v_scale", v_scale), ("device", dev),
+                            ("B", B), ("kv_heads", H), ("page_size", page), ("head_dim", d), ("max_pages", max_pages),
+                            ("dtype", k_pages.dtype), ("_struct", struct), ("_address", ctypes.addressof(struct))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a PagedKV cannot be changed (%s): write into its tensors, or build another" % name)
+
+    def __delattr__(self, name):
+        raise AttributeError("a PagedKV cannot be changed (%s)" % name)
+
+    def __copy__(self):
+        return self
 
 
 _native_module = None

@@ -1185,3 +1185,16 @@ def test_select_takes_pages_of_nan_keys_first(pkg, x, dtype, scales):
     q[..., 9] = 0
     got = pkg.attn_paged_select(c.kv, q.cuda(), 3, keep_first=0, keep_last=0)
     assert pkg.sync_status() == 0 and got[0, 0].tolist() == [41, 60, 70]
+
+
+def test_a_cache_keeps_what_it_was_built_with(pkg):
+    c = Case(pkg, [100, 20], H=2, d=64, seed=1)
+    q = c.randn(2, 4, 64)
+    _check_decode(pkg, c, q)
+    with pytest.raises(AttributeError):
+        c.kv.seq_lens = torch.tensor([5, 5], dtype=torch.int32, device="cuda")
+    assert c.kv.seq_lens is c.seq_lens and c.kv.block_table is c.block_table and c.kv.k_pages is c.k and c.kv.device == c.k.device
+    assert (c.kv.B, c.kv.kv_heads, c.kv.page_size, c.kv.head_dim, c.kv.dtype) == (2, 2, 16, 64, BF16)
+    c.lens_list = [5, 5]
+    c.seq_lens.fill_(5)
+    _check_decode(pkg, c, q)

@@ -1,5 +1,6 @@
 """Refusals of the paged-cache entry points: every bad argument is answered
 before any CUDA call, so fake pointers serve and no GPU is needed."""
+import copy
 import ctypes
 
 import pytest
@@ -178,3 +179,15 @@ def test_the_binding_refuses_what_is_no_cache(pkg):
     for f in (pkg.attn_paged_append, pkg.attn_paged_decode, pkg.attn_paged_select):
         with pytest.raises(TypeError):
             f(t, t, 1)
+
+
+def test_a_cache_description_cannot_be_changed(pkg):
+    """The calls go by the structure that was built at first: an assignment would be passed over in silence, and the
+    tensor it replaced freed while the kernels still read it."""
+    kv = object.__new__(pkg.PagedKV)
+    for name in pkg.PagedKV.__slots__ + ("other",):
+        with pytest.raises(AttributeError, match="cannot be changed"):
+            setattr(kv, name, 1)
+        with pytest.raises(AttributeError, match="cannot be changed"):
+            delattr(kv, name)
+    assert copy.copy(kv) is kv
