@@ -582,7 +582,9 @@ int paged_rows(const attn_rows_t* r, int64_t rows, int heads, int d, bool output
 
 int query_heads_ok(int q_heads, const PagedKv& kv) {
   if (q_heads < 1 || q_heads % kv.H) return kStatusInvalid;
-  return static_cast<int64_t>(kv.B) * q_heads > 65535 ? kStatusUnsupported : kStatusOk;
+  // No grid has a block to every (sequence, query head); a row of o's heads counts in int.
+  if (q_heads > 65535) return kStatusUnsupported;
+  return q_heads / kv.H > 1024 && static_cast<int64_t>(kv.B) * q_heads > 65535 ? kStatusUnsupported : kStatusOk;
 }
 
 int paged_device(PagedKv* kv, int** status) {

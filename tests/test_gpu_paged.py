@@ -1198,3 +1198,16 @@ def test_a_cache_keeps_what_it_was_built_with(pkg):
     c.lens_list = [5, 5]
     c.seq_lens.fill_(5)
     _check_decode(pkg, c, q)
+
+
+@pytest.mark.parametrize("B,H,Hq", [(520, 8, 128), (260, 16, 384), (1500, 2, 90)])
+def test_more_query_heads_in_all_than_a_grid_has_rows(pkg, B, H, Hq):
+    """B * query heads past 65535."""
+    g = torch.Generator().manual_seed(B)
+    lens = [int(v) for v in torch.randint(0, 60, (B,), generator=g)]
+    c = Case(pkg, lens, H=H, d=32, page=8, seed=B, summaries=True)
+    q = c.randn(B, Hq, 32)
+    o, lse = _check_decode(pkg, c, q)
+    pages, want = _check_select(pkg, c, q, 3)
+    keys = [[[p * 8 + i for p in row for i in range(8) if p * 8 + i < lens[b]] for row in rows] for b, rows in enumerate(want)]
+    _check_decode(pkg, c, q, pages=pages, keys=keys)

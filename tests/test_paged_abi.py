@@ -191,3 +191,15 @@ def test_a_cache_description_cannot_be_changed(pkg):
         with pytest.raises(AttributeError, match="cannot be changed"):
             delattr(kv, name)
     assert copy.copy(kv) is kv
+
+
+def test_many_sequences_of_many_heads_are_taken(pkg):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: fake pointers would launch")
+    for B, H, heads in ((512, 8, 128), (1024, 8, 64), (256, 16, 384), (4000, 16, 64)):
+        kw = dict(B=B, H=H, heads=heads, table_stride=8, P=4)
+        assert _decode(pkg, **kw) in (3, 5), kw
+        assert _select(pkg, **kw) in (3, 5), kw
+    assert _decode(pkg, B=1, H=1, heads=65535, P=4) in (3, 5)
+    assert _decode(pkg, B=1, H=1, heads=65536, P=4) == 2
+    assert _decode(pkg, B=2, H=1, heads=40000, P=4) == 2
