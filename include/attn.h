@@ -361,7 +361,7 @@ int attn_paged_decode(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_hea
 int attn_paged_select(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, int* pages, int n_select,
                       int keep_first, int keep_last, int x_type, void* workspace, void* stream);
 
-/* Bytes of workspace (0 for arguments the calls reject).  n_pages as for
+/* Bytes of workspace (0 for sizes that the calls reject).  n_pages as for
  * attn_paged_decode, 0 for all pages.  They depend on the sizes only. */
 long long attn_paged_decode_workspace(const attn_paged_kv_t* kv, int q_heads, int n_pages);
 long long attn_paged_select_workspace(const attn_paged_kv_t* kv);

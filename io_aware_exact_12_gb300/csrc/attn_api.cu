@@ -509,21 +509,36 @@ bool any_overlap(const Span& out, std::initializer_list<Span> others) {
   return false;
 }
 
+// What the calls and the workspace queries take of a cache's sizes.
+int paged_sizes(const attn_paged_kv_t* c) {
+  if (c->B < 1 || c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->max_pages < 1) return kStatusInvalid;
+  if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return kStatusUnsupported;
+  if (c->page_size % 8 || c->page_size > 1024) return kStatusUnsupported;
+  if (c->B > 65535 || c->kv_heads > 65535 || static_cast<int64_t>(c->B) * c->kv_heads > 65535)
+    return kStatusUnsupported;
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > (int64_t{1} << 30)) return kStatusUnsupported;
+  return kStatusOk;
+}
+
+int query_heads_ok(int q_heads, int B, int H) {
+  if (q_heads < 1 || q_heads % H) return kStatusInvalid;
+  // No grid has a block to every (sequence, query head); a row of o's heads counts in int.
+  if (q_heads > 65535) return kStatusUnsupported;
+  return q_heads / H > 1024 && static_cast<int64_t>(B) * q_heads > 65535 ? kStatusUnsupported : kStatusOk;
+}
+
+bool listed_pages_ok(int n, int page) { return n >= 1 && static_cast<int64_t>(n) * page <= (int64_t{1} << 30); }
+
 // What the library needs of a cache, in bytes; host logic only.
 int paged_kv(const attn_paged_kv_t* c, int x_type, PagedKv* kv, Span* ks, Span* vs) {
   if (!c || !c->k_pages || !c->v_pages || !c->block_table || !c->seq_lens) return kStatusInvalid;
-  if (c->B < 1 || c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->max_pages < 1) return kStatusInvalid;
+  if (const int rc = paged_sizes(c)) return rc;
   if (c->type != kTypeBf16 && c->type != kTypeF16 && c->type != kTypeE4m3) return kStatusInvalid;
   if (x_type != kTypeBf16 && x_type != kTypeF16) return kStatusInvalid;
   if (c->type != kTypeE4m3 && c->type != x_type) return kStatusInvalid;
   if (!std::isfinite(c->k_scale) || !std::isfinite(c->v_scale) || c->k_scale <= 0.f || c->v_scale <= 0.f)
     return kStatusInvalid;
   if (c->type != kTypeE4m3 && (c->k_scale != 1.f || c->v_scale != 1.f)) return kStatusInvalid;
-  if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return kStatusUnsupported;
-  if (c->page_size % 8 || c->page_size > 1024) return kStatusUnsupported;
-  if (c->B > 65535 || c->kv_heads > 65535 || static_cast<int64_t>(c->B) * c->kv_heads > 65535)
-    return kStatusUnsupported;
-  if (static_cast<int64_t>(c->max_pages) * c->page_size > (int64_t{1} << 30)) return kStatusUnsupported;
   if (c->table_stride < 0 || (c->B > 1 && c->table_stride < c->max_pages)) return kStatusInvalid;
   if ((c->k_min == nullptr) != (c->k_max == nullptr)) return kStatusInvalid;
   for (const void* p : {static_cast<const void*>(c->k_pages), static_cast<const void*>(c->v_pages),
@@ -578,13 +593,6 @@ int paged_rows(const attn_rows_t* r, int64_t rows, int heads, int d, bool output
   *out = {static_cast<uint8_t*>(r->data), dims[0].stride, dims[1].stride};
   *span = {r->data, span_of(dims, 2, static_cast<int64_t>(d) * 2)};
   return kStatusOk;
-}
-
-int query_heads_ok(int q_heads, const PagedKv& kv) {
-  if (q_heads < 1 || q_heads % kv.H) return kStatusInvalid;
-  // No grid has a block to every (sequence, query head); a row of o's heads counts in int.
-  if (q_heads > 65535) return kStatusUnsupported;
-  return q_heads / kv.H > 1024 && static_cast<int64_t>(kv.B) * q_heads > 65535 ? kStatusUnsupported : kStatusOk;
 }
 
 int paged_device(PagedKv* kv, int** status) {
@@ -657,8 +665,8 @@ int paged_decode_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_hea
   if (!o || !lse || !std::isfinite(scale) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return kStatusInvalid;
   if (pages && (n_pages < 1 || (reinterpret_cast<uintptr_t>(pages) & 3u))) return kStatusInvalid;
-  if ((rc = query_heads_ok(q_heads, a.kv))) return rc;
-  if (pages && static_cast<int64_t>(n_pages) * c->page_size > (int64_t{1} << 30)) return kStatusUnsupported;
+  if ((rc = query_heads_ok(q_heads, c->B, c->kv_heads))) return rc;
+  if (pages && !listed_pages_ok(n_pages, c->page_size)) return kStatusUnsupported;
   if ((rc = paged_rows(q, c->B, q_heads, c->head_dim, false, &a.q, &qn))) return rc;
   const int64_t need = paged_decode_workspace(c->B, q_heads, c->kv_heads, c->head_dim, c->page_size,
                                               pages ? n_pages : c->max_pages);
@@ -696,8 +704,8 @@ int paged_select_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_hea
   if (!c->k_min || !pages || (reinterpret_cast<uintptr_t>(pages) & 3u)) return kStatusInvalid;
   if (n_select < 1 || keep_first < 0 || keep_last < 0 || static_cast<int64_t>(keep_first) + keep_last > n_select)
     return kStatusInvalid;
-  if ((rc = query_heads_ok(q_heads, a.kv))) return rc;
-  if (static_cast<int64_t>(n_select) * c->page_size > (int64_t{1} << 30)) return kStatusUnsupported;
+  if ((rc = query_heads_ok(q_heads, c->B, c->kv_heads))) return rc;
+  if (!listed_pages_ok(n_select, c->page_size)) return kStatusUnsupported;
   if ((rc = paged_rows(q, c->B, q_heads, c->head_dim, false, &a.q, &qn))) return rc;
   const int64_t need = paged_select_workspace(c->B, c->kv_heads, c->max_pages);
   if (need && (!workspace || !aligned16(workspace))) return kStatusInvalid;
@@ -747,15 +755,15 @@ int attn_paged_select(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_hea
 }
 
 long long attn_paged_decode_workspace(const attn_paged_kv_t* kv, int q_heads, int n_pages) {
-  if (!kv || kv->B < 1 || kv->kv_heads < 1 || kv->page_size < 1 || kv->head_dim < 1 || q_heads < 1 ||
-      q_heads % kv->kv_heads || (n_pages < 1 ? kv->max_pages : n_pages) < 1)
+  if (!kv || attn::paged_sizes(kv) || attn::query_heads_ok(q_heads, kv->B, kv->kv_heads) ||
+      (n_pages >= 1 && !attn::listed_pages_ok(n_pages, kv->page_size)))
     return 0;
   return attn::paged_decode_workspace(kv->B, q_heads, kv->kv_heads, kv->head_dim, kv->page_size,
                                       n_pages < 1 ? kv->max_pages : n_pages);
 }
 
 long long attn_paged_select_workspace(const attn_paged_kv_t* kv) {
-  if (!kv || kv->B < 1 || kv->kv_heads < 1 || kv->max_pages < 1) return 0;
+  if (!kv || attn::paged_sizes(kv)) return 0;
   return attn::paged_select_workspace(kv->B, kv->kv_heads, kv->max_pages);
 }
 

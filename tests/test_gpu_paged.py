@@ -1211,3 +1211,19 @@ def test_more_query_heads_in_all_than_a_grid_has_rows(pkg, B, H, Hq):
     pages, want = _check_select(pkg, c, q, 3)
     keys = [[[p * 8 + i for p in row for i in range(8) if p * 8 + i < lens[b]] for row in rows] for b, rows in enumerate(want)]
     _check_decode(pkg, c, q, pages=pages, keys=keys)
+
+
+def test_refused_sizes_take_no_memory(pkg):
+    """A table that is too wide is refused before a workspace for it is allocated."""
+    H, page = 512, 16
+    k = torch.zeros((2, H, page, 32), dtype=BF16, device="cuda")
+    lo = torch.zeros((2, H, 32), dtype=BF16, device="cuda")
+    table = torch.zeros((1, (1 << 26) + 1), dtype=torch.int32, device="cuda")
+    kv = pkg.PagedKV(k, k.clone(), table, torch.tensor([3], dtype=torch.int32, device="cuda"), k_min=lo, k_max=lo.clone())
+    q = torch.zeros((1, H, 32), dtype=BF16, device="cuda")
+    for call in (lambda: pkg.attn_paged_select(kv, q, 4), lambda: pkg.attn_paged_decode(kv, q)):
+        torch.cuda.reset_peak_memory_stats()
+        now = torch.cuda.memory_allocated()
+        with pytest.raises(pkg.AttnError) as e:
+            call()
+        assert e.value.code == 2 and torch.cuda.max_memory_allocated() - now < 1 << 20

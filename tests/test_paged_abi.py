@@ -203,3 +203,16 @@ def test_many_sequences_of_many_heads_are_taken(pkg):
     assert _decode(pkg, B=1, H=1, heads=65535, P=4) in (3, 5)
     assert _decode(pkg, B=1, H=1, heads=65536, P=4) == 2
     assert _decode(pkg, B=2, H=1, heads=40000, P=4) == 2
+
+
+def test_workspace_sizes_of_refused_sizes_are_zero(pkg):
+    """A caller allocates what these say before the call can refuse the sizes."""
+    L, by = pkg.lib(), ctypes.byref
+    for kw in (dict(d=96), dict(d=256), dict(page=12), dict(page=2048), dict(B=40000), dict(H=70000, k_strides=(0, 0, 0), v_strides=(0, 0, 0)),
+               dict(max_pages=1 << 27, table_stride=1 << 27), dict(max_pages=2147483647, table_stride=1 << 31), dict(P=0), dict(max_pages=0)):
+        assert L.attn_paged_decode_workspace(by(_kv(pkg, **kw)), 4 * (35000 if "H" in kw else 1), 0) == 0, kw
+        assert L.attn_paged_select_workspace(by(_kv(pkg, **kw))) == 0, kw
+    assert L.attn_paged_decode_workspace(by(_kv(pkg)), 65538, 0) == 0
+    assert L.attn_paged_decode_workspace(by(_kv(pkg)), 40000, 0) == 0
+    assert L.attn_paged_decode_workspace(by(_kv(pkg)), 4, 1 << 27) == 0
+    assert L.attn_paged_decode_workspace(by(_kv(pkg)), 4, 0) > 0 and L.attn_paged_select_workspace(by(_kv(pkg))) > 0
