@@ -336,6 +336,7 @@ int attn_paged_append(const attn_paged_kv_t* kv, const attn_rows_t* k, const att
  *          negative entries behind the others (of a sequence of fewer than
  *          n_pages pages only as many entries are read as it has pages).
  *          Indices past the sequence's last page are skipped.
+ *   scale : of the logits; finite, also times k_scale log2(e).
  * A sequence without visible tokens gets o = 0, lse = -inf.  Slots behind a
  * sequence's end may hold anything (NaN too).
  *   workspace : attn_paged_decode_workspace() bytes of device memory, 16-byte

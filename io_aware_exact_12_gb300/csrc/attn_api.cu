@@ -664,6 +664,9 @@ int paged_decode_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_hea
   if (rc) return rc;
   if (!o || !lse || !std::isfinite(scale) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return kStatusInvalid;
+  // Logits in units of log2; an infinite factor would make NaN of products that are 0.
+  const float sl2 = scale * c->k_scale * 1.4426950408889634f;
+  if (!std::isfinite(sl2)) return kStatusInvalid;
   if (pages && (n_pages < 1 || (reinterpret_cast<uintptr_t>(pages) & 3u))) return kStatusInvalid;
   if ((rc = query_heads_ok(q_heads, c->B, c->kv_heads))) return rc;
   if (pages && !listed_pages_ok(n_pages, c->page_size)) return kStatusUnsupported;
@@ -685,7 +688,7 @@ int paged_decode_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_hea
   a.lse = lse;
   a.pages = pages;
   a.n_pages = n_pages;
-  a.sl2 = scale * c->k_scale * 1.4426950408889634f;
+  a.sl2 = sl2;
   a.x_type = x_type;
   a.stream = static_cast<cudaStream_t>(stream);
   a.ws = static_cast<uint8_t*>(workspace);

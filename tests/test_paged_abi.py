@@ -216,3 +216,12 @@ def test_workspace_sizes_of_refused_sizes_are_zero(pkg):
     assert L.attn_paged_decode_workspace(by(_kv(pkg)), 40000, 0) == 0
     assert L.attn_paged_decode_workspace(by(_kv(pkg)), 4, 1 << 27) == 0
     assert L.attn_paged_decode_workspace(by(_kv(pkg)), 4, 0) > 0 and L.attn_paged_select_workspace(by(_kv(pkg))) > 0
+
+
+def test_decode_refuses_scales_whose_product_overflows(pkg):
+    assert _decode(pkg, scale=3e38) == 1
+    assert _decode(pkg, scale=-3e38) == 1
+    assert _decode(pkg, type=2, scale=1e10, k_scale=1e30) == 1
+    if not torch.cuda.is_available():
+        assert _decode(pkg, scale=2e38) in (3, 5)
+        assert _decode(pkg, type=2, scale=1e-10, k_scale=1e30) in (3, 5)
