@@ -1227,3 +1227,60 @@ def test_refused_sizes_take_no_memory(pkg):
         with pytest.raises(pkg.AttnError) as e:
             call()
         assert e.value.code == 2 and torch.cuda.max_memory_allocated() - now < 1 << 20
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n", [40, 700, 9000])
+def test_decode_logits_about_the_end_of_the_shift(pkg, sign, n):
+    """Integer logits on either side of +-2^20 (in units of log2), where the weights' origin goes from 15 below the maximum to
+    the maximum itself: tiles, warps and blocks with either are joined.  The products are exact, so only the weights' words
+    and the sums err."""
+    d = 64
+    c = Case(pkg, [n], H=1, d=d, dtype=F16, seed=n)
+    k = torch.zeros(n, d, dtype=torch.float64)
+    k[:, 0] = 1024
+    k[:, 1] = torch.randint(-14, 15, (n,), generator=c.g).double()
+    k[::97, 1] += torch.randint(-1000, 5, (len(k[::97]),), generator=c.g)
+    pos = torch.arange(n)
+    _raw(c.k)[c.table[0, pos // 16].long().cuda(), 0, (pos % 16).cuda()] = k.to(F16).cuda()
+    q = torch.zeros(1, 2, d, dtype=F16)
+    q[0, :, 0], q[0, :, 1] = sign * 1024, torch.tensor([1.0, -1.0])
+    scale = math.log(2.0)
+    assert float(torch.tensor(scale) * torch.tensor(1.4426950408889634)) == 1.0  # fp32: the factor is exact too
+    o, lse = pkg.attn_paged_decode(c.kv, q.cuda(), scale=scale)
+    assert pkg.sync_status() == 0
+    s = q[0].double() @ k.T
+    w = torch.softmax((s - s.amax(-1, keepdim=True)) * math.log(2.0), -1)
+    v = c.v_ref[0, 0, :n]
+    want = w @ v
+    tol = 2.0 ** -11 * want.abs() * (1 + 1e-3) + (2.0 ** -22 + 2.0 ** -19) * (w @ v.abs() + want.abs()) + 2.0 ** -25
+    err = (o[0].double().cpu() - want).abs()
+    assert (err <= tol).all(), "off by %g of its tolerance" % (err / tol).max()
+    l = torch.logsumexp(s * math.log(2.0), -1)
+    assert ((lse[0].double().cpu() - l).abs() <= 2.0 ** -22 * l.abs()).all()
+
+
+@pytest.mark.parametrize("B,live", [(4096, 2), (60000, 3)])
+def test_long_runs_of_slots_without_a_sequence(pkg, B, live):
+    """Slots between two sequences that hold none."""
+    at = [0] + sorted(int(v) for v in torch.randint(1, B - 1, (live - 2,), generator=torch.Generator().manual_seed(B))) + [B - 1]
+    c = Case(pkg, [4000 - 7 * i for i in range(live)], H=1, d=64, seed=1, summaries=True)
+    q = c.randn(live, 2, 64).cuda()
+    want = pkg.attn_paged_decode(c.kv, q)
+    table = torch.full((B, c.table.shape[1]), 0x7FFFFFF0, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    table[at], lens[at] = c.block_table, c.seq_lens
+    wide = torch.full((B, 2, 64), math.nan, dtype=BF16, device="cuda")
+    wide[at] = q
+    kv = pkg.PagedKV(c.k, c.v, table, lens, k_min=c.k_min, k_max=c.k_max)
+    o, lse = pkg.attn_paged_decode(kv, wide)
+    assert pkg.sync_status() == 0
+    ro, rl, to, tl = _reference(c, q.cpu(), 1 / 8)
+    assert ((o[at].double().cpu() - ro).abs() <= to).all() and ((lse[at].double().cpu() - rl).abs() <= tl).all()
+    assert ((want[0].double().cpu() - ro).abs() <= to).all()
+    empty = torch.ones(B, dtype=torch.bool, device="cuda")
+    empty[at] = False
+    assert (o[empty] == 0).all() and (lse[empty] == -math.inf).all()
+    pages = pkg.attn_paged_select(kv, wide, 7)
+    assert pkg.sync_status() == 0
+    assert torch.equal(pages[at], pkg.attn_paged_select(c.kv, q, 7)) and (pages[empty] == -1).all()
