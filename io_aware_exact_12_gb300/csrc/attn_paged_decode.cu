@@ -7,12 +7,13 @@
 // is exact by the online softmax of "三招" 2: with m = max_s m_s,
 //     l = sum_s e^{m_s - m} l_s,   O = sum_s e^{m_s - m} O_s / l.
 //
-// Every cached byte is read once, so HBM bounds it: G = Hq / Hkv query heads
-// make 2 G flops per element, beyond the fp32 units' rate from G = 4 or so.  The
-// products run as m16n8k16 matrix instructions, 16 rows of the cache times 8 or 16
-// query heads.  At 6 TB/s they keep the tensor pipe 9 % busy (e4m3, widened to fp16
-// in registers: 17 %), so tcgen05, whose operands would have to lie in shared
-// memory as 64 rows at least and widened, has nothing to gain.
+// Every cached byte is read once for up to 16 query heads to a key/value head (once
+// per 16 beyond), so HBM bounds it: G = Hq / Hkv query heads make 2 G flops per
+// element, beyond the fp32 units' rate from G = 4 or so.  The products run as
+// m16n8k16 matrix instructions, 16 rows of the cache times 8 or 16 query heads.  At
+// 6 TB/s and G = 4 they keep the tensor pipe 13 % busy (e4m3, widened to fp16 in
+// registers: 24 %), so tcgen05, whose operands would have to lie in shared memory as
+// 64 rows at least and widened, has nothing to gain there.
 //
 //   attn_paged_decode_kernel : two or three CTAs per SM, each with a share of all
 //       tiles of keys (tile lists of the items (b, KV head, group of up to 16
@@ -27,13 +28,16 @@
 //   what fp32 weights give up to 2^-16 and l is the fp32 sum of the weights as they are.
 //   attn_paged_merge_kernel : joins the items that were cut by a CTA border.
 //
-// Measured (GB300; the copy's rate is 6.8 TB/s): two sequences of 131071 tokens,
-// 64 / 8 heads of 128, fp16, 1074 MB: 157 us (6.8 TB/s); 61 sequences of up to 8192,
-// 32 / 8 heads of 128, bf16, 965 MB: 152 us (6.3 TB/s); 128 of up to 4096, 16 / 16
-// heads of 64, e4m3, 511 MB: 93 us (5.5 TB/s; its items are short, an item's start
-// and end cost as much as four tiles); one of 1000 tokens: 8.7 us, of which 4 us
-// pass until the first tile has come (length, page table and tile are three trips
-// to memory, one after the other).
+// Measured (GB300, GPU time in a replayed graph; calls one by one take 1 to 3 us
+// more; the copy's rate is 6.8 TB/s): two sequences of 131071 tokens, 64 / 8 heads of
+// 128, fp16, 1074 MB: 157 us (6.8 TB/s); 61 sequences of up to 8192, 32 / 8 heads of
+// 128, bf16, 965 MB: 152 us (6.3 TB/s); 128 of up to 4096, 16 / 16 heads of 64, e4m3,
+// 511 MB: 94 us (5.4 TB/s; its items are short, an item's start and end cost as much
+// as four tiles); 16 of 8192, 64 / 4 heads of 128, bf16, 268 MB: 55 us (4.9 TB/s; two
+// groups of 8 heads share a tile's fragments, and the e4m3 form of 128 channels spills
+// 60 to 100 bytes of registers); one of 1000 tokens: 8.9 us, of which 4 us pass until
+// the first tile has come (length, page table and tile are three trips to memory, one
+// after the other).
 #include <atomic>
 #include <cmath>
 
