@@ -24,8 +24,8 @@
 //       online softmax of its own, and are merged in shared memory where an
 //       item ends.  Short items go whole to clusters of CTAs instead, which join
 //       their results through shared memory.
-//   The weights multiply V as two 16-bit words (rounding and remainder), so O keeps
-//   what fp32 weights give up to 2^-16 and l is the fp32 sum of the weights as they are.
+//   The weights multiply V as two 16-bit words (one and its remainder), so O keeps
+//   what fp32 weights give up to 3 2^-16 and l is the fp32 sum of the weights as they are.
 //   attn_paged_merge_kernel : joins the items that were cut by a CTA border.
 //
 // Measured (GB300, GPU time in a replayed graph; calls one by one take 1 to 3 us
@@ -471,6 +471,9 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   const int g = lane >> 2, t4 = lane & 3, l8 = lane & 7, mi = lane >> 3;
   const int swz = F::RBX == 128 ? l8 : F::RBX == 64 ? l8 >> 1 : l8 >> 2;
   constexpr int CPB = F::RBX / 16;  // 16-byte chunks of a box row
+  // A weight's first word is rounded from this much of it, so that no rounding reaches
+  // the weight itself.
+  constexpr float kFirstWord = BF ? 1.f - 0x1p-7f : 1.f - 0x1p-10f;
   bool ok = true;
   int cur = 0, turn = 0;       // tiles of the CTA that are done, and of this warp
   long long w0 = s.w0;         // start of the item, in weights
@@ -652,7 +655,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
           const float p2 = ex2_approx(v[2] - z0), p3 = ex2_approx(v[3] - z1);
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
-          const uint32_t u = pack2<BF>(p0, p1), w = pack2<BF>(p2, p3);
+          const uint32_t u = pack2<BF>(p0 * kFirstWord, p1 * kFirstWord), w = pack2<BF>(p2 * kFirstWord, p3 * kFirstWord);
           const float2 uf = unpack2<BF>(u), wf = unpack2<BF>(w);
           pf[nt][x][0] = transpose8(u);
           pf[nt][x][1] = transpose8(w);
@@ -660,11 +663,12 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
           pr[nt][x][1] = transpose8(pack2<BF>(p2 - wf.x, p3 - wf.y));
         }
       }
-      // O^T += V^T P^T, with every weight as two 16-bit words, its rounding and the
-      // remainder: 2^-16 (fp16: 2^-22) of it is lost, against 2^-8 (2^-11) in one word,
-      // which was an O with up to 1.3 times the error of fp32 weights.  The matrix pipe has
-      // room for the second product (two sequences of 131071 tokens 155.3 -> 155.2 us, 16 of
-      // 16384 in e4m3 94.3 -> 95.3, one of 1000 8.84 -> 8.97).
+      // O^T += V^T P^T, with every weight as two 16-bit words, a first one a little below
+      // it and the remainder: 3 2^-16 (fp16: 3 2^-22) of it is lost at most, against 2^-8
+      // (2^-11) in one word, which was an O with up to 1.3 times the error of fp32 weights.
+      // Both words are positive where the weight is, or a value of inf would become NaN.
+      // The matrix pipe has room for the second product (two sequences of 131071 tokens
+      // 155.3 -> 155.2 us, 16 of 16384 in e4m3 94.3 -> 95.3, one of 1000 8.84 -> 8.97).
 #pragma unroll
       for (int kk = 0; kk < TK / 16; ++kk) {
         if constexpr (E8) {
