@@ -380,7 +380,10 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
         h = mine.hr / RT;
         int j = e;
         // Of a list only as many entries as the sequence has pages (tiles_of), also inside the last tile.
-        if (a.pages) j = e < min(a.n_pages, (mine.len + kv.page - 1) / kv.page) ? a.pages[(static_cast<int64_t>(mine.b) * kv.H + h) * a.n_pages + e] : -1;
+        if (a.pages)
+          j = e < min(a.n_pages, (mine.len + kv.page - 1) / kv.page)
+                  ? a.pages[(static_cast<int64_t>(mine.b) * kv.H + h) * a.n_pages + e]
+                  : -1;
         const int64_t left = static_cast<int64_t>(mine.len) - (static_cast<int64_t>(j) * kv.page + row);
         if (j >= 0 && left > 0) {
           seen = static_cast<int>(min(left, static_cast<int64_t>(box_rows)));

@@ -13,6 +13,8 @@ a step, finfo(t).eps / 2 of the value.
     by 2 dt + 2^-20 relative (exp2 and the sums); P is rounded to 16 bits with
     the same rounded weights in the denominator, so by the 16-bit type's eps / 2
     about a mean of w |v|.  O then has one rounding of its own.
+    (The kernel keeps more of P, two 16-bit words and an fp32 sum, so that this
+    part is an upper bound; test_decode_weights_keep_more_than_16_bits has its own.)
 """
 import math
 
