@@ -262,8 +262,9 @@ int attn_decode(const void* q, const void* k, const void* v, void* o, float* lse
  *                k_scale (v_scale) times what is stored, finite and > 0; the
  *                scales of the other types are 1.
  *   Supported: head_dim in {32, 64, 128}; page_size a multiple of 8, at most
- *   1024; max_pages * page_size <= 2^30; B * kv_heads <= 65535; query heads
- *   <= 65535, and B * query heads too where a key/value head has more than 1024.
+ *   1024; max_pages * page_size <= 2^30; B and kv_heads <= 65535, and B * kv_heads
+ *   too (up to 8192 sequences: 2^20); query heads <= 65535, and B * query heads too
+ *   where a key/value head has more than 1024.
  * Table entries and lengths are read on the device only, so a captured graph
  * may be replayed after they changed.  A page number outside [0, num_pages) or
  * a length outside [0, max_pages * page_size] is never followed: what it would

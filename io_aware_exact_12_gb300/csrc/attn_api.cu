@@ -514,7 +514,8 @@ int paged_sizes(const attn_paged_kv_t* c) {
   if (c->B < 1 || c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->max_pages < 1) return kStatusInvalid;
   if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return kStatusUnsupported;
   if (c->page_size % 8 || c->page_size > 1024) return kStatusUnsupported;
-  if (c->B > 65535 || c->kv_heads > 65535 || static_cast<int64_t>(c->B) * c->kv_heads > 65535)
+  // B is a grid's y; (sequence, head) pairs are counted in x and in 64 bits only.
+  if (c->B > 65535 || c->kv_heads > 65535 || static_cast<int64_t>(c->B) * c->kv_heads > (c->B <= 8192 ? 1 << 20 : 65535))
     return kStatusUnsupported;
   if (static_cast<int64_t>(c->max_pages) * c->page_size > (int64_t{1} << 30)) return kStatusUnsupported;
   return kStatusOk;

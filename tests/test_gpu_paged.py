@@ -1306,3 +1306,17 @@ def test_infinite_values_stay_infinite(pkg, dtype, n):
         else:
             assert o[0, :, ch].isfinite().all(), ch
     assert o[1].isfinite().all() and lse.isfinite().all()
+
+
+def test_more_key_value_heads_in_all_than_a_grid_has_rows(pkg):
+    """B * kv_heads past 65535: a thousand slots of 64 heads, forty of them with a sequence."""
+    g = torch.Generator().manual_seed(1)
+    B, H = 1100, 64
+    lens = [0] * B
+    for b in [0, B - 1, 1023, 1024] + torch.randint(0, B, (36,), generator=g).tolist():
+        lens[b] = int(torch.randint(1, 70, (1,), generator=g))
+    c = Case(pkg, lens, H=H, d=32, page=8, seed=2, summaries=True)
+    q = c.randn(B, H, 32)
+    _check_decode(pkg, c, q)
+    _check_select(pkg, c, q, 3)
+    _check_append(pkg, c, [1] * B, BF16, Hq=H, single=True)

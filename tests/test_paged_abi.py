@@ -225,3 +225,17 @@ def test_decode_refuses_scales_whose_product_overflows(pkg):
     if not torch.cuda.is_available():
         assert _decode(pkg, scale=2e38) in (3, 5)
         assert _decode(pkg, type=2, scale=1e-10, k_scale=1e30) in (3, 5)
+
+
+def test_many_sequences_of_many_key_value_heads_are_taken(pkg):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: fake pointers would launch")
+    for B, H in ((1024, 64), (8192, 128), (4096, 20)):
+        kw = dict(B=B, H=H, P=4, d=32)
+        rows = [_rows(pkg, p, H, 32) for p in (NEWK, NEWV, Q, QOUT)]
+        assert _decode(pkg, q=rows[2], heads=H, **kw) in (3, 5), kw
+        assert _select(pkg, q=rows[2], heads=H, n=3, **kw) in (3, 5), kw
+        assert _append(pkg, k=rows[0], v=rows[1], no_q=True, heads=0, rows=B, rot=32, **kw) in (3, 5), kw
+    for B, H in ((8192, 129), (8193, 8), (20000, 4)):
+        assert _decode(pkg, heads=H, B=B, H=H, P=4) == 2
+        assert pkg.lib().attn_paged_select_workspace(ctypes.byref(_kv(pkg, B=B, H=H))) == 0
