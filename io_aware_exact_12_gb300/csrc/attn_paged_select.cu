@@ -27,8 +27,8 @@
 // Measured (GB300; the copy's rate is 6.8 TB/s), both kernels: 8 sequences of 4096
 // pages, 32 / 8 heads of 128, bf16, 134 MB of summaries: 36 us, scores 26 and pick
 // 11; 4 of up to 8192 pages, 40 / 8 heads, e4m3, 55 MB: 27 us; one of 1001 pages:
-// 10 us (GPU time in a replayed graph).  The pick runs on one SM per head and is bound by its own 7 to 11 us of
-// barriers and cold instructions.
+// 10 us (GPU time in a replayed graph).  The pick runs on one SM per head and is bound
+// by its own 7 to 11 us of barriers and cold instructions.
 #include <atomic>
 #include <cmath>
 
