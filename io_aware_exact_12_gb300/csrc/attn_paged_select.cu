@@ -390,11 +390,12 @@ __device__ __forceinline__ Sum3 add(const Sum3& a, const Sum3& b) {  // the same
 // Order-preserving key of a finite sum: the leading word's, 2^32 to a step of it, and the
 // rest in such units: 56 bits.
 __device__ __forceinline__ uint64_t key_of(const Sum3& s) {
-  const Two v = two_sum(s.mid, s.lo), w = two_sum(s.hi, v.hi), x = two_sum(w.lo, v.lo), r = two_sum(w.hi, x.hi);
-  const int e = max(static_cast<int>((__float_as_uint(r.hi) >> 23) & 255u), 60);  // below 2^-67 the rest counts for less
-  const float unit = __uint_as_float(static_cast<uint32_t>(309 - e) << 23);       // 2^32 steps of r.hi
-  const long long rest = __float2ll_rn(r.lo * unit) + __float2ll_rn(x.lo * unit);
-  return (static_cast<uint64_t>(key32(r.hi)) << 32) + static_cast<uint64_t>(rest);
+  const Two v = two_sum(s.mid, s.lo), w = two_sum(s.hi, v.hi), x = two_sum(w.lo, v.lo);
+  const float top = __fadd_rn(w.hi, x.hi), low = __fsub_rn(x.hi, __fsub_rn(top, w.hi));  // exact: w.hi is 0 or the larger
+  const int e = max(static_cast<int>((__float_as_uint(top) >> 23) & 255u), 60);  // below 2^-67 the rest counts for less
+  const float unit = __uint_as_float(static_cast<uint32_t>(309 - e) << 23);      // 2^32 steps of `top`
+  const long long rest = static_cast<long long>(__float2int_rn(low * unit)) + __float2int_rn(x.lo * unit);
+  return (static_cast<uint64_t>(key32(top)) << 32) + static_cast<uint64_t>(rest);
 }
 
 // The definition, by one warp; every lane gets it.  Eight lanes take a head,
