@@ -293,6 +293,47 @@ typedef struct {
 } attn_rows_t;
 
 /*
+ * Bookkeeping of a step: from the number of new tokens of each sequence the
+ * block table's new entries, the lengths, token_start for attn_paged_append and
+ * a slot for every new token.  Nothing is read on the host, so that a step can
+ * be captured with the calls that use its results.
+ *   kv   : block_table and seq_lens are written (the struct's other pointers are
+ *          not followed).  Entries of pages that the sequence has are kept.
+ *   n_new : in, [B] int32: new tokens of each sequence, 0 for none, or -1: the
+ *          sequence is over, its pages are free again and its length 0.
+ *   lens : in, [B] int32, tokens before the step; NULL: kv->seq_lens, in place.
+ *   free_pages : in and out, [free_cap] int32: a ring of free page numbers;
+ *          free_state : in, [2] int32: position of the first and number of them.
+ *          New pages are taken from the front, for the sequences in ascending
+ *          order and each one's pages in ascending order; pages of sequences that
+ *          are over go behind the last (and can be taken from the next step on).
+ *   free_out : out, [2] int32, free_state after the step; NULL: in place.
+ *   token_start : out, [B + 1] int32: the sequences' first rows among the new
+ *          tokens' rows, token_start[B] the number of all.
+ *   slots : out, [rows] int64, or NULL: page * page_size + slot in the page of
+ *          each new token; -1 for rows from token_start[B] on.
+ *   rows : the most new tokens that the step may have.
+ *   window, sinks : 0, 0, or those of attn_paged_decode_window.  A sequence then
+ *          holds F = ceil(sinks / page_size) pages of sinks and
+ *          R = ceil((window - 1) / page_size) + 1 others at most: entry j >= F + R
+ *          repeats entry j - R, whose tokens have left the window.  Then at most
+ *          R * page_size new tokens of one sequence in a step (they would share
+ *          slots), and an append must not be repeated after later ones.
+ * The step is done whole or, if more pages are wanted than are free, if there
+ * are more new tokens than rows, or if a length, a count or free_state is out of
+ * range, not at all: lengths and free_state as before, token_start 0, slots -1,
+ * and ATTN_ERR_DEVICE_CHECK through attn_sync_status.  A page number outside
+ * [0, num_pages) in the ring or the table is handed on as -1, with the same
+ * status.  With lens and free_out given the step can be taken again from the
+ * same state (the ring and the table keep what it needs).
+ *   workspace : attn_paged_assign_workspace() bytes, as for attn_paged_decode.
+ * Launches 1 or 2 kernels.
+ */
+int attn_paged_assign(const attn_paged_kv_t* kv, const int* n_new, const int* lens, int* free_pages, int free_cap,
+                      int* free_state, int* free_out, int* token_start, long long* slots, int rows, int window, int sinks,
+                      void* workspace, void* stream);
+
+/*
  * Appends new tokens' keys and values to the cache, with the position rotation
  * applied on the way.
  *   k, v    : in, [rows, kv_heads, head_dim] of x_type.
@@ -348,6 +389,19 @@ int attn_paged_decode(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_hea
                       const int* pages, int n_pages, float scale, int x_type, void* workspace, void* stream);
 
 /*
+ * attn_paged_decode for a model with a sliding window: the new token, which is a
+ * sequence's last, sees its last `window` tokens (itself among them) and its
+ * first `sinks` ones, as a query of attn_fwd_window.  Only the pages that hold
+ * those are looked up and read, so the table entries of others may be anything,
+ * and pages of tokens that have left the window may be in use elsewhere.
+ *   window >= 1, sinks >= 0, both at most 2^30.
+ *   workspace : attn_paged_decode_window_workspace() bytes.
+ * Everything else as for attn_paged_decode.
+ */
+int attn_paged_decode_window(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, void* o, float* lse,
+                             int window, int sinks, float scale, int x_type, void* workspace, void* stream);
+
+/*
  * For each sequence and key/value head the n_select pages on which the new
  * token's queries can have their largest logits (scale > 0):
  *   score(p) = max over the head's query heads g of
@@ -366,7 +420,56 @@ int attn_paged_select(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_hea
 /* Bytes of workspace (0 for sizes that the calls reject).  n_pages as for
  * attn_paged_decode, 0 for all pages.  They depend on the sizes only. */
 long long attn_paged_decode_workspace(const attn_paged_kv_t* kv, int q_heads, int n_pages);
+long long attn_paged_decode_window_workspace(const attn_paged_kv_t* kv, int q_heads, int window, int sinks);
 long long attn_paged_select_workspace(const attn_paged_kv_t* kv);
+long long attn_paged_assign_workspace(const attn_paged_kv_t* kv);
+
+/* [B, heads, N, d] of bf16 or fp16 with contiguous channels, strides in elements:
+ * multiples of 8 (of no effect along an extent of 1) and such that no two rows
+ * overlap; an order of dimensions is not implied, so [B, N, heads, d] and slices
+ * of a projection's output need no copy. */
+typedef struct {
+  void* data;
+  long long batch_stride, head_stride, row_stride;
+} attn_bhnd_t;
+
+/*
+ * Causal attention with a sliding window and sinks, the first tokens, which stay
+ * visible; query heads may share key/value heads.
+ *   q, o : in and out, [B, q_heads, Nq, d];  k, v : in, [B, kv_heads, Nk, d],
+ *          Nk >= Nq; q_heads a multiple of kv_heads: query heads
+ *          h * q_heads / kv_heads and following share key/value head h.
+ *   lse  : out, [B, q_heads, Nq] fp32
+ * The queries are the last Nq of Nk positions: query i stands at
+ * p = i + Nk - Nq and sees key j iff j <= p and (j > p - window or j < sinks).
+ *   window >= 1 (Nk or more: the causal mask), sinks >= 0.
+ *   type : ATTN_TYPE_BF16 or ATTN_TYPE_F16, of all four tensors.
+ * The tiles of keys that no query of a 128-row tile sees are neither loaded nor
+ * multiplied (FlashAttention深度攻略, 进阶追问 "Sparse FlashAttention", for a
+ * mask that is not made of tiles).  Keys and values must be finite: inside a tile
+ * a hidden key has weight 0, and 0 times inf is NaN.
+ * Supported: d in {32, 64, 128}, Nk <= 2^24, B * q_heads <= 65535, finite scale.
+ * The outputs must not overlap the inputs or one another; slices of one buffer
+ * whose rows take turns do not.  Launches 1 kernel.
+ */
+int attn_fwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o, float* lse,
+                    int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks, float scale, int type,
+                    void* stream);
+
+/*
+ * The gradients of attn_fwd_window's output for the same window, sinks and scale
+ * (o and lse from that call), as attn_bwd's; dk and dv are the sums over the
+ * query heads that share a key/value head, and 0 for keys that no query sees.
+ * Scratch from cudaMallocAsync on `stream`, freed on it: an fp32 dQ accumulator
+ * [B, q_heads, Nq, d], two fp32 row vectors, and fp32 partial tiles of dK and dV
+ * where a tile of keys has many more queries than others (the sinks) or there are
+ * few of them.  As in attn_bwd, dQ's sums have no fixed order.  Launches at most 3
+ * kernels.
+ */
+int attn_bwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o,
+                    const attn_bhnd_t* dO, const float* lse, const attn_bhnd_t* dq, const attn_bhnd_t* dk,
+                    const attn_bhnd_t* dv, int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks,
+                    float scale, int type, void* stream);
 
 /*
  * attn_bwd without any memory allocation (bf16).  The pages have no
@@ -411,7 +514,7 @@ const char* attn_status_string(int status);
 
 /* Number of kernel launches the most recent successful attn_fwd* / attn_bwd* /
  * attn_decode / attn_paged_* call on this thread enqueued (forward 1, backward 3,
- * decode 2, paged append 1, paged decode 1 or 2, paged select 2). */
+ * decode 2, paged append 1, paged decode 1 or 2, paged select 2, paged assign 1 or 2). */
 int attn_last_launch_count(void);
 
 #ifdef __cplusplus

@@ -9,8 +9,10 @@ There is no fallback: if the library is missing or fails to load, every call
 raises.
 
 Layout: q, k, v, o, do and the gradients are contiguous [B, H, N, d] tensors
-(bf16 or fp16) on one CUDA device; lse is fp32 [B, H, N].  The paged-cache
-calls take token-major rows [rows, heads, d] and a ``PagedKV``.
+(bf16 or fp16) on one CUDA device; lse is fp32 [B, H, N].  The windowed calls
+take [B, heads, N, d] tensors of any strides whose channels are contiguous, and
+fewer key/value heads than query heads.  The paged-cache calls take token-major
+rows [rows, heads, d] and a ``PagedKV``.
 """
 from __future__ import annotations
 
@@ -21,8 +23,8 @@ import os
 import torch
 
 __all__ = ["attention", "attn_fwd", "attn_bwd", "attn_fwd_dropout", "attn_bwd_dropout", "attn_decode", "attn_fwd_fp8", "attn_fwd_blocksparse", "attn_bwd_blocksparse",
-           "attn_fwd_blocksparse_dropout", "attn_bwd_blocksparse_dropout", "PagedKV", "attn_paged_append",
-           "attn_paged_decode", "attn_paged_select", "rotation_tables", "sync_status", "status_string", "last_launch_count", "lib",
+           "attn_fwd_blocksparse_dropout", "attn_bwd_blocksparse_dropout", "attn_fwd_window", "attn_bwd_window", "PagedKV",
+           "attn_paged_assign", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_window", "attn_paged_select", "rotation_tables", "sync_status", "status_string", "last_launch_count", "lib",
            "AttnError", "LIB_PATH", "STATUS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn.so")
@@ -53,6 +55,11 @@ class _CacheStruct(ctypes.Structure):  # what the compiled binding reads
 
 class _RowsStruct(ctypes.Structure):  # attn_rows_t
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class _BhndStruct(ctypes.Structure):  # attn_bhnd_t
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("row_stride", ctypes.c_longlong)]
 
 
 _lib = None
@@ -99,11 +106,19 @@ def lib() -> ctypes.CDLL:
         L.attn_paged_append.argtypes = [P, P, P, P, P, I, I, P, P, P, I, I, I, I, P]
         L.attn_paged_decode.argtypes = [P, P, I, P, P, P, I, F, I, P, P]
         L.attn_paged_select.argtypes = [P, P, I, P, I, I, I, I, P, P]
-        for f in (L.attn_paged_append, L.attn_paged_decode, L.attn_paged_select):
+        L.attn_paged_decode_window.argtypes = [P, P, I, P, P, I, I, F, I, P, P]
+        L.attn_paged_assign.argtypes = [P, P, P, P, I, P, P, P, P, I, I, I, P, P]
+        L.attn_fwd_window.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P]
+        L.attn_bwd_window.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P]
+        for f in (L.attn_paged_append, L.attn_paged_decode, L.attn_paged_select, L.attn_paged_decode_window,
+                  L.attn_paged_assign, L.attn_fwd_window, L.attn_bwd_window):
             f.restype = I
         L.attn_paged_decode_workspace.argtypes = [P, I, I]
+        L.attn_paged_decode_window_workspace.argtypes = [P, I, I, I]
         L.attn_paged_select_workspace.argtypes = [P]
-        for f in (L.attn_paged_decode_workspace, L.attn_paged_select_workspace):
+        L.attn_paged_assign_workspace.argtypes = [P]
+        for f in (L.attn_paged_decode_workspace, L.attn_paged_decode_window_workspace, L.attn_paged_select_workspace,
+                  L.attn_paged_assign_workspace):
             f.restype = ctypes.c_longlong
         L.attn_sync_status.argtypes = [P]
         L.attn_sync_status.restype = I
@@ -401,7 +416,7 @@ _native_module = None
 
 
 def _native():
-    """The compiled marshalling of the paged calls (raises if it has not been built)."""
+    """The compiled marshalling of the paged and windowed calls (raises if it has not been built)."""
     global _native_module
     if _native_module is None:
         lib()  # says how to build where that has not been done
@@ -411,12 +426,12 @@ def _native():
 
 
 class _OnStream:
-    """A stream of the cache's device as the current one: what a call allocates
-    then belongs to the stream that it runs on."""
+    """A stream of the cache's (or q's) device as the current one: what a call
+    allocates then belongs to the stream that it runs on."""
 
-    def __init__(self, kv, stream):
-        if stream.device != kv.device:
-            raise ValueError("the stream must be of the cache's device")
+    def __init__(self, on, stream):
+        if stream.device != on.device:
+            raise ValueError("the stream must be of the tensors' device")
         self.stream = torch.cuda.stream(stream)
 
     def __enter__(self):
@@ -479,6 +494,59 @@ def attn_paged_select(kv, q, n_select, keep_first=1, keep_last=1, pages=None, st
     if isinstance(kv, PagedKV) and kv.k_min is None:
         raise ValueError("the cache has no key summaries (k_min, k_max)")
     return _paged_call("select", kv, stream, q, n_select, keep_first, keep_last, pages)
+
+
+def attn_paged_decode_window(kv, q, window, sinks=0, scale=None, o=None, lse=None, stream=None):
+    """attn_paged_decode for a model with a sliding window: each sequence's new
+    token sees its last ``window`` tokens (itself among them) and the first
+    ``sinks`` ones.  Pages of other tokens are neither looked up nor read."""
+    return _paged_call("decode_window", kv, stream, q, window, sinks, scale, o, lse)
+
+
+def attn_paged_assign(kv, n_new, free_pages, free_state, lens=None, free_out=None, token_start=None, slots=None,
+                      rows=None, window=0, sinks=0, stream=None):
+    """Bookkeeping of a step on the device: writes kv.seq_lens and the new
+    entries of kv.block_table for n_new [B] int32 new tokens of each sequence (-1:
+    the sequence is over), and returns token_start [B + 1] for attn_paged_append.
+
+    free_pages (int32) is a ring of free page numbers, free_state [2] int32 the
+    position of its first and their number; free_out gets the new state and lens
+    [B] is the tokens before the step (None: both in place).  slots (int64) gets
+    each new row's slot in the cache, page * page_size + place, or -1 behind the
+    last.  rows is the most new tokens there may be (None: slots' size, or one
+    per sequence).  With a window (and sinks) a sequence keeps the pages that
+    they need and writes them again in turns.  A step that cannot be done whole is
+    not done at all, and sync_status() says so."""
+    return _paged_call("assign", kv, stream, n_new, free_pages, free_state, lens, free_out, token_start, slots, rows, window,
+                       sinks)
+
+
+def _window_call(name, q, stream, *args):
+    f = getattr(_native_module or _native(), name)
+    if stream is None or not isinstance(q, torch.Tensor):
+        r = f(q, *args)
+    else:
+        with _OnStream(q, stream):
+            r = f(q, *args)
+    if type(r) is int:
+        raise AttnError("attn_" + name, r)
+    return r
+
+
+def attn_fwd_window(q, k, v, window, sinks=0, scale=None, o=None, lse=None, stream=None):
+    """Causal attention with a sliding window: q [B, q_heads, Nq, d] are the last
+    Nq of the Nk positions of k, v [B, kv_heads, Nk, d]; the query at position p
+    sees the keys p - window + 1 .. p and the first ``sinks`` ones up to p.  Query heads
+    in groups of q_heads / kv_heads share a key/value head.  bf16 or fp16, any
+    strides whose channels are contiguous and whose rows do not overlap.
+    Returns (o, lse); o is dense, token-major where q is."""
+    return _window_call("fwd_window", q, stream, k, v, window, sinks, scale, o, lse)
+
+
+def attn_bwd_window(q, k, v, o, do, lse, window, sinks=0, scale=None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients of attn_fwd_window's output for the same window, sinks and scale,
+    dk and dv summed over the query heads of a key/value head.  Returns (dq, dk, dv)."""
+    return _window_call("bwd_window", q, stream, k, v, o, do, lse, window, sinks, scale, dq, dk, dv)
 
 
 def _check_block_mask(block_mask, H, N):
@@ -640,15 +708,53 @@ class _Attention(torch.autograd.Function):
         return dq, dk, dv, None, None, None, None, None, None
 
 
-def attention(q, k, v, scale=None, causal=False, dropout_p=0.0, seed=0, offset=0, block_mask=None):
+def _laid_out(t):
+    """t, or a contiguous copy where the windowed calls do not take its strides."""
+    if t.stride(-1) != 1 or t.data_ptr() % 16:
+        return t.contiguous()
+    span = t.shape[-1]
+    for stride, n in sorted((s, n) for s, n in zip(t.stride()[:-1], t.shape[:-1]) if n > 1):
+        if stride % 8 or stride < span:
+            return t.contiguous()
+        span += stride * (n - 1)
+    return t
+
+
+class _WindowAttention(torch.autograd.Function):
+    """Differentiable windowed attention: attn_fwd_window, attn_bwd_window."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, scale, window, sinks):
+        q, k, v = _laid_out(q), _laid_out(k), _laid_out(v)
+        o, lse = attn_fwd_window(q, k, v, window, sinks, scale)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.args = (window, sinks, scale)
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse = ctx.saved_tensors
+        return attn_bwd_window(q, k, v, o, _laid_out(do), lse, *ctx.args) + (None, None, None)
+
+
+def attention(q, k, v, scale=None, causal=False, dropout_p=0.0, seed=0, offset=0, block_mask=None, window=None, sinks=0):
     """O = softmax(scale q k^T [+ causal mask]) v as a differentiable op on
     [B, H, N, d] CUDA tensors (bf16 or fp16).  Gradients flow to q, k and v
     through the recomputation backward.  With dropout_p > 0 the keep
     decisions come from (seed, offset); use a new offset per step.  With a
     block_mask (uint8 [H or 1, ceil(N/128), ceil(N/128)] on the device) only
-    the enabled 128 x 128 tiles are computed, as in attn_fwd_blocksparse."""
+    the enabled 128 x 128 tiles are computed, as in attn_fwd_blocksparse.  With a
+    window (causal by itself, without dropout or block mask) a query sees the last
+    ``window`` keys and the first ``sinks``; k and v may have fewer heads and more
+    positions than q, as in attn_fwd_window."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
+    if window is not None:
+        if dropout_p or block_mask is not None:
+            raise ValueError("a window goes with neither dropout nor a block mask")
+        return _WindowAttention.apply(q, k, v, float(scale), window, sinks)
+    if sinks:
+        raise ValueError("sinks go with a window")
     return _Attention.apply(q, k, v, float(scale), bool(causal), float(dropout_p), int(seed), int(offset),
                             block_mask)
 

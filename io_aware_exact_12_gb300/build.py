@@ -3,7 +3,7 @@
 Each translation unit under csrc/ is compiled for sm_103a only
 (-gencode arch=compute_103a,code=sm_103a) in parallel, then linked as a
 shared library against the shared CUDA runtime.  Beside it, compiled at the
-same time by the C++ compiler, _paged.so: the Python binding of the paged calls
+same time by the C++ compiler, _paged.so: the Python binding of the paged and windowed calls
 (CPython and torch's C++ headers).  No cmake; a few seconds per file.  Run ``python -m io_aware_exact_12_gb300.build`` (or call ``build()``).
 """
 from __future__ import annotations
@@ -22,8 +22,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libattn.so")
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_noalloc.cu", "attn_diag.cu", "attn_decode.cu", "attn_fwd_fp8.cu",
-           "attn_paged_append.cu", "attn_paged_decode.cu", "attn_paged_select.cu"]
-HEADERS = ["attn_internal.h", "block_order.h", "tc_sm103.cuh", "dropout.cuh", "attn_paged.h"]
+           "attn_paged_append.cu", "attn_paged_decode.cu", "attn_paged_select.cu", "attn_paged_assign.cu",
+           "attn_window_fwd.cu", "attn_window_bwd.cu"]
+HEADERS = ["attn_internal.h", "block_order.h", "tc_sm103.cuh", "dropout.cuh", "attn_paged.h", "attn_window.h"]
 BINDING = "paged_binding.cpp"
 BINDING_PATH = os.path.join(PKG, "_paged.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

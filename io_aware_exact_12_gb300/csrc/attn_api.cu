@@ -12,6 +12,7 @@
 #include "attn.h"
 #include "attn_internal.h"
 #include "attn_paged.h"
+#include "attn_window.h"
 
 // Sticky device-side status (one copy per device that loads the library).
 __device__ int g_attn_status;
@@ -657,8 +658,18 @@ int paged_append_entry(const attn_paged_kv_t* c, const attn_rows_t* k, const att
   return rc;
 }
 
+// Workspace of a decode over n_pages pages, or (window > 0) over a window.
+int64_t decode_workspace(const attn_paged_kv_t* c, int q_heads, int n_pages, int window, int sinks) {
+  int64_t keys = static_cast<int64_t>(n_pages) * c->page_size;
+  if (window) keys = paged_window_keys(window, sinks, keys);
+  return paged_decode_workspace(c->B, q_heads, c->kv_heads, c->head_dim, keys);
+}
+
+bool window_ok(int window, int sinks) { return window >= 1 && sinks >= 0; }
+
 int paged_decode_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_heads, void* o, float* lse,
-                       const int* pages, int n_pages, float scale, int x_type, void* workspace, void* stream) {
+                       const int* pages, int n_pages, int window, int sinks, float scale, int x_type, void* workspace,
+                       void* stream) {
   PagedDecodeArgs a = {};
   Span ks, vs, qn;
   int rc = paged_kv(c, x_type, &a.kv, &ks, &vs);
@@ -672,8 +683,7 @@ int paged_decode_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_hea
   if ((rc = query_heads_ok(q_heads, c->B, c->kv_heads))) return rc;
   if (pages && !listed_pages_ok(n_pages, c->page_size)) return kStatusUnsupported;
   if ((rc = paged_rows(q, c->B, q_heads, c->head_dim, false, &a.q, &qn))) return rc;
-  const int64_t need = paged_decode_workspace(c->B, q_heads, c->kv_heads, c->head_dim, c->page_size,
-                                              pages ? n_pages : c->max_pages);
+  const int64_t need = decode_workspace(c, q_heads, pages ? n_pages : c->max_pages, window, sinks);
   if (need && (!workspace || !aligned16(workspace))) return kStatusInvalid;
   const size_t obytes = static_cast<size_t>(c->B) * q_heads * c->head_dim * 2, lbytes = static_cast<size_t>(c->B) * q_heads * 4;
   const Span list = {pages, pages ? static_cast<size_t>(c->B) * c->kv_heads * n_pages * 4 : 0};
@@ -689,6 +699,8 @@ int paged_decode_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_hea
   a.lse = lse;
   a.pages = pages;
   a.n_pages = n_pages;
+  a.window = window;
+  a.sinks = sinks;
   a.sl2 = sl2;
   a.x_type = x_type;
   a.stream = static_cast<cudaStream_t>(stream);
@@ -696,6 +708,57 @@ int paged_decode_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_hea
   if ((rc = paged_device(&a.kv, &a.status))) return rc;
   int launches = 0;
   if ((rc = launch_paged_decode(a, &launches)) == kStatusOk) t_last_launches = launches;
+  return rc;
+}
+
+int paged_assign_entry(const attn_paged_kv_t* c, const int* n_new, const int* lens, int* free_pages, int free_cap,
+                       int* free_state, int* free_out, int* token_start, long long* slots, int rows, int window, int sinks,
+                       void* workspace, void* stream) {
+  PagedAssignArgs a = {};
+  Span ks, vs;
+  int rc = paged_kv(c, c && c->type == kTypeF16 ? kTypeF16 : kTypeBf16, &a.kv, &ks, &vs);
+  if (rc) return rc;
+  if (!n_new || !free_pages || !free_state || !token_start || !workspace || free_cap < 1 || rows < 0 || window < 0 || sinks < 0)
+    return kStatusInvalid;
+  if (window > (1 << 30) || sinks > (1 << 30) || rows > (1 << 30)) return kStatusUnsupported;
+  for (const void* p : {static_cast<const void*>(n_new), static_cast<const void*>(lens), static_cast<const void*>(free_pages),
+                        static_cast<const void*>(free_state), static_cast<const void*>(free_out), static_cast<const void*>(token_start)})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return kStatusInvalid;
+  if ((reinterpret_cast<uintptr_t>(slots) & 7u) || !aligned16(workspace)) return kStatusInvalid;
+  const size_t each = static_cast<size_t>(c->B) * 4;
+  const bool lens_apart = lens && lens != c->seq_lens, free_apart = free_out && free_out != free_state;
+  const Span ins[5] = {{n_new, each}, {lens_apart ? lens : nullptr, each}, {free_apart ? free_state : nullptr, 8}, ks, vs};
+  const Span outs[7] = {{c->block_table, (static_cast<size_t>(c->B - 1) * c->table_stride + c->max_pages) * 4},
+                        {c->seq_lens, each},
+                        {free_pages, static_cast<size_t>(free_cap) * 4},
+                        {free_apart ? free_out : free_state, 8},
+                        {token_start, each + 4},
+                        {rows ? slots : nullptr, static_cast<size_t>(rows) * 8},
+                        {workspace, static_cast<size_t>(paged_assign_workspace(c->B))}};
+  for (int i = 0; i < 7; ++i) {
+    if (any_overlap(outs[i], {ins[0], ins[1], ins[2], ins[3], ins[4]})) return kStatusInvalid;
+    for (int j = i + 1; j < 7; ++j)
+      if (any_overlap(outs[i], {outs[j]})) return kStatusInvalid;
+  }
+  a.table = const_cast<int*>(c->block_table);
+  a.lens_out = const_cast<int*>(c->seq_lens);
+  a.lens = lens ? lens : c->seq_lens;
+  a.n_new = n_new;
+  a.free_pages = free_pages;
+  a.free_cap = free_cap;
+  a.free_state = free_state;
+  a.free_out = free_out ? free_out : free_state;
+  a.token_start = token_start;
+  a.slots = reinterpret_cast<int64_t*>(slots);
+  a.rows = rows;
+  a.first = window ? (sinks + c->page_size - 1) / c->page_size : 0;
+  a.turns = window ? (window - 1 + c->page_size - 1) / c->page_size + 1 : 0;
+  a.stream = static_cast<cudaStream_t>(stream);
+  a.ws = static_cast<uint8_t*>(workspace);
+  int* status = nullptr;
+  if ((rc = paged_device(&a.kv, &status))) return rc;
+  int launches = 0;
+  if ((rc = launch_paged_assign(a, &launches)) == kStatusOk) t_last_launches = launches;
   return rc;
 }
 
@@ -736,10 +799,108 @@ int paged_select_entry(const attn_paged_kv_t* c, const attn_rows_t* q, int q_hea
   return rc;
 }
 
+// ------------------------------------------------------------ sliding window
+
+struct Strided {  // a [B, heads, N, d] tensor, checked: dims in the order batch, head, row
+  const attn_bhnd_t* t;
+  Dim dims[3];
+  Span span;
+  int64_t inner;  // bytes from a position's first head to its last one's end
+};
+
+int strided(const attn_bhnd_t* t, int B, int heads, int N, int d, Strided* s, Bhnd* out) {
+  if (!t || !t->data || !aligned16(t->data)) return kStatusInvalid;
+  for (long long x : {t->batch_stride, t->head_stride, t->row_stride})
+    if (x < 0 || x >= (1ll << 38)) return kStatusInvalid;
+  const int64_t row = static_cast<int64_t>(d) * 2;
+  *s = {t, {{B, t->batch_stride * 2}, {heads, t->head_stride * 2}, {N, t->row_stride * 2}}, {}, 0};
+  if (!strides_ok(s->dims, 3, row, true)) return kStatusInvalid;
+  s->span = {t->data, span_of(s->dims, 3, row)};
+  s->inner = (heads - 1) * s->dims[1].stride + row;
+  *out = {static_cast<uint8_t*>(t->data), s->dims[0].stride, s->dims[1].stride, s->dims[2].stride};
+  return kStatusOk;
+}
+
+// Whether two tensors share no byte: their spans do not meet, or they are slices
+// of one buffer whose positions repeat at one distance, side by side in each.
+bool apart(const Strided& x, const Strided& y) {
+  if (!overlaps(x.span.p, x.span.n, y.span.p, y.span.n)) return true;
+  const Dim *a = x.dims, *b = y.dims;
+  if (a[2].n != b[2].n || a[0].n != b[0].n) return false;
+  const int64_t period = a[2].n > 1 ? a[2].stride : a[0].n > 1 ? a[0].stride : 0;
+  if (!period || (a[2].n > 1 && a[2].stride != b[2].stride)) return false;
+  if (a[0].n > 1 && (a[0].stride != b[0].stride || a[0].stride % period)) return false;
+  int64_t delta = (static_cast<const uint8_t*>(y.span.p) - static_cast<const uint8_t*>(x.span.p)) % period;
+  if (delta < 0) delta += period;
+  return delta >= x.inner && delta + y.inner <= period;
+}
+
+int window_sizes(int B, int Hq, int Hk, int Nq, int Nk, int d, int window, int sinks, float scale, int type) {
+  if (Hk < 1 || Nk < Nq || !window_ok(window, sinks)) return kStatusInvalid;
+  if (const int rc = validate_common(B, Hq, Nk, d, scale)) return rc;
+  if (Nq < 1 || Hq % Hk || !std::isfinite(scale * 1.4426950408889634f)) return kStatusInvalid;
+  return type == kTypeBf16 || type == kTypeF16 ? kStatusOk : kStatusInvalid;
+}
+
+int window_entry(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o, const attn_bhnd_t* dO,
+                 float* lse, const attn_bhnd_t* dq, const attn_bhnd_t* dk, const attn_bhnd_t* dv, int B, int Hq, int Hk, int Nq,
+                 int Nk, int d, int window, int sinks, float scale, int type, void* stream, bool backward) {
+  int rc = window_sizes(B, Hq, Hk, Nq, Nk, d, window, sinks, scale, type);
+  if (rc) return rc;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u)) return kStatusInvalid;
+  WindowArgs a = {};
+  Strided s[8];
+  struct {
+    const attn_bhnd_t* t;
+    Bhnd* to;
+    bool keys;
+  } const all[8] = {{q, &a.q, false}, {k, &a.k, true}, {v, &a.v, true}, {o, &a.o, false}, {dO, &a.dO, false}, {dq, &a.dq, false}, {dk, &a.dk, true}, {dv, &a.dv, true}};
+  const int n = backward ? 8 : 4, first_out = backward ? 5 : 3;
+  for (int i = 0; i < n; ++i)
+    if ((rc = strided(all[i].t, B, all[i].keys ? Hk : Hq, all[i].keys ? Nk : Nq, d, &s[i], all[i].to))) return rc;
+  const Span ls = {lse, static_cast<size_t>(B) * Hq * Nq * 4};
+  for (int i = 0; i < n; ++i) {
+    if ((i >= first_out || !backward) && any_overlap(s[i].span, {ls})) return kStatusInvalid;
+    for (int j = 0; j < i && i >= first_out; ++j)
+      if (!apart(s[i], s[j])) return kStatusInvalid;
+  }
+  int dev = 0;
+  if ((rc = current_device(&dev))) return rc;
+  if (!(a.status = status_ptr(dev))) return kStatusCuda;
+  a.lse = lse;
+  a.B = B, a.Hq = Hq, a.Hk = Hk, a.Nq = Nq, a.Nk = Nk, a.d = d;
+  a.window = std::min(window, Nk);
+  a.sinks = std::min(sinks, Nk);
+  a.scale = scale;
+  a.sl2 = std::fabs(scale) * 1.4426950408889634f;
+  a.negate = scale < 0.f ? 1 : 0;
+  a.bf16 = type == kTypeBf16;
+  a.stream = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  rc = backward ? launch_window_bwd(a, &launches) : launch_window_fwd(a, &launches);
+  if (rc == kStatusOk) t_last_launches = launches;
+  return rc;
+}
+
 }  // namespace
 }  // namespace attn
 
 extern "C" {
+
+int attn_fwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o, float* lse,
+                    int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks, float scale, int type,
+                    void* stream) {
+  return attn::window_entry(q, k, v, o, nullptr, lse, nullptr, nullptr, nullptr, B, q_heads, kv_heads, Nq, Nk, d, window,
+                            sinks, scale, type, stream, false);
+}
+
+int attn_bwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o,
+                    const attn_bhnd_t* dO, const float* lse, const attn_bhnd_t* dq, const attn_bhnd_t* dk,
+                    const attn_bhnd_t* dv, int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks,
+                    float scale, int type, void* stream) {
+  return attn::window_entry(q, k, v, o, dO, const_cast<float*>(lse), dq, dk, dv, B, q_heads, kv_heads, Nq, Nk, d, window,
+                            sinks, scale, type, stream, true);
+}
 
 int attn_paged_append(const attn_paged_kv_t* kv, const attn_rows_t* k, const attn_rows_t* v, const attn_rows_t* q,
                       const attn_rows_t* q_out, int q_heads, int rows, const int* token_start, const float* cos,
@@ -750,7 +911,21 @@ int attn_paged_append(const attn_paged_kv_t* kv, const attn_rows_t* k, const att
 
 int attn_paged_decode(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, void* o, float* lse,
                       const int* pages, int n_pages, float scale, int x_type, void* workspace, void* stream) {
-  return attn::paged_decode_entry(kv, q, q_heads, o, lse, pages, n_pages, scale, x_type, workspace, stream);
+  return attn::paged_decode_entry(kv, q, q_heads, o, lse, pages, n_pages, 0, 0, scale, x_type, workspace, stream);
+}
+
+int attn_paged_decode_window(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, void* o, float* lse,
+                             int window, int sinks, float scale, int x_type, void* workspace, void* stream) {
+  if (!attn::window_ok(window, sinks)) return ATTN_ERR_INVALID_ARG;
+  if (window > (1 << 30) || sinks > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  return attn::paged_decode_entry(kv, q, q_heads, o, lse, nullptr, 0, window, sinks, scale, x_type, workspace, stream);
+}
+
+int attn_paged_assign(const attn_paged_kv_t* kv, const int* n_new, const int* lens, int* free_pages, int free_cap,
+                      int* free_state, int* free_out, int* token_start, long long* slots, int rows, int window, int sinks,
+                      void* workspace, void* stream) {
+  return attn::paged_assign_entry(kv, n_new, lens, free_pages, free_cap, free_state, free_out, token_start, slots, rows,
+                                  window, sinks, workspace, stream);
 }
 
 int attn_paged_select(const attn_paged_kv_t* kv, const attn_rows_t* q, int q_heads, int* pages, int n_select,
@@ -762,8 +937,18 @@ long long attn_paged_decode_workspace(const attn_paged_kv_t* kv, int q_heads, in
   if (!kv || attn::paged_sizes(kv) || attn::query_heads_ok(q_heads, kv->B, kv->kv_heads) ||
       (n_pages >= 1 && !attn::listed_pages_ok(n_pages, kv->page_size)))
     return 0;
-  return attn::paged_decode_workspace(kv->B, q_heads, kv->kv_heads, kv->head_dim, kv->page_size,
-                                      n_pages < 1 ? kv->max_pages : n_pages);
+  return attn::decode_workspace(kv, q_heads, n_pages < 1 ? kv->max_pages : n_pages, 0, 0);
+}
+
+long long attn_paged_decode_window_workspace(const attn_paged_kv_t* kv, int q_heads, int window, int sinks) {
+  if (!kv || attn::paged_sizes(kv) || attn::query_heads_ok(q_heads, kv->B, kv->kv_heads) || !attn::window_ok(window, sinks) ||
+      window > (1 << 30) || sinks > (1 << 30))
+    return 0;
+  return attn::decode_workspace(kv, q_heads, kv->max_pages, window, sinks);
+}
+
+long long attn_paged_assign_workspace(const attn_paged_kv_t* kv) {
+  return !kv || attn::paged_sizes(kv) ? 0 : attn::paged_assign_workspace(kv->B);
 }
 
 long long attn_paged_select_workspace(const attn_paged_kv_t* kv) {

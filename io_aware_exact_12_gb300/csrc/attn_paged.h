@@ -65,6 +65,7 @@ struct PagedDecodeArgs {
   float* lse;  // [B][Hq]
   const int* pages;  // [B][H][n_pages] page indices of the sequence, or null: all pages
   int n_pages;
+  int window = 0, sinks = 0;  // window > 0: the last `window` tokens and the first `sinks` ones (pages is null)
   float sl2;  // scale * k_scale * log2(e), signed
   int x_type;
   cudaStream_t stream;
@@ -83,14 +84,35 @@ struct PagedSelectArgs {
   uint8_t* ws;
 };
 
+struct PagedAssignArgs {
+  PagedKv kv;
+  int* table;       // kv.table and kv.lens, which this call writes
+  int* lens_out;
+  const int* lens;  // tokens before the step; may be lens_out
+  const int* n_new;
+  int* free_pages;  // ring of free_cap page numbers
+  int free_cap;
+  const int* free_state;  // first free page's position, number of free pages
+  int* free_out;          // may be free_state
+  int* token_start;       // [B + 1]
+  int64_t* slots;         // [rows], or null
+  int rows;
+  int first, turns;  // pages of sinks, pages in turns behind them (0: no window)
+  cudaStream_t stream;
+  uint8_t* ws;
+};
+
 // Each returns a status code; the launch counts go to *launches.
 int launch_paged_append(const PagedAppendArgs& a, int* launches);
 int launch_paged_decode(const PagedDecodeArgs& a, int* launches);
 int launch_paged_select(const PagedSelectArgs& a, int* launches);
+int launch_paged_assign(const PagedAssignArgs& a, int* launches);
 
 // Scratch bytes; they depend on sizes alone.
-int64_t paged_decode_workspace(int B, int Hq, int H, int d, int page, int n_pages);
+int64_t paged_decode_workspace(int B, int Hq, int H, int d, int64_t keys);
+int64_t paged_window_keys(int window, int sinks, int64_t most);  // keys of a windowed call, for the workspace
 int64_t paged_select_workspace(int B, int H, int max_pages);
+int64_t paged_assign_workspace(int B);
 
 #ifdef __CUDACC__
 

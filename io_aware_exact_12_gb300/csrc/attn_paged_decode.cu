@@ -182,9 +182,28 @@ __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kPdWarps) : "memory");
 }
 
+// The tiles of a windowed sequence (WIN): those with sinks before the window, then
+// those from the window's first token on.  Tile t of them is key tile
+// t < sinks ? t : t + skip.
 template <int TK>
+struct WindowTiles {
+  int start, sinks, skip, n;  // the window's first token, tiles of sinks, tiles left out behind them, tiles in all
+  __device__ __forceinline__ WindowTiles(const PagedDecodeArgs& a, int len) {
+    start = max(0, len - a.window);
+    const int first = start / TK;  // a sink in the window's first tile is seen there
+    sinks = min(first, (min(a.sinks, start) + TK - 1) / TK);
+    skip = first - sinks;
+    n = (len + TK - 1) / TK - skip;
+  }
+  __device__ __forceinline__ int key_tile(int t) const { return t < sinks ? t : t + skip; }
+};
+
+__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; }
+
+template <int TK, bool WIN>
 __device__ __forceinline__ int tiles_of(const PagedDecodeArgs& a, int len) {
   if (len <= 0) return 0;
+  if constexpr (WIN) return WindowTiles<TK>(a, len).n;
   // A list without repetitions has no more entries than the sequence has pages.
   return ((a.pages ? min(a.n_pages, (len + a.kv.page - 1) / a.kv.page) * a.kv.page : len) + TK - 1) / TK;
 }
@@ -199,7 +218,7 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 // worth, laid before its tiles, so that a share of many short items gets fewer.
 // Where every item is short and there are many, items are not cut ("solo"): a
 // CTA has those that begin in its share, and a warp takes each for itself.
-template <int TK>
+template <int TK, bool WIN>
 __device__ __forceinline__ void find_share(const PagedDecodeArgs& a, int HR, Sched& s) {
   const int tid = threadIdx.x, lane = tid & 31, B = a.kv.B;
   const int per = (B + kPdThreads - 1) / kPdThreads;
@@ -207,7 +226,7 @@ __device__ __forceinline__ void find_share(const PagedDecodeArgs& a, int HR, Sch
   long long mine = 0;
   int most = 0, alive = 0;  // longest item, sequences with tokens
   for (int b = b0; b < b1; ++b) {
-    const int t = tiles_of<TK>(a, checked_len(a.kv, b));
+    const int t = tiles_of<TK, WIN>(a, checked_len(a.kv, b));
     mine += t, most = max(most, t), alive += t > 0;
   }
   mine *= HR;
@@ -255,7 +274,7 @@ __device__ __forceinline__ void find_share(const PagedDecodeArgs& a, int HR, Sch
       if (!(upto - mine <= w && w < upto)) continue;
       long long at = upto - mine, tiles = at - static_cast<long long>(before - alive) * HR * extra;
       for (int b = b0; b < b1; ++b) {
-        const int t = tiles_of<TK>(a, checked_len(a.kv, b));
+        const int t = tiles_of<TK, WIN>(a, checked_len(a.kv, b));
         if (t == 0) continue;
         if (w < at + static_cast<long long>(t + extra) * HR) {
           const int hr = static_cast<int>(divide(w - at, t + extra));
@@ -277,7 +296,7 @@ __device__ __forceinline__ void find_share(const PagedDecodeArgs& a, int HR, Sch
 struct Item {
   int b, hr, tiles, len;
 };
-template <int TK>
+template <int TK, bool WIN>
 __device__ __forceinline__ void next_item(const PagedDecodeArgs& a, int HR, Item& it) {
   if (++it.hr < HR) return;
   it.hr = 0;
@@ -287,7 +306,7 @@ __device__ __forceinline__ void next_item(const PagedDecodeArgs& a, int HR, Item
       return;
     }
     it.len = checked_len(a.kv, it.b);
-    it.tiles = tiles_of<TK>(a, it.len);
+    it.tiles = tiles_of<TK, WIN>(a, it.len);
   } while (it.tiles == 0);
 }
 
@@ -297,7 +316,7 @@ __device__ __forceinline__ void store_out4(uint8_t* p, const float (&o)[4]) {
       make_uint2(pack2<X == kTypeBf16>(o[0], o[1]), pack2<X == kTypeBf16>(o[2], o[3]));
 }
 
-template <int X, int C, int D, int NT>
+template <int X, int C, int D, int NT, bool WIN>
 __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     attn_paged_decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                              const PagedDecodeArgs a, int RT, int box_rows, int cluster, int by_item, Part* parts,
@@ -331,13 +350,13 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     if (threadIdx.x == 0) {
       const int item = blockIdx.x / cluster, rank = blockIdx.x % cluster;
       s.b = item / HR, s.hr = item % HR;
-      const long long t = tiles_of<TK>(a, checked_len(kv, s.b));
+      const long long t = tiles_of<TK, WIN>(a, checked_len(kv, s.b));
       s.bound_tile[0] = s.tile = static_cast<int>(t * rank / cluster), s.bound_tile[1] = t * (rank + 1) / cluster;
       s.w0 = 0, s.total = 1, s.n_act = 1, s.extra = 0, s.solo = 0, s.up[0] = s.up[1] = 0;
     }
     __syncthreads();
   } else {
-    find_share<TK>(a, HR, s);
+    find_share<TK, WIN>(a, HR, s);
   }
   const bool solo = s.solo;
   // Solo: from the first item that begins here to the end of the last one.
@@ -348,10 +367,10 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   volatile int* abort_flag = &s.abort_flag;
   Item it = {s.b, s.hr, 0, 0};  // sequence 0 where there is no tile
   it.len = checked_len(kv, it.b);
-  it.tiles = tiles_of<TK>(a, it.len);
+  it.tiles = tiles_of<TK, WIN>(a, it.len);
   int tile = s.tile;
   if (solo && tile) {
-    next_item<TK>(a, HR, it);
+    next_item<TK, WIN>(a, HR, it);
     tile = 0;
   }
 
@@ -370,10 +389,20 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       const bool live = i0 + lane / nb < n;
       while (live && mine.tiles > 0 && t >= mine.tiles) {
         t -= mine.tiles;
-        next_item<TK>(a, HR, mine);
+        next_item<TK, WIN>(a, HR, mine);
       }
       int id = -1, h = 0, row = 0, seen = 0;
-      if (live) {
+      uint64_t bits = 0;  // WIN: visible keys of the box
+      if (WIN && live) {
+        const WindowTiles<TK> wt(a, mine.len);
+        const int key = wt.key_tile(t) * TK + box * box_rows;
+        const int j = key / kv.page;
+        row = key - j * kv.page;
+        h = mine.hr / RT;
+        bits = low_bits(min(box_rows, mine.len - key)) & (~low_bits(wt.start - key) | low_bits(a.sinks - key));
+        // (a box without a visible key may lie in a page that the sequence no longer has)
+        if (bits && (id = checked_page(kv, mine.b, j)) < 0) bits = 0;
+      } else if (live) {
         const int key = t * TK + box * box_rows;
         const int e = key / kv.page;
         row = key - e * kv.page;
@@ -394,7 +423,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       // A box without a visible key is not loaded: its scores are masked and its
       // V rows zeroed, whatever the stage held before.
       int vis = id >= 0 ? 1 : 0;
-      uint64_t mask = (seen == 64 ? ~0ull : ((1ull << seen) - 1)) << (box * box_rows);
+      uint64_t mask = (WIN ? bits : seen == 64 ? ~0ull : ((1ull << seen) - 1)) << (box * box_rows);
       for (int x = 1; x < nb; x <<= 1) {
         mask |= __shfl_xor_sync(0xffffffffu, mask, x);
         vis += __shfl_xor_sync(0xffffffffu, vis, x);
@@ -433,7 +462,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       tile += batch;
       while (it.tiles > 0 && tile >= it.tiles && i0 + batch < n) {
         tile -= it.tiles;
-        next_item<TK>(a, HR, it);
+        next_item<TK, WIN>(a, HR, it);
       }
     }
     // No copy may be in flight when the CTA ends, also where the consumers gave
@@ -456,7 +485,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
   // ------------------------------------------------------------ consumer warps
   // Sequences without tokens: o = 0, lse = -inf; while the first loads travel.
   for (int b = c; b < kv.B && !cluster; b += gridDim.x) {
-    if (tiles_of<TK>(a, checked_len(kv, b))) continue;
+    if (tiles_of<TK, WIN>(a, checked_len(kv, b))) continue;
     for (int i = threadIdx.x; i < a.Hq * D / 8; i += 32 * kPdWarps)
       reinterpret_cast<uint4*>(a.o + static_cast<int64_t>(b) * a.Hq * D * 2)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = threadIdx.x; i < a.Hq; i += 32 * kPdWarps) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
@@ -488,7 +517,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       tiles = end - cur;
       if (item % kPdWarps != warp) {
         cur = end;
-        if (cur < n) next_item<TK>(a, HR, it);
+        if (cur < n) next_item<TK, WIN>(a, HR, it);
         continue;
       }
     }
@@ -792,7 +821,7 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
     w0 += s.extra + it.tiles;
     cur = end;
     tile = 0;
-    if (cur < n) next_item<TK>(a, HR, it);
+    if (cur < n) next_item<TK, WIN>(a, HR, it);
   }
   if (cluster) {
     // Join of the cluster's partial results, in the order of the CTAs.
@@ -961,6 +990,11 @@ constexpr int kMaxCtas = kMergeParts;  // of the decode kernel
 // CTAs that find a tile for each of their warps, if every sequence fills its table.
 int64_t most_ctas(int64_t items, int64_t keys, int tk) { return items * (((keys + tk - 1) / tk + kPdWarps - 1) / kPdWarps); }
 
+// Keys in the tiles of `tk` that a window and its sinks can lie in.
+int64_t window_keys(int64_t window, int64_t sinks, int tk) {
+  return ((sinks + tk - 1) / tk + (window + tk - 2) / tk + 1) * tk;
+}
+
 int row_tiles(int Hq, int H) { return (Hq / H + kPdRows - 1) / kPdRows; }
 
 // CTAs of a cluster for short items, or 0: the join through shared memory saves
@@ -997,13 +1031,13 @@ cudaError_t launch_clusters(Kernel kern, int ctas, int cluster, size_t smem, cud
   return cudaLaunchKernelEx(&cfg, kern, mk, mv, a, RT, box, size, 0, static_cast<Part*>(nullptr), static_cast<float*>(nullptr));
 }
 
-template <int X, int C, int D, int NT>
+template <int X, int C, int D, int NT, bool WIN>
 int launch_t(const PagedDecodeArgs& a, int* launches) {
   using F = PdCfg<C, D, NT>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kStatusCuda;
-  auto kern = attn_paged_decode_kernel<X, C, D, NT>;
+  auto kern = attn_paged_decode_kernel<X, C, D, NT, WIN>;
   if (!((ready.load() >> dev) & 1)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM) != cudaSuccess) return kStatusCuda;
     ready.fetch_or(1ull << dev);
@@ -1019,7 +1053,8 @@ int launch_t(const PagedDecodeArgs& a, int* launches) {
     return kStatusCuda;
   const int sms = device_sm_count();
   if (sms < 1) return kStatusCuda;
-  const int64_t keys = static_cast<int64_t>(a.pages ? a.n_pages : a.kv.max_pages) * a.kv.page;
+  int64_t keys = static_cast<int64_t>(a.pages ? a.n_pages : a.kv.max_pages) * a.kv.page;
+  if (WIN) keys = std::min(keys, window_keys(a.window, a.sinks, F::TK));
   const int64_t items = static_cast<int64_t>(a.kv.B) * a.kv.H * RT;
   const int cluster = cluster_size(items, (keys + F::TK - 1) / F::TK, sms);
   if (cluster) {
@@ -1051,31 +1086,41 @@ int launch_t(const PagedDecodeArgs& a, int* launches) {
              : kStatusCuda;
 }
 
-template <int X, int C>
+template <int X, int C, bool WIN>
 int launch_d(const PagedDecodeArgs& a, int* launches) {
   const bool wide = a.Hq / a.kv.H > 8;
   switch (a.kv.d) {
-    case 32: return wide ? launch_t<X, C, 32, 2>(a, launches) : launch_t<X, C, 32, 1>(a, launches);
-    case 64: return wide ? launch_t<X, C, 64, 2>(a, launches) : launch_t<X, C, 64, 1>(a, launches);
-    default: return wide ? launch_t<X, C, 128, 2>(a, launches) : launch_t<X, C, 128, 1>(a, launches);
+    case 32: return wide ? launch_t<X, C, 32, 2, WIN>(a, launches) : launch_t<X, C, 32, 1, WIN>(a, launches);
+    case 64: return wide ? launch_t<X, C, 64, 2, WIN>(a, launches) : launch_t<X, C, 64, 1, WIN>(a, launches);
+    default: return wide ? launch_t<X, C, 128, 2, WIN>(a, launches) : launch_t<X, C, 128, 1, WIN>(a, launches);
   }
+}
+
+template <int X, int C>
+int launch_w(const PagedDecodeArgs& a, int* launches) {
+  return a.window ? launch_d<X, C, true>(a, launches) : launch_d<X, C, false>(a, launches);
 }
 
 }  // namespace
 
-int64_t paged_decode_workspace(int B, int Hq, int H, int d, int page, int n_pages) {
+int64_t paged_decode_workspace(int B, int Hq, int H, int d, int64_t keys) {
   // Two partial results for each CTA, as many as the largest GPU of the family
   // could hold; a bound by the tiles keeps it small for small problems.
   const int64_t items = static_cast<int64_t>(B) * H * row_tiles(Hq, H);
-  const int64_t ctas = std::min<int64_t>(kMaxCtas, most_ctas(items, static_cast<int64_t>(n_pages) * page, 32));
+  const int64_t ctas = std::min<int64_t>(kMaxCtas, most_ctas(items, keys, 32));
   return kMaxCtas * static_cast<int64_t>(sizeof(Part)) + ctas * 2 * part_floats(d, kPdRows) * 4;
+}
+
+int64_t paged_window_keys(int window, int sinks, int64_t most) {
+  // (with tiles of 64 at least as many as with tiles of 32)
+  return std::min(most, window_keys(window, sinks, 64));
 }
 
 int launch_paged_decode(const PagedDecodeArgs& a, int* launches) {
   *launches = 2;
   if (a.x_type == kTypeBf16)
-    return a.kv.type == kTypeE4m3 ? launch_d<kTypeBf16, kTypeE4m3>(a, launches) : launch_d<kTypeBf16, kTypeBf16>(a, launches);
-  return a.kv.type == kTypeE4m3 ? launch_d<kTypeF16, kTypeE4m3>(a, launches) : launch_d<kTypeF16, kTypeF16>(a, launches);
+    return a.kv.type == kTypeE4m3 ? launch_w<kTypeBf16, kTypeE4m3>(a, launches) : launch_w<kTypeBf16, kTypeBf16>(a, launches);
+  return a.kv.type == kTypeE4m3 ? launch_w<kTypeF16, kTypeE4m3>(a, launches) : launch_w<kTypeF16, kTypeF16>(a, launches);
 }
 
 }  // namespace attn

@@ -1,0 +1,38 @@
+// attn_window.h -- argument bundle of the sliding-window kernels
+// (attn_window_fwd.cu, attn_window_bwd.cu).  Not part of the ABI.
+//
+// Query i of Nq stands at position p = i + Nk - Nq; key j is visible to it iff
+// j <= p and (j > p - window or j < sinks).  Query head h reads key/value head
+// h / (Hq / Hk).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn_internal.h"
+
+namespace attn {
+
+struct Bhnd {  // [B][heads][N][d] with contiguous channels, strides in bytes
+  uint8_t* p;
+  int64_t b, h, n;
+};
+
+struct WindowArgs {
+  Bhnd q, k, v, o;
+  Bhnd dO, dq, dk, dv;  // backward only
+  float* lse;           // [B][Hq][Nq]; the backward reads it
+  int B, Hq, Hk, Nq, Nk, d;
+  int window, sinks;    // at most Nk each
+  float sl2;            // |scale| * log2(e)
+  float scale;
+  int negate;           // scale < 0
+  bool bf16;
+  cudaStream_t stream;
+  int* status;
+};
+
+int launch_window_fwd(const WindowArgs& a, int* launches);
+int launch_window_bwd(const WindowArgs& a, int* launches);
+
+}  // namespace attn
