@@ -32,6 +32,10 @@ struct WindowArgs {
   int* status;
 };
 
+// 4-D tiled map of a [B][heads][N][d] tensor: dims (d, N, heads, B), box
+// (box_inner, 128, 1, 1), swizzled over the box's rows, zero fill.
+bool encode_strided_map(CUtensorMap* map, const Bhnd& t, int B, int heads, int N, int d, int box_inner, bool bf16);
+
 int launch_window_fwd(const WindowArgs& a, int* launches);
 int launch_window_bwd(const WindowArgs& a, int* launches);
 
