@@ -57,6 +57,13 @@ EncodeTiledFn encode_fn() {
 int current_device(int* dev) {
   if (cudaGetDevice(dev) != cudaSuccess) return kStatusCuda;
   if (*dev < 0 || *dev >= kMaxDevices) return kStatusUnsupported;
+  // A thread's first call may find no context current (autograd's own threads),
+  // and the encoding of tensor maps, a driver call, wants one.
+  thread_local uint64_t current = 0;
+  if (!((current >> *dev) & 1)) {
+    if (cudaSetDevice(*dev) != cudaSuccess) return kStatusCuda;
+    current |= uint64_t{1} << *dev;
+  }
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_arch_ok[*dev] == 0) {
     int major = 0, minor = 0;

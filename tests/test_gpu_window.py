@@ -389,6 +389,37 @@ def test_two_streams_at_once(pkg):
 
 
 @gpu
+def test_first_call_of_a_thread(pkg):
+    """A thread that has made no CUDA call yet has no current context."""
+    import threading
+    q, k, v, do = _inputs(1, 4, 2, 300, 300, 64, BF16, "tokens", 14)
+    want = _check(pkg, q, k, v, do, 100, 4)
+    outs = [torch.empty_like(x) for x in want]
+    dense = [do.contiguous() for _ in range(4)]
+    row = torch.empty_like(want[1])
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(call):
+        try:
+            call()
+        except Exception as e:
+            failed.append(e)
+
+    for call in (lambda: pkg.attn_fwd_window(q, k, v, 100, 4, o=outs[0], lse=outs[1]),
+                 lambda: pkg.attn_bwd_window(q, k, v, want[0], do, want[1], 100, 4, dq=outs[2], dk=outs[3], dv=outs[4]),
+                 lambda: pkg.attn_fwd(*dense[:3], o=dense[3], lse=row)):
+        t = threading.Thread(target=work, args=(call,))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    assert pkg.sync_status() == 0
+    for i in (0, 1, 3, 4):
+        assert torch.equal(outs[i], want[i])
+
+
+@gpu
 def test_the_binding_refuses(pkg):
     q, k, v, do = _inputs(1, 4, 2, 50, 60, 64, BF16, "tokens", 13)
     o, lse = pkg.attn_fwd_window(q, k, v, 10)
