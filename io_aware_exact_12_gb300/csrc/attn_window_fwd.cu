@@ -10,10 +10,12 @@
 //
 // The tensor cores bound it (4 d flops a pair against 4 d bytes a key for 128
 // rows).  GB300 mapping:
-//   * a CTA takes NQ tiles of 128 query rows: one, with two CTAs to an SM, or the
-//     same rows of two query heads that share a key/value head, which then share
-//     every tile that is loaded.  Their tile lists are the same, so neither walks
-//     tiles that only the other needs (two tiles of neighbouring rows would).
+//   * an item is 128 query rows of a head; two CTAs to an SM, so that one's softmax
+//     meets the other's matrix products.  Blocks take over the items of blocks that
+//     have not started (cluster launch control) and load the next item's first tiles
+//     while this one's output is written: at window 1024 an item is ten tiles, and
+//     starting a CTA, its first loads and its output took as long as three (8192
+//     queries, 32 / 8 heads of 128: 165 -> 152 us).
 //   * one warp loads (TMA, 4-D maps, so any strides of batch, head and row), one
 //     thread issues the tcgen05.mma, S = Q K^T from shared memory, O += P V with P
 //     from TMEM; a warpgroup to each query tile does its softmax, a thread to a row.
@@ -21,6 +23,9 @@
 //     grows by more than 2^8, and O is rescaled in TMEM then.  l is summed twice:
 //     in fp32 of the weights as they are, for LSE, and of the weights rounded to the
 //     input type that multiply V, to normalise O.
+#include <cfloat>
+#include <type_traits>
+
 #include "attn_internal.h"
 #include "attn_window.h"
 #include "tc_sm103.cuh"
@@ -29,6 +34,7 @@ namespace attn {
 namespace {
 
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kNarrow = 32;  // keys of a tile with a few sinks
 
 template <int D, int NQ>
 struct WfCfg {
@@ -44,7 +50,8 @@ struct WfCfg {
   static constexpr int OFF_V = OFF_K + NST * TILE;
   static constexpr int OFF_BAR = OFF_V + NST * TILE;
   static constexpr int B_Q = 0;
-  static constexpr int B_KFULL = 1;
+  static constexpr int B_QEMPTY = 1;
+  static constexpr int B_KFULL = 2;
   static constexpr int B_KEMPTY = B_KFULL + NST;
   static constexpr int B_VFULL = B_KEMPTY + NST;
   static constexpr int B_VEMPTY = B_VFULL + NST;
@@ -52,11 +59,17 @@ struct WfCfg {
   static constexpr int B_P = B_S + 2;         // P_q is in TMEM
   static constexpr int B_O = B_P + 2;         // P_q V is complete
   static constexpr int B_TAKEN = B_O + 2;     // S_q is in registers (P apart)
-  static constexpr int B_DONE = B_TAKEN + 2;
+  static constexpr int B_NEXT = B_TAKEN + 2;   // the next item is known
+  static constexpr int B_READ = B_NEXT + 2;    // and read by all
+  static constexpr int B_DONE = B_READ + 2;
   static constexpr int NBAR = B_DONE + 1;
-  static constexpr int OFF_SLOT = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_NEXT = (OFF_BAR + NBAR * 8 + 15) & ~15;  // two answers
+  static constexpr int OFF_SLOT = OFF_NEXT + 32;
   static constexpr int OFF_ABORT = OFF_SLOT + 4;
-  static constexpr int SMEM = OFF_ABORT + 4;
+  // Staging of the output at d = 128: half a row for each of a warp's 32.
+  static constexpr bool STAGE = D == 128;
+  static constexpr int OFF_STAGE = (OFF_ABORT + 4 + 15) & ~15;
+  static constexpr int SMEM = OFF_STAGE + (STAGE ? NQ * 4 * 32 * 128 : 0);
   static constexpr int THREADS = 128 * NQ + 128;
   static constexpr int W_LOAD = 4 * NQ, W_MMA = 4 * NQ + 1;  // warps
   static constexpr int CTAS = 3 - NQ;                        // per SM
@@ -86,9 +99,9 @@ __host__ __device__ constexpr uint32_t mn_step(int kk) {
   return static_cast<uint32_t>((kk * 16 * WfCfg<D, 1>::ROWB) >> 4);
 }
 
-// Byte offset of 16-byte unit u of a row of 256 bytes in the output's staging
+// Byte offset of 16-byte unit u of a row of 128 bytes in the output's staging
 // copy, swizzled so that rows by threads and units by threads meet no bank twice.
-__device__ __forceinline__ uint32_t staged(int row, int u) { return static_cast<uint32_t>(row * 256 + ((u ^ (row & 7)) << 4)); }
+__device__ __forceinline__ uint32_t staged(int row, int u) { return static_cast<uint32_t>(row * 128 + ((u ^ (row & 7)) << 4)); }
 
 // A wait for work that has been issued, also after an abort.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
@@ -97,29 +110,34 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
+// A block's item: 128 query rows of NQ heads, and the list of key tiles they see.
+struct WfItem {
+  int row0, b, h0, hk;  // first row, sequence, first query head, key/value head
+  int ns, skip, npos;   // tiles of sinks, tiles left out behind them, tiles in all
+  __device__ __forceinline__ WfItem(const WindowArgs& a, int item, int nrows, int nheads, int nq, int group) {
+    // Later rows, which under a wide window have more tiles, first.
+    int rank, hb;
+    grouped_rank_order(item, nrows, nheads, group, rank, hb);
+    row0 = (nrows - 1 - rank) * 128;
+    b = hb * nq / a.Hq, h0 = hb * nq - b * a.Hq, hk = h0 / (a.Hq / a.Hk);
+    const int off = a.Nk - a.Nq;
+    const int w0 = max(0, row0 + off - a.window + 1) >> 7;
+    ns = min(w0, (a.sinks + 127) >> 7);
+    skip = w0 - ns;
+    npos = ((min(row0 + 127, a.Nq - 1) + off) >> 7) - skip + 1;
+  }
+  __device__ __forceinline__ int key0(int p) const { return (p < ns ? p : p + skip) * 128; }
+  // The last tile of sinks may have few of them: then kNarrow of its keys are enough.
+  __device__ __forceinline__ bool narrow(const WindowArgs& a, int p) const { return p == ns - 1 && a.sinks - p * 128 <= kNarrow; }
+};
+
 template <int D, bool BF16, int NQ>
 __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
     attn_window_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                           const __grid_constant__ CUtensorMap mv, const WindowArgs a, int head_group, int overlap) {
+                           const __grid_constant__ CUtensorMap mv, const WindowArgs a, int nrows, int nheads, int group, int overlap) {
   using C = WfCfg<D, NQ>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (overlap) {  // launched overlapped (launch_serialized)
-    griddep_wait();
-    griddep_launch_dependents();
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Later rows, which under a wide window have more tiles, first.
-  int rank, hb;
-  grouped_rank_order(blockIdx.x + blockIdx.y * gridDim.x, gridDim.x, gridDim.y, head_group, rank, hb);
-  const int row0 = (gridDim.x - 1 - rank) * 128;
-  const int b = hb * NQ / a.Hq, h0 = hb * NQ - b * a.Hq, hk = h0 / (a.Hq / a.Hk);
-  const int off = a.Nk - a.Nq;
-  // Positions 0 .. npos - 1 of the CTA's list of key tiles.
-  const int w0 = max(0, row0 + off - a.window + 1) >> 7;
-  const int ns = min(w0, (a.sinks + 127) >> 7);
-  const int npos = ns + ((min(row0 + 127, a.Nq - 1) + off) >> 7) - w0 + 1;
-  auto key0 = [&](int p) { return (p < ns ? p : w0 + p - ns) * 128; };
-
   const uint32_t sbase = smem_addr(smem);
   if (sbase & 1023u) {  // the swizzle's atoms; never expected
     if (threadIdx.x == 0) atomicExch(a.status, kStatusDeviceCheck);
@@ -129,28 +147,13 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   const uint32_t sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
-  auto load = [&](uint32_t dst, const CUtensorMap* map, int full, int row, int head) {
-#pragma unroll
-    for (int c = 0; c < C::NCH; ++c) tma_load_4d(dst + c * C::CHUNK, map, bar(full), c * C::CH, row, head, b);
-  };
-  auto load_k = [&](int p) {
-    const int s = p % C::NST;
-    mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::TILE);
-    load(sK + s * C::TILE, &mk, C::B_KFULL + s, key0(p), hk);
-  };
-  auto load_v = [&](int p) {
-    const int s = p % C::NST;
-    mbar_arrive_expect_tx(bar(C::B_VFULL + s), C::TILE);
-    load(sV + s * C::TILE, &mv, C::B_VFULL + s, key0(p), hk);
-  };
-  // The first loads travel while TMEM is allocated.
-  const int pre = min(npos, C::NST);
   if (warp == C::W_LOAD && lane == 0) {
     mbar_init(bar(C::B_Q), 1);
+    mbar_init(bar(C::B_QEMPTY), NQ);  // a thread of each query tile
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(bar(C::B_KFULL + s), 1);
       mbar_init(bar(C::B_VFULL + s), 1);
-      mbar_init(bar(C::B_KEMPTY + s), NQ);  // a thread of each query tile
+      mbar_init(bar(C::B_KEMPTY + s), NQ);
       mbar_init(bar(C::B_VEMPTY + s), NQ);
     }
     for (int q = 0; q < 2; ++q) {
@@ -159,44 +162,80 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
       mbar_init(bar(C::B_O + q), 1);
       mbar_init(bar(C::B_TAKEN + q), 128);
     }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(C::B_NEXT + x), 1);
+      mbar_init(bar(C::B_READ + x), 4 * NQ + 1);  // the softmax warps and the issuer
+    }
     mbar_init(bar(C::B_DONE), 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&mq);
     prefetch_tensormap(&mk);
     prefetch_tensormap(&mv);
-    mbar_arrive_expect_tx(bar(C::B_Q), NQ * C::TILE);
-    for (int q = 0; q < NQ; ++q) load(sbase + q * C::TILE, &mq, C::B_Q, row0, h0 + q);
-    for (int p = 0; p < pre; ++p) {
-      load_k(p);
-      load_v(p);
-    }
   }
   if (warp == C::W_MMA) {
     tmem_alloc(smem_addr(slot), C::COLS);
     tmem_relinquish();
   }
+  if (overlap) {  // launched overlapped (launch_serialized): what is above reads no tensor
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *slot;
+  // Every role walks the same items and, within each, the same positions; `n`
+  // counts positions over all items and gives stages and phases.  The first item
+  // is the block's own; while it runs the loader asks for that of a block that has
+  // not started (items differ in length, so equal shares would not do), and so on.
+  const uint32_t next = sbase + C::OFF_NEXT;
+  // The item after the k-th, or -1; for all roles but the loader, a warp's lanes (or one) together.
+  auto next_item = [&](int k, bool& ok) {
+    ok = ok && mbar_wait(bar(C::B_NEXT + (k & 1)), (k >> 1) & 1, abort_flag, a.status);
+    return ok ? block_answer(next + (k & 1) * 16) : -1;
+  };
 
   if (warp >= C::W_LOAD) {
     regs_decrease<C::REGS_CTRL>();
     if (warp == C::W_LOAD && lane == 0) {
       // ------------------------------------------------------------ loads
-      int nk = pre, nv = pre;  // issued
-      for (int p = pre; p < npos; ++p) {
-        const int s = p % C::NST, turn = (p / C::NST - 1) & 1;
-        if (!mbar_wait(bar(C::B_KEMPTY + s), turn, abort_flag, a.status)) break;
-        load_k(p);
-        ++nk;
-        if (!mbar_wait(bar(C::B_VEMPTY + s), turn, abort_flag, a.status)) break;
-        load_v(p);
-        ++nv;
+      auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t full, int row, int head, int b) {
+#pragma unroll
+        for (int c = 0; c < C::NCH; ++c) tma_load_4d(dst + c * C::CHUNK, map, full, c * C::CH, row, head, b);
+      };
+      int nk = 0, nv = 0, nq = 0;  // issued
+      bool ok = true;
+      int asked = 0;
+      for (int i = blockIdx.x; ok && i >= 0;) {
+        const int x = asked & 1;
+        if (asked >= 2 && !(ok = mbar_wait(bar(C::B_READ + x), ((asked >> 1) - 1) & 1, abort_flag, a.status))) break;
+        mbar_arrive_expect_tx(bar(C::B_NEXT + x), 16);
+        block_request(next + x * 16, bar(C::B_NEXT + x));
+        ++asked;
+        const WfItem it(a, i, nrows, nheads, NQ, group);
+        for (int p = 0; p < it.npos; ++p) {
+          const int s = nk % C::NST, turn = (nk / C::NST - 1) & 1;
+          if (nk >= C::NST && !(ok = mbar_wait(bar(C::B_KEMPTY + s), turn, abort_flag, a.status))) break;
+          mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::TILE);
+          load(sK + s * C::TILE, &mk, bar(C::B_KFULL + s), it.key0(p), it.hk, it.b);
+          ++nk;
+          if (p == 0) {
+            if (nq > 0 && !(ok = mbar_wait(bar(C::B_QEMPTY), (nq - 1) & 1, abort_flag, a.status))) break;
+            mbar_arrive_expect_tx(bar(C::B_Q), NQ * C::TILE);
+            for (int q = 0; q < NQ; ++q) load(sbase + q * C::TILE, &mq, bar(C::B_Q), it.row0, it.h0 + q, it.b);
+            ++nq;
+          }
+          if (nv >= C::NST && !(ok = mbar_wait(bar(C::B_VEMPTY + s), turn, abort_flag, a.status))) break;
+          mbar_arrive_expect_tx(bar(C::B_VFULL + s), C::TILE);
+          load(sV + s * C::TILE, &mv, bar(C::B_VFULL + s), it.key0(p), it.hk, it.b);
+          ++nv;
+        }
+        i = next_item(asked - 1, ok);
       }
-      if (*abort_flag) {  // copies in flight land before the shared memory goes
-        drain(bar(C::B_Q), 0);
+      if (*abort_flag) {  // what is in flight lands before the shared memory goes
+        if (asked) drain(bar(C::B_NEXT + ((asked - 1) & 1)), ((asked - 1) >> 1) & 1);
+        if (nq) drain(bar(C::B_Q), (nq - 1) & 1);
         for (int s = 0; s < C::NST; ++s) {
           if (nk > s) drain(bar(C::B_KFULL + s), ((nk - 1 - s) / C::NST) & 1);
           if (nv > s) drain(bar(C::B_VFULL + s), ((nv - 1 - s) / C::NST) & 1);
@@ -205,51 +244,67 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
     } else if (warp == C::W_MMA && lane == 0) {
       // ----------------------------------------------- matrix instructions
       // A chain S, P V, S, P V, ... for each query tile; whichever next step is
-      // ready goes out.  At d = 128 S(p + 1) is issued right behind the P V(p)
-      // whose P it overwrites: one thread's MMAs run in the order of issue.  K and
-      // V stages are handed back by the softmax, whose waits tell when the MMAs
-      // that read them are complete.
+      // ready goes out.  At d = 128 S(p + 1) is issued right behind the P V(p) whose
+      // P it overwrites: one thread's MMAs run in the order of issue.  K and V stages
+      // and Q are handed back by the softmax, whose waits tell when the MMAs that read
+      // them are complete.  An item's first P V overwrites the O of the one before,
+      // which the threads that wrote this P have read.
       constexpr uint32_t HI = smem_desc_hi(C::SBO, C::SWZ);
       const uint32_t id_s = instr_desc_f16(128, 128, BF16, false, false, a.negate != 0);
+      const uint32_t id_sn = instr_desc_f16(128, kNarrow, BF16, false, false, a.negate != 0);
       const uint32_t id_o = instr_desc_f16(128, D, BF16, false, true);
-      bool ok = mbar_wait(bar(C::B_Q), 0, abort_flag, a.status);
-      tc_fence_after_sync();
-      int js[2] = {0, 0}, jp[2] = {0, 0};  // next S and P V of each tile
-      int k_seen = 0, v_seen = 0;          // positions whose loads have been seen to land
+      bool ok = true;
+      int n0 = 0;  // positions of the items before
       IdleWatch watch;
-      while (ok && (jp[0] < npos || (NQ > 1 && jp[1] < npos))) {
-        bool progress = false;
+      for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
+        const WfItem it(a, i, nrows, nheads, NQ, group);
+        const int end = n0 + it.npos, thin = it.ns > 0 && it.narrow(a, it.ns - 1) ? n0 + it.ns - 1 : -1;
+        ok = mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
+        int js[2] = {n0, n0}, jp[2] = {n0, n0};  // next S and P V of each tile
+        int k_seen = n0, v_seen = n0;            // positions whose loads have been seen to land
+        while (ok && (jp[0] < end || (NQ > 1 && jp[1] < end))) {
+          bool progress = false;
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const int jv = jp[q];
-          if (jv < js[q] && mbar_probe(bar(C::B_P + q), jv & 1) &&
-              (jv < v_seen || mbar_probe(bar(C::B_VFULL + jv % C::NST), (jv / C::NST) & 1))) {
-            v_seen = max(v_seen, jv + 1);
-            tc_fence_after_sync();
-            const uint32_t d_o = tmem + C::T_O + q * D, a_p = tmem + C::T_P + q * C::T_PSTEP;
-            const uint32_t v_lo = smem_desc_lo(sV + (jv % C::NST) * C::TILE, C::CHUNK);
+          for (int q = 0; q < NQ; ++q) {
+            const int jv = jp[q], sv = jv % C::NST;
+            if (jv < js[q] && mbar_probe(bar(C::B_P + q), jv & 1) &&
+                (jv < v_seen || mbar_probe(bar(C::B_VFULL + sv), (jv / C::NST) & 1))) {
+              v_seen = max(v_seen, jv + 1);
+              tc_fence_after_sync();
+              const uint32_t d_o = tmem + C::T_O + q * D, a_p = tmem + C::T_P + q * C::T_PSTEP;
+              const uint32_t v_lo = smem_desc_lo(sV + sv * C::TILE, C::CHUNK);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) mma_ts_w(d_o, a_p + kk * 8, v_lo + mn_step<D>(kk), HI, id_o, (jv > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(bar(C::B_O + q));
-            jp[q] = jv + 1;
-            progress = true;
+              for (int kk = 0; kk < kNarrow / 16; ++kk) mma_ts_w(d_o, a_p + kk * 8, v_lo + mn_step<D>(kk), HI, id_o, (jv > n0 || kk > 0) ? 1u : 0u);
+              if (jv != thin) {
+#pragma unroll
+                for (int kk = kNarrow / 16; kk < 8; ++kk) mma_ts_w(d_o, a_p + kk * 8, v_lo + mn_step<D>(kk), HI, id_o, 1u);
+              }
+              tc_commit(bar(C::B_O + q));
+              jp[q] = jv + 1;
+              progress = true;
+            }
+            const int jk = js[q], sk = jk % C::NST;
+            if (jk < end && (C::APART ? jk == 0 || mbar_probe(bar(C::B_TAKEN + q), (jk - 1) & 1) : jk == jp[q]) &&
+                (jk < k_seen || mbar_probe(bar(C::B_KFULL + sk), (jk / C::NST) & 1))) {
+              k_seen = max(k_seen, jk + 1);
+              tc_fence_after_sync();
+              const uint32_t d_s = tmem + q * 128, q_lo = smem_desc_lo(sbase + q * C::TILE, 16);
+              const uint32_t k_lo = smem_desc_lo(sK + sk * C::TILE, 16);
+              const uint32_t id = jk == thin ? id_sn : id_s;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) mma_ss_w(d_s, q_lo + k_step<D>(kk), HI, k_lo + k_step<D>(kk), HI, id, kk > 0 ? 1u : 0u);
+              tc_commit(bar(C::B_S + q));
+              js[q] = jk + 1;
+              progress = true;
+            }
           }
-          const int jk = js[q];
-          if (jk < npos && (C::APART ? jk == 0 || mbar_probe(bar(C::B_TAKEN + q), (jk - 1) & 1) : jk == jp[q]) &&
-              (jk < k_seen || mbar_probe(bar(C::B_KFULL + jk % C::NST), (jk / C::NST) & 1))) {
-            k_seen = max(k_seen, jk + 1);
-            tc_fence_after_sync();
-            const uint32_t d_s = tmem + q * 128, q_lo = smem_desc_lo(sbase + q * C::TILE, 16);
-            const uint32_t k_lo = smem_desc_lo(sK + (jk % C::NST) * C::TILE, 16);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) mma_ss_w(d_s, q_lo + k_step<D>(kk), HI, k_lo + k_step<D>(kk), HI, id_s, kk > 0 ? 1u : 0u);
-            tc_commit(bar(C::B_S + q));
-            js[q] = jk + 1;
-            progress = true;
-          }
+          if (progress) watch.progress();
+          else ok = watch.idle(abort_flag, a.status, kWaitLimitNs);
         }
-        if (progress) watch.progress();
-        else ok = watch.idle(abort_flag, a.status, kWaitLimitNs);
+        n0 = end;
+        i = next_item(k, ok);
+        fence_proxy_async_smem();  // the answer is read before the next one is written
+        mbar_arrive(bar(C::B_READ + (k & 1)));
       }
       tc_commit(bar(C::B_DONE));  // before TMEM is released
       drain(bar(C::B_DONE), 0);
@@ -258,160 +313,183 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
   } else {
     // --------------------------------------------------------------- softmax
     regs_increase<C::REGS_ROW>();
-    const int q = warp >> 2, r = threadIdx.x & 127, row = row0 + r;
+    const int q = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + q * 128, tO = tmem + lanes + C::T_O + q * D, tP = tmem + lanes + C::T_P + q * C::T_PSTEP;
-    const float sl2 = a.sl2;
+    const float sl2 = fmaxf(a.sl2, FLT_MIN);  // a scale of 0: hidden keys are -inf, and that times 0 is NaN
     const float2 sl2x2 = make_float2(sl2, sl2);
-    float m = -INFINITY, l_exact = 0.f, l_round = 0.f;
-    bool ok = true;
-    auto release = [&](int first, int p) {
-      if (r == 0) mbar_arrive(bar(first + p % C::NST));
+    const int off = a.Nk - a.Nq, wnd = a.window, nsk = a.sinks;
+    auto release = [&](int first, int n) {
+      if (r == 0) mbar_arrive(bar(first + n % C::NST));
     };
-    for (int p = 0; p < npos; ++p) {
-      // (a warp's lanes go on or stop together: they vote below)
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_S + q), p & 1, abort_flag, a.status)))) break;
-      tc_fence_after_sync();
-      release(C::B_KEMPTY, p);
-      if (!C::APART && p > 0) release(C::B_VEMPTY, p - 1);  // S(p)'s commit covers P V(p - 1)
-      float sv[128];
-      {
-        uint32_t u[64];
-        tmem_ld64(tS, u);
-#pragma unroll
-        for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(u[c]);
-        tmem_ld64(tS + 64, u);
-#pragma unroll
-        for (int c = 0; c < 64; ++c) sv[64 + c] = __uint_as_float(u[c]);
-      }
-      if constexpr (C::APART) {
-        tc_fence_before_sync();
-        mbar_arrive(bar(C::B_TAKEN + q));
-      }
-      // Key kv0 + c is visible iff c <= last and (c >= first or c < sinks).
-      const int kv0 = key0(p);
-      const int at = row + off - kv0;
-      const bool right = kv0 + 127 > row0 + off;
-      const bool left = kv0 < row0 + 127 + off - a.window + 1 && kv0 + 128 > a.sinks;
-      if (right) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > at) sv[c] = -INFINITY;
-      }
-      if (left) {
-        const int first = at - a.window + 1, sinks = a.sinks - kv0;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c < first && c >= sinks) sv[c] = -INFINITY;
-      }
-      float mx;
-      {
-        float a0 = sv[0], a1 = sv[1], a2 = sv[2], a3 = sv[3];
-#pragma unroll
-        for (int c = 4; c < 128; c += 8) {
-          a0 = max3f(a0, sv[c], sv[c + 1]);
-          a1 = max3f(a1, sv[c + 2], sv[c + 3]);
-          a2 = max3f(a2, sv[c + 4], sv[c + 5]);
-          a3 = max3f(a3, sv[c + 6], sv[c + 7]);
-        }
-        mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
-      }
-      const float m_new = fmaxf(m, mx * sl2);
-      float alpha = 1.f;
-      if (m_new > m + kRescaleLog2) {  // also with the row's first visible key (m = -inf)
-        alpha = ex2_approx(m - m_new);
-        m = m_new;
-      }
-      const float neg_m = m == -INFINITY ? 0.f : -m;
-      const float2 nm2 = make_float2(neg_m, neg_m);
-#pragma unroll
-      for (int c = 0; c < 128; c += 2) {
-        const float2 t = fma2(make_float2(sv[c], sv[c + 1]), sl2x2, nm2);
-        sv[c] = ex2_approx(t.x);
-        sv[c + 1] = ex2_approx(t.y);
-      }
-      if (sl2 == 0.f && (left || right)) {  // -inf times 0 is NaN: hidden keys once more
-        const int first = at - a.window + 1, sinks = a.sinks - kv0;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > at || (c < first && c >= sinks)) sv[c] = 0.f;
-      }
-      if (C::APART && p > 0) {  // P V(p - 1) is complete: P may be written, O is what it will be
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O + q), (p - 1) & 1, abort_flag, a.status));
-        if (!ok) break;
+    bool ok = true;
+    int n = 0;
+    for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
+      const WfItem it(a, i, nrows, nheads, NQ, group);
+      const int row = it.row0 + r;
+      float m = -INFINITY, l_exact = 0.f, l_round = 0.f;
+      // A position with W of its tile's keys.
+      auto step = [&](int p, auto width) {
+        constexpr int W = decltype(width)::value;
+        // (a warp's lanes go on or stop together: they vote below)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_S + q), n & 1, abort_flag, a.status)))) return;
         tc_fence_after_sync();
-        release(C::B_VEMPTY, p - 1);
-      }
-      if (p > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-        for (int c0 = 0; c0 < D / 32; ++c0) {
-          uint32_t ov[32];
-          tmem_ld32(tO + c0 * 32, ov);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-          tmem_st32(tO + c0 * 32, ov);
+        if (r == 0) {
+          mbar_arrive(bar(C::B_KEMPTY + n % C::NST));
+          if (!C::APART && p > 0) mbar_arrive(bar(C::B_VEMPTY + (n - 1) % C::NST));
+          if (p == it.npos - 1) mbar_arrive(bar(C::B_QEMPTY));
         }
+        float sv[W];
+        if constexpr (W == 128) {
+          uint32_t u[64];
+          tmem_ld64(tS, u);
+#pragma unroll
+          for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(u[c]);
+          tmem_ld64(tS + 64, u);
+#pragma unroll
+          for (int c = 0; c < 64; ++c) sv[64 + c] = __uint_as_float(u[c]);
+        } else {
+          uint32_t u[32];
+          tmem_ld32(tS, u);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) sv[c] = __uint_as_float(u[c]);
+        }
+        if constexpr (C::APART) {
+          tc_fence_before_sync();
+          mbar_arrive(bar(C::B_TAKEN + q));
+        }
+        // Key kv0 + c is visible iff c <= at and (c >= first or c < sinks).
+        const int kv0 = it.key0(p);
+        const int at = row + off - kv0;
+        const bool right = kv0 + 127 > it.row0 + off;
+        const bool left = kv0 < it.row0 + 127 + off - wnd + 1 && kv0 + W > nsk;
+        if (right) {
+#pragma unroll
+          for (int c = 0; c < W; ++c)
+            if (c > at) sv[c] = -INFINITY;
+        }
+        if (left) {
+          const int first = at - wnd + 1, sinks = nsk - kv0;
+#pragma unroll
+          for (int c = 0; c < W; ++c)
+            if (c < first && c >= sinks) sv[c] = -INFINITY;
+        }
+        float mx;
+        {
+          float a0 = sv[0], a1 = sv[1], a2 = sv[2], a3 = sv[3];
+#pragma unroll
+          for (int c = 4; c + 8 <= W; c += 8) {
+            a0 = max3f(a0, sv[c], sv[c + 1]);
+            a1 = max3f(a1, sv[c + 2], sv[c + 3]);
+            a2 = max3f(a2, sv[c + 4], sv[c + 5]);
+            a3 = max3f(a3, sv[c + 6], sv[c + 7]);
+          }
+          a0 = max3f(a0, sv[W - 4], sv[W - 3]);
+          a1 = max3f(a1, sv[W - 2], sv[W - 1]);
+          mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
+        }
+        const float m_new = fmaxf(m, mx * sl2);
+        float alpha = 1.f;
+        if (m_new > m + kRescaleLog2) {  // also with the row's first visible key (m = -inf)
+          alpha = ex2_approx(m - m_new);
+          m = m_new;
+        }
+        const float neg_m = m == -INFINITY ? 0.f : -m;
+        const float2 nm2 = make_float2(neg_m, neg_m);
+#pragma unroll
+        for (int c = 0; c < W; c += 2) {
+          const float2 t = fma2(make_float2(sv[c], sv[c + 1]), sl2x2, nm2);
+          sv[c] = ex2_approx(t.x);
+          sv[c + 1] = ex2_approx(t.y);
+        }
+        if (C::APART && p > 0) {  // P V(n - 1) is complete: P may be written, O is what it will be
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O + q), (n - 1) & 1, abort_flag, a.status));
+          if (!ok) return;
+          tc_fence_after_sync();
+          release(C::B_VEMPTY, n - 1);
+        }
+        if (p > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int c0 = 0; c0 < D / 32; ++c0) {
+            uint32_t ov[32];
+            tmem_ld32(tO + c0 * 32, ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st32(tO + c0 * 32, ov);
+          }
+        }
+        // P goes out first, the sums follow while P V runs.
+        uint32_t pk[W / 64 + 1][32];
+#pragma unroll
+        for (int x = 0; x < (W + 63) / 64; ++x) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) pk[x][e] = x * 64 + 2 * e < W ? pack2<BF16>(sv[(x * 64 + 2 * e) % W], sv[(x * 64 + 2 * e + 1) % W]) : 0u;
+          tmem_st32(tP + x * 32, pk[x]);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(bar(C::B_P + q));
+        float2 e0 = make_float2(0.f, 0.f), e1 = e0;
+        float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+#pragma unroll
+        for (int c = 0; c < W; c += 4) {
+          e0 = add2(e0, make_float2(sv[c], sv[c + 1]));
+          e1 = add2(e1, make_float2(sv[c + 2], sv[c + 3]));
+        }
+#pragma unroll
+        for (int e = 0; e < W / 4; e += 2) {
+          r0 = add_halves<BF16>(r0, pk[0][e]);
+          r1 = add_halves<BF16>(r1, pk[0][e + 1]);
+          r2 = add_halves<BF16>(r2, W == 128 ? pk[W / 128][e] : pk[0][W / 4 + e]);
+          r3 = add_halves<BF16>(r3, W == 128 ? pk[W / 128][e + 1] : pk[0][W / 4 + e + 1]);
+        }
+        l_exact = l_exact * alpha + ((e0.x + e0.y) + (e1.x + e1.y));
+        l_round = l_round * alpha + ((r0 + r1) + (r2 + r3));
+        ++n;
+      };
+      for (int p = 0; ok && p < it.npos; ++p) {
+        if (it.narrow(a, p)) step(p, std::integral_constant<int, kNarrow>{});
+        else step(p, std::integral_constant<int, 128>{});
       }
-      // P goes out first, the sums follow while P V runs.
-      uint32_t pk0[32], pk1[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) pk0[i] = pack2<BF16>(sv[2 * i], sv[2 * i + 1]);
-      tmem_st32(tP, pk0);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) pk1[i] = pack2<BF16>(sv[64 + 2 * i], sv[64 + 2 * i + 1]);
-      tmem_st32(tP + 32, pk1);
-      tmem_st_wait();
-      tc_fence_before_sync();
-      mbar_arrive(bar(C::B_P + q));
-      float2 e0 = make_float2(0.f, 0.f), e1 = e0;
-      float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
-#pragma unroll
-      for (int c = 0; c < 128; c += 4) {
-        e0 = add2(e0, make_float2(sv[c], sv[c + 1]));
-        e1 = add2(e1, make_float2(sv[c + 2], sv[c + 3]));
-      }
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        r0 = add_halves<BF16>(r0, pk0[i]);
-        r1 = add_halves<BF16>(r1, pk0[i + 1]);
-        r2 = add_halves<BF16>(r2, pk1[i]);
-        r3 = add_halves<BF16>(r3, pk1[i + 1]);
-      }
-      l_exact = l_exact * alpha + ((e0.x + e0.y) + (e1.x + e1.y));
-      l_round = l_round * alpha + ((r0 + r1) + (r2 + r3));
-    }
-    // ---------------------------------------------------------------- output
-    // At d = 128 through the tile's Q in shared memory, which no MMA reads any
-    // more, so that a warp stores whole rows.
-    constexpr bool STAGE = D == 128;
-    if (__all_sync(0xffffffffu, ok && mbar_wait(bar(C::B_O + q), (npos - 1) & 1, abort_flag, a.status))) {
+      // -------------------------------------------------------------- output
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(C::B_O + q), (n - 1) & 1, abort_flag, a.status));
+      if (!ok) break;
       tc_fence_after_sync();
+      release(C::B_VEMPTY, n - 1);
       const float inv = 1.0f / l_round;
-      uint8_t* stage = smem + q * C::TILE;
-      uint8_t* out = a.o.p + b * a.o.b + (h0 + q) * a.o.h;
+      uint8_t* stage = smem + C::OFF_STAGE + warp * 32 * 128;
+      uint8_t* out = a.o.p + it.b * a.o.b + (it.h0 + q) * a.o.h;
 #pragma unroll
       for (int c0 = 0; c0 < D / 32; ++c0) {
         uint32_t ov[32], pk[16];
         tmem_ld32(tO + c0 * 32, ov);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = pack2<BF16>(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
-        if (STAGE || row < a.Nq) {
+        for (int e = 0; e < 16; ++e) pk[e] = pack2<BF16>(__uint_as_float(ov[2 * e]) * inv, __uint_as_float(ov[2 * e + 1]) * inv);
+        if (C::STAGE || row < a.Nq) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(STAGE ? stage + staged(r, c0 * 4 + i) : out + row * a.o.n + c0 * 64 + i * 16) =
-                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(C::STAGE ? stage + staged(lane, (c0 & 1) * 4 + e) : out + row * a.o.n + c0 * 64 + e * 16) =
+                make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+        }
+        if (C::STAGE && (c0 & 1)) {  // half a row of each of the warp's: whole 128-byte lines
+          __syncwarp();
+          const int row_w = it.row0 + (r & ~31);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int rr = x * 4 + (lane >> 3), u = lane & 7;
+            const uint4 val = *reinterpret_cast<const uint4*>(stage + staged(rr, u));
+            if (row_w + rr < a.Nq) *reinterpret_cast<uint4*>(out + (row_w + rr) * a.o.n + (c0 >> 1) * 128 + u * 16) = val;
+          }
+          __syncwarp();
         }
       }
-      if constexpr (STAGE) {
-        __syncwarp();
-#pragma unroll
-        for (int it = 0; it < 16; ++it) {
-          const int rr = (r & ~31) + it * 2 + (lane >> 4), u = lane & 15;
-          const uint4 val = *reinterpret_cast<const uint4*>(stage + staged(rr, u));
-          if (row0 + rr < a.Nq) *reinterpret_cast<uint4*>(out + (row0 + rr) * a.o.n + u * 16) = val;
-        }
-      }
-      if (row < a.Nq) a.lse[(static_cast<int64_t>(b) * a.Hq + h0 + q) * a.Nq + row] = (m + log2f(l_exact)) * 0.69314718055994531f;
+      if (row < a.Nq) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h0 + q) * a.Nq + row] = (m + log2f(l_exact)) * 0.69314718055994531f;
+      tc_fence_before_sync();  // O is read before this thread's next P lets it be overwritten
+      i = next_item(k, ok);
+      ok = __all_sync(0xffffffffu, ok);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_READ + (k & 1)));
     }
   }
   tc_fence_before_sync();
@@ -432,10 +510,12 @@ int launch_t(const WindowArgs& a) {
   auto kern = attn_window_fwd_kernel<D, BF16, NQ>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return kStatusCuda;
   if (!check_launch_regs(reinterpret_cast<const void*>(kern), C::REGS)) return kStatusDeviceCheck;  // the split's sum
-  const dim3 grid((a.Nq + 127) / 128, a.B * a.Hq / NQ);
-  const bool overlap = overlap_launches(static_cast<int64_t>(grid.x) * grid.y, C::CTAS);
-  const int group = order_head_group(grid.y, int64_t{4} * a.Nk * D, int64_t{128} << 20);
-  return launch_serialized(overlap, kern, grid, dim3(C::THREADS), C::SMEM, a.stream, mq, mk, mv, a, group, overlap ? 1 : 0) == cudaSuccess
+  const int nrows = (a.Nq + 127) / 128, nheads = a.B * a.Hq / NQ;
+  const int64_t items = static_cast<int64_t>(nrows) * nheads;
+  if (items > 0x7fffffff - 4096) return kStatusUnsupported;
+  const int group = order_head_group(nheads, int64_t{4} * a.Nk * D, int64_t{128} << 20);
+  return launch_serialized(true, kern, dim3(static_cast<unsigned>(items)), dim3(C::THREADS), C::SMEM, a.stream, mq, mk, mv, a, nrows, nheads, group, 1) ==
+                 cudaSuccess
              ? kStatusOk
              : kStatusCuda;
 }

@@ -197,6 +197,29 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// ------------------------------------------------- work of blocks not started
+// Asks for the index of a block of this grid that has not started, which then
+// never will: a running block takes its work (16 bytes at `addr`, signalled as
+// transaction bytes on `bar`).  Once refused, a block must not ask again.
+__device__ __forceinline__ void block_request(uint32_t addr, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(addr), "r"(bar)
+               : "memory");
+}
+// The answer: blockIdx.x, or -1.
+__device__ __forceinline__ int block_answer(uint32_t addr) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+      : "=r"(x)
+      : "r"(addr)
+      : "memory");
+  return x;
+}
+
 // ------------------------------------------------------------- tcgen05 TMEM
 // Allocation is warp-collective; the TMEM base address is written to smem.
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
