@@ -71,26 +71,25 @@ struct Tile {
 template <int D>
 struct DqCfg : Tile<D> {
   using T = Tile<D>;
-  static constexpr int NST = 2;
+  static constexpr int NK = 3, NV = 2;  // a K tile is held until its dQ step is complete
   static constexpr int OFF_DO = T::TILE;
   static constexpr int OFF_K = 2 * T::TILE;
-  static constexpr int OFF_V = OFF_K + NST * T::TILE;
-  static constexpr int OFF_STAGE = OFF_V + NST * T::TILE;  // 4 KB a warp
-  static constexpr int OFF_SUM = OFF_STAGE + (T::STAGE ? 8 * 4096 : 0);  // [2][2][128] fp32
-  static constexpr int OFF_BAR = OFF_SUM + 2048;
+  static constexpr int OFF_V = OFF_K + NK * T::TILE;
+  static constexpr int OFF_ROWS = OFF_V + NV * T::TILE;  // [4][128] fp32: -D of the items that can be under way
+  static constexpr int OFF_BAR = OFF_ROWS + 4 * 512;
   static constexpr int B_Q = 0;
   static constexpr int B_QEMPTY = 1;
   static constexpr int B_KFULL = 2;
-  static constexpr int B_KEMPTY = B_KFULL + NST;
-  static constexpr int B_VFULL = B_KEMPTY + NST;
-  static constexpr int B_VEMPTY = B_VFULL + NST;
-  static constexpr int B_S = B_VEMPTY + NST;   // S(n) is in buffer n & 1
+  static constexpr int B_KEMPTY = B_KFULL + NK;
+  static constexpr int B_VFULL = B_KEMPTY + NK;
+  static constexpr int B_VEMPTY = B_VFULL + NV;
+  static constexpr int B_S = B_VEMPTY + NV;   // S(n) is in buffer n & 1
   static constexpr int B_DP = B_S + 2;
   static constexpr int B_TAKEN = B_DP + 1;     // dP is in registers
   static constexpr int B_DS = B_TAKEN + 1;     // dS(n) is in buffer n & 1
   static constexpr int B_OUT = B_DS + 2;       // the item's dQ is complete
-  static constexpr int B_SUM = B_OUT + 1;      // both halves of the rows' D are in shared memory
-  static constexpr int B_NEXT = B_SUM + 1;
+  static constexpr int B_ROWS = B_OUT + 1;     // the rows' vectors are in shared memory
+  static constexpr int B_NEXT = B_ROWS + 4;
   static constexpr int B_READ = B_NEXT + 2;
   static constexpr int B_DONE = B_READ + 2;
   static constexpr int NBAR = B_DONE + 1;
@@ -244,10 +243,10 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   const uint32_t sDO = sbase + C::OFF_DO, sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
   if (warp == C::W_LOAD && lane == 0) {
-    for (int x = 0; x < C::NBAR; ++x) {
-      const bool rows = x == C::B_TAKEN || x == C::B_DS || x == C::B_DS + 1 || x == C::B_SUM;
-      mbar_init(bar(x), rows ? 256 : x == C::B_READ || x == C::B_READ + 1 ? 9 : 1);  // (read by 8 warps and the issuer)
-    }
+    for (int x = 0; x < C::NBAR; ++x) mbar_init(bar(x), 1);
+    for (int x : {C::B_TAKEN, C::B_DS, C::B_DS + 1}) mbar_init(bar(x), 256);
+    for (int x = 0; x < 4; ++x) mbar_init(bar(C::B_ROWS + x), 64);
+    for (int x = 0; x < 2; ++x) mbar_init(bar(C::B_READ + x), 11);  // 8 + 2 warps and the issuer
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&mq);
@@ -283,8 +282,8 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
         ++asked;
         const DqItem it(a, i, nrows, group);
         for (int p = 0; p < it.npos; ++p) {
-          const int s = nk % C::NST, turn = (nk / C::NST - 1) & 1;
-          if (nk >= C::NST && !(ok = mbar_wait(bar(C::B_KEMPTY + s), turn, abort_flag, a.status))) break;
+          const int s = nk % C::NK, sv = nv % C::NV;
+          if (nk >= C::NK && !(ok = mbar_wait(bar(C::B_KEMPTY + s), (nk / C::NK - 1) & 1, abort_flag, a.status))) break;
           mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::TILE);
           load(sK + s * C::TILE, &mk, bar(C::B_KFULL + s), it.key0(p), it.hk, it.b);
           ++nk;
@@ -295,9 +294,9 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
             load(sDO, &mdo, bar(C::B_Q), it.row0, it.h, it.b);
             ++nq;
           }
-          if (nv >= C::NST && !(ok = mbar_wait(bar(C::B_VEMPTY + s), turn, abort_flag, a.status))) break;
-          mbar_arrive_expect_tx(bar(C::B_VFULL + s), C::TILE);
-          load(sV + s * C::TILE, &mv, bar(C::B_VFULL + s), it.key0(p), it.hk, it.b);
+          if (nv >= C::NV && !(ok = mbar_wait(bar(C::B_VEMPTY + sv), (nv / C::NV - 1) & 1, abort_flag, a.status))) break;
+          mbar_arrive_expect_tx(bar(C::B_VFULL + sv), C::TILE);
+          load(sV + sv * C::TILE, &mv, bar(C::B_VFULL + sv), it.key0(p), it.hk, it.b);
           ++nv;
         }
         i = items.after(asked - 1, ok);
@@ -305,10 +304,10 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       if (*abort_flag) {  // what is in flight lands before the shared memory goes
         items.drain_last(asked);
         if (nq) drain(bar(C::B_Q), (nq - 1) & 1);
-        for (int s = 0; s < C::NST; ++s) {
-          if (nk > s) drain(bar(C::B_KFULL + s), ((nk - 1 - s) / C::NST) & 1);
-          if (nv > s) drain(bar(C::B_VFULL + s), ((nv - 1 - s) / C::NST) & 1);
-        }
+        for (int s = 0; s < C::NK; ++s)
+          if (nk > s) drain(bar(C::B_KFULL + s), ((nk - 1 - s) / C::NK) & 1);
+        for (int s = 0; s < C::NV; ++s)
+          if (nv > s) drain(bar(C::B_VFULL + s), ((nv - 1 - s) / C::NV) & 1);
       }
     } else if (warp == C::W_MMA && lane == 0) {
       // ------------------------------------------------- matrix instructions
@@ -331,9 +330,9 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
         while (ok && iq < end) {
           bool progress = false;
           if (ip < end && (ip == 0 || mbar_probe(bar(C::B_TAKEN), (ip - 1) & 1)) &&
-              mbar_probe(bar(C::B_VFULL + ip % C::NST), (ip / C::NST) & 1)) {
+              mbar_probe(bar(C::B_VFULL + ip % C::NV), (ip / C::NV) & 1)) {
             tc_fence_after_sync();
-            const uint32_t v_lo = smem_desc_lo(sV + (ip % C::NST) * C::TILE, 16);
+            const uint32_t v_lo = smem_desc_lo(sV + (ip % C::NV) * C::TILE, 16);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ss_w(tmem + C::T_DP, do_lo + k_step<D>(kk), HI, v_lo + k_step<D>(kk), HI, id_dp, kk > 0 ? 1u : 0u);
@@ -341,9 +340,9 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
             ++ip;
             progress = true;
           }
-          if (is < end && is <= iq + 1 && mbar_probe(bar(C::B_KFULL + is % C::NST), (is / C::NST) & 1)) {
+          if (is < end && is <= iq + 1 && mbar_probe(bar(C::B_KFULL + is % C::NK), (is / C::NK) & 1)) {
             tc_fence_after_sync();
-            const uint32_t k_lo = smem_desc_lo(sK + (is % C::NST) * C::TILE, 16);
+            const uint32_t k_lo = smem_desc_lo(sK + (is % C::NK) * C::TILE, 16);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ss_w(tmem + C::T_S + (is & 1) * 128, q_lo + k_step<D>(kk), HI, k_lo + k_step<D>(kk), HI, id_s, kk > 0 ? 1u : 0u);
@@ -353,12 +352,12 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
           }
           if (iq < ip && mbar_probe(bar(C::B_DS + (iq & 1)), (iq >> 1) & 1)) {
             tc_fence_after_sync();
-            const uint32_t k_lo = smem_desc_lo(sK + (iq % C::NST) * C::TILE, C::CHUNK);
+            const uint32_t k_lo = smem_desc_lo(sK + (iq % C::NK) * C::TILE, C::CHUNK);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_ts_w(tmem + C::T_DQ, tmem + C::T_S + (iq & 1) * 128 + half_step(kk), k_lo + mn_step<D>(kk), HI, id_dq,
                        (iq > n0 || kk > 0) ? 1u : 0u);
-            tc_commit(bar(C::B_KEMPTY + iq % C::NST));
+            tc_commit(bar(C::B_KEMPTY + iq % C::NK));
             if (++iq == end) tc_commit(bar(C::B_OUT));
             progress = true;
           }
@@ -371,6 +370,50 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       }
       tc_commit(bar(C::B_DONE));  // before TMEM is released
       drain(bar(C::B_DONE), 0);
+    } else if (warp > C::W_MMA) {
+      // -------------------------------------------------------- row vectors
+      // Two warps, ahead of the row warps by an item or two.  D / 8 lanes to a row, 16
+      // bytes a lane, four rows of a lane at a time.
+      constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp's load
+      bool ok = true;
+      for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
+        const DqItem it(a, i, nrows, group);
+        const int64_t bh = static_cast<int64_t>(it.b) * a.Hq + it.h;
+        const uint8_t *o = a.o.p + it.b * a.o.b + it.h * a.o.h + lane % LPR * 16, *dO = a.dO.p + it.b * a.dO.b + it.h * a.dO.h + lane % LPR * 16;
+        float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS) + (k & 3) * 128;
+        for (int r0 = (warp & 1) * 64; r0 < (warp & 1) * 64 + 64; r0 += 4 * RPW) {
+          uint4 x[4], y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int row = it.row0 + r0 + u * RPW + lane / LPR;
+            x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < a.Nq) x[u] = *reinterpret_cast<const uint4*>(o + row * a.o.n), y[u] = *reinterpret_cast<const uint4*>(dO + row * a.dO.n);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, yw[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+            float d = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack2<BF16>(xw[e]), g = unpack2<BF16>(yw[e]);
+              d = fmaf(f.x, g.x, fmaf(f.y, g.y, d));
+            }
+#pragma unroll
+            for (int m = 1; m < LPR; m <<= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+            const int r = r0 + u * RPW + lane / LPR, row = it.row0 + r;
+            if (lane % LPR == 0) {
+              const float lse2 = row < a.Nq ? -a.lse[bh * a.Nq + row] * kLog2e : -INFINITY;
+              rows[r] = -d;
+              pl.dvec[bh * pl.npad + row] = -d, pl.lse2[bh * pl.npad + row] = lse2;
+            }
+          }
+        }
+        mbar_arrive(bar(C::B_ROWS + (k & 3)));
+        i = items.after(k, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        __syncwarp();
+        if (lane == 0) items.read(k);
+      }
     }
     __syncwarp();
   } else {
@@ -379,39 +422,14 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
     const int half = warp >> 2, r = threadIdx.x & 127, off = a.Nk - a.Nq;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float2 sl2x2 = make_float2(a.sl2, a.sl2);
-    float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
     bool ok = true;
     int n = 0;
     for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
       const DqItem it(a, i, nrows, group);
       const int row = it.row0 + r;
-      // D, half a row a thread, while the first tiles travel.
-      const int64_t bh = static_cast<int64_t>(it.b) * a.Hq + it.h;
-      float d_part = 0.f, lse2 = -INFINITY;
-      if (row < a.Nq) {
-        const uint8_t *o = a.o.p + it.b * a.o.b + it.h * a.o.h + row * a.o.n + half * D, *dO = a.dO.p + it.b * a.dO.b + it.h * a.dO.h + row * a.dO.n + half * D;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4*>(o + c * 16), y = *reinterpret_cast<const uint4*>(dO + c * 16);
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 u = unpack2<BF16>(xw[e]), w = unpack2<BF16>(yw[e]);
-            d_part = fmaf(u.x, w.x, d_part);
-            d_part = fmaf(u.y, w.y, d_part);
-          }
-        }
-        lse2 = -a.lse[bh * a.Nq + row] * kLog2e;
-      }
-      float* sum = sums + (k & 1) * 256 + r;  // (who writes here again has waited for the item between)
-      sum[half * 128] = d_part;
-      mbar_arrive(bar(C::B_SUM));
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_SUM), k & 1, abort_flag, a.status)))) break;
-      const float nd = -(sum[0] + sum[128]);
-      if (half == 0) {
-        pl.lse2[bh * pl.npad + row] = lse2;
-        pl.dvec[bh * pl.npad + row] = nd;
-      }
+      const float lse2 = row < a.Nq ? -a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] * kLog2e : -INFINITY;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_ROWS + (k & 3)), (k >> 2) & 1, abort_flag, a.status)))) break;
+      const float nd = reinterpret_cast<const float*>(smem + C::OFF_ROWS)[(k & 3) * 128 + r];
       const float2 l2 = make_float2(lse2, lse2), nd2 = make_float2(nd, nd);
       for (int p = 0; p < it.npos; ++p, ++n) {
         // (a warp's lanes go on or stop together: what follows wants all of them)
@@ -447,7 +465,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_DP), n & 1, abort_flag, a.status)))) break;
         tc_fence_after_sync();
         if (threadIdx.x == 0) {
-          mbar_arrive(bar(C::B_VEMPTY + n % C::NST));
+          mbar_arrive(bar(C::B_VEMPTY + n % C::NV));
           if (p == it.npos - 1) mbar_arrive(bar(C::B_QEMPTY));  // (S of this position is complete too)
         }
         uint32_t dp[64], pk[32];
@@ -469,16 +487,13 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(C::B_OUT), k & 1, abort_flag, a.status)))) break;
       tc_fence_after_sync();
       uint8_t* out = a.dq.p + it.b * a.dq.b + it.h * a.dq.h;
-      if constexpr (C::STAGE) {  // 64 channels a thread
-        uint32_t x[64], w[32];
-        tmem_ld64(tmem + lanes + C::T_DQ + half * 64, x);
+      // A thread's channels: 64 at d = 128, else 32 (a line or half of one).
 #pragma unroll
-        for (int e = 0; e < 32; ++e) w[e] = pack2<BF16>(__uint_as_float(x[2 * e]) * a.scale, __uint_as_float(x[2 * e + 1]) * a.scale);
-        const int row_w = it.row0 + (warp & 3) * 32;
-        store_rows(smem + C::OFF_STAGE + warp * 4096, lane, w, out + row_w * a.dq.n + half * 128, a.dq.n, a.Nq - row_w);
-      } else if (half * 32 < D) {  // 32 channels
+      for (int c0 = 0; c0 < (D == 128 ? 2 : 1); ++c0) {
+        const int c = half * (D == 128 ? 64 : 32) + c0 * 32;
+        if (c >= D) break;
         uint32_t x[32];
-        tmem_ld32(tmem + lanes + C::T_DQ + half * 32, x);
+        tmem_ld32(tmem + lanes + C::T_DQ + c, x);
         if (row < a.Nq) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -486,7 +501,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
 #pragma unroll
             for (int f = 0; f < 4; ++f)
               w[f] = pack2<BF16>(__uint_as_float(x[8 * e + 2 * f]) * a.scale, __uint_as_float(x[8 * e + 2 * f + 1]) * a.scale);
-            *reinterpret_cast<uint4*>(out + row * a.dq.n + half * 64 + e * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out + row * a.dq.n + c * 2 + e * 16) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
