@@ -61,7 +61,7 @@ struct Tile {
   static constexpr int CHUNK = 128 * ROWB;
   static constexpr int TILE = 128 * D * 2;
   static constexpr int THREADS = 384;
-  static constexpr int REGS = 168, REGS_ROW = 208, REGS_CTRL = 88;
+  static constexpr int REGS = 168, REGS_ROW = 184, REGS_CTRL = 136;
   static_assert(256 * REGS_ROW + 128 * REGS_CTRL <= THREADS * REGS, "register split");
   static constexpr int W_LOAD = 8, W_MMA = 9;
   static constexpr bool STAGE = D == 128;  // outputs leave through shared memory, whole lines at a time
@@ -373,24 +373,24 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
     } else if (warp > C::W_MMA) {
       // -------------------------------------------------------- row vectors
       // Two warps, ahead of the row warps by an item or two.  D / 8 lanes to a row, 16
-      // bytes a lane, four rows of a lane at a time.
-      constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp's load
+      // bytes a lane, eight rows of a lane in flight: a load takes 5000 cycles here.
+      constexpr int LPR = D / 8, RPW = 32 / LPR, U = 64 / RPW < 8 ? 64 / RPW : 8;  // lanes of a row, rows of a warp's load, loads
       bool ok = true;
       for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
         const DqItem it(a, i, nrows, group);
         const int64_t bh = static_cast<int64_t>(it.b) * a.Hq + it.h;
         const uint8_t *o = a.o.p + it.b * a.o.b + it.h * a.o.h + lane % LPR * 16, *dO = a.dO.p + it.b * a.dO.b + it.h * a.dO.h + lane % LPR * 16;
         float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS) + (k & 3) * 128;
-        for (int r0 = (warp & 1) * 64; r0 < (warp & 1) * 64 + 64; r0 += 4 * RPW) {
-          uint4 x[4], y[4];
+        for (int r0 = (warp & 1) * 64; r0 < (warp & 1) * 64 + 64; r0 += U * RPW) {
+          uint4 x[U], y[U];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < U; ++u) {
             const int row = it.row0 + r0 + u * RPW + lane / LPR;
             x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
             if (row < a.Nq) x[u] = *reinterpret_cast<const uint4*>(o + row * a.o.n), y[u] = *reinterpret_cast<const uint4*>(dO + row * a.dO.n);
           }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < U; ++u) {
             const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, yw[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
             float d = 0.f;
 #pragma unroll
@@ -650,6 +650,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       //   dP(n) needs dO_n, and dK(n - 1) issued, whose dS^T it overwrites
       //   dV(n) needs P^T(n), dK(n) needs dS^T(n); the item's first overwrite a dV, dK
       //         that have been read
+      // S(n + 1) goes out before dK(n), so that P^T(n + 1) is worked on while dK(n) and
+      // dP(n + 1) run.
       constexpr uint32_t HI = smem_desc_hi(C::SBO, C::SWZ);
       const uint32_t id_s = instr_desc_f16(128, 128, BF16, false, false, a.negate != 0);
       const uint32_t id_dp = instr_desc_f16(128, 128, BF16, false, false);
@@ -668,6 +670,15 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         int is = n0, ip = n0, iv = n0, ik = n0;
         while (ok && ik < end) {
           bool progress = false;
+          if (iv < is && mbar_probe(bar(C::B_P), iv & 1)) {
+            tc_fence_after_sync();
+            const uint32_t do_lo = smem_desc_lo(sDO + (iv % C::NST) * C::TILE, C::CHUNK);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts_w(tmem + C::T_DV, tmem + C::T_S + half_step(kk), do_lo + mn_step<D>(kk), HI, id_out, (iv > n0 || kk > 0) ? 1u : 0u);
+            ++iv;
+            progress = true;
+          }
           if (is < end && is == iv && mbar_probe(bar(C::B_QFULL + is % C::NST), (is / C::NST) & 1)) {
             tc_fence_after_sync();
             const uint32_t q_lo = smem_desc_lo(sQ + (is % C::NST) * C::TILE, 16);
@@ -678,24 +689,6 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
             ++is;
             progress = true;
           }
-          if (ip < is && ip == ik) {  // (Q_n and dO_n land together)
-            const uint32_t do_lo = smem_desc_lo(sDO + (ip % C::NST) * C::TILE, 16);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss_w(tmem + C::T_DP, v_lo + k_step<D>(kk), HI, do_lo + k_step<D>(kk), HI, id_dp, kk > 0 ? 1u : 0u);
-            tc_commit(bar(C::B_DP));
-            ++ip;
-            progress = true;
-          }
-          if (iv < is && mbar_probe(bar(C::B_P), iv & 1)) {
-            tc_fence_after_sync();
-            const uint32_t do_lo = smem_desc_lo(sDO + (iv % C::NST) * C::TILE, C::CHUNK);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts_w(tmem + C::T_DV, tmem + C::T_S + half_step(kk), do_lo + mn_step<D>(kk), HI, id_out, (iv > n0 || kk > 0) ? 1u : 0u);
-            ++iv;
-            progress = true;
-          }
           if (ik < iv && ik < ip && mbar_probe(bar(C::B_DS), ik & 1)) {
             tc_fence_after_sync();
             const uint32_t q_lo = smem_desc_lo(sQ + (ik % C::NST) * C::TILE, C::CHUNK);
@@ -704,6 +697,15 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
               mma_ts_w(tmem + C::T_DK, tmem + C::T_DP + half_step(kk), q_lo + mn_step<D>(kk), HI, id_out, (ik > n0 || kk > 0) ? 1u : 0u);
             tc_commit(bar(C::B_QEMPTY + ik % C::NST));
             if (++ik == end) tc_commit(bar(C::B_OUT));
+            progress = true;
+          }
+          if (ip < is && ip == ik) {  // (Q_n and dO_n land together)
+            const uint32_t do_lo = smem_desc_lo(sDO + (ip % C::NST) * C::TILE, 16);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss_w(tmem + C::T_DP, v_lo + k_step<D>(kk), HI, do_lo + k_step<D>(kk), HI, id_dp, kk > 0 ? 1u : 0u);
+            tc_commit(bar(C::B_DP));
+            ++ip;
             progress = true;
           }
           if (progress) watch.progress();
