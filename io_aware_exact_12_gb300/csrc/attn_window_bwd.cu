@@ -67,7 +67,8 @@ struct Tile {
   static constexpr bool STAGE = D == 128;  // outputs leave through shared memory, whole lines at a time
 };
 
-// dQ: Q and dO of an item, a ring of K and V tiles.
+// dQ: Q and dO of an item, rings of K and V tiles.  The item's O, of which only D is
+// wanted, passes through the K ring before the keys.
 template <int D>
 struct DqCfg : Tile<D> {
   using T = Tile<D>;
@@ -75,7 +76,7 @@ struct DqCfg : Tile<D> {
   static constexpr int OFF_DO = T::TILE;
   static constexpr int OFF_K = 2 * T::TILE;
   static constexpr int OFF_V = OFF_K + NK * T::TILE;
-  static constexpr int OFF_ROWS = OFF_V + NV * T::TILE;  // [4][128] fp32: -D of the items that can be under way
+  static constexpr int OFF_ROWS = OFF_V + NV * T::TILE;  // [2][2][128] fp32: halves of D, of two items
   static constexpr int OFF_BAR = OFF_ROWS + 4 * 512;
   static constexpr int B_Q = 0;
   static constexpr int B_QEMPTY = 1;
@@ -88,8 +89,8 @@ struct DqCfg : Tile<D> {
   static constexpr int B_TAKEN = B_DP + 1;     // dP is in registers
   static constexpr int B_DS = B_TAKEN + 1;     // dS(n) is in buffer n & 1
   static constexpr int B_OUT = B_DS + 2;       // the item's dQ is complete
-  static constexpr int B_ROWS = B_OUT + 1;     // the rows' vectors are in shared memory
-  static constexpr int B_NEXT = B_ROWS + 4;
+  static constexpr int B_ROWS = B_OUT + 1;     // both halves of the rows' D are in shared memory
+  static constexpr int B_NEXT = B_ROWS + 1;
   static constexpr int B_READ = B_NEXT + 2;
   static constexpr int B_DONE = B_READ + 2;
   static constexpr int NBAR = B_DONE + 1;
@@ -150,6 +151,13 @@ __host__ __device__ constexpr uint32_t mn_step(int kk) {
   return static_cast<uint32_t>((kk * 16 * Tile<D>::ROWB) >> 4);
 }
 __host__ __device__ constexpr uint32_t half_step(int kk) { return static_cast<uint32_t>((kk >> 2) * 64 + (kk & 3) * 8); }
+
+// Byte offset of 16-byte unit u of a row in a tile, as TMA has laid it.
+template <int D>
+__device__ __forceinline__ uint32_t tile_unit(int row, int u) {
+  if constexpr (D >= 64) return static_cast<uint32_t>((u >> 3) * Tile<D>::CHUNK + row * 128 + (((u & 7) ^ (row & 7)) << 4));
+  else return static_cast<uint32_t>(row * 64 + ((u ^ ((row >> 1) & 3)) << 4));
+}
 
 // Byte offset of 16-byte unit u of a row of 128 bytes in a warp's staging copy,
 // swizzled so that rows by threads and units by threads meet no bank twice.
@@ -228,8 +236,8 @@ struct DqItem {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
     attn_window_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const WindowArgs a,
-                          const WbPlan pl, int nrows, int group) {
+                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                          const __grid_constant__ CUtensorMap mo, const WindowArgs a, const WbPlan pl, int nrows, int group) {
   using C = DqCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -244,15 +252,15 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
   const uint32_t sDO = sbase + C::OFF_DO, sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
   if (warp == C::W_LOAD && lane == 0) {
     for (int x = 0; x < C::NBAR; ++x) mbar_init(bar(x), 1);
-    for (int x : {C::B_TAKEN, C::B_DS, C::B_DS + 1}) mbar_init(bar(x), 256);
-    for (int x = 0; x < 4; ++x) mbar_init(bar(C::B_ROWS + x), 64);
-    for (int x = 0; x < 2; ++x) mbar_init(bar(C::B_READ + x), 11);  // 8 + 2 warps and the issuer
+    for (int x : {C::B_TAKEN, C::B_DS, C::B_DS + 1, C::B_ROWS}) mbar_init(bar(x), 256);
+    for (int x = 0; x < 2; ++x) mbar_init(bar(C::B_READ + x), 9);  // 8 warps and the issuer
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&mq);
     prefetch_tensormap(&mk);
     prefetch_tensormap(&mv);
     prefetch_tensormap(&mdo);
+    prefetch_tensormap(&mo);
   }
   if (warp == C::W_MMA) {
     tmem_alloc(smem_addr(slot), 512);
@@ -265,7 +273,8 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *slot;
   const Items items = {sbase + C::OFF_NEXT, bar(C::B_NEXT), bar(C::B_READ), abort_flag, a.status};
-  // `n` counts positions over all items and gives stages, buffers and phases.
+  // `n` counts positions over all items and gives buffers, V stages and phases; the K
+  // ring has item k's O at n + k, its first key tile behind it.
 
   if (warp >= C::W_LOAD) {
     regs_decrease<C::REGS_CTRL>();
@@ -281,12 +290,18 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
         if (!(ok = items.ask(asked))) break;
         ++asked;
         const DqItem it(a, i, nrows, group);
-        for (int p = 0; p < it.npos; ++p) {
-          const int s = nk % C::NK, sv = nv % C::NV;
-          if (nk >= C::NK && !(ok = mbar_wait(bar(C::B_KEMPTY + s), (nk / C::NK - 1) & 1, abort_flag, a.status))) break;
+        auto load_k = [&](const CUtensorMap* map, int row, int head) {
+          const int s = nk % C::NK;
+          if (nk >= C::NK && !(ok = mbar_wait(bar(C::B_KEMPTY + s), (nk / C::NK - 1) & 1, abort_flag, a.status))) return;
           mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::TILE);
-          load(sK + s * C::TILE, &mk, bar(C::B_KFULL + s), it.key0(p), it.hk, it.b);
+          load(sK + s * C::TILE, map, bar(C::B_KFULL + s), row, head, it.b);
           ++nk;
+        };
+        load_k(&mo, it.row0, it.h);
+        for (int p = 0; ok && p < it.npos; ++p) {
+          const int sv = nv % C::NV;
+          load_k(&mk, it.key0(p), it.hk);
+          if (!ok) break;
           if (p == 0) {
             if (nq > 0 && !(ok = mbar_wait(bar(C::B_QEMPTY), (nq - 1) & 1, abort_flag, a.status))) break;
             mbar_arrive_expect_tx(bar(C::B_Q), 2 * C::TILE);
@@ -327,6 +342,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
         const int end = n0 + DqItem(a, i, nrows, group).npos;
         ok = mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
         int is = n0, ip = n0, iq = n0;
+        const int ahead = k + 1;  // O tiles in the K ring so far
         while (ok && iq < end) {
           bool progress = false;
           if (ip < end && (ip == 0 || mbar_probe(bar(C::B_TAKEN), (ip - 1) & 1)) &&
@@ -340,9 +356,9 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
             ++ip;
             progress = true;
           }
-          if (is < end && is <= iq + 1 && mbar_probe(bar(C::B_KFULL + is % C::NK), (is / C::NK) & 1)) {
+          if (is < end && is <= iq + 1 && mbar_probe(bar(C::B_KFULL + (is + ahead) % C::NK), ((is + ahead) / C::NK) & 1)) {
             tc_fence_after_sync();
-            const uint32_t k_lo = smem_desc_lo(sK + (is % C::NK) * C::TILE, 16);
+            const uint32_t k_lo = smem_desc_lo(sK + ((is + ahead) % C::NK) * C::TILE, 16);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ss_w(tmem + C::T_S + (is & 1) * 128, q_lo + k_step<D>(kk), HI, k_lo + k_step<D>(kk), HI, id_s, kk > 0 ? 1u : 0u);
@@ -352,12 +368,12 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
           }
           if (iq < ip && mbar_probe(bar(C::B_DS + (iq & 1)), (iq >> 1) & 1)) {
             tc_fence_after_sync();
-            const uint32_t k_lo = smem_desc_lo(sK + (iq % C::NK) * C::TILE, C::CHUNK);
+            const uint32_t k_lo = smem_desc_lo(sK + ((iq + ahead) % C::NK) * C::TILE, C::CHUNK);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_ts_w(tmem + C::T_DQ, tmem + C::T_S + (iq & 1) * 128 + half_step(kk), k_lo + mn_step<D>(kk), HI, id_dq,
                        (iq > n0 || kk > 0) ? 1u : 0u);
-            tc_commit(bar(C::B_KEMPTY + iq % C::NK));
+            tc_commit(bar(C::B_KEMPTY + (iq + ahead) % C::NK));
             if (++iq == end) tc_commit(bar(C::B_OUT));
             progress = true;
           }
@@ -370,50 +386,6 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       }
       tc_commit(bar(C::B_DONE));  // before TMEM is released
       drain(bar(C::B_DONE), 0);
-    } else if (warp > C::W_MMA) {
-      // -------------------------------------------------------- row vectors
-      // Two warps, ahead of the row warps by an item or two.  D / 8 lanes to a row, 16
-      // bytes a lane, eight rows of a lane in flight: a load takes 5000 cycles here.
-      constexpr int LPR = D / 8, RPW = 32 / LPR, U = 64 / RPW < 8 ? 64 / RPW : 8;  // lanes of a row, rows of a warp's load, loads
-      bool ok = true;
-      for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
-        const DqItem it(a, i, nrows, group);
-        const int64_t bh = static_cast<int64_t>(it.b) * a.Hq + it.h;
-        const uint8_t *o = a.o.p + it.b * a.o.b + it.h * a.o.h + lane % LPR * 16, *dO = a.dO.p + it.b * a.dO.b + it.h * a.dO.h + lane % LPR * 16;
-        float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS) + (k & 3) * 128;
-        for (int r0 = (warp & 1) * 64; r0 < (warp & 1) * 64 + 64; r0 += U * RPW) {
-          uint4 x[U], y[U];
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int row = it.row0 + r0 + u * RPW + lane / LPR;
-            x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < a.Nq) x[u] = *reinterpret_cast<const uint4*>(o + row * a.o.n), y[u] = *reinterpret_cast<const uint4*>(dO + row * a.dO.n);
-          }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, yw[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
-            float d = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2<BF16>(xw[e]), g = unpack2<BF16>(yw[e]);
-              d = fmaf(f.x, g.x, fmaf(f.y, g.y, d));
-            }
-#pragma unroll
-            for (int m = 1; m < LPR; m <<= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
-            const int r = r0 + u * RPW + lane / LPR, row = it.row0 + r;
-            if (lane % LPR == 0) {
-              const float lse2 = row < a.Nq ? -a.lse[bh * a.Nq + row] * kLog2e : -INFINITY;
-              rows[r] = -d;
-              pl.dvec[bh * pl.npad + row] = -d, pl.lse2[bh * pl.npad + row] = lse2;
-            }
-          }
-        }
-        mbar_arrive(bar(C::B_ROWS + (k & 3)));
-        i = items.after(k, ok);
-        ok = __all_sync(0xffffffffu, ok);
-        __syncwarp();
-        if (lane == 0) items.read(k);
-      }
     }
     __syncwarp();
   } else {
@@ -427,9 +399,38 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
     for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
       const DqItem it(a, i, nrows, group);
       const int row = it.row0 + r;
-      const float lse2 = row < a.Nq ? -a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] * kLog2e : -INFINITY;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_ROWS + (k & 3)), (k >> 2) & 1, abort_flag, a.status)))) break;
-      const float nd = reinterpret_cast<const float*>(smem + C::OFF_ROWS)[(k & 3) * 128 + r];
+      const int64_t bh = static_cast<int64_t>(it.b) * a.Hq + it.h;
+      const float lse2 = row < a.Nq ? -a.lse[bh * a.Nq + row] * kLog2e : -INFINITY;
+      // D, half a row a thread, while the first products run.
+      ok = mbar_wait(bar(C::B_KFULL + (n + k) % C::NK), ((n + k) / C::NK) & 1, abort_flag, a.status) &&
+           mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      float d = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint32_t at = tile_unit<D>(r, half * (D / 16) + c);
+        const uint4 x = *reinterpret_cast<const uint4*>(smem + C::OFF_K + (n + k) % C::NK * C::TILE + at);
+        const uint4 y = *reinterpret_cast<const uint4*>(smem + C::OFF_DO + at);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack2<BF16>(xw[e]), g = unpack2<BF16>(yw[e]);
+          d = fmaf(f.x, g.x, fmaf(f.y, g.y, d));
+        }
+      }
+      float* sum = reinterpret_cast<float*>(smem + C::OFF_ROWS) + (k & 1) * 256 + r;  // (who writes here again has waited for the item between)
+      sum[half * 128] = d;
+      mbar_arrive(bar(C::B_ROWS));
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_ROWS), k & 1, abort_flag, a.status)))) break;
+      if (threadIdx.x == 0) {
+        fence_proxy_async_smem();  // O is read before its stage is loaded again
+        mbar_arrive(bar(C::B_KEMPTY + (n + k) % C::NK));
+      }
+      const float nd = -(sum[0] + sum[128]);
+      if (half == 0) {
+        pl.lse2[bh * pl.npad + row] = lse2;
+        pl.dvec[bh * pl.npad + row] = nd;
+      }
       const float2 l2 = make_float2(lse2, lse2), nd2 = make_float2(nd, nd);
       for (int p = 0; p < it.npos; ++p, ++n) {
         // (a warp's lanes go on or stop together: what follows wants all of them)
@@ -898,9 +899,13 @@ __global__ void __launch_bounds__(256) attn_window_sum_kernel(const WindowArgs a
 }
 
 // Which tiles are cut, and into how many runs.  One CTA to an SM and tiles of about
-// equal length: the SMs that the last round of whole tiles would leave without one
-// get runs of its tiles instead (of two visits or more), and the tiles with sinks,
-// longer by the ratio of sequence to window, come last in runs of that length.
+// equal length: the last round of whole tiles, which would leave SMs without one, goes
+// out in runs instead, and the tiles with sinks, longer by the ratio of sequence to
+// window, come last in runs about as long.  A run costs its partial tiles and as much
+// time as two visits, and with the first of them the sum kernel costs as much as four:
+// below a gain of kCutGain visits tiles stay whole.
+constexpr int kCutGain = 8;
+
 void plan_runs(const WindowArgs& a, int sms, WbPlan* p) {
   const int64_t G = a.Hq / a.Hk, heads = static_cast<int64_t>(a.B) * a.Hk, ntq = (a.Nq + 127) / 128;
   const int64_t near = std::min<int64_t>(ntq, (static_cast<int64_t>(a.window) + 126) / 128 + 1);
@@ -909,23 +914,24 @@ void plan_runs(const WindowArgs& a, int sms, WbPlan* p) {
   p->sink_tiles = std::min(p->tiles, (a.sinks + 127) / 128);
   const int64_t w_tiles = heads * (p->tiles - p->sink_tiles), s_tiles = heads * p->sink_tiles;
   int64_t cut = w_tiles % sms, runs = 1;
-  if (cut) runs = std::min({(2 * sms + cut - 1) / cut, (vw + 1) / 2, int64_t{16}});
-  if (runs < 2 || w_tiles >= int64_t{16} * sms) cut = 0, runs = 1;
+  if (cut) runs = std::min({sms / cut, (vw + 1) / 2, int64_t{16}});
+  if (vw - (vw + runs - 1) / runs < kCutGain || w_tiles >= int64_t{16} * sms) cut = 0, runs = 1;
   p->whole = static_cast<int>(w_tiles - cut);
   p->cut = static_cast<int>(cut);
   p->runs = static_cast<int>(runs);
   // (no more than about 8 runs of sinks to an SM)
-  const int64_t len = std::max({(vw + 2) / 3, s_tiles * vs / (8 * static_cast<int64_t>(sms)), int64_t{2}});
-  p->sink_runs = p->sink_tiles ? static_cast<int>((vs + len - 1) / len) : 1;
+  const int64_t len = std::max({(vw + 2) / 3, s_tiles * vs / (8 * static_cast<int64_t>(sms)), int64_t{kCutGain} / 2});
+  p->sink_runs = p->sink_tiles && vs - vw >= kCutGain ? static_cast<int>((vs + len - 1) / len) : 1;
 }
 
 template <int D, bool BF16>
 int launch_t(const WindowArgs& a, int* launches) {
   using Q = DqCfg<D>;
   using K = DkvCfg<D>;
-  CUtensorMap mq, mk, mv, mdo;
+  CUtensorMap mq, mk, mv, mdo, mo;
   if (!encode_strided_map(&mq, a.q, a.B, a.Hq, a.Nq, D, Q::CH, BF16) || !encode_strided_map(&mk, a.k, a.B, a.Hk, a.Nk, D, Q::CH, BF16) ||
-      !encode_strided_map(&mv, a.v, a.B, a.Hk, a.Nk, D, Q::CH, BF16) || !encode_strided_map(&mdo, a.dO, a.B, a.Hq, a.Nq, D, Q::CH, BF16))
+      !encode_strided_map(&mv, a.v, a.B, a.Hk, a.Nk, D, Q::CH, BF16) || !encode_strided_map(&mdo, a.dO, a.B, a.Hq, a.Nq, D, Q::CH, BF16) ||
+      !encode_strided_map(&mo, a.o, a.B, a.Hq, a.Nq, D, Q::CH, BF16))
     return kStatusCuda;
   auto kq = attn_window_dq_kernel<D, BF16>;
   auto kk = attn_window_dkv_kernel<D, BF16>;
@@ -954,8 +960,8 @@ int launch_t(const WindowArgs& a, int* launches) {
   p.part = reinterpret_cast<float*>(at + 2 * vec_bytes);
   *launches = split ? 3 : 2;
   const int group = order_head_group(static_cast<int>(bh), int64_t{4} * a.Nk * D, int64_t{128} << 20);
-  bool ok = launch_serialized(true, kq, dim3(static_cast<unsigned>(bh * nrows)), dim3(Q::THREADS), Q::SMEM, a.stream, mq, mk, mv, mdo, a, p,
-                              nrows, group) == cudaSuccess;
+  bool ok = launch_serialized(true, kq, dim3(static_cast<unsigned>(bh * nrows)), dim3(Q::THREADS), Q::SMEM, a.stream, mq, mk, mv, mdo, mo, a,
+                              p, nrows, group) == cudaSuccess;
   ok = ok && launch_serialized(true, kk, dim3(static_cast<unsigned>(items)), dim3(K::THREADS), K::SMEM, a.stream, mq, mk, mv, mdo, a, p) ==
                  cudaSuccess;
   if (split) {
