@@ -312,7 +312,7 @@ typedef struct {
  *          tokens' rows, token_start[B] the number of all.
  *   slots : out, [rows] int64, or NULL: page * page_size + slot in the page of
  *          each new token; -1 for rows from token_start[B] on.
- *   rows : the most new tokens that the step may have.
+ *   rows : the most new tokens that the step may have; rows and free_cap at most 2^30.
  *   window, sinks : 0, 0, or those of attn_paged_decode_window.  A sequence then
  *          holds F = ceil(sinks / page_size) pages of sinks and
  *          R = ceil((window - 1) / page_size) + 1 others at most: entry j >= F + R
@@ -460,16 +460,20 @@ int attn_fwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_
  * The gradients of attn_fwd_window's output for the same window, sinks and scale
  * (o and lse from that call), as attn_bwd's; dk and dv are the sums over the
  * query heads that share a key/value head, and 0 for keys that no query sees.
- * Scratch from cudaMallocAsync on `stream`, freed on it: an fp32 dQ accumulator
- * [B, q_heads, Nq, d], two fp32 row vectors, and fp32 partial tiles of dK and dV
- * where a tile of keys has many more queries than others (the sinks) or there are
- * few of them.  As in attn_bwd, dQ's sums have no fixed order.  Launches at most 3
- * kernels.
+ * A call repeats bit for bit.
+ *   workspace : attn_bwd_window_workspace() bytes of device memory, 16-byte aligned,
+ *          the call's own until it is done: two fp32 row vectors, and fp32 partial
+ *          tiles of dK and dV where a tile of keys has many more queries than others
+ *          (the sinks) or there are few of them.
+ * Launches 2 or 3 kernels.
  */
 int attn_bwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o,
                     const attn_bhnd_t* dO, const float* lse, const attn_bhnd_t* dq, const attn_bhnd_t* dk,
                     const attn_bhnd_t* dv, int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks,
-                    float scale, int type, void* stream);
+                    float scale, int type, void* workspace, void* stream);
+
+/* Bytes of workspace (0 for sizes that the call rejects).  They depend on the sizes only. */
+long long attn_bwd_window_workspace(int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks);
 
 /*
  * attn_bwd without any memory allocation (bf16).  The pages have no

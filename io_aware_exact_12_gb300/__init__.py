@@ -109,7 +109,9 @@ def lib() -> ctypes.CDLL:
         L.attn_paged_decode_window.argtypes = [P, P, I, P, P, I, I, F, I, P, P]
         L.attn_paged_assign.argtypes = [P, P, P, P, I, P, P, P, P, I, I, I, P, P]
         L.attn_fwd_window.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P]
-        L.attn_bwd_window.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P]
+        L.attn_bwd_window.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P, P]
+        L.attn_bwd_window_workspace.argtypes = [I, I, I, I, I, I, I, I]
+        L.attn_bwd_window_workspace.restype = ctypes.c_longlong
         for f in (L.attn_paged_append, L.attn_paged_decode, L.attn_paged_select, L.attn_paged_decode_window,
                   L.attn_paged_assign, L.attn_fwd_window, L.attn_bwd_window):
             f.restype = I

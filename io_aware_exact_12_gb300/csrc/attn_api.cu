@@ -740,7 +740,7 @@ int paged_assign_entry(const attn_paged_kv_t* c, const int* n_new, const int* le
   if (rc) return rc;
   if (!n_new || !free_pages || !free_state || !token_start || !workspace || free_cap < 1 || rows < 0 || window < 0 || sinks < 0)
     return kStatusInvalid;
-  if (window > (1 << 30) || sinks > (1 << 30) || rows > (1 << 30)) return kStatusUnsupported;
+  if (window > (1 << 30) || sinks > (1 << 30) || rows > (1 << 30) || free_cap > (1 << 30)) return kStatusUnsupported;
   for (const void* p : {static_cast<const void*>(n_new), static_cast<const void*>(lens), static_cast<const void*>(free_pages),
                         static_cast<const void*>(free_state), static_cast<const void*>(free_out), static_cast<const void*>(token_start)})
     if (reinterpret_cast<uintptr_t>(p) & 3u) return kStatusInvalid;
@@ -862,13 +862,22 @@ int window_sizes(int B, int Hq, int Hk, int Nq, int Nk, int d, int window, int s
   return type == kTypeBf16 || type == kTypeF16 ? kStatusOk : kStatusInvalid;
 }
 
+void set_window_sizes(WindowArgs* a, int B, int Hq, int Hk, int Nq, int Nk, int d, int window, int sinks) {
+  a->B = B, a->Hq = Hq, a->Hk = Hk, a->Nq = Nq, a->Nk = Nk, a->d = d;
+  a->window = std::min(window, Nk);
+  a->sinks = std::min(sinks, Nk);
+}
+
 int window_entry(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o, const attn_bhnd_t* dO,
                  float* lse, const attn_bhnd_t* dq, const attn_bhnd_t* dk, const attn_bhnd_t* dv, int B, int Hq, int Hk, int Nq,
-                 int Nk, int d, int window, int sinks, float scale, int type, void* stream, bool backward) {
+                 int Nk, int d, int window, int sinks, float scale, int type, void* workspace, void* stream, bool backward) {
   int rc = window_sizes(B, Hq, Hk, Nq, Nk, d, window, sinks, scale, type);
   if (rc) return rc;
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u)) return kStatusInvalid;
   WindowArgs a = {};
+  set_window_sizes(&a, B, Hq, Hk, Nq, Nk, d, window, sinks);
+  const Span ws = {workspace, backward ? static_cast<size_t>(window_bwd_workspace(a)) : 0};
+  if (backward && (!workspace || !aligned16(workspace))) return kStatusInvalid;
   Strided s[8];
   struct {
     const attn_bhnd_t* t;
@@ -881,6 +890,7 @@ int window_entry(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* 
   const Span ls = {lse, static_cast<size_t>(B) * Hq * Nq * 4};
   for (int i = 0; i < n; ++i) {
     if ((i >= first_out || !backward) && any_overlap(s[i].span, {ls})) return kStatusInvalid;
+    if (backward && any_overlap(ws, {s[i].span, ls})) return kStatusInvalid;
     for (int j = 0; j < i && i >= first_out; ++j)
       if (!apart(s[i], s[j])) return kStatusInvalid;
   }
@@ -888,9 +898,7 @@ int window_entry(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* 
   if ((rc = current_device(&dev))) return rc;
   if (!(a.status = status_ptr(dev))) return kStatusCuda;
   a.lse = lse;
-  a.B = B, a.Hq = Hq, a.Hk = Hk, a.Nq = Nq, a.Nk = Nk, a.d = d;
-  a.window = std::min(window, Nk);
-  a.sinks = std::min(sinks, Nk);
+  a.ws = static_cast<uint8_t*>(workspace);
   a.scale = scale;
   a.sl2 = std::fabs(scale) * 1.4426950408889634f;
   a.negate = scale < 0.f ? 1 : 0;
@@ -911,15 +919,22 @@ int attn_fwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_
                     int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks, float scale, int type,
                     void* stream) {
   return attn::window_entry(q, k, v, o, nullptr, lse, nullptr, nullptr, nullptr, B, q_heads, kv_heads, Nq, Nk, d, window,
-                            sinks, scale, type, stream, false);
+                            sinks, scale, type, nullptr, stream, false);
 }
 
 int attn_bwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o,
                     const attn_bhnd_t* dO, const float* lse, const attn_bhnd_t* dq, const attn_bhnd_t* dk,
                     const attn_bhnd_t* dv, int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks,
-                    float scale, int type, void* stream) {
+                    float scale, int type, void* workspace, void* stream) {
   return attn::window_entry(q, k, v, o, dO, const_cast<float*>(lse), dq, dk, dv, B, q_heads, kv_heads, Nq, Nk, d, window,
-                            sinks, scale, type, stream, true);
+                            sinks, scale, type, workspace, stream, true);
+}
+
+long long attn_bwd_window_workspace(int B, int q_heads, int kv_heads, int Nq, int Nk, int d, int window, int sinks) {
+  if (attn::window_sizes(B, q_heads, kv_heads, Nq, Nk, d, window, sinks, 1.f, ATTN_TYPE_BF16)) return 0;
+  attn::WindowArgs a = {};
+  attn::set_window_sizes(&a, B, q_heads, kv_heads, Nq, Nk, d, window, sinks);
+  return attn::window_bwd_workspace(a);
 }
 
 int attn_paged_append(const attn_paged_kv_t* kv, const attn_rows_t* k, const attn_rows_t* v, const attn_rows_t* q,

@@ -66,6 +66,7 @@ struct PagedDecodeArgs {
   const int* pages;  // [B][H][n_pages] page indices of the sequence, or null: all pages
   int n_pages;
   int window = 0, sinks = 0;  // window > 0: the last `window` tokens and the first `sinks` ones (pages is null)
+  int box_shift = 0;          // log2 of the keys of a box; the launcher's
   float sl2;  // scale * k_scale * log2(e), signed
   int x_type;
   cudaStream_t stream;
@@ -98,6 +99,7 @@ struct PagedAssignArgs {
   int64_t* slots;         // [rows], or null
   int rows;
   int first, turns;  // pages of sinks, pages in turns behind them (0: no window)
+  uint32_t page_mul, page_shift;  // division by the page size; the launcher's
   cudaStream_t stream;
   uint8_t* ws;
 };

@@ -174,20 +174,20 @@ __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kPdWarps) : "memory");
 }
 
-// The tiles of a windowed sequence (WIN): those with sinks before the window, then
-// those from the window's first token on.  Tile t of them is key tile
-// t < sinks ? t : t + skip.
-template <int TK>
-struct WindowTiles {
-  int start, sinks, skip, n;  // the window's first token, tiles of sinks, tiles left out behind them, tiles in all
-  __device__ __forceinline__ WindowTiles(const PagedDecodeArgs& a, int len) {
+// The boxes of a windowed sequence (WIN): those with sinks before the window, then
+// those from the window's first token on, packed into tiles one after the other.  The
+// v-th of them is the sequence's box v < sinks ? v : v + skip.
+struct WindowBoxes {
+  int start, sinks, skip, n;  // the window's first token, boxes of sinks, boxes left out behind them, boxes in all
+  __device__ __forceinline__ WindowBoxes(const PagedDecodeArgs& a, int len) {
+    const int up = (1 << a.box_shift) - 1;
     start = max(0, len - a.window);
-    const int first = start / TK;  // a sink in the window's first tile is seen there
-    sinks = min(first, (min(a.sinks, start) + TK - 1) / TK);
+    const int first = start >> a.box_shift;  // a sink in the window's first box is seen there
+    sinks = min(first, (min(a.sinks, start) + up) >> a.box_shift);
     skip = first - sinks;
-    n = (len + TK - 1) / TK - skip;
+    n = ((len + up) >> a.box_shift) - skip;
   }
-  __device__ __forceinline__ int key_tile(int t) const { return t < sinks ? t : t + skip; }
+  __device__ __forceinline__ int box(int v) const { return v < sinks ? v : v + skip; }
 };
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; }
@@ -195,7 +195,7 @@ __device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n
 template <int TK, bool WIN>
 __device__ __forceinline__ int tiles_of(const PagedDecodeArgs& a, int len) {
   if (len <= 0) return 0;
-  if constexpr (WIN) return WindowTiles<TK>(a, len).n;
+  if constexpr (WIN) return ((WindowBoxes(a, len).n << a.box_shift) + TK - 1) / TK;
   // A list without repetitions has no more entries than the sequence has pages.
   return ((a.pages ? min(a.n_pages, (len + a.kv.page - 1) / a.kv.page) * a.kv.page : len) + TK - 1) / TK;
 }
@@ -386,14 +386,16 @@ __global__ void __launch_bounds__(kPdThreads, (PdCfg<C, D, NT>::MINB))
       int id = -1, h = 0, row = 0, seen = 0;
       uint64_t bits = 0;  // WIN: visible keys of the box
       if (WIN && live) {
-        const WindowTiles<TK> wt(a, mine.len);
-        const int key = wt.key_tile(t) * TK + box * box_rows;
-        const int j = key / kv.page;
-        row = key - j * kv.page;
-        h = mine.hr / RT;
-        bits = low_bits(min(box_rows, mine.len - key)) & (~low_bits(wt.start - key) | low_bits(a.sinks - key));
-        // (a box without a visible key may lie in a page that the sequence no longer has)
-        if (bits && (id = checked_page(kv, mine.b, j)) < 0) bits = 0;
+        const WindowBoxes wb(a, mine.len);
+        const int v = t * nb + box;
+        if (v < wb.n) {
+          const int key = wb.box(v) * box_rows, j = key / kv.page;
+          row = key - j * kv.page;
+          h = mine.hr / RT;
+          bits = low_bits(min(box_rows, mine.len - key)) & (~low_bits(wb.start - key) | low_bits(a.sinks - key));
+          // (a box without a visible key may lie in a page that the sequence no longer has)
+          if (bits && (id = checked_page(kv, mine.b, j)) < 0) bits = 0;
+        }
       } else if (live) {
         const int key = t * TK + box * box_rows;
         const int e = key / kv.page;
@@ -1024,7 +1026,8 @@ cudaError_t launch_clusters(Kernel kern, int ctas, int cluster, size_t smem, cud
 }
 
 template <int X, int C, int D, int NT, bool WIN>
-int launch_t(const PagedDecodeArgs& a, int* launches) {
+int launch_t(const PagedDecodeArgs& args, int* launches) {
+  PagedDecodeArgs a = args;
   using F = PdCfg<C, D, NT>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
@@ -1037,6 +1040,7 @@ int launch_t(const PagedDecodeArgs& a, int* launches) {
   const int RT = row_tiles(a.Hq, a.kv.H);
   int box = 8;
   while (box < F::TK && a.kv.page % (2 * box) == 0) box *= 2;
+  while ((1 << a.box_shift) < box) ++a.box_shift;
   CUtensorMap mk, mv;
   if (!encode_pages_map(&mk, a.kv.k, F::ROW, a.kv.page, a.kv.H, a.kv.num_pages, a.kv.k_tok, a.kv.k_head, a.kv.k_page, F::RBX,
                         box) ||

@@ -30,6 +30,7 @@ struct WindowArgs {
   bool bf16;
   cudaStream_t stream;
   int* status;
+  uint8_t* ws;          // backward only: window_bwd_workspace() bytes
 };
 
 // 4-D tiled map of a [B][heads][N][d] tensor: dims (d, N, heads, B), box
@@ -38,5 +39,6 @@ bool encode_strided_map(CUtensorMap* map, const Bhnd& t, int B, int heads, int N
 
 int launch_window_fwd(const WindowArgs& a, int* launches);
 int launch_window_bwd(const WindowArgs& a, int* launches);
+int64_t window_bwd_workspace(const WindowArgs& a);  // from the sizes alone
 
 }  // namespace attn

@@ -906,7 +906,8 @@ __global__ void __launch_bounds__(256) attn_window_sum_kernel(const WindowArgs a
 // below a gain of kCutGain visits tiles stay whole.
 constexpr int kCutGain = 8;
 
-void plan_runs(const WindowArgs& a, int sms, WbPlan* p) {
+void plan_runs(const WindowArgs& a, WbPlan* p) {
+  const int64_t sms = 152;  // of the GPU this is for; with others the plan is as good as right
   const int64_t G = a.Hq / a.Hk, heads = static_cast<int64_t>(a.B) * a.Hk, ntq = (a.Nq + 127) / 128;
   const int64_t near = std::min<int64_t>(ntq, (static_cast<int64_t>(a.window) + 126) / 128 + 1);
   const int64_t vs = G * ntq, vw = G * near;  // visits of a tile, at most
@@ -920,8 +921,16 @@ void plan_runs(const WindowArgs& a, int sms, WbPlan* p) {
   p->cut = static_cast<int>(cut);
   p->runs = static_cast<int>(runs);
   // (no more than about 8 runs of sinks to an SM)
-  const int64_t len = std::max({(vw + 2) / 3, s_tiles * vs / (8 * static_cast<int64_t>(sms)), int64_t{kCutGain} / 2});
+  const int64_t len = std::max({(vw + 2) / 3, s_tiles * vs / (8 * sms), int64_t{kCutGain} / 2});
   p->sink_runs = p->sink_tiles && vs - vw >= kCutGain ? static_cast<int>((vs + len - 1) / len) : 1;
+}
+
+// The plan but for its pointers; returns the number of partial tiles.
+int64_t plan(const WindowArgs& a, WbPlan* p) {
+  plan_runs(a, p);
+  p->npad = (a.Nq + 127) / 128 * 128;
+  return (p->runs > 1 ? static_cast<int64_t>(p->cut) * p->runs : 0) +
+         (p->sink_runs > 1 ? static_cast<int64_t>(a.B) * a.Hk * p->sink_tiles * p->sink_runs : 0);
 }
 
 template <int D, bool BF16>
@@ -939,25 +948,16 @@ int launch_t(const WindowArgs& a, int* launches) {
     return kStatusCuda;
   if (!check_launch_regs(reinterpret_cast<const void*>(kq), Q::REGS) || !check_launch_regs(reinterpret_cast<const void*>(kk), K::REGS))
     return kStatusDeviceCheck;  // the splits' sums
-  const int sms = device_sm_count();
-  if (sms < 1) return kStatusCuda;
   WbPlan p = {};
-  plan_runs(a, sms, &p);
-  const int nrows = (a.Nq + 127) / 128;
-  const int64_t heads = static_cast<int64_t>(a.B) * a.Hk, bh = static_cast<int64_t>(a.B) * a.Hq, rows = bh * nrows * 128;
-  const int64_t cut_items = static_cast<int64_t>(p.cut) * p.runs, sink_items = heads * p.sink_tiles * p.sink_runs;
-  const int64_t items = p.whole + cut_items + sink_items;
+  const int64_t split = plan(a, &p);
+  const int nrows = p.npad / 128;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hk, bh = static_cast<int64_t>(a.B) * a.Hq;
+  const int64_t items = p.whole + static_cast<int64_t>(p.cut) * p.runs + heads * p.sink_tiles * p.sink_runs;
   if (items > 0x7fffffff || bh * nrows > 0x7fffffff) return kStatusUnsupported;
-  p.npad = nrows * 128;
   p.group = order_head_group(static_cast<int>(heads), int64_t{4} * a.Nq * D * (a.Hq / a.Hk), int64_t{64} << 20);
-  const int64_t split = (p.runs > 1 ? cut_items : 0) + (p.sink_runs > 1 ? sink_items : 0);
-  const int64_t vec_bytes = rows * 4;  // whole tiles: a multiple of 512
-  void* ws = nullptr;
-  if (cudaMallocAsync(&ws, 2 * vec_bytes + split * 2 * 128 * D * 4, a.stream) != cudaSuccess) return kStatusCuda;
-  uint8_t* at = static_cast<uint8_t*>(ws);
-  p.lse2 = reinterpret_cast<float*>(at);
-  p.dvec = reinterpret_cast<float*>(at + vec_bytes);
-  p.part = reinterpret_cast<float*>(at + 2 * vec_bytes);
+  p.lse2 = reinterpret_cast<float*>(a.ws);
+  p.dvec = p.lse2 + bh * p.npad;
+  p.part = p.dvec + bh * p.npad;
   *launches = split ? 3 : 2;
   const int group = order_head_group(static_cast<int>(bh), int64_t{4} * a.Nk * D, int64_t{128} << 20);
   bool ok = launch_serialized(true, kq, dim3(static_cast<unsigned>(bh * nrows)), dim3(Q::THREADS), Q::SMEM, a.stream, mq, mk, mv, mdo, mo, a,
@@ -966,10 +966,9 @@ int launch_t(const WindowArgs& a, int* launches) {
                  cudaSuccess;
   if (split) {
     const int64_t tiles = (p.runs > 1 ? p.cut : 0) + (p.sink_runs > 1 ? heads * p.sink_tiles : 0);
-    ok = ok && launch_serialized(true, attn_window_sum_kernel<D, BF16>, dim3(static_cast<unsigned>(std::min<int64_t>(tiles * D / 8, 16 * sms))),
+    ok = ok && launch_serialized(true, attn_window_sum_kernel<D, BF16>, dim3(static_cast<unsigned>(std::min<int64_t>(tiles * D / 8, 16 * 152))),
                                  dim3(256), 0, a.stream, a, p) == cudaSuccess;
   }
-  ok = cudaFreeAsync(ws, a.stream) == cudaSuccess && ok;
   return ok && cudaGetLastError() == cudaSuccess ? kStatusOk : kStatusCuda;
 }
 
@@ -979,6 +978,12 @@ int launch_d(const WindowArgs& a, int* launches) {
 }
 
 }  // namespace
+
+int64_t window_bwd_workspace(const WindowArgs& a) {
+  WbPlan p = {};
+  const int64_t split = plan(a, &p);
+  return 2 * static_cast<int64_t>(a.B) * a.Hq * p.npad * 4 + split * 2 * 128 * a.d * 4;
+}
 
 int launch_window_bwd(const WindowArgs& a, int* launches) {
   return a.d == 32 ? launch_d<32>(a, launches) : a.d == 64 ? launch_d<64>(a, launches) : launch_d<128>(a, launches);

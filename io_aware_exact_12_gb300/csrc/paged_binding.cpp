@@ -535,11 +535,12 @@ PyObject* bwd_window(PyObject*, PyObject* const* arg, Py_ssize_t nargs) {
       if (!t || !same_sizes(names[i], *t, like, i ? "k" : "q")) return nullptr;
     }
   }
+  const c10::DataPtr ws = scratch(attn_bwd_window_workspace(w.B, w.Hq, w.Hk, w.Nq, w.Nk, w.d, w.window, w.sinks));
   void* stream = c10::cuda::getCurrentCUDAStream(w.q->get_device()).stream();
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = attn_bwd_window(&w.rq, &w.rk, &w.rv, &ro, &rdo, static_cast<const float*>(lse->data_ptr()), &rd[0], &rd[1], &rd[2], w.B, w.Hq,
-                       w.Hk, w.Nq, w.Nk, w.d, w.window, w.sinks, static_cast<float>(w.scale), w.type, stream);
+                       w.Hk, w.Nq, w.Nk, w.d, w.window, w.sinks, static_cast<float>(w.scale), w.type, ws.get(), stream);
   Py_END_ALLOW_THREADS
   return rc ? PyLong_FromLong(rc) : outputs(arg + 9, made, 3);
   END_HANDLE_TH_ERRORS

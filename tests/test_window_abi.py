@@ -27,9 +27,9 @@ def _fwd(pkg, q=None, k=None, v=None, o=None, lse=LSE, B=2, Hq=4, Hk=2, nq=16, n
                                      sinks, scale, type, None)
 
 
-def _bwd(pkg, o=None, do=None, lse=LSE, dq=None, dk=None, dv=None, window=8, **kw):
+def _bwd(pkg, o=None, do=None, lse=LSE, dq=None, dk=None, dv=None, window=8, ws=WS):
     return pkg.lib().attn_bwd_window(_t(pkg, Q, 4, 16), _t(pkg, K, 2, 32), _t(pkg, V, 2, 32), o or _t(pkg, O, 4, 16), do or _t(pkg, DO, 4, 16), lse,
-                                     dq or _t(pkg, DQ, 4, 16), dk or _t(pkg, DK, 2, 32), dv or _t(pkg, DV, 2, 32), 2, 4, 2, 16, 32, 64, window, 1, 0.1, 0, None)
+                                     dq or _t(pkg, DQ, 4, 16), dk or _t(pkg, DK, 2, 32), dv or _t(pkg, DV, 2, 32), 2, 4, 2, 16, 32, 64, window, 1, 0.1, 0, ws, None)
 
 
 def _past_checks(rc):
@@ -55,6 +55,16 @@ def test_sizes(pkg):
         assert _fwd(pkg, **kw) == 2, kw
 
 
+def test_backward_workspace(pkg):
+    need = pkg.lib().attn_bwd_window_workspace
+    good = (2, 4, 2, 16, 32, 64, 8, 1)
+    assert need(*good) >= 2 * 2 * 4 * 128 * 4
+    for at, bad in ((0, 0), (1, 3), (2, 0), (3, 0), (4, 8), (5, 48), (6, 0), (7, -1), (0, 20000)):
+        assert need(*(bad if i == at else x for i, x in enumerate(good))) == 0, (at, bad)
+    # two row vectors, runs of sinks (8 to an SM) and of cut tiles (16 to each of fewer than 152) at most, however long the sequence
+    assert need(1, 1, 1, 1 << 24, 1 << 24, 128, 128, 4) <= 2 * (1 << 24) * 4 + (8 * 152 + 1 + 16 * 152) * 2 * 128 * 128 * 4
+
+
 def test_tensors(pkg):
     for name, heads, n in (("q", 4, 16), ("k", 2, 32), ("v", 2, 32), ("o", 4, 16)):
         p = {"q": Q, "k": K, "v": V, "o": O}[name]
@@ -75,6 +85,8 @@ def test_overlaps(pkg):
     assert _bwd(pkg, dk=_t(pkg, DV, 2, 32)) == 1
     assert _bwd(pkg, dv=_t(pkg, DO, 2, 32)) == 1
     assert _bwd(pkg, dq=_t(pkg, LSE, 4, 16)) == 1
+    for ws in (None, WS + 8, Q, LSE, DK, DO):
+        assert _bwd(pkg, ws=ws) == 1, ws
     # slices of one buffer side by side are apart, unless they reach into one another
     row = 10 * 64
     s = lambda at, heads, n=32: _t(pkg, TABLE + at * 128, heads, n, batch=n * row, head=64, row=row)  # noqa: E731
@@ -121,7 +133,7 @@ def test_assign(pkg):
                dict(n_new=NEW + 2), dict(lens=OLD + 1), dict(ring=RING + 2), dict(state=STATE + 1), dict(out=STATE2 + 2), dict(start=START + 2), dict(slots=SLOTS + 4),
                dict(ws=WS + 4), dict(block_table=None), dict(seq_lens=None)):
         assert _assign(pkg, **kw) == 1, kw
-    for kw in (dict(window=(1 << 30) + 1), dict(sinks=(1 << 30) + 1), dict(rows=(1 << 30) + 1)):
+    for kw in (dict(window=(1 << 30) + 1), dict(sinks=(1 << 30) + 1), dict(rows=(1 << 30) + 1), dict(cap=(1 << 30) + 1)):
         assert _assign(pkg, **kw) == 2, kw
     # overlaps: what is written with what is read, or with what else is written
     for kw in (dict(n_new=LENS), dict(n_new=TABLE), dict(lens=LENS + 4), dict(ring=NEW), dict(ring=OLD), dict(out=STATE + 4), dict(out=NEW), dict(start=NEW), dict(slots=START),
