@@ -36,7 +36,7 @@ namespace {
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kNarrow = 32;  // keys of a tile with a few sinks
 
-template <int D, int NQ>
+template <int D>
 struct WfCfg {
   static constexpr int ROWB = D >= 64 ? 128 : 64;  // bytes of a swizzled row
   static constexpr int CH = ROWB / 2;              // elements of it
@@ -45,8 +45,8 @@ struct WfCfg {
   static constexpr int SBO = 8 * ROWB;
   static constexpr int CHUNK = 128 * ROWB;         // bytes of a chunk of 128 rows
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int NST = NQ == 1 && D == 128 ? 1 : 2;  // K and V stages
-  static constexpr int OFF_K = NQ * TILE;
+  static constexpr int NST = D == 128 ? 1 : 2;  // K and V stages
+  static constexpr int OFF_K = TILE;
   static constexpr int OFF_V = OFF_K + NST * TILE;
   static constexpr int OFF_BAR = OFF_V + NST * TILE;
   static constexpr int B_Q = 0;
@@ -55,11 +55,11 @@ struct WfCfg {
   static constexpr int B_KEMPTY = B_KFULL + NST;
   static constexpr int B_VFULL = B_KEMPTY + NST;
   static constexpr int B_VEMPTY = B_VFULL + NST;
-  static constexpr int B_S = B_VEMPTY + NST;  // S_q is in TMEM
-  static constexpr int B_P = B_S + 2;         // P_q is in TMEM
-  static constexpr int B_O = B_P + 2;         // P_q V is complete
-  static constexpr int B_TAKEN = B_O + 2;     // S_q is in registers (P apart)
-  static constexpr int B_NEXT = B_TAKEN + 2;   // the next item is known
+  static constexpr int B_S = B_VEMPTY + NST;  // S is in TMEM
+  static constexpr int B_P = B_S + 1;         // P is in TMEM
+  static constexpr int B_O = B_P + 1;         // P V is complete
+  static constexpr int B_TAKEN = B_O + 1;     // S is in registers (P apart)
+  static constexpr int B_NEXT = B_TAKEN + 1;   // the next item is known
   static constexpr int B_READ = B_NEXT + 2;    // and read by all
   static constexpr int B_DONE = B_READ + 2;
   static constexpr int NBAR = B_DONE + 1;
@@ -69,21 +69,20 @@ struct WfCfg {
   // Staging of the output at d = 128: half a row for each of a warp's 32.
   static constexpr bool STAGE = D == 128;
   static constexpr int OFF_STAGE = (OFF_ABORT + 4 + 15) & ~15;
-  static constexpr int SMEM = OFF_STAGE + (STAGE ? NQ * 4 * 32 * 128 : 0);
-  static constexpr int THREADS = 128 * NQ + 128;
-  static constexpr int W_LOAD = 4 * NQ, W_MMA = 4 * NQ + 1;  // warps
-  static constexpr int CTAS = 3 - NQ;                        // per SM
+  static constexpr int SMEM = OFF_STAGE + (STAGE ? 4 * 32 * 128 : 0);
+  static constexpr int THREADS = 256;
+  static constexpr int W_LOAD = 4, W_MMA = 5;  // warps
+  static constexpr int CTAS = 2;                // per SM
   static constexpr int REGS = (65536 / (THREADS * CTAS)) & ~7;
-  static constexpr int REGS_ROW = NQ == 2 ? 224 : 208, REGS_CTRL = NQ == 2 ? 56 : 48;
-  static_assert(NQ * 128 * REGS_ROW + 128 * REGS_CTRL <= THREADS * REGS, "register split");
-  static constexpr uint32_t COLS = NQ == 2 ? 512 : 256;
+  static constexpr int REGS_ROW = 208, REGS_CTRL = 48;
+  static_assert(128 * REGS_ROW + 128 * REGS_CTRL <= THREADS * REGS, "register split");
+  static constexpr uint32_t COLS = 256;
   // P has TMEM columns of its own at d <= 64: the next S can then be formed while
   // P V is pending.  At d = 128 the columns are full and P lies over half of S.
   static constexpr bool APART = D <= 64;
-  static constexpr uint32_t T_O = NQ * 128;                        // + D q
-  static constexpr uint32_t T_P = APART ? NQ * 128 + NQ * D : 0;   // + T_PSTEP q
-  static constexpr uint32_t T_PSTEP = APART ? 64 : 128;
-  static_assert(NQ * 128 + NQ * D + (APART ? NQ * 64 : 0) <= COLS, "TMEM");
+  static constexpr uint32_t T_O = 128;
+  static constexpr uint32_t T_P = APART ? 128 + D : 0;
+  static_assert(128 + D + (APART ? 64 : 0) <= COLS, "TMEM");
   static_assert(CTAS * (SMEM + 1024) <= 233472, "shared memory");
 };
 
@@ -91,12 +90,12 @@ struct WfCfg {
 // (rows of D channels) and of an MN-major one (16 rows on).
 template <int D>
 __host__ __device__ constexpr uint32_t k_step(int kk) {
-  using C = WfCfg<D, 1>;
+  using C = WfCfg<D>;
   return static_cast<uint32_t>(((kk * 16) / C::CH * C::CHUNK + (kk * 16) % C::CH * 2) >> 4);
 }
 template <int D>
 __host__ __device__ constexpr uint32_t mn_step(int kk) {
-  return static_cast<uint32_t>((kk * 16 * WfCfg<D, 1>::ROWB) >> 4);
+  return static_cast<uint32_t>((kk * 16 * WfCfg<D>::ROWB) >> 4);
 }
 
 // Byte offset of 16-byte unit u of a row of 128 bytes in the output's staging
@@ -110,16 +109,16 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     if (global_timer_ns() - t0 > kWaitLimitNs) return;
 }
 
-// A block's item: 128 query rows of NQ heads, and the list of key tiles they see.
+// A block's item: 128 query rows of a head, and the list of key tiles they see.
 struct WfItem {
-  int row0, b, h0, hk;  // first row, sequence, first query head, key/value head
+  int row0, b, h, hk;   // first row, sequence, query head, key/value head
   int ns, skip, npos;   // tiles of sinks, tiles left out behind them, tiles in all
-  __device__ __forceinline__ WfItem(const WindowArgs& a, int item, int nrows, int nheads, int nq, int group) {
+  __device__ __forceinline__ WfItem(const WindowArgs& a, int item, int nrows, int group) {
     // Later rows, which under a wide window have more tiles, first.
-    int rank, hb;
-    grouped_rank_order(item, nrows, nheads, group, rank, hb);
+    int rank, bh;
+    grouped_rank_order(item, nrows, a.B * a.Hq, group, rank, bh);
     row0 = (nrows - 1 - rank) * 128;
-    b = hb * nq / a.Hq, h0 = hb * nq - b * a.Hq, hk = h0 / (a.Hq / a.Hk);
+    b = bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
     const int off = a.Nk - a.Nq;
     const int w0 = max(0, row0 + off - a.window + 1) >> 7;
     ns = min(w0, (a.sinks + 127) >> 7);
@@ -131,11 +130,11 @@ struct WfItem {
   __device__ __forceinline__ bool narrow(const WindowArgs& a, int p) const { return p == ns - 1 && a.sinks - p * 128 <= kNarrow; }
 };
 
-template <int D, bool BF16, int NQ>
-__global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
+template <int D, bool BF16>
+__global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
     attn_window_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                           const __grid_constant__ CUtensorMap mv, const WindowArgs a, int nrows, int nheads, int group, int overlap) {
-  using C = WfCfg<D, NQ>;
+                           const __grid_constant__ CUtensorMap mv, const WindowArgs a, int nrows, int group) {
+  using C = WfCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_addr(smem);
@@ -148,25 +147,10 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   const uint32_t sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
   if (warp == C::W_LOAD && lane == 0) {
-    mbar_init(bar(C::B_Q), 1);
-    mbar_init(bar(C::B_QEMPTY), NQ);  // a thread of each query tile
-    for (int s = 0; s < C::NST; ++s) {
-      mbar_init(bar(C::B_KFULL + s), 1);
-      mbar_init(bar(C::B_VFULL + s), 1);
-      mbar_init(bar(C::B_KEMPTY + s), NQ);
-      mbar_init(bar(C::B_VEMPTY + s), NQ);
-    }
-    for (int q = 0; q < 2; ++q) {
-      mbar_init(bar(C::B_S + q), 1);
-      mbar_init(bar(C::B_P + q), 128);
-      mbar_init(bar(C::B_O + q), 1);
-      mbar_init(bar(C::B_TAKEN + q), 128);
-    }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(bar(C::B_NEXT + x), 1);
-      mbar_init(bar(C::B_READ + x), 4 * NQ + 1);  // the softmax warps and the issuer
-    }
-    mbar_init(bar(C::B_DONE), 1);
+    for (int x = 0; x < C::NBAR; ++x) mbar_init(bar(x), 1);
+    mbar_init(bar(C::B_P), 128);
+    mbar_init(bar(C::B_TAKEN), 128);
+    for (int x = 0; x < 2; ++x) mbar_init(bar(C::B_READ + x), 5);  // the softmax warps and the issuer
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(&mq);
@@ -177,10 +161,8 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
     tmem_alloc(smem_addr(slot), C::COLS);
     tmem_relinquish();
   }
-  if (overlap) {  // launched overlapped (launch_serialized): what is above reads no tensor
-    griddep_wait();
-    griddep_launch_dependents();
-  }
+  griddep_wait();  // launched overlapped (launch_serialized): what is above reads no tensor
+  griddep_launch_dependents();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -213,7 +195,7 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
         mbar_arrive_expect_tx(bar(C::B_NEXT + x), 16);
         block_request(next + x * 16, bar(C::B_NEXT + x));
         ++asked;
-        const WfItem it(a, i, nrows, nheads, NQ, group);
+        const WfItem it(a, i, nrows, group);
         for (int p = 0; p < it.npos; ++p) {
           const int s = nk % C::NST, turn = (nk / C::NST - 1) & 1;
           if (nk >= C::NST && !(ok = mbar_wait(bar(C::B_KEMPTY + s), turn, abort_flag, a.status))) break;
@@ -222,8 +204,8 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
           ++nk;
           if (p == 0) {
             if (nq > 0 && !(ok = mbar_wait(bar(C::B_QEMPTY), (nq - 1) & 1, abort_flag, a.status))) break;
-            mbar_arrive_expect_tx(bar(C::B_Q), NQ * C::TILE);
-            for (int q = 0; q < NQ; ++q) load(sbase + q * C::TILE, &mq, bar(C::B_Q), it.row0, it.h0 + q, it.b);
+            mbar_arrive_expect_tx(bar(C::B_Q), C::TILE);
+            load(sbase, &mq, bar(C::B_Q), it.row0, it.h, it.b);
             ++nq;
           }
           if (nv >= C::NST && !(ok = mbar_wait(bar(C::B_VEMPTY + s), turn, abort_flag, a.status))) break;
@@ -243,8 +225,7 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
       }
     } else if (warp == C::W_MMA && lane == 0) {
       // ----------------------------------------------- matrix instructions
-      // A chain S, P V, S, P V, ... for each query tile; whichever next step is
-      // ready goes out.  At d = 128 S(p + 1) is issued right behind the P V(p) whose
+      // A chain S, P V, S, P V, ...; whichever next step is ready goes out.  At d = 128 S(p + 1) is issued right behind the P V(p) whose
       // P it overwrites: one thread's MMAs run in the order of issue.  K and V stages
       // and Q are handed back by the softmax, whose waits tell when the MMAs that read
       // them are complete.  An item's first P V overwrites the O of the one before,
@@ -257,46 +238,41 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
       int n0 = 0;  // positions of the items before
       IdleWatch watch;
       for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
-        const WfItem it(a, i, nrows, nheads, NQ, group);
+        const WfItem it(a, i, nrows, group);
         const int end = n0 + it.npos, thin = it.ns > 0 && it.narrow(a, it.ns - 1) ? n0 + it.ns - 1 : -1;
         ok = mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
-        int js[2] = {n0, n0}, jp[2] = {n0, n0};  // next S and P V of each tile
-        int k_seen = n0, v_seen = n0;            // positions whose loads have been seen to land
-        while (ok && (jp[0] < end || (NQ > 1 && jp[1] < end))) {
+        int js = n0, jp = n0;          // next S and P V
+        int k_seen = n0, v_seen = n0;  // positions whose loads have been seen to land
+        const uint32_t q_lo = smem_desc_lo(sbase, 16);
+        while (ok && jp < end) {
           bool progress = false;
+          const int sv = jp % C::NST;
+          if (jp < js && mbar_probe(bar(C::B_P), jp & 1) && (jp < v_seen || mbar_probe(bar(C::B_VFULL + sv), (jp / C::NST) & 1))) {
+            v_seen = max(v_seen, jp + 1);
+            tc_fence_after_sync();
+            const uint32_t v_lo = smem_desc_lo(sV + sv * C::TILE, C::CHUNK);
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const int jv = jp[q], sv = jv % C::NST;
-            if (jv < js[q] && mbar_probe(bar(C::B_P + q), jv & 1) &&
-                (jv < v_seen || mbar_probe(bar(C::B_VFULL + sv), (jv / C::NST) & 1))) {
-              v_seen = max(v_seen, jv + 1);
-              tc_fence_after_sync();
-              const uint32_t d_o = tmem + C::T_O + q * D, a_p = tmem + C::T_P + q * C::T_PSTEP;
-              const uint32_t v_lo = smem_desc_lo(sV + sv * C::TILE, C::CHUNK);
+            for (int kk = 0; kk < kNarrow / 16; ++kk)
+              mma_ts_w(tmem + C::T_O, tmem + C::T_P + kk * 8, v_lo + mn_step<D>(kk), HI, id_o, (jp > n0 || kk > 0) ? 1u : 0u);
+            if (jp != thin) {
 #pragma unroll
-              for (int kk = 0; kk < kNarrow / 16; ++kk) mma_ts_w(d_o, a_p + kk * 8, v_lo + mn_step<D>(kk), HI, id_o, (jv > n0 || kk > 0) ? 1u : 0u);
-              if (jv != thin) {
-#pragma unroll
-                for (int kk = kNarrow / 16; kk < 8; ++kk) mma_ts_w(d_o, a_p + kk * 8, v_lo + mn_step<D>(kk), HI, id_o, 1u);
-              }
-              tc_commit(bar(C::B_O + q));
-              jp[q] = jv + 1;
-              progress = true;
+              for (int kk = kNarrow / 16; kk < 8; ++kk) mma_ts_w(tmem + C::T_O, tmem + C::T_P + kk * 8, v_lo + mn_step<D>(kk), HI, id_o, 1u);
             }
-            const int jk = js[q], sk = jk % C::NST;
-            if (jk < end && (C::APART ? jk == 0 || mbar_probe(bar(C::B_TAKEN + q), (jk - 1) & 1) : jk == jp[q]) &&
-                (jk < k_seen || mbar_probe(bar(C::B_KFULL + sk), (jk / C::NST) & 1))) {
-              k_seen = max(k_seen, jk + 1);
-              tc_fence_after_sync();
-              const uint32_t d_s = tmem + q * 128, q_lo = smem_desc_lo(sbase + q * C::TILE, 16);
-              const uint32_t k_lo = smem_desc_lo(sK + sk * C::TILE, 16);
-              const uint32_t id = jk == thin ? id_sn : id_s;
+            tc_commit(bar(C::B_O));
+            ++jp;
+            progress = true;
+          }
+          const int sk = js % C::NST;
+          if (js < end && (C::APART ? js == 0 || mbar_probe(bar(C::B_TAKEN), (js - 1) & 1) : js == jp) &&
+              (js < k_seen || mbar_probe(bar(C::B_KFULL + sk), (js / C::NST) & 1))) {
+            k_seen = max(k_seen, js + 1);
+            tc_fence_after_sync();
+            const uint32_t k_lo = smem_desc_lo(sK + sk * C::TILE, 16), id = js == thin ? id_sn : id_s;
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) mma_ss_w(d_s, q_lo + k_step<D>(kk), HI, k_lo + k_step<D>(kk), HI, id, kk > 0 ? 1u : 0u);
-              tc_commit(bar(C::B_S + q));
-              js[q] = jk + 1;
-              progress = true;
-            }
+            for (int kk = 0; kk < D / 16; ++kk) mma_ss_w(tmem, q_lo + k_step<D>(kk), HI, k_lo + k_step<D>(kk), HI, id, kk > 0 ? 1u : 0u);
+            tc_commit(bar(C::B_S));
+            ++js;
+            progress = true;
           }
           if (progress) watch.progress();
           else ok = watch.idle(abort_flag, a.status, kWaitLimitNs);
@@ -313,9 +289,9 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
   } else {
     // --------------------------------------------------------------- softmax
     regs_increase<C::REGS_ROW>();
-    const int q = warp >> 2, r = threadIdx.x & 127;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + q * 128, tO = tmem + lanes + C::T_O + q * D, tP = tmem + lanes + C::T_P + q * C::T_PSTEP;
+    const int r = threadIdx.x;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tS = tmem + lanes, tO = tmem + lanes + C::T_O, tP = tmem + lanes + C::T_P;
     const float sl2 = fmaxf(a.sl2, FLT_MIN);  // a scale of 0: hidden keys are -inf, and that times 0 is NaN
     const float2 sl2x2 = make_float2(sl2, sl2);
     const int off = a.Nk - a.Nq, wnd = a.window, nsk = a.sinks;
@@ -325,14 +301,14 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
     bool ok = true;
     int n = 0;
     for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
-      const WfItem it(a, i, nrows, nheads, NQ, group);
+      const WfItem it(a, i, nrows, group);
       const int row = it.row0 + r;
       float m = -INFINITY, l_exact = 0.f, l_round = 0.f;
       // A position with W of its tile's keys.
       auto step = [&](int p, auto width) {
         constexpr int W = decltype(width)::value;
         // (a warp's lanes go on or stop together: they vote below)
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_S + q), n & 1, abort_flag, a.status)))) return;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_S), n & 1, abort_flag, a.status)))) return;
         tc_fence_after_sync();
         if (r == 0) {
           mbar_arrive(bar(C::B_KEMPTY + n % C::NST));
@@ -356,7 +332,7 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
         }
         if constexpr (C::APART) {
           tc_fence_before_sync();
-          mbar_arrive(bar(C::B_TAKEN + q));
+          mbar_arrive(bar(C::B_TAKEN));
         }
         // Key kv0 + c is visible iff c <= at and (c >= first or c < sinks).
         const int kv0 = it.key0(p);
@@ -403,7 +379,7 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
           sv[c + 1] = ex2_approx(t.y);
         }
         if (C::APART && p > 0) {  // P V(n - 1) is complete: P may be written, O is what it will be
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O + q), (n - 1) & 1, abort_flag, a.status));
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O), (n - 1) & 1, abort_flag, a.status));
           if (!ok) return;
           tc_fence_after_sync();
           release(C::B_VEMPTY, n - 1);
@@ -428,7 +404,7 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(bar(C::B_P + q));
+        mbar_arrive(bar(C::B_P));
         float2 e0 = make_float2(0.f, 0.f), e1 = e0;
         float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
 #pragma unroll
@@ -452,13 +428,13 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
         else step(p, std::integral_constant<int, 128>{});
       }
       // -------------------------------------------------------------- output
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(C::B_O + q), (n - 1) & 1, abort_flag, a.status));
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(C::B_O), (n - 1) & 1, abort_flag, a.status));
       if (!ok) break;
       tc_fence_after_sync();
       release(C::B_VEMPTY, n - 1);
       const float inv = 1.0f / l_round;
       uint8_t* stage = smem + C::OFF_STAGE + warp * 32 * 128;
-      uint8_t* out = a.o.p + it.b * a.o.b + (it.h0 + q) * a.o.h;
+      uint8_t* out = a.o.p + it.b * a.o.b + it.h * a.o.h;
 #pragma unroll
       for (int c0 = 0; c0 < D / 32; ++c0) {
         uint32_t ov[32], pk[16];
@@ -483,7 +459,7 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
           __syncwarp();
         }
       }
-      if (row < a.Nq) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h0 + q) * a.Nq + row] = (m + log2f(l_exact)) * 0.69314718055994531f;
+      if (row < a.Nq) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] = (m + log2f(l_exact)) * 0.69314718055994531f;
       tc_fence_before_sync();  // O is read before this thread's next P lets it be overwritten
       i = next_item(k, ok);
       ok = __all_sync(0xffffffffu, ok);
@@ -500,21 +476,21 @@ __global__ void __launch_bounds__(WfCfg<D, NQ>::THREADS, WfCfg<D, NQ>::CTAS)
   }
 }
 
-template <int D, bool BF16, int NQ>
+template <int D, bool BF16>
 int launch_t(const WindowArgs& a) {
-  using C = WfCfg<D, NQ>;
+  using C = WfCfg<D>;
   CUtensorMap mq, mk, mv;
   if (!encode_strided_map(&mq, a.q, a.B, a.Hq, a.Nq, D, C::CH, BF16) || !encode_strided_map(&mk, a.k, a.B, a.Hk, a.Nk, D, C::CH, BF16) ||
       !encode_strided_map(&mv, a.v, a.B, a.Hk, a.Nk, D, C::CH, BF16))
     return kStatusCuda;
-  auto kern = attn_window_fwd_kernel<D, BF16, NQ>;
+  auto kern = attn_window_fwd_kernel<D, BF16>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return kStatusCuda;
   if (!check_launch_regs(reinterpret_cast<const void*>(kern), C::REGS)) return kStatusDeviceCheck;  // the split's sum
-  const int nrows = (a.Nq + 127) / 128, nheads = a.B * a.Hq / NQ;
-  const int64_t items = static_cast<int64_t>(nrows) * nheads;
-  if (items > 0x7fffffff - 4096) return kStatusUnsupported;
-  const int group = order_head_group(nheads, int64_t{4} * a.Nk * D, int64_t{128} << 20);
-  return launch_serialized(true, kern, dim3(static_cast<unsigned>(items)), dim3(C::THREADS), C::SMEM, a.stream, mq, mk, mv, a, nrows, nheads, group, 1) ==
+  const int nrows = (a.Nq + 127) / 128, heads = a.B * a.Hq;
+  const int64_t items = static_cast<int64_t>(nrows) * heads;
+  if (items > 0x7fffffff) return kStatusUnsupported;
+  const int group = order_head_group(heads, int64_t{4} * a.Nk * D, int64_t{128} << 20);
+  return launch_serialized(true, kern, dim3(static_cast<unsigned>(items)), dim3(C::THREADS), C::SMEM, a.stream, mq, mk, mv, a, nrows, group) ==
                  cudaSuccess
              ? kStatusOk
              : kStatusCuda;
@@ -522,7 +498,7 @@ int launch_t(const WindowArgs& a) {
 
 template <int D>
 int launch_d(const WindowArgs& a) {
-  return a.bf16 ? launch_t<D, true, 1>(a) : launch_t<D, false, 1>(a);
+  return a.bf16 ? launch_t<D, true>(a) : launch_t<D, false>(a);
 }
 
 }  // namespace
