@@ -65,13 +65,13 @@ struct PagedDecodeArgs {
   float* lse;  // [B][Hq]
   const int* pages;  // [B][H][n_pages] page indices of the sequence, or null: all pages
   int n_pages;
-  int window = 0, sinks = 0;  // window > 0: the last `window` tokens and the first `sinks` ones (pages is null)
-  int box_shift = 0;          // log2 of the keys of a box; the launcher's
   float sl2;  // scale * k_scale * log2(e), signed
   int x_type;
   cudaStream_t stream;
   uint8_t* ws;
   int* status;  // sticky word of bounded waits
+  int window = 0, sinks = 0;  // window > 0: the last `window` tokens and the first `sinks` ones (pages is null)
+  int box_shift = 0;          // log2 of the keys of a box; the launcher's
 };
 
 struct PagedSelectArgs {

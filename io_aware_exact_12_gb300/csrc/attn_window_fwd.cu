@@ -74,7 +74,7 @@ struct WfCfg {
   static constexpr int W_LOAD = 4, W_MMA = 5;  // warps
   static constexpr int CTAS = 2;                // per SM
   static constexpr int REGS = (65536 / (THREADS * CTAS)) & ~7;
-  static constexpr int REGS_ROW = 208, REGS_CTRL = 48;
+  static constexpr int REGS_ROW = D == 128 ? 200 : 208, REGS_CTRL = D == 128 ? 56 : 48;
   static_assert(128 * REGS_ROW + 128 * REGS_CTRL <= THREADS * REGS, "register split");
   static constexpr uint32_t COLS = 256;
   // P has TMEM columns of its own at d <= 64: the next S can then be formed while
