@@ -318,7 +318,8 @@ typedef struct {
  *          R = ceil((window - 1) / page_size) + 1 others at most: entry j >= F + R
  *          repeats entry j - R, whose tokens have left the window.  Then at most
  *          R * page_size new tokens of one sequence in a step (they would share
- *          slots), and an append must not be repeated after later ones.
+ *          slots); of the calls that read a cache only attn_paged_decode_window, with
+ *          that window or a narrower one and no more sinks, reads such a sequence rightly.
  * The step is done whole or, if more pages are wanted than are free, if there
  * are more new tokens than rows, or if a length, a count or free_state is out of
  * range, not at all: lengths and free_state as before, token_start 0, slots -1,
@@ -446,8 +447,9 @@ typedef struct {
  *   type : ATTN_TYPE_BF16 or ATTN_TYPE_F16, of all four tensors.
  * The tiles of keys that no query of a 128-row tile sees are neither loaded nor
  * multiplied (FlashAttention深度攻略, 进阶追问 "Sparse FlashAttention", for a
- * mask that is not made of tiles).  Keys and values must be finite: inside a tile
- * a hidden key has weight 0, and 0 times inf is NaN.
+ * mask that is not made of tiles).  The inputs must be finite, also where the mask
+ * hides them (padding at a sequence's end, say): inside a tile a hidden key has
+ * weight 0, and 0 times inf is NaN.
  * Supported: d in {32, 64, 128}, Nk <= 2^24, B * q_heads <= 65535, finite scale.
  * The outputs must not overlap the inputs or one another; slices of one buffer
  * whose rows take turns do not.  Launches 1 kernel.

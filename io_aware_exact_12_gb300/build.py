@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, "libattn.so")
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_noalloc.cu", "attn_diag.cu", "attn_decode.cu", "attn_fwd_fp8.cu",
            "attn_paged_append.cu", "attn_paged_decode.cu", "attn_paged_select.cu", "attn_paged_assign.cu",
            "attn_window_fwd.cu", "attn_window_bwd.cu"]
-HEADERS = ["attn_internal.h", "block_order.h", "tc_sm103.cuh", "dropout.cuh", "attn_paged.h", "attn_window.h"]
+HEADERS = ["attn_internal.h", "block_order.h", "tc_sm103.cuh", "dropout.cuh", "attn_paged.h", "attn_window.h", "attn_window_tiles.cuh"]
 BINDING = "paged_binding.cpp"
 BINDING_PATH = os.path.join(PKG, "_paged.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -30,8 +30,7 @@
 // is issued right behind the one that reads it: one thread's MMAs run in the order of
 // issue.
 #include "attn_internal.h"
-#include "attn_window.h"
-#include "tc_sm103.cuh"
+#include "attn_window_tiles.cuh"
 
 namespace attn {
 namespace {
@@ -50,16 +49,9 @@ struct WbPlan {
   float* part;                 // [item in runs][dK, dV][128][d]
 };
 
-// What both kernels share: tiles of 128 rows of D channels, swizzled.
+// What both kernels share.
 template <int D>
-struct Tile {
-  static constexpr int ROWB = D >= 64 ? 128 : 64;
-  static constexpr int CH = ROWB / 2;
-  static constexpr int NCH = D / CH;
-  static constexpr uint32_t SWZ = ROWB == 128 ? kSwizzle128B : kSwizzle64B;
-  static constexpr int SBO = 8 * ROWB;
-  static constexpr int CHUNK = 128 * ROWB;
-  static constexpr int TILE = 128 * D * 2;
+struct Tile : TileLayout<D> {
   static constexpr int THREADS = 384;
   static constexpr int REGS = 168, REGS_ROW = 184, REGS_CTRL = 136;
   static_assert(256 * REGS_ROW + 128 * REGS_CTRL <= THREADS * REGS, "register split");
@@ -138,18 +130,7 @@ struct DkvCfg : Tile<D> {
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-// Descriptor steps (16-byte units) of the 16-deep slice kk: of a K-major tile (rows
-// of D channels) and of an MN-major one (16 rows on); TMEM columns of the slice of an
-// operand whose halves lie 64 columns apart.
-template <int D>
-__host__ __device__ constexpr uint32_t k_step(int kk) {
-  using C = Tile<D>;
-  return static_cast<uint32_t>(((kk * 16) / C::CH * C::CHUNK + (kk * 16) % C::CH * 2) >> 4);
-}
-template <int D>
-__host__ __device__ constexpr uint32_t mn_step(int kk) {
-  return static_cast<uint32_t>((kk * 16 * Tile<D>::ROWB) >> 4);
-}
+// TMEM columns of the 16-deep slice kk of an operand whose halves lie 64 columns apart.
 __host__ __device__ constexpr uint32_t half_step(int kk) { return static_cast<uint32_t>((kk >> 2) * 64 + (kk & 3) * 8); }
 
 // Byte offset of 16-byte unit u of a row in a tile, as TMA has laid it.
@@ -162,13 +143,6 @@ __device__ __forceinline__ uint32_t tile_unit(int row, int u) {
 // Byte offset of 16-byte unit u of a row of 128 bytes in a warp's staging copy,
 // swizzled so that rows by threads and units by threads meet no bank twice.
 __device__ __forceinline__ uint32_t staged(int row, int u) { return static_cast<uint32_t>(row * 128 + ((u ^ (row & 7)) << 4)); }
-
-// A wait for work that has been issued, also after an abort.
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_test(bar, parity))
-    if (global_timer_ns() - t0 > kWaitLimitNs) return;
-}
 
 // A warp's 32 rows of 64 channels, 16 packed words of 32 channels in `lo` and `hi`, to
 // out + row * stride: through shared memory, 128 contiguous bytes a row.
@@ -186,53 +160,7 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint3
   __syncwarp();
 }
 
-// The loop over items that every role runs: the first is the block's own; while it
-// runs the loader asks for that of a block that has not started, and so on.
-struct Items {
-  uint32_t answers, b_next, b_read;  // two answers, their barriers
-  volatile int* abort_flag;
-  int* status;
-  // The item after the k-th, or -1.
-  __device__ __forceinline__ int after(int k, bool& ok) const {
-    ok = ok && mbar_wait(b_next + (k & 1) * 8, (k >> 1) & 1, abort_flag, status);
-    return ok ? block_answer(answers + (k & 1) * 16) : -1;
-  }
-  // By each other role once it has it: a whole warp, or the issuer's thread.
-  __device__ __forceinline__ void read(int k) const {
-    fence_proxy_async_smem();  // the answer is read before the next one is written
-    mbar_arrive(b_read + (k & 1) * 8);
-  }
-  // The loader's k-th question.
-  __device__ __forceinline__ bool ask(int k) const {
-    if (k >= 2 && !mbar_wait(b_read + (k & 1) * 8, ((k >> 1) - 1) & 1, abort_flag, status)) return false;
-    mbar_arrive_expect_tx(b_next + (k & 1) * 8, 16);
-    block_request(answers + (k & 1) * 16, b_next + (k & 1) * 8);
-    return true;
-  }
-  __device__ __forceinline__ void drain_last(int asked) const {
-    if (asked) drain(b_next + ((asked - 1) & 1) * 8, ((asked - 1) >> 1) & 1);
-  }
-};
-
 // ------------------------------------------------------------------------- dQ
-// 128 query rows of a head, and the list of key tiles they see.
-struct DqItem {
-  int row0, b, h, hk;
-  int ns, skip, npos;  // tiles of sinks, tiles left out behind them, tiles in all
-  __device__ __forceinline__ DqItem(const WindowArgs& a, int item, int nrows, int group) {
-    int rank, bh;
-    grouped_rank_order(item, nrows, a.B * a.Hq, group, rank, bh);
-    row0 = (nrows - 1 - rank) * 128;  // later rows, which under a wide window have more tiles, first
-    b = bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
-    const int off = a.Nk - a.Nq;
-    const int w0 = max(0, row0 + off - a.window + 1) >> 7;
-    ns = min(w0, (a.sinks + 127) >> 7);
-    skip = w0 - ns;
-    npos = ((min(row0 + 127, a.Nq - 1) + off) >> 7) - skip + 1;
-  }
-  __device__ __forceinline__ int key0(int p) const { return (p < ns ? p : p + skip) * 128; }
-};
-
 template <int D, bool BF16>
 __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
     attn_window_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -289,7 +217,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       for (int i = blockIdx.x; ok && i >= 0;) {
         if (!(ok = items.ask(asked))) break;
         ++asked;
-        const DqItem it(a, i, nrows, group);
+        const RowItem it(a, i, nrows, group);
         auto load_k = [&](const CUtensorMap* map, int row, int head) {
           const int s = nk % C::NK;
           if (nk >= C::NK && !(ok = mbar_wait(bar(C::B_KEMPTY + s), (nk / C::NK - 1) & 1, abort_flag, a.status))) return;
@@ -339,7 +267,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       int n0 = 0;
       IdleWatch watch;
       for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
-        const int end = n0 + DqItem(a, i, nrows, group).npos;
+        const int end = n0 + RowItem(a, i, nrows, group).npos;
         ok = mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
         int is = n0, ip = n0, iq = n0;
         const int ahead = k + 1;  // O tiles in the K ring so far
@@ -397,7 +325,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
     bool ok = true;
     int n = 0;
     for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
-      const DqItem it(a, i, nrows, group);
+      const RowItem it(a, i, nrows, group);
       const int row = it.row0 + r;
       const int64_t bh = static_cast<int64_t>(it.b) * a.Hq + it.h;
       const float lse2 = row < a.Nq ? -a.lse[bh * a.Nq + row] * kLog2e : -INFINITY;
@@ -508,9 +436,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       }
       tc_fence_before_sync();  // dQ is read before this thread's next dS lets it be overwritten
       i = items.after(k, ok);
-      ok = __all_sync(0xffffffffu, ok);
-      __syncwarp();
-      if (lane == 0) items.read(k);
+      items.read_by_warp(k, lane, ok);
     }
   }
   tc_fence_before_sync();
@@ -846,9 +772,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(out + j * dst.n + e * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
       i = items.after(k, ok);
-      ok = __all_sync(0xffffffffu, ok);
-      __syncwarp();
-      if (lane == 0) items.read(k);
+      items.read_by_warp(k, lane, ok);
     }
   }
   tc_fence_before_sync();

@@ -27,8 +27,7 @@
 #include <type_traits>
 
 #include "attn_internal.h"
-#include "attn_window.h"
-#include "tc_sm103.cuh"
+#include "attn_window_tiles.cuh"
 
 namespace attn {
 namespace {
@@ -37,18 +36,12 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr int kNarrow = 32;  // keys of a tile with a few sinks
 
 template <int D>
-struct WfCfg {
-  static constexpr int ROWB = D >= 64 ? 128 : 64;  // bytes of a swizzled row
-  static constexpr int CH = ROWB / 2;              // elements of it
-  static constexpr int NCH = D / CH;               // column chunks of a tile
-  static constexpr uint32_t SWZ = ROWB == 128 ? kSwizzle128B : kSwizzle64B;
-  static constexpr int SBO = 8 * ROWB;
-  static constexpr int CHUNK = 128 * ROWB;         // bytes of a chunk of 128 rows
-  static constexpr int TILE = 128 * D * 2;
+struct WfCfg : TileLayout<D> {
+  using T = TileLayout<D>;
   static constexpr int NST = D == 128 ? 1 : 2;  // K and V stages
-  static constexpr int OFF_K = TILE;
-  static constexpr int OFF_V = OFF_K + NST * TILE;
-  static constexpr int OFF_BAR = OFF_V + NST * TILE;
+  static constexpr int OFF_K = T::TILE;
+  static constexpr int OFF_V = OFF_K + NST * T::TILE;
+  static constexpr int OFF_BAR = OFF_V + NST * T::TILE;
   static constexpr int B_Q = 0;
   static constexpr int B_QEMPTY = 1;
   static constexpr int B_KFULL = 2;
@@ -86,49 +79,9 @@ struct WfCfg {
   static_assert(CTAS * (SMEM + 1024) <= 233472, "shared memory");
 };
 
-// Descriptor steps (16-byte units) of the 16-deep slice kk: of a K-major tile
-// (rows of D channels) and of an MN-major one (16 rows on).
-template <int D>
-__host__ __device__ constexpr uint32_t k_step(int kk) {
-  using C = WfCfg<D>;
-  return static_cast<uint32_t>(((kk * 16) / C::CH * C::CHUNK + (kk * 16) % C::CH * 2) >> 4);
-}
-template <int D>
-__host__ __device__ constexpr uint32_t mn_step(int kk) {
-  return static_cast<uint32_t>((kk * 16 * WfCfg<D>::ROWB) >> 4);
-}
-
 // Byte offset of 16-byte unit u of a row of 128 bytes in the output's staging
 // copy, swizzled so that rows by threads and units by threads meet no bank twice.
 __device__ __forceinline__ uint32_t staged(int row, int u) { return static_cast<uint32_t>(row * 128 + ((u ^ (row & 7)) << 4)); }
-
-// A wait for work that has been issued, also after an abort.
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_test(bar, parity))
-    if (global_timer_ns() - t0 > kWaitLimitNs) return;
-}
-
-// A block's item: 128 query rows of a head, and the list of key tiles they see.
-struct WfItem {
-  int row0, b, h, hk;   // first row, sequence, query head, key/value head
-  int ns, skip, npos;   // tiles of sinks, tiles left out behind them, tiles in all
-  __device__ __forceinline__ WfItem(const WindowArgs& a, int item, int nrows, int group) {
-    // Later rows, which under a wide window have more tiles, first.
-    int rank, bh;
-    grouped_rank_order(item, nrows, a.B * a.Hq, group, rank, bh);
-    row0 = (nrows - 1 - rank) * 128;
-    b = bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
-    const int off = a.Nk - a.Nq;
-    const int w0 = max(0, row0 + off - a.window + 1) >> 7;
-    ns = min(w0, (a.sinks + 127) >> 7);
-    skip = w0 - ns;
-    npos = ((min(row0 + 127, a.Nq - 1) + off) >> 7) - skip + 1;
-  }
-  __device__ __forceinline__ int key0(int p) const { return (p < ns ? p : p + skip) * 128; }
-  // The last tile of sinks may have few of them: then kNarrow of its keys are enough.
-  __device__ __forceinline__ bool narrow(const WindowArgs& a, int p) const { return p == ns - 1 && a.sinks - p * 128 <= kNarrow; }
-};
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
@@ -167,16 +120,10 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *slot;
-  // Every role walks the same items and, within each, the same positions; `n`
-  // counts positions over all items and gives stages and phases.  The first item
-  // is the block's own; while it runs the loader asks for that of a block that has
-  // not started (items differ in length, so equal shares would not do), and so on.
-  const uint32_t next = sbase + C::OFF_NEXT;
-  // The item after the k-th, or -1; for all roles but the loader, a warp's lanes (or one) together.
-  auto next_item = [&](int k, bool& ok) {
-    ok = ok && mbar_wait(bar(C::B_NEXT + (k & 1)), (k >> 1) & 1, abort_flag, a.status);
-    return ok ? block_answer(next + (k & 1) * 16) : -1;
-  };
+  const Items items = {sbase + C::OFF_NEXT, bar(C::B_NEXT), bar(C::B_READ), abort_flag, a.status};
+  // `n` counts positions over all items and gives stages and phases.
+  // The last tile of sinks may have few of them: then kNarrow of its keys are enough.
+  auto narrow = [&](const RowItem& it, int p) { return p == it.ns - 1 && a.sinks - p * 128 <= kNarrow; };
 
   if (warp >= C::W_LOAD) {
     regs_decrease<C::REGS_CTRL>();
@@ -190,12 +137,9 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
       bool ok = true;
       int asked = 0;
       for (int i = blockIdx.x; ok && i >= 0;) {
-        const int x = asked & 1;
-        if (asked >= 2 && !(ok = mbar_wait(bar(C::B_READ + x), ((asked >> 1) - 1) & 1, abort_flag, a.status))) break;
-        mbar_arrive_expect_tx(bar(C::B_NEXT + x), 16);
-        block_request(next + x * 16, bar(C::B_NEXT + x));
+        if (!(ok = items.ask(asked))) break;
         ++asked;
-        const WfItem it(a, i, nrows, group);
+        const RowItem it(a, i, nrows, group);
         for (int p = 0; p < it.npos; ++p) {
           const int s = nk % C::NST, turn = (nk / C::NST - 1) & 1;
           if (nk >= C::NST && !(ok = mbar_wait(bar(C::B_KEMPTY + s), turn, abort_flag, a.status))) break;
@@ -213,10 +157,10 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
           load(sV + s * C::TILE, &mv, bar(C::B_VFULL + s), it.key0(p), it.hk, it.b);
           ++nv;
         }
-        i = next_item(asked - 1, ok);
+        i = items.after(asked - 1, ok);
       }
       if (*abort_flag) {  // what is in flight lands before the shared memory goes
-        if (asked) drain(bar(C::B_NEXT + ((asked - 1) & 1)), ((asked - 1) >> 1) & 1);
+        items.drain_last(asked);
         if (nq) drain(bar(C::B_Q), (nq - 1) & 1);
         for (int s = 0; s < C::NST; ++s) {
           if (nk > s) drain(bar(C::B_KFULL + s), ((nk - 1 - s) / C::NST) & 1);
@@ -238,8 +182,8 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
       int n0 = 0;  // positions of the items before
       IdleWatch watch;
       for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
-        const WfItem it(a, i, nrows, group);
-        const int end = n0 + it.npos, thin = it.ns > 0 && it.narrow(a, it.ns - 1) ? n0 + it.ns - 1 : -1;
+        const RowItem it(a, i, nrows, group);
+        const int end = n0 + it.npos, thin = it.ns > 0 && narrow(it, it.ns - 1) ? n0 + it.ns - 1 : -1;
         ok = mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
         int js = n0, jp = n0;          // next S and P V
         int k_seen = n0, v_seen = n0;  // positions whose loads have been seen to land
@@ -278,9 +222,8 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
           else ok = watch.idle(abort_flag, a.status, kWaitLimitNs);
         }
         n0 = end;
-        i = next_item(k, ok);
-        fence_proxy_async_smem();  // the answer is read before the next one is written
-        mbar_arrive(bar(C::B_READ + (k & 1)));
+        i = items.after(k, ok);
+        items.read(k);
       }
       tc_commit(bar(C::B_DONE));  // before TMEM is released
       drain(bar(C::B_DONE), 0);
@@ -301,7 +244,7 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
     bool ok = true;
     int n = 0;
     for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
-      const WfItem it(a, i, nrows, group);
+      const RowItem it(a, i, nrows, group);
       const int row = it.row0 + r;
       float m = -INFINITY, l_exact = 0.f, l_round = 0.f;
       // A position with W of its tile's keys.
@@ -424,7 +367,7 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
         ++n;
       };
       for (int p = 0; ok && p < it.npos; ++p) {
-        if (it.narrow(a, p)) step(p, std::integral_constant<int, kNarrow>{});
+        if (narrow(it, p)) step(p, std::integral_constant<int, kNarrow>{});
         else step(p, std::integral_constant<int, 128>{});
       }
       // -------------------------------------------------------------- output
@@ -461,11 +404,8 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
       }
       if (row < a.Nq) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] = (m + log2f(l_exact)) * 0.69314718055994531f;
       tc_fence_before_sync();  // O is read before this thread's next P lets it be overwritten
-      i = next_item(k, ok);
-      ok = __all_sync(0xffffffffu, ok);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::B_READ + (k & 1)));
+      i = items.after(k, ok);
+      items.read_by_warp(k, lane, ok);
     }
   }
   tc_fence_before_sync();

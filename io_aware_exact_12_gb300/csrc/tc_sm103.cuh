@@ -166,16 +166,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// The same of four dimensions.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
 // 1-D bulk copy global -> shared (both addresses 16-byte aligned, size a
 // multiple of 16 bytes).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -195,29 +185,6 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
 // async-proxy reads (tensor-core operand fetches).
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// ------------------------------------------------- work of blocks not started
-// Asks for the index of a block of this grid that has not started, which then
-// never will: a running block takes its work (16 bytes at `addr`, signalled as
-// transaction bytes on `bar`).  Once refused, a block must not ask again.
-__device__ __forceinline__ void block_request(uint32_t addr, uint32_t bar) {
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(addr), "r"(bar)
-               : "memory");
-}
-// The answer: blockIdx.x, or -1.
-__device__ __forceinline__ int block_answer(uint32_t addr) {
-  int x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
-      "ld.shared.b128 h, [%1];\n\t"
-      "mov.b32 %0, -1;\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
-      : "=r"(x)
-      : "r"(addr)
-      : "memory");
-  return x;
 }
 
 // ------------------------------------------------------------- tcgen05 TMEM

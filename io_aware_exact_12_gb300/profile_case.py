@@ -15,6 +15,10 @@ capture can skip them with ``-s``.
       of 16, H key/value heads and 4 H query heads; append writes all N tokens with
       rotation and summaries, select takes an eighth of the pages; --dtype e4m3 for
       an 8-bit cache
+  --op window_fwd / window_bwd: sliding window (--window, --sinks), H query heads and
+      H / 4 key/value heads, token-major tensors (one window_bwd = 2 or 3 launches)
+  --op paged_window: paged_decode with the window and the sinks
+  --op paged_assign: the bookkeeping of N new tokens for each of B sequences
 """
 from __future__ import annotations
 
@@ -45,6 +49,13 @@ def paged(attn, a):
                                              token_start=start, cos=cos, sin=sin)
     elif a.op == "paged_decode":
         run = lambda: attn.attn_paged_decode(kv, q)  # noqa: E731
+    elif a.op == "paged_window":
+        run = lambda: attn.attn_paged_decode_window(kv, q, a.window, a.sinks)  # noqa: E731
+    elif a.op == "paged_assign":
+        i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        new, none, ring = kv.seq_lens.clone(), torch.zeros_like(kv.seq_lens), table.flatten().clone()
+        free, after, slots = i32(0, ring.numel()), i32(0, 0), torch.zeros(a.B * a.N, dtype=torch.int64, device="cuda")
+        run = lambda: attn.attn_paged_assign(kv, new, ring, free, lens=none, free_out=after, slots=slots)  # noqa: E731
     else:
         run = lambda: attn.attn_paged_select(kv, q, max(2, pages // 8))  # noqa: E731
     for _ in range(a.warmup + a.launches):
@@ -55,16 +66,37 @@ def paged(attn, a):
     return 1 if st else 0
 
 
+def window(attn, a):
+    """Both passes under a sliding window."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = {"bf16": torch.bfloat16, "f16": torch.float16}[a.dtype]
+    q, k, v, do = (torch.randn((a.B, a.N, h, a.d), generator=g, device="cuda", dtype=x).transpose(1, 2)
+                   for h in (a.H, max(1, a.H // 4), max(1, a.H // 4), a.H))
+    o, lse = attn.attn_fwd_window(q, k, v, a.window, a.sinks)
+    for _ in range(a.warmup + a.launches):
+        if a.op == "window_fwd":
+            attn.attn_fwd_window(q, k, v, a.window, a.sinks, o=o, lse=lse)
+        else:
+            attn.attn_bwd_window(q, k, v, o, do, lse, a.window, a.sinks)
+    torch.cuda.synchronize()
+    st = attn.sync_status()
+    print("done op=%s status=%d" % (a.op, st))
+    return 1 if st else 0
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", choices=["fwd", "bwd", "naive", "fwd_dropout", "bwd_dropout", "decode",
                                      "fwd_blocksparse", "bwd_blocksparse", "fwd_fp8", "paged_append",
-                                     "paged_decode", "paged_select"], default="fwd")
+                                     "paged_decode", "paged_select", "paged_window", "paged_assign", "window_fwd",
+                                     "window_bwd"], default="fwd")
     ap.add_argument("--B", type=int, default=2)
     ap.add_argument("--H", type=int, default=16)
     ap.add_argument("--N", type=int, default=8192)
     ap.add_argument("--d", type=int, default=128)
     ap.add_argument("--causal", action="store_true")
+    ap.add_argument("--window", type=int, default=1024)
+    ap.add_argument("--sinks", type=int, default=4)
     ap.add_argument("--dtype", default="bf16")
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--launches", type=int, default=2)
@@ -73,6 +105,8 @@ def main(argv=None):
     import io_aware_exact_12_gb300 as attn
     if a.op.startswith("paged"):
         return paged(attn, a)
+    if a.op.startswith("window"):
+        return window(attn, a)
     from io_aware_exact_12_gb300.synth import AttnShape, make_inputs
     x = make_inputs(AttnShape(a.B, a.H, a.N, a.d), a.dtype, seed=4, device="cuda")
     q, k, v, do = x["q"], x["k"], x["v"], x["do"]

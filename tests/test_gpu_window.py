@@ -372,6 +372,88 @@ def test_captured_step_replays(pkg):
 
 
 @gpu
+def test_two_graphs_of_one_pool(pkg):
+    """Two captured steps that share a memory pool, their workspaces among it, replayed in turns."""
+    sets = [_inputs(1, 4, 2, n, n, 64, BF16, "tokens", n) for n in (500, 900)]
+    want = [_check(pkg, *x, 200, 4) for x in sets]
+    pool, graphs, outs = torch.cuda.graph_pool_handle(), [], []
+    for q, k, v, do in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            o, lse = pkg.attn_fwd_window(q, k, v, 200, 4)
+            outs.append((o, lse) + pkg.attn_bwd_window(q, k, v, o, do, lse, 200, 4))
+        graphs.append(graph)
+    for i in (0, 1, 1, 0, 1):
+        graphs[i].replay()
+        got = [x.clone() for x in outs[i]]
+        torch.cuda.synchronize()
+        for x, w in zip(got, want[i]):
+            assert torch.equal(x, w)
+    assert pkg.sync_status() == 0
+
+
+@gpu
+def test_a_padded_batch(pkg):
+    """Sequences padded at their end: what stands there changes nothing before it, and without a gradient adds none."""
+    q, k, v, do = _inputs(2, 4, 2, 300, 300, 64, F16, "tokens", 15)
+    real = 211
+    do[1, :, real:] = 0
+    a = pkg.attn_fwd_window(q, k, v, 70, 3)
+    ga = pkg.attn_bwd_window(q, k, v, a[0], do, a[1], 70, 3)
+    q2, k2, v2 = q.clone(), k.clone(), v.clone()
+    for x in (q2, k2, v2):
+        x[1, :, real:] = 55.0
+    b = pkg.attn_fwd_window(q2, k2, v2, 70, 3)
+    gb = pkg.attn_bwd_window(q2, k2, v2, b[0], do, b[1], 70, 3)
+    assert torch.equal(a[0][1, :, :real], b[0][1, :, :real]) and torch.equal(a[1][1, :, :real], b[1][1, :, :real])
+    for x, y in zip(ga, gb):
+        assert torch.equal(x[1, :, :real], y[1, :, :real]) and torch.equal(x[0], y[0])
+        assert (x[1, :, real:] == 0).all() and (y[1, :, real:] == 0).all()
+
+
+@gpu
+def test_past_32_bit_offsets(pkg):
+    """Tensors of more than 2^31 elements; the last head's last rows and keys, and the sinks' gradients of a short run of rows."""
+    B, Hq, Hk, n, d, window, sinks = 1, 72, 2, 262144, 128, 100, 4
+    g = torch.Generator(device="cuda").manual_seed(16)
+    r = lambda h: torch.randn((B, n, h, d), generator=g, device="cuda", dtype=BF16).transpose(1, 2)  # noqa: E731
+    q, k, v, do = r(Hq), r(Hk), r(Hk), r(Hq)
+    assert q.numel() > 2 ** 31
+    do[:, :, :-600] = 0  # gradients of the last rows only, so that a float64 form of them is small
+    o, lse = pkg.attn_fwd_window(q, k, v, window, sinks)
+    dq, dk, dv = pkg.attn_bwd_window(q, k, v, o, do, lse, window, sinks)
+    assert pkg.sync_status() == 0
+    h, G, first = Hq - 1, Hq // Hk, n - 600
+    keys = torch.cat([torch.arange(sinks), torch.arange(first - window, n)]).cuda()  # all that the last rows see
+    rows = slice(first, n)
+    f = lambda x: x.double()  # noqa: E731
+    group = slice(Hq - G, Hq)
+    kk, vv, qq, oo, dd, ll = f(k[:, 1:, keys]), f(v[:, 1:, keys]), f(q[:, group, rows]), f(o[:, group, rows]), f(do[:, group, rows]), f(lse[:, group, rows])
+    # as a problem of its own: keys 0 .. are the sinks and those before the rows, in their order; the mask of positions is the same
+    u, scale = torch.finfo(BF16).eps / 2, d ** -0.5
+    pos = torch.arange(first, n, device="cuda")[:, None]
+    seen = (keys <= pos) & ((keys > pos - window) | (keys < sinks))
+    s = (scale * (qq @ kk.mT)).masked_fill(~seen, -math.inf)
+    p = torch.softmax(s, -1)
+    big = (scale * (qq.abs() @ kk.abs().mT)).masked_fill(~seen, 0).amax(-1, keepdim=True)
+    err = 2.0 ** -15 * (1 + big)
+    _near("o", o[:, group, rows], p @ vv, u * (p @ vv).abs() + (2 * u + 2 * err) * (p @ vv.abs()))
+    _near("lse", lse[:, group, rows], torch.logsumexp(s, -1), err[..., 0])
+    pp = torch.where(seen, torch.exp(s - ll[..., None]), 0.0)
+    ds = pp * (dd @ vv.mT - (dd * oo).sum(-1, keepdim=True))
+    mag = pp * (dd.abs() @ vv.abs().mT + (dd.abs() * oo.abs()).sum(-1, keepdim=True))
+    n_rows = G * 600 * 2.0 ** -24
+    want = scale * (ds @ kk)
+    _near("dq", dq[:, group, rows], want, u * want.abs() + scale * ((u * ds.abs() + 2 * err * mag) @ kk.abs()))
+    want = scale * (ds.mT @ qq).sum(1)
+    _near("dk", dk[:, 1, keys], want, u * want.abs() + scale * ((u * ds.abs() + (2 * err + n_rows) * mag).mT @ qq.abs()).sum(1))
+    want = (pp.mT @ dd).sum(1)
+    _near("dv", dv[:, 1, keys], want, u * want.abs() + (((u + 2 * err + n_rows) * pp).mT @ dd.abs()).sum(1))
+    assert (dq[:, :, :first] == 0).all()
+    assert (dk[:, :, sinks:first - window - 128] == 0).all() and (dv[:, :, sinks:first - window - 128] == 0).all()
+
+
+@gpu
 def test_two_streams_at_once(pkg):
     sets = [_inputs(1, 4, 2, 900, 900, 64, BF16, "tokens", s) for s in (11, 12)]
     want = [_check(pkg, *x, 200, 4) for x in sets]
