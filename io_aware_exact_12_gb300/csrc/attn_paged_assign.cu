@@ -14,13 +14,17 @@
 //   attn_paged_plan_kernel : one block; checks, the three prefix sums (tokens,
 //       pages taken, pages handed back), lengths and starts.  With ALL, for a step of
 //       few tokens, it does the second kernel's work too, its sums in shared memory.
-//   attn_paged_fill_kernel : a warp to 128 rows of new tokens, four to
-//       a thread: the token's sequence, searched for between those of the
-//       warp's first and last row, its slot, and the table entry where it is a page's
-//       first; then the pages of ended sequences.
+//   attn_paged_fill_kernel : a warp to 128 rows of new tokens, four to a thread: the
+//       token's sequence, searched for between those of the warp's first and last
+//       row, its slot, and the table entry where it is a page's first; then the pages
+//       of ended sequences.
 //
 // Few bytes and no arithmetic to speak of: latency bounds it, a handful of dependent
-// loads in the one block, as many in the fill.
+// loads in the one block, as many in the fill.  A step of 64 sequences takes 4.3 us a
+// call, one of 4096 with 962000 new tokens 20.6 (plan 10, fill 12; its 8.4 MB would
+// take 1.3).  What counted (33 -> 20.6): one round of sums, taken back if a check
+// fails, instead of one round of checks and another of sums; a thread's rows in
+// flight together; divisions by the page size as products.
 #include "attn_paged.h"
 #include "tc_sm103.cuh"
 

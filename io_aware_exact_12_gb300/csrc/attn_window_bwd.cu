@@ -17,11 +17,22 @@
 //
 // Seven products a tile instead of the five of one pass that adds dQ up in memory:
 // there the additions (64 KB of fp32 a visit at d = 128) paced everything, 7000
-// cycles a visit against 3200 of five products, although the L2 alone takes such a
-// tile from every SM in 3000; the accumulator's zeros and its conversion cost another
-// tenth.  Two sequences of 8192, 16 / 4 heads of 128, window 1024: 624 us that way,
-// @LONG@ so; eight of 1024, 12 heads of 64, window 256: 88 and @SHORT@.  No sum depends on
-// the order of CTAs, so a call repeats bit for bit.
+// cycles a visit against 4000 of the five products, although the L2 alone takes such
+// a tile from every SM in 3000, and the accumulator's zeros and its conversion cost
+// another tenth.  Two sequences of 8192, 16 / 4 heads of 128, window 1024, 4 sinks:
+// 624 us that way, 488 so (dQ 223, dK and dV 256, sums 13); eight of 1024, 12 heads of
+// 64, window 256: 88 and 77.  No sum depends on the order of CTAs, so a call repeats
+// bit for bit.
+//
+// What bounds both loops is how fast the tensor core takes 128 x 128 x 16 products: 96
+// cycles with an operand from TMEM, 118 with both from shared memory (whose 8 KB are
+// 64 cycles of its bandwidth), whether 64 or 128 columns wide: 2700 cycles a tile for
+// dQ, of the 3300 that it takes, 3400 for dK and dV, of 3700; an item's start and end
+// are the rest.
+//
+// P and dS are fp32 until they become operands of 16-bit products, rounded to the
+// inputs' type; everything is summed in fp32.  (Gradients are off by 2.4e-3 in norm
+// with bf16, where fp32 operands and the results' own rounding make 1.7e-3.)
 //
 // Both loops run on tcgen05, one CTA to an SM: warps 0-7 work on rows, two threads to
 // each, 64 columns a thread; warp 8 loads by TMA; one thread of warp 9 issues the

@@ -9,7 +9,11 @@
 // that end the sinks are masked, key by key.
 //
 // The tensor cores bound it (4 d flops a pair against 4 d bytes a key for 128
-// rows).  GB300 mapping:
+// rows): a tile of 128 keys at d = 128 is 16 products of 128 x 128 x 16, which take 118
+// cycles each from shared memory and 96 with P from TMEM, 1700 in all, and goes by in
+// 1900 where the list is long (32768 queries, 32 / 8 heads, window 4096: 1.72 ms, 1200
+// TFLOP/s of visible pairs); edge tiles, half of which is hidden, and an item's start
+// and end make window 1024 slower (8192 queries: 151 us, 857).  GB300 mapping:
 //   * an item is 128 query rows of a head; two CTAs to an SM, so that one's softmax
 //     meets the other's matrix products.  Blocks take over the items of blocks that
 //     have not started (cluster launch control) and load the next item's first tiles
@@ -18,11 +22,19 @@
 //     queries, 32 / 8 heads of 128: 165 -> 152 us).
 //   * one warp loads (TMA, 4-D maps, so any strides of batch, head and row), one
 //     thread issues the tcgen05.mma, S = Q K^T from shared memory, O += P V with P
-//     from TMEM; a warpgroup to each query tile does its softmax, a thread to a row.
+//     from TMEM; a warpgroup does the softmax, a thread to a row.  (Two threads to a
+//     row, who exchange its maximum, gained nothing at d = 64, where the products pace
+//     it too, and do not have the registers at d = 128.)
+//   * few sinks (kNarrow at most in their last tile): that tile's S is formed for 32
+//     keys and its P V summed over 32 (4 sinks, window 1024: 157 -> 151 us; 16384
+//     queries, 16 / 4 heads, window 256: 93 -> 79).
 //   * scale log2(e) is folded into exp2; the reference maximum moves only when it
 //     grows by more than 2^8, and O is rescaled in TMEM then.  l is summed twice:
 //     in fp32 of the weights as they are, for LSE, and of the weights rounded to the
-//     input type that multiply V, to normalise O.
+//     input type that multiply V, to normalise O.  (Weights of 16 bits are what a
+//     16-bit product takes; O is off by 2.2e-3 in norm with bf16, where fp32 weights
+//     and O's own rounding make 1.6e-3; a second product with the remainders would
+//     double P V.)
 #include <cfloat>
 #include <type_traits>
 
