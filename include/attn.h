@@ -520,7 +520,8 @@ const char* attn_status_string(int status);
 
 /* Number of kernel launches the most recent successful attn_fwd* / attn_bwd* /
  * attn_decode / attn_paged_* call on this thread enqueued (forward 1, backward 3,
- * decode 2, paged append 1, paged decode 1 or 2, paged select 2, paged assign 1 or 2). */
+ * decode 2, window backward 2 or 3, paged append 1, paged decode 1 or 2, paged select 2,
+ * paged assign 1 or 2). */
 int attn_last_launch_count(void);
 
 #ifdef __cplusplus
