@@ -25,6 +25,10 @@
 //     from TMEM; a warpgroup does the softmax, a thread to a row.  (Two threads to a
 //     row, who exchange its maximum, gained nothing at d = 64, where the products pace
 //     it too, and do not have the registers at d = 128.)
+//   * few items with long lists of tiles (a chunk of a prompt, a handful of tokens): a
+//     cluster to an item (SPLIT), its positions in equal runs, joined in the order of
+//     the runs through the cluster's shared memory (16 queries of 32 heads over window
+//     4096: 58 -> 19 us; one over 32768 keys: 419 -> 72).
 //   * few sinks (kNarrow at most in their last tile): that tile's S is formed for 32
 //     keys and its P V summed over 32 (4 sinks, window 1024: 157 -> 151 us; 16384
 //     queries, 16 / 4 heads, window 256: 93 -> 79).
@@ -46,6 +50,7 @@ namespace {
 
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kNarrow = 32;  // keys of a tile with a few sinks
+constexpr int kParts = 8;     // blocks to an item, at most
 
 template <int D>
 struct WfCfg : TileLayout<D> {
@@ -95,10 +100,11 @@ struct WfCfg : TileLayout<D> {
 // copy, swizzled so that rows by threads and units by threads meet no bank twice.
 __device__ __forceinline__ uint32_t staged(int row, int u) { return static_cast<uint32_t>(row * 128 + ((u ^ (row & 7)) << 4)); }
 
-template <int D, bool BF16>
+// SPLIT: a cluster of `parts` blocks to an item, each with its share of the positions.
+template <int D, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
     attn_window_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                           const __grid_constant__ CUtensorMap mv, const WindowArgs a, int nrows, int group) {
+                           const __grid_constant__ CUtensorMap mv, const WindowArgs a, int nrows, int group, int parts) {
   using C = WfCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -133,6 +139,9 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
   tc_fence_after_sync();
   const uint32_t tmem = *slot;
   const Items items = {sbase + C::OFF_NEXT, bar(C::B_NEXT), bar(C::B_READ), abort_flag, a.status};
+  const int first_item = SPLIT ? blockIdx.x / parts : blockIdx.x, part = SPLIT ? blockIdx.x % parts : 0;
+  auto from = [&](const RowItem& it) { return SPLIT ? it.npos * part / parts : 0; };
+  auto upto = [&](const RowItem& it) { return SPLIT ? it.npos * (part + 1) / parts : it.npos; };
   // `n` counts positions over all items and gives stages and phases.
   // The last tile of sinks may have few of them: then kNarrow of its keys are enough.
   auto narrow = [&](const RowItem& it, int p) { return p == it.ns - 1 && a.sinks - p * 128 <= kNarrow; };
@@ -148,17 +157,20 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
       int nk = 0, nv = 0, nq = 0;  // issued
       bool ok = true;
       int asked = 0;
-      for (int i = blockIdx.x; ok && i >= 0;) {
-        if (!(ok = items.ask(asked))) break;
-        ++asked;
+      for (int i = first_item; ok && i >= 0;) {
+        if (!SPLIT) {
+          if (!(ok = items.ask(asked))) break;
+          ++asked;
+        }
         const RowItem it(a, i, nrows, group);
-        for (int p = 0; p < it.npos; ++p) {
+        const int p0 = from(it), p1 = upto(it);
+        for (int p = p0; p < p1; ++p) {
           const int s = nk % C::NST, turn = (nk / C::NST - 1) & 1;
           if (nk >= C::NST && !(ok = mbar_wait(bar(C::B_KEMPTY + s), turn, abort_flag, a.status))) break;
           mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::TILE);
           load(sK + s * C::TILE, &mk, bar(C::B_KFULL + s), it.key0(p), it.hk, it.b);
           ++nk;
-          if (p == 0) {
+          if (p == p0) {
             if (nq > 0 && !(ok = mbar_wait(bar(C::B_QEMPTY), (nq - 1) & 1, abort_flag, a.status))) break;
             mbar_arrive_expect_tx(bar(C::B_Q), C::TILE);
             load(sbase, &mq, bar(C::B_Q), it.row0, it.h, it.b);
@@ -169,7 +181,7 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
           load(sV + s * C::TILE, &mv, bar(C::B_VFULL + s), it.key0(p), it.hk, it.b);
           ++nv;
         }
-        i = items.after(asked - 1, ok);
+        i = SPLIT ? -1 : items.after(asked - 1, ok);
       }
       if (*abort_flag) {  // what is in flight lands before the shared memory goes
         items.drain_last(asked);
@@ -193,10 +205,10 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
       bool ok = true;
       int n0 = 0;  // positions of the items before
       IdleWatch watch;
-      for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
+      for (int i = first_item, k = 0; ok && i >= 0; ++k) {
         const RowItem it(a, i, nrows, group);
-        const int end = n0 + it.npos, thin = it.ns > 0 && narrow(it, it.ns - 1) ? n0 + it.ns - 1 : -1;
-        ok = mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
+        const int p0 = from(it), end = n0 + upto(it) - p0, thin = it.ns > 0 && narrow(it, it.ns - 1) ? n0 + it.ns - 1 - p0 : -1;
+        if (!SPLIT || n0 < end) ok = mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
         int js = n0, jp = n0;          // next S and P V
         int k_seen = n0, v_seen = n0;  // positions whose loads have been seen to land
         const uint32_t q_lo = smem_desc_lo(sbase, 16);
@@ -234,6 +246,7 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
           else ok = watch.idle(abort_flag, a.status, kWaitLimitNs);
         }
         n0 = end;
+        if (SPLIT) break;
         i = items.after(k, ok);
         items.read(k);
       }
@@ -255,9 +268,9 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
     };
     bool ok = true;
     int n = 0;
-    for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
+    for (int i = first_item, k = 0; ok && i >= 0; ++k) {
       const RowItem it(a, i, nrows, group);
-      const int row = it.row0 + r;
+      const int p0 = from(it), p1 = upto(it), row = it.row0 + r;
       float m = -INFINITY, l_exact = 0.f, l_round = 0.f;
       // A position with W of its tile's keys.
       auto step = [&](int p, auto width) {
@@ -267,8 +280,8 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
         tc_fence_after_sync();
         if (r == 0) {
           mbar_arrive(bar(C::B_KEMPTY + n % C::NST));
-          if (!C::APART && p > 0) mbar_arrive(bar(C::B_VEMPTY + (n - 1) % C::NST));
-          if (p == it.npos - 1) mbar_arrive(bar(C::B_QEMPTY));
+          if (!C::APART && p > p0) mbar_arrive(bar(C::B_VEMPTY + (n - 1) % C::NST));
+          if (p == p1 - 1) mbar_arrive(bar(C::B_QEMPTY));
         }
         float sv[W];
         if constexpr (W == 128) {
@@ -333,13 +346,13 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
           sv[c] = ex2_approx(t.x);
           sv[c + 1] = ex2_approx(t.y);
         }
-        if (C::APART && p > 0) {  // P V(n - 1) is complete: P may be written, O is what it will be
+        if (C::APART && p > p0) {  // P V(n - 1) is complete: P may be written, O is what it will be
           ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O), (n - 1) & 1, abort_flag, a.status));
           if (!ok) return;
           tc_fence_after_sync();
           release(C::B_VEMPTY, n - 1);
         }
-        if (p > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (p > p0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
           for (int c0 = 0; c0 < D / 32; ++c0) {
             uint32_t ov[32];
@@ -378,9 +391,27 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
         l_round = l_round * alpha + ((r0 + r1) + (r2 + r3));
         ++n;
       };
-      for (int p = 0; ok && p < it.npos; ++p) {
+      for (int p = p0; ok && p < p1; ++p) {
         if (narrow(it, p)) step(p, std::integral_constant<int, kNarrow>{});
         else step(p, std::integral_constant<int, 128>{});
+      }
+      if constexpr (SPLIT) {
+        // O as it is, in fp32, m and l, where Q, K and V were, whose loads and products are
+        // complete; 16 bytes of a warp's rows side by side.
+        if (p1 > p0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_O), (n - 1) & 1, abort_flag, a.status));
+        tc_fence_after_sync();
+        float* mine = reinterpret_cast<float*>(smem);
+        if (p1 > p0 && ok) {
+#pragma unroll
+          for (int c0 = 0; c0 < D / 32; ++c0) {
+            uint32_t ov[32];
+            tmem_ld32(tO + c0 * 32, ov);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(mine)[(c0 * 8 + e) * 128 + r] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          }
+        }
+        mine[128 * D + r] = ok ? m : -INFINITY, mine[128 * D + 128 + r] = l_exact, mine[128 * D + 256 + r] = l_round;
+        break;
       }
       // -------------------------------------------------------------- output
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(C::B_O), (n - 1) & 1, abort_flag, a.status));
@@ -420,12 +451,72 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
       items.read_by_warp(k, lane, ok);
     }
   }
+  if constexpr (SPLIT) {
+    static_assert(128 * D * 4 + 3 * 512 <= C::OFF_BAR, "a part's results");
+    cluster_sync();
+    if (warp < C::W_LOAD) {
+      // A block has 128 / parts of the rows, a thread D / parts channels of one; parts in order.
+      const RowItem it(a, first_item, nrows, group);
+      const int rows = 128 / parts, rr = part * rows + threadIdx.x % rows, row = it.row0 + rr;  // (parts is a power of two)
+      const int c0 = threadIdx.x / rows * (D / 4 / parts), c1 = c0 + D / 4 / parts;              // in fours
+      if (row < a.Nq) {
+        float f[kParts], e[kParts], l[kParts], m = -INFINITY, l_exact = 0.f, l_round = 0.f;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          const uint32_t at = in_block(sbase, k < parts ? k : 0) + (128 * D + rr) * 4;
+          f[k] = load_cluster4(at), e[k] = load_cluster4(at + 512), l[k] = load_cluster4(at + 1024);
+          if (k >= parts) f[k] = -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) m = fmaxf(m, f[k]);
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          f[k] = f[k] == -INFINITY ? 0.f : ex2_approx(f[k] - m);  // 0: sees none of this row's keys
+          l_exact += f[k] * e[k], l_round += f[k] * l[k];
+        }
+        const float inv = 1.0f / l_round;
+        uint8_t* out = a.o.p + it.b * a.o.b + it.h * a.o.h + row * a.o.n;
+        for (int c = c0; c < c1; c += 2) {  // (an odd one out at the end goes alone)
+          float o[8] = {};
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) {
+            if (f[k] == 0.f) continue;  // also where there is no O
+            const uint32_t at = in_block(sbase, k) + rr * 16;
+            const float4 u = load_cluster16(at + c * 2048), v = load_cluster16(at + min(c + 1, c1 - 1) * 2048);
+            o[0] += f[k] * u.x, o[1] += f[k] * u.y, o[2] += f[k] * u.z, o[3] += f[k] * u.w;
+            o[4] += f[k] * v.x, o[5] += f[k] * v.y, o[6] += f[k] * v.z, o[7] += f[k] * v.w;
+          }
+          *reinterpret_cast<uint2*>(out + c * 8) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
+          if (c + 1 < c1)
+            *reinterpret_cast<uint2*>(out + c * 8 + 8) = make_uint2(pack2<BF16>(o[4] * inv, o[5] * inv), pack2<BF16>(o[6] * inv, o[7] * inv));
+        }
+        if (c0 == 0) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] = (m + log2f(l_exact)) * 0.69314718055994531f;
+      }
+    }
+    cluster_sync();  // nobody's shared memory goes before it is read
+  }
   tc_fence_before_sync();
   __syncthreads();
   if (warp == C::W_MMA) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::COLS);
   }
+}
+
+// Blocks to an item, a power of two: as many as the GPU holds, two to an SM, if that
+// takes enough positions out of the longest item's chain.  A position in one CTA takes
+// 0.9 (d = 32) to 1.2 us (128), the join 2 to 3 us, more with two CTAs to every SM and most
+// with two parts, who have the most rows each to join.  128 queries, d = 128, one block
+// and several: 8 heads, window 256 14.0 and 12.4 us, 1024 23.2 and 12.2, 4096 58.2 and
+// 16.5; 64 heads, window 256 14.1 and 16.9, 512 17.2 and 17.8, 768 20.4 and 18.7; 120
+// heads, window 1024 24.0 and 26.1, 2048 36.4 and 33.6.
+int parts_of(const WindowArgs& a, int64_t items) {
+  const int64_t most = std::min<int64_t>((a.Nk + 127) / 128, (a.window + 254) / 128 + 1 + (a.sinks + 127) / 128);  // positions
+  const int64_t sms = device_sm_count();
+  int parts = 1;
+  while (parts < kParts && items * parts * 2 <= 2 * sms && most >= 2 * parts) parts *= 2;
+  const int least = items * parts <= sms ? 3 : parts > 2 ? 6 : 8;
+  return most - (most + parts - 1) / parts >= least ? parts : 1;
 }
 
 template <int D, bool BF16>
@@ -435,14 +526,15 @@ int launch_t(const WindowArgs& a) {
   if (!encode_strided_map(&mq, a.q, a.B, a.Hq, a.Nq, D, C::CH, BF16) || !encode_strided_map(&mk, a.k, a.B, a.Hk, a.Nk, D, C::CH, BF16) ||
       !encode_strided_map(&mv, a.v, a.B, a.Hk, a.Nk, D, C::CH, BF16))
     return kStatusCuda;
-  auto kern = attn_window_fwd_kernel<D, BF16>;
-  if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return kStatusCuda;
-  if (!check_launch_regs(reinterpret_cast<const void*>(kern), C::REGS)) return kStatusDeviceCheck;  // the split's sum
   const int nrows = (a.Nq + 127) / 128, heads = a.B * a.Hq;
   const int64_t items = static_cast<int64_t>(nrows) * heads;
   if (items > 0x7fffffff) return kStatusUnsupported;
+  const int parts = parts_of(a, items);
+  auto kern = parts > 1 ? attn_window_fwd_kernel<D, BF16, true> : attn_window_fwd_kernel<D, BF16, false>;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return kStatusCuda;
+  if (!check_launch_regs(reinterpret_cast<const void*>(kern), C::REGS)) return kStatusDeviceCheck;  // the split's sum
   const int group = order_head_group(heads, int64_t{4} * a.Nk * D, int64_t{128} << 20);
-  return launch_serialized(true, kern, dim3(static_cast<unsigned>(items)), dim3(C::THREADS), C::SMEM, a.stream, mq, mk, mv, a, nrows, group) ==
+  return launch_clusters(parts, kern, static_cast<unsigned>(items * parts), C::THREADS, C::SMEM, a.stream, mq, mk, mv, a, nrows, group, parts) ==
                  cudaSuccess
              ? kStatusOk
              : kStatusCuda;

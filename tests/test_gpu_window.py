@@ -228,6 +228,56 @@ def test_drawn_shapes(pkg, seed):
     _check(pkg, *_inputs(*args), int(2 ** r.uniform(0, 11)), r.choice([0, 1, 4, 127, 128, 129, 500]))
 
 
+FEW = [
+    # several blocks to an item: eight, four, two; items shorter than the blocks are many (the causal masks)
+    (1, 8, 2, 1, 9000, 9000, 0),
+    (1, 4, 4, 16, 3000, 2500, 130),
+    (1, 2, 1, 130, 2500, 1100, 4),
+    (2, 1, 1, 1500, 1500, 1500, 0),
+    (1, 4, 1, 100, 700, 256, 4),
+    (1, 64, 8, 128, 1500, 1300, 4),
+    (1, 100, 4, 100, 2600, 2500, 1),
+]
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype,layout", [(32, BF16, "tokens"), (64, F16, "slices"), (128, BF16, "heads"), (128, F16, "tokens")])
+@pytest.mark.parametrize("shape", FEW, ids=lambda s: "x".join(map(str, s)))
+def test_few_rows_over_many_keys(pkg, shape, d, dtype, layout):
+    B, Hq, Hk, nq, nk, window, sinks = shape
+    q, k, v, _ = _inputs(B, Hq, Hk, nq, nk, d, dtype, layout, nk + d)
+    o, lse = _check(pkg, q, k, v, None, window, sinks)
+    again = pkg.attn_fwd_window(q, k, v, window, sinks)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@gpu
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_parts_of_very_different_weight(pkg, d):
+    """Logits of a hundred, and a part that holds nearly all of a row's weight."""
+    q, k, v, do = _inputs(1, 2, 1, 40, 4000, d, BF16, "tokens", 8, spread=4.0)
+    _check(pkg, q, k, v, do, 3500, 9)
+    k[:, :, 1000:1128] *= 2
+    _check(pkg, q, k, v, None, 3500, 9, scale=-0.2)
+
+
+@gpu
+def test_captured_parts_replay(pkg):
+    q, k, v, _ = _inputs(1, 4, 2, 8, 5000, 64, F16, "heads", 9)
+    pkg.attn_fwd_window(q, k, v, 4096, 4)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = pkg.attn_fwd_window(q, k, v, 4096, 4)
+    for seed in (10, 11):
+        fresh = _inputs(1, 4, 2, 8, 5000, 64, F16, "heads", seed)
+        for x, y in zip((q, k, v), fresh):
+            x.copy_(y)
+        graph.replay()
+        want = pkg.attn_fwd_window(q, k, v, 4096, 4)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert pkg.sync_status() == 0
+
+
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_long_sequence(pkg, d):
