@@ -11,9 +11,9 @@
 // The tensor cores bound it (4 d flops a pair against 4 d bytes a key for 128
 // rows): a tile of 128 keys at d = 128 is 16 products of 128 x 128 x 16, which take 118
 // cycles each from shared memory and 96 with P from TMEM, 1700 in all, and goes by in
-// 1900 where the list is long (32768 queries, 32 / 8 heads, window 4096: 1.72 ms, 1200
+// 1900 where the list is long (32768 queries, 32 / 8 heads, window 4096: 1.74 ms, 1190
 // TFLOP/s of visible pairs); edge tiles, half of which is hidden, and an item's start
-// and end make window 1024 slower (8192 queries: 151 us, 857).  GB300 mapping:
+// and end make window 1024 slower (8192 queries: 152 us, 850).  GB300 mapping:
 //   * an item is 128 query rows of a head; two CTAs to an SM, so that one's softmax
 //     meets the other's matrix products.  Blocks take over the items of blocks that
 //     have not started (cluster launch control) and load the next item's first tiles
