@@ -24,7 +24,8 @@ import torch
 
 __all__ = ["attention", "attn_fwd", "attn_bwd", "attn_fwd_dropout", "attn_bwd_dropout", "attn_decode", "attn_fwd_fp8", "attn_fwd_blocksparse", "attn_bwd_blocksparse",
            "attn_fwd_blocksparse_dropout", "attn_bwd_blocksparse_dropout", "attn_fwd_window", "attn_bwd_window", "PagedKV",
-           "attn_paged_assign", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_window", "attn_paged_select", "rotation_tables", "sync_status", "status_string", "last_launch_count", "lib",
+           "attn_paged_assign", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_window", "attn_paged_select",
+           "rotation_tables", "sync_status", "status_string", "last_launch_count", "lib",
            "AttnError", "LIB_PATH", "STATUS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn.so")
