@@ -51,6 +51,14 @@ namespace {
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kNarrow = 32;  // keys of a tile with a few sinks
 constexpr int kParts = 8;     // blocks to an item, at most
+// Weights are 2^kShift at the maximum.  fp16 ends at 2^16 and is normal from 2^-14 on:
+// with 2^7 under a maximum that may lie 2^8 behind, weights keep their bits down to
+// 2^-21 of the largest, as those beside a sink are that holds nearly all of it, where
+// 2^0 keeps them to 2^-14.  bf16 has fp32's range.
+template <bool BF16>
+constexpr float kShift = BF16 ? 0.f : 7.f;
+template <bool BF16>
+constexpr float kUnshift = BF16 ? 1.f : 1.f / 128;  // 2^-kShift
 
 template <int D>
 struct WfCfg : TileLayout<D> {
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
           alpha = ex2_approx(m - m_new);
           m = m_new;
         }
-        const float neg_m = m == -INFINITY ? 0.f : -m;
+        const float neg_m = m == -INFINITY ? 0.f : BF16 ? -m : kShift<BF16> - m;
         const float2 nm2 = make_float2(neg_m, neg_m);
 #pragma unroll
         for (int c = 0; c < W; c += 2) {
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
           __syncwarp();
         }
       }
-      if (row < a.Nq) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] = (m + log2f(l_exact)) * 0.69314718055994531f;
+      if (row < a.Nq) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] = (m + log2f(l_exact * kUnshift<BF16>)) * 0.69314718055994531f;
       tc_fence_before_sync();  // O is read before this thread's next P lets it be overwritten
       i = items.after(k, ok);
       items.read_by_warp(k, lane, ok);
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
           if (c + 1 < c1)
             *reinterpret_cast<uint2*>(out + c * 8 + 8) = make_uint2(pack2<BF16>(o[4] * inv, o[5] * inv), pack2<BF16>(o[6] * inv, o[7] * inv));
         }
-        if (c0 == 0) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] = (m + log2f(l_exact)) * 0.69314718055994531f;
+        if (c0 == 0) a.lse[(static_cast<int64_t>(it.b) * a.Hq + it.h) * a.Nq + row] = (m + log2f(l_exact * kUnshift<BF16>)) * 0.69314718055994531f;
       }
     }
     cluster_sync();  // nobody's shared memory goes before it is read
