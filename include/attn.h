@@ -463,11 +463,15 @@ int attn_fwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_
  * (o and lse from that call), as attn_bwd's; dk and dv are the sums over the
  * query heads that share a key/value head, and 0 for keys that no query sees.
  * A call repeats bit for bit.
+ * With fp16 P and dS are operands of 16-bit products in a range of their own, by
+ * powers of two taken from the largest rows of dO and v, so that gradients far below
+ * or above 1 keep their bits: for dQ down to 2^-28 of 2 |dO row| |v row|, for dK of
+ * that with the largest row of dO of the query heads that share the key.
  *   workspace : attn_bwd_window_workspace() bytes of device memory, 16-byte aligned,
- *          the call's own until it is done: two fp32 row vectors, and fp32 partial
- *          tiles of dK and dV where a tile of keys has many more queries than others
- *          (the sinks) or there are few of them.
- * Launches 2 or 3 kernels.
+ *          the call's own until it is done: two fp32 row vectors, fp32 partial tiles
+ *          of dK and dV where a tile of keys has many more queries than others
+ *          (the sinks) or there are few of them, and those largest rows.
+ * Launches 2 or 3 kernels, with fp16 one more.
  */
 int attn_bwd_window(const attn_bhnd_t* q, const attn_bhnd_t* k, const attn_bhnd_t* v, const attn_bhnd_t* o,
                     const attn_bhnd_t* dO, const float* lse, const attn_bhnd_t* dq, const attn_bhnd_t* dk,
@@ -520,7 +524,7 @@ const char* attn_status_string(int status);
 
 /* Number of kernel launches the most recent successful attn_fwd* / attn_bwd* /
  * attn_decode / attn_paged_* call on this thread enqueued (forward 1, backward 3,
- * decode 2, window backward 2 or 3, paged append 1, paged decode 1 or 2, paged select 2,
+ * decode 2, window backward 2 to 4, paged append 1, paged decode 1 or 2, paged select 2,
  * paged assign 1 or 2). */
 int attn_last_launch_count(void);
 

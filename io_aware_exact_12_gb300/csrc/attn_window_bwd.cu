@@ -5,6 +5,8 @@
 // the sums also over the query heads that share the key/value head
 // (FlashAttention (PKM page), "三招" 3 Recomputation; FlashAttention深度攻略 §6).
 //
+//   attn_window_range_kernel : fp16 only: the largest rows of dO and v, from which come
+//       the powers of two that keep dS in fp16's range (F16Range).
 //   attn_window_dq_kernel  : an item is 128 query rows of a head, which walk the key
 //       tiles they see as the forward does: S = Q K^T, dP = dO V^T, dQ += dS K.  It
 //       also leaves -D and -LSE log2(e) of its rows for the next kernel.
@@ -31,7 +33,7 @@
 // are the rest.
 //
 // P and dS are fp32 until they become operands of 16-bit products, rounded to the
-// inputs' type; everything is summed in fp32.  (Gradients are off by 2.4e-3 in norm
+// inputs' type (fp16: times powers of two); everything is summed in fp32.  (Gradients are off by 2.4e-3 in norm
 // with bf16, where fp32 operands and the results' own rounding make 1.7e-3.)
 //
 // Both loops run on tcgen05, one CTA to an SM: warps 0-7 work on rows, two threads to
@@ -56,9 +58,46 @@ struct WbPlan {
   int runs, sink_runs;         // CTAs to a cut tile and to one with sinks
   int group;                   // heads in flight together
   int npad;                    // rows of a head's row vectors
-  float *lse2, *dvec;          // row vectors, padded to whole tiles (-inf, 0)
+  float *lse2, *dvec;          // row vectors, padded to whole tiles (-inf, 0), as F16Range has them
   float* part;                 // [item in runs][dK, dV][128][d]
+  int blocks;                  // of the range kernel to a key/value head (fp16)
+  float2* most;                // [B * Hk][blocks] largest |dO row|^2 and |v|^2
 };
+
+// What brings P and dS into fp16's range, normal from 2^-14 to 2^16, where they are
+// operands: P = 1 / 1000 of a window times a dO of 1 / 1000 is below it, and a dO of
+// 1000 times v of 20 past it.  P is at most 1 and goes as 2^kP P.  O is a mean of rows
+// of v, so |dP - D| <= 2 |dO| |v| with the rows' norms, and dS goes as 2^e dS with the
+// largest whole e for which that is at most 2^kP (a factor of 4 is left for
+// roundings).  The norms are a row's own and v's largest for dQ; for dK, which sums over
+// rows, the largest of all rows of the query heads that share the key.  Powers of two
+// round nothing, and 2^14 above fp16's last normal number leaves 2^28 for rows and
+// weights below the largest.  bf16 has fp32's range.
+struct F16Range {
+  static constexpr float kP = 14.f;
+  static constexpr float kInvP = 1.f / 16384;
+  float in, out;  // 2^(e - kP), which makes 2^e dS of 2^kP P, and 2^-e
+  // From squared norms, of finite fp16 rows (their product is in fp32's range).
+  __device__ __forceinline__ F16Range(float rows, float values) {
+    const float m = rows * values;
+    const int e = m > 0.f && m < INFINITY ? 12 - (((__float_as_int(m) >> 23) - 127) >> 1) : 0;  // |dO| |v| < 2^(13 - e)
+    in = __int_as_float((e - 14 + 127) << 23);
+    out = __int_as_float((127 - e) << 23);
+  }
+};
+
+// Maximum of the warp's values, none below 0: as whole numbers, their bits have the same order.
+__device__ __forceinline__ float warp_max(float x) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x))); }
+
+// The largest squared norms that the range kernel's blocks found for a key/value head; by a whole warp.
+__device__ __forceinline__ float2 most_of(const WbPlan& p, int64_t head, int lane) {
+  float2 m = make_float2(0.f, 0.f);
+  for (int x = lane; x < p.blocks; x += 32) {
+    const float2 y = p.most[head * p.blocks + x];
+    m = make_float2(fmaxf(m.x, y.x), fmaxf(m.y, y.y));
+  }
+  return make_float2(warp_max(m.x), warp_max(m.y));
+}
 
 // What both kernels share.
 template <int D>
@@ -80,7 +119,8 @@ struct DqCfg : Tile<D> {
   static constexpr int OFF_K = 2 * T::TILE;
   static constexpr int OFF_V = OFF_K + NK * T::TILE;
   static constexpr int OFF_ROWS = OFF_V + NV * T::TILE;  // [2][2][128] fp32: halves of D, of two items
-  static constexpr int OFF_BAR = OFF_ROWS + 4 * 512;
+  static constexpr int OFF_NORMS = OFF_ROWS + 4 * 512;   // [2][2][128] bytes: exponents of halves of |dO|^2 (fp16)
+  static constexpr int OFF_BAR = OFF_NORMS + 512;
   static constexpr int B_Q = 0;
   static constexpr int B_QEMPTY = 1;
   static constexpr int B_KFULL = 2;
@@ -169,6 +209,67 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint3
     if (r < rows) *reinterpret_cast<uint4*>(out + r * stride + u * 16) = val;
   }
   __syncwarp();
+}
+
+template <bool BF16>
+__device__ __forceinline__ float scaled(uint32_t x, float unmul, float scale) {
+  return (BF16 ? __uint_as_float(x) : __uint_as_float(x) * unmul) * scale;
+}
+
+// Sum of squares of eight fp16 values.
+__device__ __forceinline__ float square_of(const uint4& v) {
+  const float2 a = unpack2<false>(v.x), b = unpack2<false>(v.y), c = unpack2<false>(v.z), d = unpack2<false>(v.w);
+  return ((a.x * a.x + a.y * a.y) + (b.x * b.x + b.y * b.y)) + ((c.x * c.x + c.y * c.y) + (d.x * d.x + d.y * d.y));
+}
+
+// ---------------------------------------------------------------------- range
+// Largest squared norms of the rows of dO and of the v that are seen, a block's share of a key/value
+// head's; the row kernels join the blocks' (most_of).  16 bytes a thread, D / 8 threads
+// to a row.  Bytes bound it where it is more than a launch: 84 MB of two sequences of
+// 8192, 16 / 4 heads of 128, in 20 us, of 12.4 at the copy's rate.  With it and what
+// the row kernels do with it, fp16's backward takes 528 us there where bf16's takes 487,
+// 86 against 77 for eight of 1024, 12 heads of 64, 21.6 against 18.6 for two of 500, 8 heads of 32.
+constexpr int kRangeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kRangeThreads) attn_window_range_kernel(const WindowArgs a, const WbPlan p) {
+  griddep_wait();  // launched overlapped (launch_serialized)
+  griddep_launch_dependents();
+  constexpr int U = D / 8, ROWS = kRangeThreads / U, AHEAD = 4;
+  const int part = blockIdx.x, hb = blockIdx.y, b = hb / a.Hk, hk = hb - b * a.Hk, G = a.Hq / a.Hk;
+  const int u = threadIdx.x % U, in_warp = threadIdx.x % 32 / U, step = p.blocks * ROWS;
+  const int first = part * ROWS + static_cast<int>(threadIdx.x) / 32 * (32 / U);  // of the warp's rows
+  auto most = [&](const uint8_t* base, int64_t stride, int from, int n) {
+    float m = 0.f;
+    for (int w0 = from + first; w0 < n; w0 += AHEAD * step) {
+      const int r0 = w0 + in_warp;
+      uint4 v[AHEAD];
+#pragma unroll
+      for (int x = 0; x < AHEAD; ++x)
+        v[x] = r0 + x * step < n ? *reinterpret_cast<const uint4*>(base + (r0 + x * step) * stride + u * 16) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int x = 0; x < AHEAD; ++x) {
+        float s = square_of(v[x]);
+#pragma unroll
+        for (int y = 1; y < U; y <<= 1) s += __shfl_xor_sync(0xffffffffu, s, y);
+        m = fmaxf(m, s);
+      }
+    }
+    return m;
+  };
+  // Keys that some query sees: the sinks, and from the first query's window on.
+  const uint8_t* v = a.v.p + b * a.v.b + hk * a.v.h;
+  const int near = max(0, a.Nk - a.Nq - a.window + 1);
+  float2 m = make_float2(0.f, fmaxf(most(v, a.v.n, 0, min(a.sinks, near)), most(v, a.v.n, near, a.Nk)));
+  for (int g = 0; g < G; ++g) m.x = fmaxf(m.x, most(a.dO.p + b * a.dO.b + (hk * G + g) * a.dO.h, a.dO.n, 0, a.Nq));
+  __shared__ float2 warps[kRangeThreads / 32];
+  m = make_float2(warp_max(m.x), warp_max(m.y));
+  if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (const float2& w : warps) m = make_float2(fmaxf(m.x, w.x), fmaxf(m.y, w.y));
+    p.most[static_cast<int64_t>(hb) * p.blocks + part] = m;
+  }
 }
 
 // ------------------------------------------------------------------------- dQ
@@ -339,12 +440,14 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       const RowItem it(a, i, nrows, group);
       const int row = it.row0 + r;
       const int64_t bh = static_cast<int64_t>(it.b) * a.Hq + it.h;
-      const float lse2 = row < a.Nq ? -a.lse[bh * a.Nq + row] * kLog2e : -INFINITY;
+      const float lse2 = row < a.Nq ? -a.lse[bh * a.Nq + row] * kLog2e + (BF16 ? 0.f : F16Range::kP) : -INFINITY;
+      float2 most = make_float2(0.f, 0.f);
+      if constexpr (!BF16) most = most_of(pl, static_cast<int64_t>(it.b) * a.Hk + it.hk, lane);
       // D, half a row a thread, while the first products run.
       ok = mbar_wait(bar(C::B_KFULL + (n + k) % C::NK), ((n + k) / C::NK) & 1, abort_flag, a.status) &&
            mbar_wait(bar(C::B_Q), k & 1, abort_flag, a.status);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      float d = 0.f;
+      float d = 0.f, norm = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const uint32_t at = tile_unit<D>(r, half * (D / 16) + c);
@@ -355,22 +458,30 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
         for (int e = 0; e < 4; ++e) {
           const float2 f = unpack2<BF16>(xw[e]), g = unpack2<BF16>(yw[e]);
           d = fmaf(f.x, g.x, fmaf(f.y, g.y, d));
+          if (!BF16) norm = fmaf(g.x, g.x, fmaf(g.y, g.y, norm));
         }
       }
       float* sum = reinterpret_cast<float*>(smem + C::OFF_ROWS) + (k & 1) * 256 + r;  // (who writes here again has waited for the item between)
+      uint8_t* norms = smem + C::OFF_NORMS + (k & 1) * 256 + r;
       sum[half * 128] = d;
+      if (!BF16) norms[half * 128] = static_cast<uint8_t>(__float_as_uint(norm) >> 23);
       mbar_arrive(bar(C::B_ROWS));
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_ROWS), k & 1, abort_flag, a.status)))) break;
       if (threadIdx.x == 0) {
         fence_proxy_async_smem();  // O is read before its stage is loaded again
         mbar_arrive(bar(C::B_KEMPTY + (n + k) % C::NK));
       }
-      const float nd = -(sum[0] + sum[128]);
+      float nd = -(sum[0] + sum[128]), mul = 1.f, unmul = 1.f;
       if (half == 0) {
         pl.lse2[bh * pl.npad + row] = lse2;
-        pl.dvec[bh * pl.npad + row] = nd;
+        pl.dvec[bh * pl.npad + row] = BF16 ? nd : nd * F16Range(most.x, most.y).in;
       }
-      const float2 l2 = make_float2(lse2, lse2), nd2 = make_float2(nd, nd);
+      if constexpr (!BF16) {
+        const int up = max(norms[0], norms[128]);  // |dO|^2 < 2^(up - 125)
+        const F16Range range(up ? __int_as_float((up + 2) << 23) : 0.f, most.y);
+        mul = range.in, unmul = range.out, nd *= mul;
+      }
+      const float2 l2 = make_float2(lse2, lse2), nd2 = make_float2(nd, nd), mul2x2 = make_float2(mul, mul);
       for (int p = 0; p < it.npos; ++p, ++n) {
         // (a warp's lanes go on or stop together: what follows wants all of them)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_S + (n & 1)), (n >> 1) & 1, abort_flag, a.status)))) break;
@@ -414,7 +525,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
         mbar_arrive(bar(C::B_TAKEN));
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float2 gd = add2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd2);
+          const float2 x = make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), gd = BF16 ? add2(x, nd2) : fma2(x, mul2x2, nd2);
           const float2 ds = mul2(make_float2(pr[2 * e], pr[2 * e + 1]), gd);
           pk[e] = pack2<BF16>(ds.x, ds.y);
         }
@@ -440,7 +551,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
             uint32_t w[4];
 #pragma unroll
             for (int f = 0; f < 4; ++f)
-              w[f] = pack2<BF16>(__uint_as_float(x[8 * e + 2 * f]) * a.scale, __uint_as_float(x[8 * e + 2 * f + 1]) * a.scale);
+              w[f] = pack2<BF16>(scaled<BF16>(x[8 * e + 2 * f], unmul, a.scale), scaled<BF16>(x[8 * e + 2 * f + 1], unmul, a.scale));
             *reinterpret_cast<uint4*>(out + row * a.dq.n + c * 2 + e * 16) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
@@ -674,6 +785,13 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       // Row i sees this key iff from <= i < to.
       const int from = j < a.Nk ? j - off : a.Nq, to = j < a.sinks ? a.Nq : j - off + a.window;
       Visit v = w.first;
+      float2 mul2x2 = make_float2(1.f, 1.f);
+      float unmul = 1.f;
+      if (!BF16 && w.nv > 0) {  // (D's vector has `in` already)
+        const float2 most = most_of(p, static_cast<int64_t>(w.b) * a.Hk + w.hk, lane);
+        const F16Range range(most.x, most.y);
+        mul2x2 = make_float2(range.in, range.in), unmul = half ? F16Range::kInvP : range.out;
+      }
       for (int it = 0; it < w.nv; ++it, ++n, w.advance(v)) {
         const int s = n % C::NST, q0 = v.qt * 128 + half * 64;
         // (a warp's lanes go on or stop together: what follows wants all of them)
@@ -719,7 +837,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         tmem_ld64(tDP, dp);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float2 gd = add2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd[e]);
+          const float2 x = make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), gd = BF16 ? add2(x, nd[e]) : fma2(x, mul2x2, nd[e]);
           const float2 ds = mul2(make_float2(pr[2 * e], pr[2 * e + 1]), gd);
           pk[e] = pack2<BF16>(ds.x, ds.y);
         }
@@ -746,8 +864,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
             tmem_ld32(col + c0 * 32, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              partial[c0 * 8 + e] = make_float4(__uint_as_float(x[4 * e]) * mul, __uint_as_float(x[4 * e + 1]) * mul,
-                                                __uint_as_float(x[4 * e + 2]) * mul, __uint_as_float(x[4 * e + 3]) * mul);
+              partial[c0 * 8 + e] = make_float4(scaled<BF16>(x[4 * e], unmul, mul), scaled<BF16>(x[4 * e + 1], unmul, mul),
+                                                scaled<BF16>(x[4 * e + 2], unmul, mul), scaled<BF16>(x[4 * e + 3], unmul, mul));
           }
         } else if constexpr (C::STAGE) {
           const int row_w = w.kv0 + (warp & 3) * 32;
@@ -756,7 +874,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
             uint32_t x[64], y[32];
             tmem_ld64(col + c0 * 64, x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = pack2<BF16>(__uint_as_float(x[2 * e]) * mul, __uint_as_float(x[2 * e + 1]) * mul);
+            for (int e = 0; e < 32; ++e) y[e] = pack2<BF16>(scaled<BF16>(x[2 * e], unmul, mul), scaled<BF16>(x[2 * e + 1], unmul, mul));
             store_rows(smem + C::OFF_STAGE + warp * 4096, lane, y, out + row_w * dst.n + c0 * 128, dst.n, a.Nk - row_w);
           }
         } else {
@@ -770,7 +888,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
                 uint32_t y[4];
 #pragma unroll
                 for (int f = 0; f < 4; ++f)
-                  y[f] = pack2<BF16>(__uint_as_float(x[8 * e + 2 * f]) * mul, __uint_as_float(x[8 * e + 2 * f + 1]) * mul);
+                  y[f] = pack2<BF16>(scaled<BF16>(x[8 * e + 2 * f], unmul, mul), scaled<BF16>(x[8 * e + 2 * f + 1], unmul, mul));
                 *reinterpret_cast<uint4*>(out + j * dst.n + c0 * 64 + e * 16) = make_uint4(y[0], y[1], y[2], y[3]);
               }
             }
@@ -864,6 +982,9 @@ void plan_runs(const WindowArgs& a, WbPlan* p) {
 int64_t plan(const WindowArgs& a, WbPlan* p) {
   plan_runs(a, p);
   p->npad = (a.Nq + 127) / 128 * 128;
+  // Blocks of the range kernel to a head: four rounds of loads each, about eight to an SM in all.
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hk, rows = std::min<int64_t>(a.Nk, static_cast<int64_t>(a.Nq) + a.window), round = 4 * kRangeThreads * 8 / a.d;
+  p->blocks = static_cast<int>(std::max<int64_t>(1, std::min({(rows + round - 1) / round, 8 * 152 / heads, int64_t{128}})));
   return (p->runs > 1 ? static_cast<int64_t>(p->cut) * p->runs : 0) +
          (p->sink_runs > 1 ? static_cast<int64_t>(a.B) * a.Hk * p->sink_tiles * p->sink_runs : 0);
 }
@@ -893,10 +1014,13 @@ int launch_t(const WindowArgs& a, int* launches) {
   p.lse2 = reinterpret_cast<float*>(a.ws);
   p.dvec = p.lse2 + bh * p.npad;
   p.part = p.dvec + bh * p.npad;
-  *launches = split ? 3 : 2;
+  p.most = reinterpret_cast<float2*>(p.part + split * 2 * 128 * D);
+  *launches = (split ? 3 : 2) + (BF16 ? 0 : 1);
   const int group = order_head_group(static_cast<int>(bh), int64_t{4} * a.Nk * D, int64_t{128} << 20);
-  bool ok = launch_serialized(true, kq, dim3(static_cast<unsigned>(bh * nrows)), dim3(Q::THREADS), Q::SMEM, a.stream, mq, mk, mv, mdo, mo, a,
-                              p, nrows, group) == cudaSuccess;
+  bool ok = BF16 || launch_serialized(true, attn_window_range_kernel<D>, dim3(static_cast<unsigned>(p.blocks), static_cast<unsigned>(heads)),
+                                      dim3(kRangeThreads), 0, a.stream, a, p) == cudaSuccess;
+  ok = ok && launch_serialized(true, kq, dim3(static_cast<unsigned>(bh * nrows)), dim3(Q::THREADS), Q::SMEM, a.stream, mq, mk, mv, mdo, mo, a, p,
+                               nrows, group) == cudaSuccess;
   ok = ok && launch_serialized(true, kk, dim3(static_cast<unsigned>(items)), dim3(K::THREADS), K::SMEM, a.stream, mq, mk, mv, mdo, a, p) ==
                  cudaSuccess;
   if (split) {
@@ -917,7 +1041,7 @@ int launch_d(const WindowArgs& a, int* launches) {
 int64_t window_bwd_workspace(const WindowArgs& a) {
   WbPlan p = {};
   const int64_t split = plan(a, &p);
-  return 2 * static_cast<int64_t>(a.B) * a.Hq * p.npad * 4 + split * 2 * 128 * a.d * 4;
+  return 2 * static_cast<int64_t>(a.B) * a.Hq * p.npad * 4 + split * 2 * 128 * a.d * 4 + static_cast<int64_t>(a.B) * a.Hk * p.blocks * 8;
 }
 
 int launch_window_bwd(const WindowArgs& a, int* launches) {
