@@ -39,18 +39,25 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+void* driver_fn(const char* name) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  return cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                 q == cudaDriverEntryPointSuccess
+             ? p
+             : nullptr;
+}
+
 EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
+  static const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(driver_fn("cuTensorMapEncodeTiled"));
   return fn;
+}
+
+// Whether the thread has a current context (a caller's own among them).
+bool has_context() {
+  static const auto fn = reinterpret_cast<CUresult (*)(CUcontext*)>(driver_fn("cuCtxGetCurrent"));
+  CUcontext ctx = nullptr;
+  return fn && fn(&ctx) == CUDA_SUCCESS && ctx;
 }
 
 // Current device, checked to be compute capability 10.3; returns a status.
@@ -58,12 +65,10 @@ int current_device(int* dev) {
   if (cudaGetDevice(dev) != cudaSuccess) return kStatusCuda;
   if (*dev < 0 || *dev >= kMaxDevices) return kStatusUnsupported;
   // A thread's first call may find no context current (autograd's own threads),
-  // and the encoding of tensor maps, a driver call, wants one.
-  thread_local uint64_t current = 0;
-  if (!((current >> *dev) & 1)) {
-    if (cudaSetDevice(*dev) != cudaSuccess) return kStatusCuda;
-    current |= uint64_t{1} << *dev;
-  }
+  // and the encoding of tensor maps, a driver call, wants one.  One that is current
+  // stays: cudaSetDevice would put the device's primary context in its place, in which
+  // the pointers of a caller's own context mean nothing.
+  if (!has_context() && cudaSetDevice(*dev) != cudaSuccess) return kStatusCuda;
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_arch_ok[*dev] == 0) {
     int major = 0, minor = 0;
