@@ -962,7 +962,10 @@ constexpr int kCutGain = 8;
 void plan_runs(const WindowArgs& a, WbPlan* p) {
   const int64_t sms = 152;  // of the GPU this is for; with others the plan is as good as right
   const int64_t G = a.Hq / a.Hk, heads = static_cast<int64_t>(a.B) * a.Hk, ntq = (a.Nq + 127) / 128;
-  const int64_t near = std::min<int64_t>(ntq, (static_cast<int64_t>(a.window) + 126) / 128 + 1);
+  // Query tiles that see a tile of keys: window + 127 rows, the first of them row
+  // -(Nk - Nq) modulo 128 of its tile.
+  const int64_t in_tile = (128 - (a.Nk - a.Nq) % 128) % 128;
+  const int64_t near = std::min<int64_t>(ntq, (in_tile + a.window + 126) / 128 + 1);
   const int64_t vs = G * ntq, vw = G * near;  // visits of a tile, at most
   p->tiles = (a.Nk + 127) / 128;
   p->sink_tiles = std::min(p->tiles, (a.sinks + 127) / 128);
