@@ -320,13 +320,18 @@ typedef struct {
  *          R * page_size new tokens of one sequence in a step (they would share
  *          slots); of the calls that read a cache only attn_paged_decode_window, with
  *          that window or a narrower one and no more sinks, reads such a sequence rightly.
- * The step is done whole or, if more pages are wanted than are free, if there
- * are more new tokens than rows, or if a length, a count or free_state is out of
- * range, not at all: lengths and free_state as before, token_start 0, slots -1,
- * and ATTN_ERR_DEVICE_CHECK through attn_sync_status.  A page number outside
- * [0, num_pages) in the ring or the table is handed on as -1, with the same
- * status.  With lens and free_out given the step can be taken again from the
- * same state (the ring and the table keep what it needs).
+ * The step is done whole or not at all: lengths and free_state as before,
+ * token_start 0, slots -1, and ATTN_ERR_DEVICE_CHECK through attn_sync_status.  It
+ * is not done if
+ *   - more pages are wanted than are free,
+ *   - the pages that are free before the step and those that come back in it are
+ *     more than free_cap, also where the step takes some, whose numbers the ring
+ *     keeps (a ring of num_pages entries is never too small),
+ *   - there are more new tokens than rows, or
+ *   - a length, a count or free_state is out of range.
+ * A page number outside [0, num_pages) in the ring or the table is handed on as
+ * -1, with the same status.  With lens and free_out given the step can be taken
+ * again from the same state (the ring and the table keep what it needs).
  *   workspace : attn_paged_assign_workspace() bytes, as for attn_paged_decode.
  * Launches 1 or 2 kernels.
  */

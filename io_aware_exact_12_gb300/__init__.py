@@ -519,7 +519,9 @@ def attn_paged_assign(kv, n_new, free_pages, free_state, lens=None, free_out=Non
     last.  rows is the most new tokens there may be (None: slots' size, or one
     per sequence).  With a window (and sinks) a sequence keeps the pages that
     they need and writes them again in turns.  A step that cannot be done whole is
-    not done at all, and sync_status() says so."""
+    not done at all, and sync_status() says so: too few free pages or rows, a
+    length or count out of range, or a ring without room for the pages that are free
+    before the step and those that come back in it (one of all pages has it)."""
     return _paged_call("assign", kv, stream, n_new, free_pages, free_state, lens, free_out, token_start, slots, rows, window,
                        sinks)
 
