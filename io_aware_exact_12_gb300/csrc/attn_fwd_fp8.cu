@@ -356,12 +356,14 @@ __global__ void __launch_bounds__(Fp8Cfg::THREADS, 1)
       {
         float a0 = sv[0], a1 = sv[1], a2 = sv[2], a3 = sv[3];
 #pragma unroll
-        for (int c = 4; c < 128; c += 8) {
+        for (int c = 4; c < 124; c += 8) {
           a0 = max3f(a0, sv[c], sv[c + 1]);
           a1 = max3f(a1, sv[c + 2], sv[c + 3]);
           a2 = max3f(a2, sv[c + 4], sv[c + 5]);
           a3 = max3f(a3, sv[c + 6], sv[c + 7]);
         }
+        a0 = max3f(a0, sv[124], sv[125]);
+        a1 = max3f(a1, sv[126], sv[127]);
         mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
       }
       const float m_new = fmaxf(m, mx * sl2);
