@@ -133,7 +133,8 @@ struct DqCfg : Tile<D> {
   static constexpr int B_DP = B_S + 2;
   static constexpr int B_TAKEN = B_DP + 1;     // dP is in registers
   static constexpr int B_DS = B_TAKEN + 1;     // dS(n) is in buffer n & 1
-  static constexpr int B_OUT = B_DS + 2;       // the item's dQ is complete
+  static constexpr int B_READ_DS = B_DS + 2;   // dQ(n), which reads buffer n & 1, is complete
+  static constexpr int B_OUT = B_READ_DS + 2;  // the item's dQ is complete
   static constexpr int B_ROWS = B_OUT + 1;     // both halves of the rows' D are in shared memory
   static constexpr int B_NEXT = B_ROWS + 1;
   static constexpr int B_READ = B_NEXT + 2;
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
       const uint32_t id_dq = instr_desc_f16(128, D, BF16, false, true);
       const uint32_t q_lo = smem_desc_lo(sbase, 16), do_lo = smem_desc_lo(sDO, 16);
       bool ok = true;
-      int n0 = 0, before1 = 0, before2 = 0;  // places in the K ring of S(is - 1) and S(is - 2)
+      int n0 = 0;
       IdleWatch watch;
       for (int i = blockIdx.x, k = 0; ok && i >= 0; ++k) {
         const int end = n0 + RowItem(a, i, nrows, group).npos;
@@ -399,9 +400,8 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
             ++ip;
             progress = true;
           }
-          if (is < end && is <= iq + 1 && (is < 2 || mbar_probe(bar(C::B_KEMPTY + before2 % C::NK), (before2 / C::NK) & 1)) &&
+          if (is < end && is <= iq + 1 && (is < 2 || mbar_probe(bar(C::B_READ_DS + (is & 1)), (is / 2 - 1) & 1)) &&
               mbar_probe(bar(C::B_KFULL + (is + ahead) % C::NK), ((is + ahead) / C::NK) & 1)) {
-            before2 = before1, before1 = is + ahead;
             tc_fence_after_sync();
             const uint32_t k_lo = smem_desc_lo(sK + ((is + ahead) % C::NK) * C::TILE, 16);
 #pragma unroll
@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, 1)
               mma_ts_w(tmem + C::T_DQ, tmem + C::T_S + (iq & 1) * 128 + half_step(kk), k_lo + mn_step<D>(kk), HI, id_dq,
                        (iq > n0 || kk > 0) ? 1u : 0u);
             tc_commit(bar(C::B_KEMPTY + (iq + ahead) % C::NK));
+            tc_commit(bar(C::B_READ_DS + (iq & 1)));
             if (++iq == end) tc_commit(bar(C::B_OUT));
             progress = true;
           }

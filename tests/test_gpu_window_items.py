@@ -57,6 +57,17 @@ def test_whole_tiles_cut_tiles_and_runs_of_sinks(pkg):
     assert partial > 13 * 8 and (partial - 13 * 8) % 15 == 0
 
 
+@pytest.mark.parametrize("d,dtype", [(32, F16), (64, BF16), (64, F16), (128, BF16)])
+@pytest.mark.parametrize("B,H,n", [(300, 12, 100), (200, 12, 129), (400, 8, 1)])
+def test_items_of_one_tile(pkg, B, H, n, d, dtype):
+    """Items that see one tile of keys follow one another in a block: each hands its stages on while the next has begun."""
+    x = _inputs(B, H, H, n, n, d, dtype, "heads", n)
+    first = _check(pkg, *x, 1000, 0)
+    for _ in range(40):
+        _same(_both(pkg, *x, 1000, 0, scale=1 / math.sqrt(d)), first)
+    assert pkg.sync_status() == 0
+
+
 @pytest.mark.parametrize("B,Hq,Hk,nq,nk,d,dtype,window,sinks", [
     (1, 8, 2, 5000, 5000, 128, BF16, 300, 4),
     (1, 8, 2, 5000, 5000, 64, F16, 300, 4),
