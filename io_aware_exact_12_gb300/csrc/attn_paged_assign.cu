@@ -19,10 +19,11 @@
 //       row, its slot, and the table entry where it is a page's first; then the pages
 //       of ended sequences.
 //
-// Few bytes and no arithmetic to speak of: latency bounds it, a handful of dependent
-// loads in the one block, as many in the fill.  A step of 64 sequences takes 4.3 us a
-// call, one of 4096 with 962000 new tokens 20.6 (plan 10, fill 12; its 8.4 MB would
-// take 1.3).  What counted (33 -> 20.6): one round of sums, taken back if a check
+// Few bytes and no arithmetic to speak of.  A step of 64 sequences, 4.6 us a call, is a
+// launch and a handful of dependent loads in the one block.  One of 4096 with 962000 new
+// tokens takes 20.5 (plan 10, fill 12; its 8.4 MB would take 1.3): the sums are one
+// block's, in four rounds, and the fill searches, looks up and stores for each token (issue
+// active 56 %).  What counted (33 -> 20.5): one round of sums, taken back if a check
 // fails, instead of one round of checks and another of sums; a thread's rows in
 // flight together; divisions by the page size as products.
 #include "attn_paged.h"

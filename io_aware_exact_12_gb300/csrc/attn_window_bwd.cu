@@ -22,19 +22,19 @@
 // cycles a visit against 4000 of the five products, although the L2 alone takes such
 // a tile from every SM in 3000, and the accumulator's zeros and its conversion cost
 // another tenth.  Two sequences of 8192, 16 / 4 heads of 128, window 1024, 4 sinks:
-// 624 us that way, 488 so (dQ 223, dK and dV 256, sums 13); eight of 1024, 12 heads of
+// 624 us that way, 504 so (dQ 232, dK and dV 266, sums 13); eight of 1024, 12 heads of
 // 64, window 256: 88 and 77.  No sum depends on the order of CTAs, so a call repeats
 // bit for bit.
 //
-// What bounds both loops is how fast the tensor core takes 128 x 128 x 16 products: 96
-// cycles with an operand from TMEM, 118 with both from shared memory (whose 8 KB are
-// 64 cycles of its bandwidth), whether 64 or 128 columns wide: 2700 cycles a tile for
-// dQ, of the 3300 that it takes, 3400 for dK and dV, of 3700; an item's start and end
-// are the rest.
+// What bounds both loops is a tile's chain, S and dP, the rows' P and dS, the products
+// that take those: with one CTA to an SM the tensor pipe waits for the rows and they
+// for it.  The products, 128 x 128 x 16 in 64 cycles each at d = 128, are 1536 cycles of
+// the 3450 that a tile of dQ takes (pipe active 44 %), 2048 of 3800 for dK and dV (54 %).
 //
 // P and dS are fp32 until they become operands of 16-bit products, rounded to the
-// inputs' type (fp16: times powers of two); everything is summed in fp32.  (Gradients are off by 2.4e-3 in norm
-// with bf16, where fp32 operands and the results' own rounding make 1.7e-3.)
+// inputs' type (fp16: times powers of two); everything is summed in fp32.  (Gradients
+// are off by 2.4e-3 in norm with bf16, where fp32 operands and the results' own rounding
+// make 1.7e-3; fp16 3.0e-4 and 2.2e-4.)
 //
 // Both loops run on tcgen05, one CTA to an SM: warps 0-7 work on rows, two threads to
 // each, 64 columns a thread; warp 8 loads by TMA; one thread of warp 9 issues the

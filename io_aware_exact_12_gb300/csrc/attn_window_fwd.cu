@@ -8,12 +8,14 @@
 // loaded or multiplied, and only the tiles at either edge of the window and those
 // that end the sinks are masked, key by key.
 //
-// The tensor cores bound it (4 d flops a pair against 4 d bytes a key for 128
-// rows): a tile of 128 keys at d = 128 is 16 products of 128 x 128 x 16, which take 118
-// cycles each from shared memory and 96 with P from TMEM, 1700 in all, and goes by in
-// 1900 where the list is long (32768 queries, 32 / 8 heads, window 4096: 1.74 ms, 1190
-// TFLOP/s of visible pairs); edge tiles, half of which is hidden, and an item's start
-// and end make window 1024 slower (8192 queries: 152 us, 850).  GB300 mapping:
+// A tile's chain bounds it: S, the softmax of its rows, P, P V, each behind the one
+// before, in two CTAs to an SM that cover one another in part.  A tile of 128 keys at
+// d = 128 is 16 products of 128 x 128 x 16, 64 cycles each; where the list is long it
+// goes by in 2000 cycles, the tensor pipe active 50 % of them (32768 queries, 32 / 8
+// heads, window 4096: 1.81 ms, 1140 TFLOP/s of visible pairs).  At window 1024 it takes
+// 2280 (42 %): edge tiles, half of which is hidden, and an item's start and end (8192
+// queries: 152 us, 850).  At d = 128 the row threads spill 72 to 76 bytes, the clusters'
+// form 40 to 56 at every d.  GB300 mapping:
 //   * an item is 128 query rows of a head; two CTAs to an SM, so that one's softmax
 //     meets the other's matrix products.  Blocks take over the items of blocks that
 //     have not started (cluster launch control) and load the next item's first tiles
@@ -204,9 +206,8 @@ __global__ void __launch_bounds__(WfCfg<D>::THREADS, WfCfg<D>::CTAS)
       // A chain S, P V, S, P V, ...; whichever next step is ready goes out.  At d = 128
       // S(p + 1) overwrites the P that P V(p) reads, so it waits for that to complete:
       // MMAs run in the order of issue where they have one accumulator, no others are
-      // promised to.  (The wait costs nothing that shows: 152 us and 1.77 ms in the cases
-      // above with it and without; fp16 0.7 %.)  K and V stages
-      // and Q are handed back by the softmax, whose waits tell when the MMAs that read
+      // promised to.  (The wait costs nothing that shows with bf16, 0.7 % with fp16.)  K
+      // and V stages and Q are handed back by the softmax, whose waits tell when the MMAs that read
       // them are complete.  An item's first P V overwrites the O of the one before,
       // which the threads that wrote this P have read.
       constexpr uint32_t HI = smem_desc_hi(C::SBO, C::SWZ);
